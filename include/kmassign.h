@@ -355,6 +355,137 @@ int kmassign_topk_ex(const void *X, const void *C, const float *cnorm, int64_t N
                      int32_t ksplit, void *stream);
 
 /*
+ * ---- Learned assignments --------------------------------------------------
+ * The operators around an assignment that is trained by gradient: the rows a
+ * point goes to (kmassign_route), what those rows hold (kmassign_lookup), the
+ * gradients of both, the inverted lists of any assignment (kmassign_lists) and
+ * the clipping of gradients (kmassign_clip).  They follow the rules above
+ * (row-major contiguous device buffers, asynchronous on `stream`, temporaries
+ * from the library's stream-ordered pool, errors before any launch), with two
+ * differences: floating buffers are of one of the types below, and pointers
+ * need only be aligned to their elements (16-byte aligned rows are fastest).
+ * Every result is the same from run to run: no sum is formed by atomics on
+ * floating values.  Outputs must not overlap inputs unless said so.
+ */
+enum kmassign_dtype { KMASSIGN_FP32 = 0, KMASSIGN_BF16 = 1, KMASSIGN_FP16 = 2 };
+enum kmassign_score { KMASSIGN_SOFTMAX = 0, KMASSIGN_SIGMOID = 1 };
+
+/* Largest E kmassign_route accepts. */
+#define KMASSIGN_ROUTE_MAX 1024
+
+/*
+ * Routing: the k experts (rows, codes) of each point and their weights.
+ *   logits   dtype [N, E]; x = logits[i] widened to fp32.  An expert with x
+ *            = -inf or NaN is masked: score 0, never selected
+ *   score    KMASSIGN_SOFTMAX: s = softmax of x over the unmasked experts;
+ *            KMASSIGN_SIGMOID: s = 1 / (1 + exp(-x))
+ *   bias     fp32 [E] or NULL.  Experts are ordered by the fp32 sum s + bias,
+ *            or without a bias by x (the order of s without its rounding);
+ *            a key of -inf or NaN is never selected; equal keys: lower index
+ *            first.  The bias changes the choice only, not the weights
+ *   groups   1 to 32, dividing E: group g holds the experts [g E / groups,
+ *            (g + 1) E / groups).  With topk_groups < groups only the
+ *            topk_groups best groups take part, by the sum of their group_top
+ *            (1 or 2) best keys (without a bias and for group_top = 2: of
+ *            their best scores; a missing second one counts 0; a group with
+ *            nothing selectable comes last; lower index first on ties)
+ *   k        1 <= k <= min(E, 32, topk_groups * E / groups)
+ *   idx      int32 [N, k], written: the selected experts by descending key; -1
+ *            where fewer than k can be selected (all of a fully masked row)
+ *   weights  fp32 [N, k], written: scale * s, or with renorm = 1 scale * s /
+ *            (sum of the row's selected s); 0 at idx -1, and where a sigmoid
+ *            row's sum is 0.  The renormalised softmax is taken over the
+ *            selection, so it does not underflow.  A +inf logit makes the
+ *            softmax weights of its row NaN, as the formula does
+ * N = 0 launches nothing.  Errors: N, E or N * k out of range
+ * KMASSIGN_ERR_SHAPE; k, groups, a flag, a type or a non-finite scale
+ * KMASSIGN_ERR_ARG.
+ */
+int kmassign_route(const void *logits, int32_t dtype, int64_t N, int64_t E, int32_t k,
+                   int32_t score, const float *bias, int32_t groups, int32_t topk_groups,
+                   int32_t group_top, int32_t renorm, float scale, int32_t *idx, float *weights,
+                   void *stream);
+
+/*
+ * Gradient of kmassign_route's weights with respect to the logits, for the
+ * choice idx it made (the choice itself has no gradient; the bias none).
+ *   idx       int32 [N, k]: distinct experts in each row; ids outside [0, E)
+ *             are skipped
+ *   dweights  fp32 [N, k]; what stands at skipped ids is ignored
+ *   dlogits   dtype [N, E], every element written (0 where there is none)
+ * logits, dtype, N, E, k (<= min(E, 32)), score, renorm, scale, errors: as in
+ * kmassign_route.
+ */
+int kmassign_route_grad(const void *logits, int32_t dtype, int64_t N, int64_t E, int32_t k,
+                        int32_t score, int32_t renorm, float scale, const int32_t *idx,
+                        const float *dweights, void *dlogits, void *stream);
+
+/*
+ * Inverted lists: the positions of idx grouped by the row they name.
+ *   idx      int32 [M], 0 <= M < 2^31; ids outside [0, K) are left out
+ *   order    int32 [M], written: the positions i sorted by (idx[i], i); -1
+ *            after the last valid one
+ *   offsets  int32 [K + 1], written: row r's positions are order[offsets[r] ..
+ *            offsets[r + 1]); offsets[K] is the number of valid ids
+ */
+int kmassign_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *order, int32_t *offsets,
+                   void *stream);
+
+/*
+ * Lookup: out[i] = scale * sum over j < k of w[i][j] * table[idx[i][j]].
+ *   table    dtype [K, D], 1 <= D <= 65536
+ *   idx      int32 [N, k], N * k < 2^31; ids outside [0, K) add nothing (and
+ *            their weights are not read into the sum)
+ *   weights  fp32 [N, k], or NULL: all 1
+ *   out      dtype [N, D], written; fp32 sums over j in order, rounded once
+ */
+int kmassign_lookup(const void *table, int32_t dtype, int64_t K, int64_t D, const int32_t *idx,
+                    const float *weights, int64_t N, int32_t k, float scale, void *out,
+                    void *stream);
+
+/*
+ * Gradients of kmassign_lookup:
+ *     dtable[r]      = scale * sum over idx[i][j] == r of w[i][j] * dout[i]
+ *     dweights[i][j] = scale * <dout[i], table[idx[i][j]]>   (0 at skipped ids)
+ *   dout        dtype [N, D]
+ *   table       dtype [K, D]; only read for dweights (NULL without it)
+ *   padding     a row whose dtable stays 0 (accumulating: untouched), or -1
+ *   accumulate  0: every row of dtable is written (0 where no id names it);
+ *               1: the gradient is added to what dtable holds, rows without
+ *               an id are not touched
+ *   dtable      grad_dtype [K, D], or NULL; grad_dtype is KMASSIGN_FP32 or dtype
+ *   dweights    fp32 [N, k], or NULL (not both NULL)
+ * The ids are sorted by row first; sums are fp32 in an order fixed by the
+ * sizes, each element rounded once.  N = 0 zeroes dtable (accumulate 0).
+ */
+int kmassign_lookup_grad(const void *dout, int32_t dtype, const int32_t *idx, const float *weights,
+                         const void *table, int64_t N, int32_t k, int64_t K, int64_t D,
+                         float scale, int32_t padding, int32_t accumulate, void *dtable,
+                         int32_t grad_dtype, float *dweights, void *stream);
+
+/*
+ * norm = sqrt(sum of the squares of all elements of n tensors) (fp32, formed
+ * in fp64 above 64 bytes at a time: right over the whole range of the types).
+ *   grads   HOST array of n device pointers (NULL allowed for empty tensors)
+ *   sizes   host array of n element counts, >= 0
+ *   dtypes  host array of n kmassign_dtype values
+ *   norm    device fp32 [1], written (0 for n = 0)
+ * The host arrays are read before the call returns.
+ */
+int kmassign_grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                       int32_t n, float *norm, void *stream);
+
+/*
+ * Clipping by the global norm: with norm as above and
+ *     c = min(1, max_norm / (norm + 1e-6))   (NaN where the quotient is NaN)
+ * writes c * grads[i] (fp32 product, rounded once) to out[i], of the same type
+ * and size.  out: HOST array of n device pointers (out[i] may equal grads[i]),
+ * or NULL: in place, where c = 1 writes nothing.  max_norm >= 0.
+ */
+int kmassign_clip(const void *const *grads, void *const *out, const int64_t *sizes,
+                  const int32_t *dtypes, int32_t n, float max_norm, float *norm, void *stream);
+
+/*
  * Bound, in nanoseconds of the GPU's global timer, on every pipeline wait in
  * the kernels launched afterwards by this process (0 restores the default,
  * 2 s).  A wait that runs out aborts its kernel cleanly and makes

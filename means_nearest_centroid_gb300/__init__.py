@@ -26,6 +26,8 @@ __all__ = [
     "kmassign_noalloc", "kmassign_set_wait_timeout", "shard_rows", "kmassign_update",
     "kmassign_centroids", "kmassign_lloyd",
     "kmassign_plan", "kmassign_plan_for", "kmassign_check", "kmassign_strerror", "assign", "norms", "assign_host",
+    "kmassign_route", "kmassign_route_grad", "kmassign_lists", "kmassign_lookup",
+    "kmassign_lookup_grad", "kmassign_grad_norm", "kmassign_clip",
     "STATUS",
 ]
 
@@ -91,6 +93,23 @@ def _declare(lib):
     lib.kmassign_topk.restype = i32
     lib.kmassign_topk_ex.argtypes = [vp, vp, vp, i64, i64, i64, i32, vp, vp, i32, i32, vp]
     lib.kmassign_topk_ex.restype = i32
+    f32 = ctypes.c_float
+    lib.kmassign_route.argtypes = [vp, i32, i64, i64, i32, i32, vp, i32, i32, i32, i32, f32, vp,
+                                   vp, vp]
+    lib.kmassign_route.restype = i32
+    lib.kmassign_route_grad.argtypes = [vp, i32, i64, i64, i32, i32, i32, f32, vp, vp, vp, vp]
+    lib.kmassign_route_grad.restype = i32
+    lib.kmassign_lists.argtypes = [vp, i64, i64, vp, vp, vp]
+    lib.kmassign_lists.restype = i32
+    lib.kmassign_lookup.argtypes = [vp, i32, i64, i64, vp, vp, i64, i32, f32, vp, vp]
+    lib.kmassign_lookup.restype = i32
+    lib.kmassign_lookup_grad.argtypes = [vp, i32, vp, vp, vp, i64, i32, i64, i64, f32, i32, i32,
+                                         vp, i32, vp, vp]
+    lib.kmassign_lookup_grad.restype = i32
+    lib.kmassign_grad_norm.argtypes = [vp, vp, vp, i32, vp, vp]
+    lib.kmassign_grad_norm.restype = i32
+    lib.kmassign_clip.argtypes = [vp, vp, vp, vp, i32, f32, vp, vp]
+    lib.kmassign_clip.restype = i32
     lib.kmassign_set_wait_timeout.argtypes = [ctypes.c_uint64]
     lib.kmassign_set_wait_timeout.restype = i32
     lib.kmassign_check.argtypes = [vp]
@@ -363,6 +382,276 @@ def kmassign_lloyd(X, C, iters: int, idx=None, stream=None):
     _check(library().kmassign_lloyd(_ptr(X), _ptr(C), N, K, D, int(iters), _ptr(idx),
                                     _stream_ptr(stream, X.device)), "kmassign_lloyd")
     return idx
+
+
+# ---- learned assignments: routing, lookup, inverted lists, clipping ----------
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _need_float(t, name) -> int:
+    """The kmassign_dtype of a contiguous CUDA tensor of a supported type."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous():
+        code = _DTYPES.get(t.dtype)
+        if code is not None:
+            return code
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _need_shape(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _score_code(score) -> int:
+    code = _SCORES.get(score)
+    if code is None:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    return code
+
+
+def _need_matrix(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
+    return t.shape
+
+
+def _need_ids(idx):
+    """N and k of ids [N] (one a point) or [N, k]."""
+    _need_cuda(idx, "idx", torch.int32)
+    if idx.dim() == 1:
+        return idx.shape[0], 1
+    if idx.dim() == 2:
+        return idx.shape
+    raise ValueError(f"idx must have one or two dimensions, got {idx.dim()}")
+
+
+def kmassign_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1,
+                   topk_groups: int | None = None, group_top: int = 2, renorm: bool = True,
+                   scale: float = 1.0, idx=None, weights=None, stream=None):
+    """The k experts (rows) of every point: (idx int32 [N, k], weights fp32 [N, k]).
+
+    ``logits`` is fp32, bf16 or fp16 [N, E] (E <= 1024); an expert whose logit
+    is -inf or NaN is masked.  ``score`` is "softmax" or "sigmoid"; ``bias``
+    (fp32 [E]) is added to the scores for the choice only.  With
+    ``topk_groups`` < ``groups`` the choice is made within the best groups, by
+    the sum of each group's ``group_top`` (1 or 2) best keys.  Row i lists its
+    experts by descending key, lower index first on ties, and -1 (weight 0)
+    where fewer than k can be selected.  The weights are the scores, divided
+    by their sum over the selection with ``renorm``, times ``scale``.  See
+    ``kmassign_route`` in ``include/kmassign.h``.
+    """
+    dtype = _need_float(logits, "logits")
+    N, E = _need_matrix(logits, "logits")
+    k, groups = int(k), int(groups)
+    if bias is not None:
+        _need_cuda(bias, "bias", torch.float32)
+        _need_shape(bias, "bias", (E,))
+    if idx is None:
+        idx = torch.empty((N, max(k, 0)), dtype=torch.int32, device=logits.device)
+    else:
+        _need_cuda(idx, "idx", torch.int32)
+        _need_shape(idx, "idx", (N, k))
+    if weights is None:
+        weights = torch.empty((N, max(k, 0)), dtype=torch.float32, device=logits.device)
+    else:
+        _need_cuda(weights, "weights", torch.float32)
+        _need_shape(weights, "weights", (N, k))
+    rc = library().kmassign_route(
+        logits.data_ptr(), dtype, N, E, k, _score_code(score), _ptr(bias), groups,
+        groups if topk_groups is None else int(topk_groups), int(group_top), int(bool(renorm)),
+        float(scale), idx.data_ptr(), weights.data_ptr(), _stream_ptr(stream, logits.device))
+    _check(rc, "kmassign_route")
+    return idx, weights
+
+
+def kmassign_route_grad(logits, idx, dweights, score: str = "softmax", renorm: bool = True,
+                        scale: float = 1.0, dlogits=None, stream=None):
+    """The gradient of the logits [N, E] (their type) from that of the weights.
+
+    ``idx`` (int32 [N, k], distinct in each row; ids outside [0, E) skipped) is
+    the choice ``kmassign_route`` made with the same ``score``, ``renorm`` and
+    ``scale``; ``dweights`` is fp32 [N, k].
+    """
+    dtype = _need_float(logits, "logits")
+    N, E = _need_matrix(logits, "logits")
+    _need_cuda(idx, "idx", torch.int32)
+    k = _need_matrix(idx, "idx")[1]
+    _need_shape(idx, "idx", (N, k))
+    _need_cuda(dweights, "dweights", torch.float32)
+    _need_shape(dweights, "dweights", (N, k))
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    else:
+        _need_cuda(dlogits, "dlogits", logits.dtype)
+        _need_shape(dlogits, "dlogits", (N, E))
+    rc = library().kmassign_route_grad(
+        logits.data_ptr(), dtype, N, E, k, _score_code(score), int(bool(renorm)), float(scale),
+        idx.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(),
+        _stream_ptr(stream, logits.device))
+    _check(rc, "kmassign_route_grad")
+    return dlogits
+
+
+def kmassign_lists(idx, K: int, order=None, offsets=None, stream=None):
+    """Inverted lists of ids: (order int32 [M], offsets int32 [K + 1]).
+
+    ``idx`` is int32 of any shape, M ids in all; row r's (flat) positions are
+    ``order[offsets[r]:offsets[r + 1]]``, ascending.  Ids outside [0, K) are
+    left out, and as many places at the end of ``order`` hold -1.
+    """
+    _need_cuda(idx, "idx", torch.int32)
+    M, K = idx.numel(), int(K)
+    if order is None:
+        order = torch.empty(M, dtype=torch.int32, device=idx.device)
+    else:
+        _need_cuda(order, "order", torch.int32)
+        _need_shape(order, "order", (M,))
+    if offsets is None:
+        offsets = torch.empty(max(K, 0) + 1, dtype=torch.int32, device=idx.device)
+    else:
+        _need_cuda(offsets, "offsets", torch.int32)
+        _need_shape(offsets, "offsets", (K + 1,))
+    rc = library().kmassign_lists(idx.data_ptr(), M, K, order.data_ptr(), offsets.data_ptr(),
+                                  _stream_ptr(stream, idx.device))
+    _check(rc, "kmassign_lists")
+    return order, offsets
+
+
+def kmassign_lookup(table, idx, weights=None, scale: float = 1.0, out=None, stream=None):
+    """out[i] = scale * sum_j weights[i, j] * table[idx[i, j]], in the table's type.
+
+    ``table`` is fp32, bf16 or fp16 [K, D]; ``idx`` int32 [N] (one row a
+    point) or [N, k]; ``weights`` fp32 of idx's shape, or None for all 1.  Ids
+    outside [0, K) add nothing.  Returns out [N, D].
+    """
+    dtype = _need_float(table, "table")
+    K, D = _need_matrix(table, "table")
+    N, k = _need_ids(idx)
+    if weights is not None:
+        _need_cuda(weights, "weights", torch.float32)
+        _need_shape(weights, "weights", idx.shape)
+    if out is None:
+        out = torch.empty((N, D), dtype=table.dtype, device=table.device)
+    else:
+        _need_cuda(out, "out", table.dtype)
+        _need_shape(out, "out", (N, D))
+    rc = library().kmassign_lookup(table.data_ptr(), dtype, K, D, idx.data_ptr(), _ptr(weights),
+                                   N, k, float(scale), out.data_ptr(),
+                                   _stream_ptr(stream, table.device))
+    _check(rc, "kmassign_lookup")
+    return out
+
+
+def kmassign_lookup_grad(dout, idx, K: int, weights=None, table=None, scale: float = 1.0,
+                         padding: int = -1, dtable=None, accumulate: bool = False, dtype=None,
+                         dweights=None, stream=None):
+    """Gradients of ``kmassign_lookup``: (dtable [K, D], dweights or None).
+
+    ``dout`` is fp32, bf16 or fp16 [N, D].  ``dtable`` is allocated in
+    ``dtype`` (fp32, the default, or dout's type) unless given; with
+    ``accumulate`` the gradient is added to a given one.  The row ``padding``
+    takes no gradient.  The gradient of the weights (fp32, idx's shape) is
+    formed when ``weights`` are given, and needs ``table`` (dout's type).
+    """
+    code = _need_float(dout, "dout")
+    N, D = _need_matrix(dout, "dout")
+    rows, k = _need_ids(idx)
+    if rows != N:
+        raise ValueError("idx must hold one row of ids per row of dout")
+    K = int(K)
+    if weights is not None:
+        _need_cuda(weights, "weights", torch.float32)
+        _need_shape(weights, "weights", idx.shape)
+        if table is None:
+            raise ValueError("the gradient of the weights needs the table")
+        _need_cuda(table, "table", dout.dtype)
+        _need_shape(table, "table", (K, D))
+        if dweights is None:
+            dweights = torch.empty(idx.shape, dtype=torch.float32, device=dout.device)
+        else:
+            _need_cuda(dweights, "dweights", torch.float32)
+            _need_shape(dweights, "dweights", idx.shape)
+    elif dweights is not None:
+        raise ValueError("dweights needs weights")
+    if dtable is None:
+        if accumulate:
+            raise ValueError("accumulate needs a given dtable")
+        dtable = torch.empty((max(K, 0), D), dtype=dtype or torch.float32, device=dout.device)
+    elif dtype is not None and dtable.dtype != dtype:
+        raise TypeError(f"dtable must be {dtype}, got {dtable.dtype}")
+    grad = _need_float(dtable, "dtable")
+    _need_shape(dtable, "dtable", (K, D))
+    rc = library().kmassign_lookup_grad(
+        dout.data_ptr(), code, idx.data_ptr(), _ptr(weights),
+        table.data_ptr() if weights is not None else None, N, k, K, D, float(scale), int(padding),
+        int(bool(accumulate)), dtable.data_ptr(), grad, _ptr(dweights),
+        _stream_ptr(stream, dout.device))
+    _check(rc, "kmassign_lookup_grad")
+    return dtable, dweights
+
+
+def _tensor_arrays(tensors, name):
+    """Pointers, sizes and type codes of a list of tensors, as C arrays."""
+    codes = [_need_float(t, name) for t in tensors]
+    n = len(codes)
+    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors])
+    sizes = (ctypes.c_int64 * n)(*[t.numel() for t in tensors])
+    return ptrs, sizes, (ctypes.c_int32 * n)(*codes), n
+
+
+def _norm_out(tensors, norm):
+    if norm is None:
+        return torch.empty((), dtype=torch.float32,
+                           device=tensors[0].device if tensors else "cuda")
+    _need_cuda(norm, "norm", torch.float32)
+    if norm.numel() != 1:
+        raise ValueError("norm must hold one element")
+    return norm
+
+
+def kmassign_grad_norm(tensors, norm=None, stream=None):
+    """The 2-norm over all elements of a list of tensors, an fp32 scalar on the GPU."""
+    tensors = list(tensors)
+    ptrs, sizes, codes, n = _tensor_arrays(tensors, "tensors")
+    norm = _norm_out(tensors, norm)
+    rc = library().kmassign_grad_norm(ptrs, sizes, codes, n, norm.data_ptr(),
+                                      _stream_ptr(stream, norm.device))
+    _check(rc, "kmassign_grad_norm")
+    return norm
+
+
+def kmassign_clip(grads, max_norm: float, out=None, norm=None, stream=None):
+    """Clip a list of gradients by their global norm; returns the norm (fp32 scalar).
+
+    Each gradient (fp32, bf16 or fp16) is multiplied by min(1, max_norm /
+    (norm + 1e-6)): in place, or into ``out``, a list of tensors of the same
+    shapes and types.
+    """
+    grads = list(grads)
+    ptrs, sizes, codes, n = _tensor_arrays(grads, "grads")
+    outs = None
+    if out is not None:
+        out = list(out)
+        if len(out) != n:
+            raise ValueError("out must hold one tensor per gradient")
+        for g, o in zip(grads, out):
+            _need_cuda(o, "out", g.dtype)
+            if o.shape != g.shape:
+                raise ValueError("out must have the gradients' shapes")
+        outs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
+    norm = _norm_out(grads, norm)
+    rc = library().kmassign_clip(ptrs, outs, sizes, codes, n, float(max_norm), norm.data_ptr(),
+                                 _stream_ptr(stream, norm.device))
+    _check(rc, "kmassign_clip")
+    return norm
 
 
 def kmassign_set_wait_timeout(ns: int) -> None:

@@ -10,9 +10,49 @@
 #include <cstdint>
 #include <mutex>
 
+namespace kma {
+
+// Host or foreign pointers would make the copy engine fault: reject them.
+// Every non-NULL pointer must be device (or managed) memory of one device;
+// that device is made current for this library's runtime before launching
+// (the caller's framework may track its current device separately), and the
+// entry point's DeviceRestore puts the caller's current device back.
+int check_device_ptrs(const void *const *ptrs, int n)
+{
+    int owner = -1;
+    for (int i = 0; i < n; ++i) {
+        if (ptrs[i] == nullptr)
+            continue;
+        cudaPointerAttributes a;
+        if (cudaPointerGetAttributes(&a, ptrs[i]) != cudaSuccess) {
+            cudaGetLastError();
+            return KMASSIGN_ERR_NOT_DEVICE;
+        }
+        if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged)
+            return KMASSIGN_ERR_NOT_DEVICE;
+        if (a.type == cudaMemoryTypeDevice) {
+            if (owner >= 0 && a.device != owner)
+                return KMASSIGN_ERR_NOT_DEVICE;
+            owner = a.device;
+        }
+    }
+    if (owner >= 0) {
+        int cur = -1;
+        if (cudaGetDevice(&cur) != cudaSuccess)
+            return KMASSIGN_ERR_CUDA;
+        if (cur != owner && cudaSetDevice(owner) != cudaSuccess)
+            return KMASSIGN_ERR_CUDA;
+    }
+    return KMASSIGN_OK;
+}
+
+}  // namespace kma
+
 namespace {
 
 using kma::AssignParams;
+using kma::check_device_ptrs;
+using kma::DeviceRestore;
 
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;   // 2 s per pipeline wait
 constexpr int kMaxDevices = 64;
@@ -55,6 +95,8 @@ int current_device_info(DeviceInfo *out)
             for (int kb = 1; kb <= 4; ++kb)
                 if (kma::topk_prepare(kb, list, static_cast<size_t>(d.smem_optin)) != cudaSuccess)
                     return KMASSIGN_ERR_CUDA;
+        if (kma::lists_prepare() != cudaSuccess)
+            return KMASSIGN_ERR_CUDA;
         cudaMemPoolProps props = {};
         props.allocType = cudaMemAllocationTypePinned;
         props.location.type = cudaMemLocationTypeDevice;
@@ -131,65 +173,6 @@ bool aligned(const void *p, uintptr_t a)
 {
     return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
-
-// Host or foreign pointers would make the copy engine fault: reject them.
-// Every non-NULL pointer must be device (or managed) memory of one device;
-// that device is made current for this library's runtime before launching
-// (the caller's framework may track its current device separately), and the
-// entry point's DeviceRestore puts the caller's current device back.
-int check_device_ptrs(const void *const *ptrs, int n)
-{
-    int owner = -1;
-    for (int i = 0; i < n; ++i) {
-        if (ptrs[i] == nullptr)
-            continue;
-        cudaPointerAttributes a;
-        if (cudaPointerGetAttributes(&a, ptrs[i]) != cudaSuccess) {
-            cudaGetLastError();
-            return KMASSIGN_ERR_NOT_DEVICE;
-        }
-        if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged)
-            return KMASSIGN_ERR_NOT_DEVICE;
-        if (a.type == cudaMemoryTypeDevice) {
-            if (owner >= 0 && a.device != owner)
-                return KMASSIGN_ERR_NOT_DEVICE;
-            owner = a.device;
-        }
-    }
-    if (owner >= 0) {
-        int cur = -1;
-        if (cudaGetDevice(&cur) != cudaSuccess)
-            return KMASSIGN_ERR_CUDA;
-        if (cur != owner && cudaSetDevice(owner) != cudaSuccess)
-            return KMASSIGN_ERR_CUDA;
-    }
-    return KMASSIGN_OK;
-}
-
-// Puts back the calling thread's current device when an entry point returns
-// (check_device_ptrs makes the pointers' device current for the launches;
-// the caller's own notion of its current device must not change).
-class DeviceRestore {
-public:
-    DeviceRestore()
-    {
-        if (cudaGetDevice(&dev_) != cudaSuccess) {
-            cudaGetLastError();
-            dev_ = -1;
-        }
-    }
-    ~DeviceRestore()
-    {
-        int cur = -1;
-        if (dev_ >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != dev_)
-            cudaSetDevice(dev_);
-    }
-    DeviceRestore(const DeviceRestore &) = delete;
-    DeviceRestore &operator=(const DeviceRestore &) = delete;
-
-private:
-    int dev_ = -1;
-};
 
 int check_shape(int64_t N, int64_t K, int64_t D)
 {
@@ -594,6 +577,17 @@ int run_assign(const void *X, const void *C, const float *cnorm, int64_t N, int6
 }  // namespace
 
 namespace kma {
+
+int library_device(cudaMemPool_t *pool, int *sms)
+{
+    DeviceInfo dev;
+    const int rc = current_device_info(&dev);
+    if (rc == KMASSIGN_OK) {
+        *pool = dev.pool;
+        *sms = dev.sms;
+    }
+    return rc;
+}
 
 int library_pool(cudaMemPool_t *pool)
 {
@@ -1203,11 +1197,12 @@ const char *kmassign_strerror(int code)
     case KMASSIGN_ERR_NULL:
         return "a required pointer is NULL";
     case KMASSIGN_ERR_ALIGN:
-        return "X and C (and cnorm) must be 16-byte aligned; idx and minscore 4-byte aligned";
+        return "X and C (and cnorm) must be 16-byte aligned; idx and minscore 4-byte aligned; "
+               "the buffers of learned assignments to their elements";
     case KMASSIGN_ERR_SHAPE:
-        return "shape out of range: need 0 <= N < 2^31 and 1 <= K < 2^31";
+        return "shape out of range: need 0 <= N < 2^31 and 1 <= K < 2^31 (routing: 1 <= E <= 1024)";
     case KMASSIGN_ERR_UNSUPPORTED_D:
-        return "unsupported D: need a multiple of 16 in [16, 256]";
+        return "unsupported D: need a multiple of 16 in [16, 256] (lookup: 1 to 65536)";
     case KMASSIGN_ERR_CUDA:
         return "a CUDA runtime or driver call failed";
     case KMASSIGN_ERR_TIMEOUT:
@@ -1223,7 +1218,8 @@ const char *kmassign_strerror(int code)
     case KMASSIGN_ERR_ARG:
         return "invalid argument (plan values: ksplit != -1, rows_per_cta 128/256, "
                "centroids_per_tile 128/256, consumer_warps 4/8/16 matching a compiled shape; "
-               "top-k: 1 <= k <= min(K, 32), distances 0 or 1)";
+               "top-k: 1 <= k <= min(K, 32), distances 0 or 1; routing: k, groups and flags as "
+               "kmassign.h says; element types fp32, bf16, fp16; max_norm >= 0)";
     default:
         return "unknown kmassign status code";
     }
