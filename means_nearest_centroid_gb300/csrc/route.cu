@@ -267,8 +267,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
         const int j = lane + s * W;
         if (j < a.k) {
             float f = w[s];
-            if (divide)
-                f = f == 0.0f ? 0.0f : f / total;   // also where nothing is selected
+            if (divide)   // nothing selected, or sigmoids that are all 0: weight 0
+                f = mine[s] < 0 || total == 0.0f ? 0.0f : f / total;
             a.idx[row * a.k + j] = mine[s];
             a.weights[row * a.k + j] = f * a.scale;
         }
@@ -370,14 +370,14 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const Rout
             total = row_sum<32>(total);
             p = on ? expf(x - top) : 0.0f;
         }
-        p = p == 0.0f ? 0.0f : p / total;
+        p = on ? p / total : 0.0f;
         const float mean = row_sum<32>(p * g);
         d = p * (g - mean);
         if (!a.renorm)
             for (int i = lane; i < a.E; i += 32) {
                 const float f = Elem<T>::up(x_row[i]);
-                const float q = is_masked(f) ? 0.0f : expf(f - top) / total;
-                out[i] = Elem<T>::down(q == 0.0f ? 0.0f : -q * mean * a.scale);
+                out[i] = Elem<T>::down(
+                    is_masked(f) ? 0.0f : -(expf(f - top) / total) * mean * a.scale);
             }
     }
     __syncwarp();
