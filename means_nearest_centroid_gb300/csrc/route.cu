@@ -81,20 +81,84 @@ struct RouteArgs {
     int32_t E, k;
     int32_t groups, topk_groups, group_top;
     int32_t per_group;      // E / groups
+    int32_t group_lanes;    // lanes per group where each lane's experts are of one group, else 0
     uint32_t group_magic;   // e / per_group == e * group_magic >> 20 for e < 1024
     bool renorm;
+    bool wide;              // every lane's experts can be loaded as one vector
     float scale;
 };
 
-// One row per W lanes; lane l of them holds experts l, l + W, ... (V of them).
-// The k selections are k rounds of a maximum over the row.
+// Compare-exchange towards descending order, and the smallest networks of 2, 4
+// and 8 values.
+__device__ __forceinline__ void down(uint32_t &a, uint32_t &b)
+{
+    const uint32_t hi = max(a, b);
+    b = min(a, b);
+    a = hi;
+}
+template <int V>
+__device__ __forceinline__ void sort_down(uint32_t (&s)[V])
+{
+    static_assert(V == 1 || V == 2 || V == 4 || V == 8, "sizes with a network");
+    if constexpr (V == 2) {
+        down(s[0], s[1]);
+    } else if constexpr (V == 4) {
+        down(s[0], s[1]), down(s[2], s[3]);
+        down(s[0], s[2]), down(s[1], s[3]);
+        down(s[1], s[2]);
+    } else if constexpr (V == 8) {
+        down(s[0], s[1]), down(s[2], s[3]), down(s[4], s[5]), down(s[6], s[7]);
+        down(s[0], s[2]), down(s[1], s[3]), down(s[4], s[6]), down(s[5], s[7]);
+        down(s[1], s[2]), down(s[5], s[6]), down(s[0], s[4]), down(s[3], s[7]);
+        down(s[1], s[5]), down(s[2], s[6]);
+        down(s[1], s[4]), down(s[3], s[6]);
+        down(s[2], s[4]), down(s[3], s[5]);
+        down(s[3], s[4]);
+    }
+}
+
+// The best two of a group's keys, held by several lanes.
+struct Best2 {
+    float first = -INFINITY, second = -INFINITY;
+    __device__ __forceinline__ void add(float f)
+    {
+        second = fmaxf(second, fminf(first, f));
+        first = fmaxf(first, f);
+    }
+    __device__ __forceinline__ void join(int off)
+    {
+        const float f1 = __shfl_xor_sync(kAll, first, off);
+        const float f2 = __shfl_xor_sync(kAll, second, off);
+        second = fmaxf(fminf(first, f1), fmaxf(second, f2));
+        first = fmaxf(first, f1);
+    }
+    __device__ __forceinline__ float key(int32_t top) const
+    {
+        return top == 1 || second == -INFINITY ? first : first + second;
+    }
+};
+
+// One row per W lanes; lane l of them holds the V experts from l V on, so
+// that of equal keys the lowest lane's come first.  What bounds the kernel is
+// issue: the logits are read once (N E elements), a score costs an exponential
+// and a division, and the selection has to order k of E keys.  So each lane
+// sorts its V <= 8 keys once (a network of minima and maxima, without
+// indices), and each of the k rounds takes the maximum over the lanes' heads
+// and advances the list of the lowest lane that holds it; which expert a key
+// belonged to is found once at the end, round j's by lane j, from a copy of
+// the keys in shared memory (equal keys of a lane leave it in consecutive
+// rounds: the how-manieth is counted).  Lists of 16 and 32 keys (E > 256) are
+// not sorted: each round finds their maximum again.
 template <typename T, int W, int V, bool SIGMOID, bool GROUPS>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs a)
 {
-    constexpr int kRows = 32 / W;        // rows per warp
-    constexpr int kSlots = 32 / W;       // selections a lane can hold (k <= 32)
-    constexpr int kKeys = W * V + (W * V >> 5);
-    __shared__ float s_key[GROUPS ? kRouteWarps * kRows : 1][GROUPS ? kKeys : 1];
+    constexpr int kRows = 32 / W;           // rows per warp
+    constexpr int kSlots = 32 / W;          // selections a lane can hold (k <= 32)
+    constexpr bool kSorted = V <= 8;
+    constexpr int kPad = V >= 4 ? 4 : 1;    // words after each lane's keys, against bank conflicts
+    constexpr int kKeys = W * (V + kPad);
+    constexpr bool kStore = kSorted || GROUPS;
+    __shared__ alignas(16) uint32_t s_key[kStore ? kRouteWarps * kRows : 1][kStore ? kKeys : 4];
     __shared__ float s_group[GROUPS ? kRouteWarps * kRows : 1][GROUPS ? 32 : 1];
     const int lane = threadIdx.x & (W - 1);
     const int local = threadIdx.x / W;
@@ -102,24 +166,40 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
     const bool live = row_any < a.N;
     const int64_t row = live ? row_any : a.N - 1;   // spare lanes repeat the last row
     const T *x_row = static_cast<const T *>(a.logits) + row * a.E;
+    const int e0 = lane * V;
 
     float x[V];
+    if (a.wide) {
+        constexpr int VE = V < 8 ? V : 8;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int e = lane + v * W;
-        x[v] = e < a.E ? Elem<T>::up(x_row[e]) : -INFINITY;
+        for (int v = 0; v < V; v += VE) {
+            float f[VE];
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                f[i] = -INFINITY;
+            if (e0 + v < a.E)
+                widen<T, VE>(load_raw<T, VE>(x_row + e0 + v), f);
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                x[v + i] = f[i];
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            x[v] = e0 + v < a.E ? Elem<T>::up(x_row[e0 + v]) : -INFINITY;
     }
 
-    // scores (softmax: exp(x - max), normalised by `total` below)
+    // scores (softmax: exp(x - max), normalised by `total`)
     float part[V];
     float top = 0.0f, total = 1.0f;
+    const bool scores = GROUPS || a.bias != nullptr;
     if constexpr (SIGMOID) {
-        if (GROUPS || a.bias != nullptr) {
+        if (scores) {
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 part[v] = is_masked(x[v]) ? 0.0f : sigmoid(x[v]);
         }
-    } else {
+    } else if (scores || !a.renorm) {
         uint32_t most = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -139,47 +219,50 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         float f = x[v];
-        if (a.bias != nullptr) {
-            const int e = lane + v * W;
-            f = (SIGMOID ? part[v] : part[v] / total) + (e < a.E ? __ldg(a.bias + e) : 0.0f);
-        }
+        if (a.bias != nullptr)
+            f = (SIGMOID ? part[v] : part[v] / total) +
+                (e0 + v < a.E ? __ldg(a.bias + e0 + v) : 0.0f);
         key[v] = is_masked(x[v]) || is_masked(f) ? 0u : ordered(f);
     }
 
+    uint32_t *keys = s_key[kStore ? local : 0];
     if constexpr (GROUPS) {
-        float *keys = s_key[local];
         float *of_group = s_group[local];
         const bool by_key = a.bias != nullptr || a.group_top == 1;
+        if (a.group_lanes > 0) {
+            // a lane's experts are of one group: its lanes join theirs directly
+            Best2 b;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = lane + v * W;
-            keys[e + (e >> 5)] =
-                key[v] == 0 ? -INFINITY : by_key ? unordered(key[v]) : part[v];
-        }
-        __syncwarp();
-        // lanes_per lanes form one group's key, all groups in one round where they fit
-        int lanes_per = W;
-        while (lanes_per > 1 && W / lanes_per < a.groups)
-            lanes_per >>= 1;
-        const int part_of = lane & (lanes_per - 1);
-        for (int g0 = 0; g0 < a.groups; g0 += W / lanes_per) {
-            const int g = g0 + lane / lanes_per;
-            float first = -INFINITY, second = -INFINITY;
-            if (g < a.groups)
-                for (int m = part_of; m < a.per_group; m += lanes_per) {
-                    const int e = g * a.per_group + m;
-                    const float f = keys[e + (e >> 5)];
-                    second = fmaxf(second, fminf(first, f));
-                    first = fmaxf(first, f);
-                }
-            for (int off = lanes_per >> 1; off > 0; off >>= 1) {
-                const float f1 = __shfl_xor_sync(kAll, first, off);
-                const float f2 = __shfl_xor_sync(kAll, second, off);
-                second = fmaxf(fminf(first, f1), fmaxf(second, f2));
-                first = fmaxf(first, f1);
+            for (int v = 0; v < V; ++v)
+                b.add(key[v] == 0 ? -INFINITY : by_key ? unordered(key[v]) : part[v]);
+            for (int off = a.group_lanes >> 1; off > 0; off >>= 1)
+                b.join(off);
+            if ((lane & (a.group_lanes - 1)) == 0 && e0 < a.E)
+                of_group[lane / a.group_lanes] = b.key(a.group_top);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                keys[lane * (V + kPad) + v] = __float_as_uint(
+                    key[v] == 0 ? -INFINITY : by_key ? unordered(key[v]) : part[v]);
+            __syncwarp();
+            // lanes_per lanes form one group's key, all groups in one round where they fit
+            int lanes_per = W;
+            while (lanes_per > 1 && W / lanes_per < a.groups)
+                lanes_per >>= 1;
+            const int part_of = lane & (lanes_per - 1);
+            for (int g0 = 0; g0 < a.groups; g0 += W / lanes_per) {
+                const int g = g0 + lane / lanes_per;
+                Best2 b;
+                if (g < a.groups)
+                    for (int m = part_of; m < a.per_group; m += lanes_per) {
+                        const int e = g * a.per_group + m;
+                        b.add(__uint_as_float(keys[e / V * (V + kPad) + e % V]));
+                    }
+                for (int off = lanes_per >> 1; off > 0; off >>= 1)
+                    b.join(off);
+                if (part_of == 0 && g < a.groups)
+                    of_group[g] = b.key(a.group_top);
             }
-            if (part_of == 0 && g < a.groups)
-                of_group[g] = a.group_top == 1 || second == -INFINITY ? first : first + second;
         }
         __syncwarp();
         // a group stays if fewer than topk_groups are ahead of it
@@ -195,37 +278,92 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
                 stays |= 1u << g;
         }
         stays = row_or<W>(stays);
+        if (a.group_lanes > 0) {
+            const bool mine = ((stays >> ((lane / a.group_lanes) & 31)) & 1u) != 0;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const uint32_t g = (static_cast<uint32_t>(lane + v * W) * a.group_magic) >> 20;
-            if (((stays >> (g & 31)) & 1u) == 0)
-                key[v] = 0;
+            for (int v = 0; v < V; ++v)
+                key[v] = mine ? key[v] : 0u;
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const uint32_t g = (static_cast<uint32_t>(e0 + v) * a.group_magic) >> 20;
+                if (((stays >> (g & 31)) & 1u) == 0)
+                    key[v] = 0;
+            }
         }
+        __syncwarp();
     }
 
     int32_t mine[kSlots];
 #pragma unroll
     for (int s = 0; s < kSlots; ++s)
         mine[s] = -1;
-    for (int j = 0; j < a.k; ++j) {
-        uint32_t best = 0;
-        int32_t at = 0;
+    if constexpr (kSorted) {
+        uint32_t s[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (key[v] > best) {
-                best = key[v];
-                at = lane + v * W;
+        for (int v = 0; v < V; ++v) {
+            s[v] = key[v];
+            keys[lane * (V + kPad) + v] = key[v];
+        }
+        sort_down<V>(s);
+        // round j's key, the lane it came from, and how many equal ones that lane gave before
+        uint32_t got[kSlots] = {};
+        int32_t from[kSlots] = {}, nth[kSlots] = {};
+        uint32_t last_key = 0;
+        int32_t last_lane = -1, equal = 0;
+        for (int j = 0; j < a.k; ++j) {
+            const uint32_t most = row_max<W>(s[0]);
+            const uint32_t holds = __ballot_sync(kAll, s[0] == most) >> (threadIdx.x & (32 - W));
+            const int32_t winner = __ffs(holds) - 1;   // within the row: it holds it or a lower row's
+            equal = most == last_key && winner == last_lane ? equal + 1 : 0;
+            last_key = most;
+            last_lane = winner;
+            if (lane == winner) {
+#pragma unroll
+                for (int v = 0; v + 1 < V; ++v)
+                    s[v] = s[v + 1];
+                s[V - 1] = 0;
             }
-        const uint32_t most = row_max<W>(best);
-        const uint32_t e = row_min<W>(best == most ? static_cast<uint32_t>(at) : ~0u);
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (e == static_cast<uint32_t>(lane + v * W))
-                key[v] = 0;
+            for (int q = 0; q < kSlots; ++q)
+                if (j == lane + q * W) {
+                    got[q] = most;
+                    from[q] = winner;
+                    nth[q] = equal;
+                }
+        }
+        __syncwarp();
 #pragma unroll
-        for (int s = 0; s < kSlots; ++s)
-            if (j == lane + s * W)
-                mine[s] = most != 0 ? static_cast<int32_t>(e) : -1;
+        for (int q = 0; q < kSlots; ++q)
+            if (got[q] != 0) {
+                int32_t left = nth[q];
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (keys[from[q] * (V + kPad) + v] == got[q]) {
+                        if (left == 0)
+                            mine[q] = from[q] * V + v;
+                        --left;
+                    }
+            }
+    } else {
+        for (int j = 0; j < a.k; ++j) {
+            uint32_t best = 0;
+            int32_t at = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (key[v] > best) {
+                    best = key[v];
+                    at = e0 + v;
+                }
+            const uint32_t most = row_max<W>(best);
+            const int32_t e = __shfl_sync(kAll, at, __ffs(__ballot_sync(kAll, best == most)) - 1);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (most != 0 && e == e0 + v)
+                    key[v] = 0;
+            if (j == lane)
+                mine[0] = most != 0 ? e : -1;
+        }
     }
 
     // weights, from the selected logits (just read: in L1)
@@ -276,6 +414,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
 }
 
 // ---- gradient -------------------------------------------------------------
+//
+//     sigmoid:             scale s_j (1 - s_j) g_j
+//     sigmoid, renorm:     scale s_j (1 - s_j) / S (g_j - sum_l s_l g_l / S), S = sum_l s_l
+//     softmax (, renorm):  scale p_e (g_e - sum_l p_l g_l), p over all (the selected)
+// Bound by the writes of the N E gradients.
 
 struct RouteGradArgs {
     const void *logits;
@@ -285,109 +428,192 @@ struct RouteGradArgs {
     int64_t N;
     int32_t E, k;
     bool renorm;
+    bool wide;            // dense form: as in RouteArgs, for logits and dlogits
     float scale;
-    int32_t zero_bytes;   // width of the zeroing stores: 16, 8, 4 or 2
 };
 
-template <typename Z>
-__device__ __forceinline__ void zero_row(void *p, int64_t bytes, int lane)
+// Selection j of a row: expert, its logit and its weight's gradient; off where
+// the id names no expert or the expert is masked.
+template <typename T>
+struct Chosen {
+    int32_t e;
+    float x = -INFINITY, g = 0.0f;
+    bool on;
+    __device__ __forceinline__ Chosen(const RouteGradArgs &a, int64_t row, int j, bool live)
+    {
+        e = live && j < a.k ? __ldg(a.idx + row * a.k + j) : -1;
+        on = e >= 0 && e < a.E;
+        if (on) {
+            g = __ldg(a.dweights + row * a.k + j);
+            x = Elem<T>::up(static_cast<const T *>(a.logits)[row * a.E + e]);
+            on = !is_masked(x);
+        }
+        if (!on)
+            g = 0.0f;
+    }
+};
+
+// n elements set to 0 by a warp: 16 bytes a lane between the aligned ends.
+template <typename T>
+__device__ __forceinline__ void zero_span(T *p, int n, int lane)
 {
-    Z *q = static_cast<Z *>(p);
-    const int n = static_cast<int>(bytes / sizeof(Z));
-    const Z zero{};
-    for (int i = lane; i < n; i += 32)
-        q[i] = zero;
+    constexpr int VE = 16 / sizeof(T);
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(T));
+    const int head = min(n, off == 0 ? 0 : VE - off);
+    const int vecs = (n - head) / VE;
+    if (lane < head)
+        p[lane] = Elem<T>::down(0.0f);
+    uint4 *q = reinterpret_cast<uint4 *>(p + head);
+#pragma unroll 8
+    for (int i = lane; i < vecs; i += 32)
+        q[i] = make_uint4(0u, 0u, 0u, 0u);
+    const int rest = head + vecs * VE + lane;
+    if (rest < n)
+        p[rest] = Elem<T>::down(0.0f);
 }
 
-// One warp per row, lane j < k holds selection j.  The sigmoid and the
-// renormalised softmax have a gradient on the selected experts only: the row
-// is zeroed with wide stores, then the selected elements are written over (a
-// warp's barrier orders the two).  The plain softmax has one on every expert.
-//     sigmoid:             scale s_j (1 - s_j) g_j
-//     sigmoid, renorm:     scale s_j (1 - s_j) / S (g_j - sum_l s_l g_l / S), S = sum_l s_l
-//     softmax (, renorm):  scale p_e (g_e - sum_l p_l g_l), p over all (the selected)
-template <typename T, bool SIGMOID>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const RouteGradArgs a)
+// Gradients on the selected experts only (sigmoid, renormalised softmax): a
+// warp zeroes 32 / KW rows with wide stores, which wait for nothing, and forms
+// the selected elements meanwhile, lane j of a row's KW lanes selection j;
+// they are written over the zeros behind a warp barrier.
+template <typename T, int KW, bool SIGMOID>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_grad_sparse_kernel(const RouteGradArgs a)
 {
+    constexpr int kRows = 32 / KW;
     const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
-    if (row >= a.N)
+    const int64_t row0 =
+        (static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5)) * kRows;
+    if (row0 >= a.N)
         return;
-    const T *x_row = static_cast<const T *>(a.logits) + row * a.E;
-    T *out = static_cast<T *>(a.dlogits) + row * a.E;
-    int32_t e = lane < a.k ? __ldg(a.idx + row * a.k + lane) : -1;
-    float g = 0.0f, x = -INFINITY;
-    if (e < 0 || e >= a.E)
-        e = -1;
-    if (e >= 0) {
-        g = __ldg(a.dweights + row * a.k + lane);
-        x = Elem<T>::up(x_row[e]);
-    }
-    const bool on = e >= 0 && !is_masked(x);
-    if (!on)
-        g = 0.0f;
+    const int64_t row = row0 + lane / KW;
+    const bool live = row < a.N;
+    T *out = static_cast<T *>(a.dlogits);
+    zero_span<T>(out + row0 * a.E,
+                 static_cast<int>(min(static_cast<int64_t>(kRows), a.N - row0)) * a.E, lane);
+    const Chosen<T> c(a, row, lane & (KW - 1), live);
     float d;
-    if (SIGMOID || a.renorm) {
-        if (a.zero_bytes == 16)
-            zero_row<uint4>(out, static_cast<int64_t>(a.E) * sizeof(T), lane);
-        else if (a.zero_bytes == 8)
-            zero_row<uint2>(out, static_cast<int64_t>(a.E) * sizeof(T), lane);
-        else if (a.zero_bytes == 4)
-            zero_row<uint32_t>(out, static_cast<int64_t>(a.E) * sizeof(T), lane);
-        else
-            zero_row<uint16_t>(out, static_cast<int64_t>(a.E) * sizeof(T), lane);
-    }
     if constexpr (SIGMOID) {
         // s and s (1 - s) without cancellation, from t = exp(-|x|)
-        const float t = on ? expf(-fabsf(x)) : 0.0f;
-        const float s = on ? (x >= 0.0f ? 1.0f : t) / (1.0f + t) : 0.0f;
+        const float t = c.on ? expf(-fabsf(c.x)) : 0.0f;
+        const float s = c.on ? (c.x >= 0.0f ? 1.0f : t) / (1.0f + t) : 0.0f;
         const float slope = t / ((1.0f + t) * (1.0f + t));
         if (a.renorm) {
-            const float total = row_sum<32>(s);
-            const float mean = row_sum<32>(s * g) / total;
-            d = total > 0.0f ? slope / total * (g - mean) : 0.0f;
+            const float total = row_sum<KW>(s);
+            const float mean = row_sum<KW>(s * c.g) / total;
+            d = total > 0.0f ? slope / total * (c.g - mean) : 0.0f;
         } else {
-            d = slope * g;
+            d = slope * c.g;
         }
     } else {
-        float top, total, p;
-        if (a.renorm) {
-            top = unordered(__reduce_max_sync(kAll, on ? ordered(x) : 0u));
-            p = on ? expf(x - top) : 0.0f;
-            total = row_sum<32>(p);
-        } else {
-            uint32_t most = 0;
-            for (int i = lane; i < a.E; i += 32) {
-                const float f = Elem<T>::up(x_row[i]);
-                most = max(most, is_masked(f) ? 0u : ordered(f));
-            }
-            top = unordered(__reduce_max_sync(kAll, most));
-            total = 0.0f;
-            for (int i = lane; i < a.E; i += 32) {
-                const float f = Elem<T>::up(x_row[i]);
-                total += is_masked(f) ? 0.0f : expf(f - top);
-            }
-            total = row_sum<32>(total);
-            p = on ? expf(x - top) : 0.0f;
-        }
-        p = on ? p / total : 0.0f;
-        const float mean = row_sum<32>(p * g);
-        d = p * (g - mean);
-        if (!a.renorm)
-            for (int i = lane; i < a.E; i += 32) {
-                const float f = Elem<T>::up(x_row[i]);
-                out[i] = Elem<T>::down(
-                    is_masked(f) ? 0.0f : -(expf(f - top) / total) * mean * a.scale);
-            }
+        const float top = unordered(row_max<KW>(c.on ? ordered(c.x) : 0u));
+        float p = c.on ? expf(c.x - top) : 0.0f;
+        const float total = row_sum<KW>(p);
+        p = c.on ? p / total : 0.0f;
+        d = p * (c.g - row_sum<KW>(p * c.g));
     }
     __syncwarp();
-    if (on)
-        out[e] = Elem<T>::down(d * a.scale);
+    if (c.on)
+        out[row * a.E + c.e] = Elem<T>::down(d * a.scale);
+}
+
+// The softmax over all experts: a gradient on each of them.  Lanes and experts
+// as in route_kernel; the row is read once.
+template <typename T, int W, int V>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_grad_dense_kernel(const RouteGradArgs a)
+{
+    constexpr int kRows = 32 / W;
+    constexpr int kSlots = 32 / W;
+    constexpr int VE = V < 8 ? V : 8;
+    const int lane = threadIdx.x & (W - 1);
+    const int64_t row_any =
+        static_cast<int64_t>(blockIdx.x) * (kRouteWarps * kRows) + threadIdx.x / W;
+    const bool live = row_any < a.N;
+    const int64_t row = live ? row_any : a.N - 1;
+    const T *x_row = static_cast<const T *>(a.logits) + row * a.E;
+    T *out = static_cast<T *>(a.dlogits) + row * a.E;
+    const int e0 = lane * V;
+    float x[V];
+#pragma unroll
+    for (int v = 0; v < V; v += VE) {
+        float f[VE];
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+            f[i] = -INFINITY;
+        if (a.wide) {
+            if (e0 + v < a.E)
+                widen<T, VE>(load_raw<T, VE>(x_row + e0 + v), f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                if (e0 + v + i < a.E)
+                    f[i] = Elem<T>::up(x_row[e0 + v + i]);
+        }
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+            x[v + i] = f[i];
+    }
+    uint32_t most = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        most = max(most, is_masked(x[v]) ? 0u : ordered(x[v]));
+    const float top = unordered(row_max<W>(most));
+    float total = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        x[v] = is_masked(x[v]) ? 0.0f : expf(x[v] - top);
+        total += x[v];
+    }
+    total = row_sum<W>(total);
+    float mean = 0.0f, p[kSlots], g[kSlots];
+    int32_t e[kSlots];
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+        p[s] = g[s] = 0.0f;
+        e[s] = -1;
+        if (s * W < a.k) {
+            const Chosen<T> c(a, row, lane + s * W, live);
+            e[s] = c.on ? c.e : -1;
+            g[s] = c.g;
+            p[s] = c.on ? expf(c.x - top) / total : 0.0f;
+            mean += p[s] * g[s];
+        }
+    }
+    mean = row_sum<W>(mean);
+    if (live) {
+        // a row without a single unmasked expert has total 0 and x 0
+        const float share = total == 0.0f ? 0.0f : mean / total;
+#pragma unroll
+        for (int v = 0; v < V; v += VE) {
+            float f[VE];
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                f[i] = -x[v + i] * share * a.scale;
+            if (a.wide) {
+                if (e0 + v < a.E)
+                    store_raw<T, VE>(out + e0 + v, narrow<T, VE>(f));
+            } else {
+#pragma unroll
+                for (int i = 0; i < VE; ++i)
+                    if (e0 + v + i < a.E)
+                        out[e0 + v + i] = Elem<T>::down(f[i]);
+            }
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s)
+        if (e[s] >= 0)
+            out[e[s]] = Elem<T>::down(p[s] * (g[s] - mean) * a.scale);
 }
 
 template <typename T, int W, int V>
-cudaError_t route_shape(const RouteArgs &a, bool sigmoid, cudaStream_t stream)
+cudaError_t route_shape(RouteArgs a, bool sigmoid, cudaStream_t stream)
 {
+    const uintptr_t vec = std::min<uintptr_t>(16, (V < 8 ? V : 8) * sizeof(T));
+    a.wide = a.E % (V < 8 ? V : 8) == 0 && a.E * sizeof(T) % vec == 0 &&
+             reinterpret_cast<uintptr_t>(a.logits) % vec == 0;
+    const int lanes = a.per_group % V == 0 ? a.per_group / V : 0;
+    a.group_lanes = lanes > 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
     const int rows = kRouteWarps * (32 / W);
     const unsigned blocks = static_cast<unsigned>((a.N + rows - 1) / rows);
     if (sigmoid) {
@@ -414,14 +640,65 @@ cudaError_t route_type(const RouteArgs &a, bool sigmoid, cudaStream_t stream)
     if (a.E <= 32)
         return route_shape<T, 8, 4>(a, sigmoid, stream);
     if (a.E <= 64)
-        return route_shape<T, 32, 2>(a, sigmoid, stream);
+        return route_shape<T, 8, 8>(a, sigmoid, stream);
     if (a.E <= 128)
-        return route_shape<T, 32, 4>(a, sigmoid, stream);
+        return route_shape<T, 16, 8>(a, sigmoid, stream);
     if (a.E <= 256)
         return route_shape<T, 32, 8>(a, sigmoid, stream);
     if (a.E <= 512)
         return route_shape<T, 32, 16>(a, sigmoid, stream);
     return route_shape<T, 32, 32>(a, sigmoid, stream);
+}
+
+template <typename T, int W, int V>
+cudaError_t dense_shape(RouteGradArgs a, cudaStream_t stream)
+{
+    const uintptr_t vec = std::min<uintptr_t>(16, (V < 8 ? V : 8) * sizeof(T));
+    a.wide = a.E % (V < 8 ? V : 8) == 0 && a.E * sizeof(T) % vec == 0 &&
+             (reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.dlogits)) %
+                     vec == 0;
+    const int rows = kRouteWarps * (32 / W);
+    route_grad_dense_kernel<T, W, V>
+        <<<static_cast<unsigned>((a.N + rows - 1) / rows), 32 * kRouteWarps, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int KW>
+cudaError_t sparse_shape(const RouteGradArgs &a, bool sigmoid, cudaStream_t stream)
+{
+    const int rows = kRouteWarps * (32 / KW);
+    const unsigned blocks = static_cast<unsigned>((a.N + rows - 1) / rows);
+    if (sigmoid)
+        route_grad_sparse_kernel<T, KW, true><<<blocks, 32 * kRouteWarps, 0, stream>>>(a);
+    else
+        route_grad_sparse_kernel<T, KW, false><<<blocks, 32 * kRouteWarps, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t route_grad_type(const RouteGradArgs &a, bool sigmoid, cudaStream_t stream)
+{
+    if (sigmoid || a.renorm) {
+        if (a.k <= 8)
+            return sparse_shape<T, 8>(a, sigmoid, stream);
+        return a.k <= 16 ? sparse_shape<T, 16>(a, sigmoid, stream)
+                         : sparse_shape<T, 32>(a, sigmoid, stream);
+    }
+    if (a.E <= 8)
+        return dense_shape<T, 8, 1>(a, stream);
+    if (a.E <= 16)
+        return dense_shape<T, 8, 2>(a, stream);
+    if (a.E <= 32)
+        return dense_shape<T, 8, 4>(a, stream);
+    if (a.E <= 64)
+        return dense_shape<T, 8, 8>(a, stream);
+    if (a.E <= 128)
+        return dense_shape<T, 16, 8>(a, stream);
+    if (a.E <= 256)
+        return dense_shape<T, 32, 8>(a, stream);
+    if (a.E <= 512)
+        return dense_shape<T, 32, 16>(a, stream);
+    return dense_shape<T, 32, 32>(a, stream);
 }
 
 }  // namespace
@@ -470,31 +747,14 @@ cudaError_t launch_route_grad(const void *logits, int dtype, int64_t N, int64_t 
     a.k = k;
     a.renorm = renorm;
     a.scale = scale;
-    const uintptr_t bits = reinterpret_cast<uintptr_t>(dlogits) |
-                           static_cast<uintptr_t>(E * dtype_bytes(dtype));
-    a.zero_bytes = bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2;
-    const unsigned blocks = static_cast<unsigned>((N + kRouteWarps - 1) / kRouteWarps);
-    const int threads = 32 * kRouteWarps;
     switch (dtype) {
     case kFp32:
-        if (sigmoid)
-            route_grad_kernel<float, true><<<blocks, threads, 0, stream>>>(a);
-        else
-            route_grad_kernel<float, false><<<blocks, threads, 0, stream>>>(a);
-        break;
+        return route_grad_type<float>(a, sigmoid, stream);
     case kBf16:
-        if (sigmoid)
-            route_grad_kernel<__nv_bfloat16, true><<<blocks, threads, 0, stream>>>(a);
-        else
-            route_grad_kernel<__nv_bfloat16, false><<<blocks, threads, 0, stream>>>(a);
-        break;
+        return route_grad_type<__nv_bfloat16>(a, sigmoid, stream);
     default:
-        if (sigmoid)
-            route_grad_kernel<__half, true><<<blocks, threads, 0, stream>>>(a);
-        else
-            route_grad_kernel<__half, false><<<blocks, threads, 0, stream>>>(a);
+        return route_grad_type<__half>(a, sigmoid, stream);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace kma
