@@ -22,32 +22,20 @@ namespace {
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kRouteWarps = 8;
 
-// Floats as unsigned numbers of the same order; 0 is below every float.
-__device__ __forceinline__ uint32_t ordered(float f)
-{
-    const uint32_t b = __float_as_uint(f + 0.0f);   // -0 equals +0
-    return (b & 0x80000000u) != 0 ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float unordered(uint32_t u)
-{
-    return __uint_as_float((u & 0x80000000u) != 0 ? u & 0x7fffffffu : ~u);
-}
-
 // Reductions over the W lanes of a row (all lanes of the warp take part).
+// fmaxf's order: a NaN loses to every number.
 template <int W>
-__device__ __forceinline__ uint32_t row_max(uint32_t v)
+__device__ __forceinline__ float row_max(float v)
 {
-    if constexpr (W == 32)
-        return __reduce_max_sync(kAll, v);
+    if constexpr (W == 32) {
+        float m;
+        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+        return m;
+    }
 #pragma unroll
     for (int off = W / 2; off > 0; off >>= 1)
-        v = max(v, __shfl_xor_sync(kAll, v, off));
+        v = fmaxf(v, __shfl_xor_sync(kAll, v, off));
     return v;
-}
-template <int W>
-__device__ __forceinline__ uint32_t row_min(uint32_t v)
-{
-    return ~row_max<W>(~v);
 }
 template <int W>
 __device__ __forceinline__ uint32_t row_or(uint32_t v)
@@ -72,6 +60,18 @@ __device__ __forceinline__ bool is_masked(float x) { return !(x > -INFINITY); }
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
+// 1 / y correctly rounded for 1 <= y <= 2^125: one Newton step with fused
+// multiply-adds from the hardware's approximation, which is within one ulp
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990; over all 2^23 significands
+// it gave the quotient's bits on GB300).
+__device__ __forceinline__ float reciprocal(float y)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+    return fmaf(r, fmaf(-y, r, 1.0f), r);
+}
+
 struct RouteArgs {
     const void *logits;
     const float *bias;
@@ -85,19 +85,21 @@ struct RouteArgs {
     uint32_t group_magic;   // e / per_group == e * group_magic >> 20 for e < 1024
     bool renorm;
     bool wide;              // every lane's experts can be loaded as one vector
+    bool bias_wide;         // and their biases
+    bool scored;            // the choice needs the scores, not the logits alone
     float scale;
 };
 
 // Compare-exchange towards descending order, and the smallest networks of 2, 4
 // and 8 values.
-__device__ __forceinline__ void down(uint32_t &a, uint32_t &b)
+__device__ __forceinline__ void down(float &a, float &b)
 {
-    const uint32_t hi = max(a, b);
-    b = min(a, b);
+    const float hi = fmaxf(a, b);
+    b = fminf(a, b);
     a = hi;
 }
 template <int V>
-__device__ __forceinline__ void sort_down(uint32_t (&s)[V])
+__device__ __forceinline__ void sort_down(float (&s)[V])
 {
     static_assert(V == 1 || V == 2 || V == 4 || V == 8, "sizes with a network");
     if constexpr (V == 2) {
@@ -139,16 +141,16 @@ struct Best2 {
 };
 
 // One row per W lanes; lane l of them holds the V experts from l V on, so
-// that of equal keys the lowest lane's come first.  What bounds the kernel is
-// issue: the logits are read once (N E elements), a score costs an exponential
-// and a division, and the selection has to order k of E keys.  So each lane
-// sorts its V <= 8 keys once (a network of minima and maxima, without
-// indices), and each of the k rounds takes the maximum over the lanes' heads
-// and advances the list of the lowest lane that holds it; which expert a key
-// belonged to is found once at the end, round j's by lane j, from a copy of
-// the keys in shared memory (equal keys of a lane leave it in consecutive
-// rounds: the how-manieth is counted).  Lists of 16 and 32 keys (E > 256) are
-// not sorted: each round finds their maximum again.
+// that of equal keys the lowest lane's come first.  A key of -inf is never
+// selected.  What bounds the kernel is issue: the logits are read once, but a
+// score costs an exponential and a reciprocal, and the selection has to order
+// k of E keys.  So each lane sorts its V <= 8 keys once (a network of minima
+// and maxima, without indices), and each of the k rounds takes the maximum
+// over the lanes' heads and advances the list of the lowest lane that holds
+// it; which expert a key belonged to is found once at the end, round j's by
+// lane j, from a copy of the keys in shared memory (equal keys of a lane leave
+// it in consecutive rounds: the how-manieth is counted).  Lists of 16 and 32
+// keys (E > 256) are not sorted: each round finds their maximum again.
 template <typename T, int W, int V, bool SIGMOID, bool GROUPS>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs a)
 {
@@ -156,9 +158,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
     constexpr int kSlots = 32 / W;          // selections a lane can hold (k <= 32)
     constexpr bool kSorted = V <= 8;
     constexpr int kPad = V >= 4 ? 4 : 1;    // words after each lane's keys, against bank conflicts
-    constexpr int kKeys = W * (V + kPad);
+    constexpr int kStride = V + kPad;
     constexpr bool kStore = kSorted || GROUPS;
-    __shared__ alignas(16) uint32_t s_key[kStore ? kRouteWarps * kRows : 1][kStore ? kKeys : 4];
+    __shared__ alignas(16) float s_key[kStore ? kRouteWarps * kRows : 1][kStore ? W * kStride : 4];
     __shared__ float s_group[GROUPS ? kRouteWarps * kRows : 1][GROUPS ? 32 : 1];
     const int lane = threadIdx.x & (W - 1);
     const int local = threadIdx.x / W;
@@ -188,62 +190,114 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
         for (int v = 0; v < V; ++v)
             x[v] = e0 + v < a.E ? Elem<T>::up(x_row[e0 + v]) : -INFINITY;
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        x[v] = fmaxf(x[v], -INFINITY);   // NaN is masked as -inf is
 
     // scores (softmax: exp(x - max), normalised by `total`)
     float part[V];
     float top = 0.0f, total = 1.0f;
-    const bool scores = GROUPS || a.bias != nullptr;
     if constexpr (SIGMOID) {
-        if (scores) {
+        if (a.scored) {
+            float most = 1.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                part[v] = 1.0f + (x[v] == -INFINITY ? 0.0f : expf(-x[v]));
+                most = fmaxf(most, part[v]);
+            }
+            if (__any_sync(kAll, most > 0x1p125f)) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    part[v] = 1.0f / part[v];
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    part[v] = reciprocal(part[v]);
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                part[v] = is_masked(x[v]) ? 0.0f : sigmoid(x[v]);
+                part[v] = x[v] == -INFINITY ? 0.0f : part[v];
         }
-    } else if (scores || !a.renorm) {
-        uint32_t most = 0;
+    } else if (a.scored || !a.renorm) {
+        float most = -INFINITY;
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            most = max(most, is_masked(x[v]) ? 0u : ordered(x[v]));
-        top = unordered(row_max<W>(most));
+            most = fmaxf(most, x[v]);
+        top = row_max<W>(most);
         total = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            part[v] = is_masked(x[v]) ? 0.0f : expf(x[v] - top);
+            part[v] = x[v] == -INFINITY ? 0.0f : expf(x[v] - top);
             total += part[v];
         }
         total = row_sum<W>(total);
     }
 
-    // keys: 0 is never selected
-    uint32_t key[V];
+    float key[V];
+    if (a.bias != nullptr) {
+        float b[V];
+        if (a.bias_wide) {
+            constexpr int VE = V < 4 ? V : 4;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float f = x[v];
-        if (a.bias != nullptr)
-            f = (SIGMOID ? part[v] : part[v] / total) +
-                (e0 + v < a.E ? __ldg(a.bias + e0 + v) : 0.0f);
-        key[v] = is_masked(x[v]) || is_masked(f) ? 0u : ordered(f);
+            for (int v = 0; v < V; v += VE) {
+                float f[VE] = {};
+                if (e0 + v < a.E)
+                    widen<float, VE>(load_raw<float, VE>(a.bias + e0 + v), f);
+#pragma unroll
+                for (int i = 0; i < VE; ++i)
+                    b[v + i] = f[i];
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                b[v] = e0 + v < a.E ? __ldg(a.bias + e0 + v) : 0.0f;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float f = (SIGMOID ? part[v] : part[v] / total) + b[v];
+            key[v] = x[v] == -INFINITY ? -INFINITY : fmaxf(f, -INFINITY);
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            key[v] = x[v];
     }
 
-    uint32_t *keys = s_key[kStore ? local : 0];
+    float *keys = s_key[kStore ? local : 0];
     if constexpr (GROUPS) {
         float *of_group = s_group[local];
         const bool by_key = a.bias != nullptr || a.group_top == 1;
         if (a.group_lanes > 0) {
-            // a lane's experts are of one group: its lanes join theirs directly
+            // a lane's experts are of one group: its lanes join theirs directly, then share
+            // out the comparisons with the other groups
             Best2 b;
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                b.add(key[v] == 0 ? -INFINITY : by_key ? unordered(key[v]) : part[v]);
+                b.add(by_key ? key[v] : key[v] == -INFINITY ? -INFINITY : part[v]);
             for (int off = a.group_lanes >> 1; off > 0; off >>= 1)
                 b.join(off);
-            if ((lane & (a.group_lanes - 1)) == 0 && e0 < a.E)
-                of_group[lane / a.group_lanes] = b.key(a.group_top);
+            const float own = b.key(a.group_top);
+            const int part_of = lane & (a.group_lanes - 1);
+            const int g = lane / a.group_lanes;
+            if (part_of == 0 && g < a.groups)
+                of_group[g] = own;
+            __syncwarp();
+            int ahead = 0;
+            for (int h = part_of; h < a.groups; h += a.group_lanes) {
+                const float f = of_group[h];
+                ahead += f > own || (f == own && h < g);
+            }
+            for (int off = a.group_lanes >> 1; off > 0; off >>= 1)
+                ahead += __shfl_xor_sync(kAll, ahead, off);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                key[v] = ahead < a.topk_groups ? key[v] : -INFINITY;
         } else {
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                keys[lane * (V + kPad) + v] = __float_as_uint(
-                    key[v] == 0 ? -INFINITY : by_key ? unordered(key[v]) : part[v]);
+                keys[lane * kStride + v] = by_key                ? key[v]
+                                           : key[v] == -INFINITY ? -INFINITY
+                                                                 : part[v];
             __syncwarp();
             // lanes_per lanes form one group's key, all groups in one round where they fit
             int lanes_per = W;
@@ -256,74 +310,72 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
                 if (g < a.groups)
                     for (int m = part_of; m < a.per_group; m += lanes_per) {
                         const int e = g * a.per_group + m;
-                        b.add(__uint_as_float(keys[e / V * (V + kPad) + e % V]));
+                        b.add(keys[e / V * kStride + e % V]);
                     }
                 for (int off = lanes_per >> 1; off > 0; off >>= 1)
                     b.join(off);
                 if (part_of == 0 && g < a.groups)
                     of_group[g] = b.key(a.group_top);
             }
-        }
-        __syncwarp();
-        // a group stays if fewer than topk_groups are ahead of it
-        uint32_t stays = 0;
-        for (int g = lane; g < a.groups; g += W) {
-            const float mine = of_group[g];
-            int ahead = 0;
-            for (int h = 0; h < a.groups; ++h) {
-                const float f = of_group[h];
-                ahead += f > mine || (f == mine && h < g);
+            __syncwarp();
+            // a group stays if fewer than topk_groups are ahead of it
+            uint32_t stays = 0;
+            for (int g = lane; g < a.groups; g += W) {
+                const float own = of_group[g];
+                int ahead = 0;
+                for (int h = 0; h < a.groups; ++h) {
+                    const float f = of_group[h];
+                    ahead += f > own || (f == own && h < g);
+                }
+                if (ahead < a.topk_groups)
+                    stays |= 1u << g;
             }
-            if (ahead < a.topk_groups)
-                stays |= 1u << g;
-        }
-        stays = row_or<W>(stays);
-        if (a.group_lanes > 0) {
-            const bool mine = ((stays >> ((lane / a.group_lanes) & 31)) & 1u) != 0;
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                key[v] = mine ? key[v] : 0u;
-        } else {
+            stays = row_or<W>(stays);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const uint32_t g = (static_cast<uint32_t>(e0 + v) * a.group_magic) >> 20;
                 if (((stays >> (g & 31)) & 1u) == 0)
-                    key[v] = 0;
+                    key[v] = -INFINITY;
             }
+            __syncwarp();
         }
-        __syncwarp();
     }
 
     int32_t mine[kSlots];
 #pragma unroll
-    for (int s = 0; s < kSlots; ++s)
-        mine[s] = -1;
+    for (int q = 0; q < kSlots; ++q)
+        mine[q] = -1;
     if constexpr (kSorted) {
-        uint32_t s[V];
+        float s[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             s[v] = key[v];
-            keys[lane * (V + kPad) + v] = key[v];
+            keys[lane * kStride + v] = key[v];
         }
         sort_down<V>(s);
         // round j's key, the lane it came from, and how many equal ones that lane gave before
-        uint32_t got[kSlots] = {};
-        int32_t from[kSlots] = {}, nth[kSlots] = {};
-        uint32_t last_key = 0;
-        int32_t last_lane = -1, equal = 0;
-        for (int j = 0; j < a.k; ++j) {
-            const uint32_t most = row_max<W>(s[0]);
-            const uint32_t holds = __ballot_sync(kAll, s[0] == most) >> (threadIdx.x & (32 - W));
-            const int32_t winner = __ffs(holds) - 1;   // within the row: it holds it or a lower row's
-            equal = most == last_key && winner == last_lane ? equal + 1 : 0;
-            last_key = most;
-            last_lane = winner;
-            if (lane == winner) {
+        float got[kSlots];
+        int32_t from[kSlots], nth[kSlots];
 #pragma unroll
-                for (int v = 0; v + 1 < V; ++v)
-                    s[v] = s[v + 1];
-                s[V - 1] = 0;
+        for (int q = 0; q < kSlots; ++q) {
+            got[q] = -INFINITY;
+            from[q] = nth[q] = 0;
+        }
+        float last_key = 0.0f;
+        int32_t last_lane = -1, equal = 0;
+        auto round = [&](int j, int shift) {
+            const float most = row_max<W>(s[0]);
+            const uint32_t holds = __ballot_sync(kAll, s[0] == most) >> (threadIdx.x & (32 - W));
+            const int32_t winner = __ffs(holds) - 1;   // its row's lanes come first in holds
+            if constexpr (W < 32) {
+                equal = most == last_key && winner == last_lane ? equal + 1 : 0;
+                last_key = most;
+                last_lane = winner;
             }
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (v < shift)
+                    s[v] = lane != winner ? s[v] : v + 1 < V ? s[v + 1] : -INFINITY;
 #pragma unroll
             for (int q = 0; q < kSlots; ++q)
                 if (j == lane + q * W) {
@@ -331,15 +383,28 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
                     from[q] = winner;
                     nth[q] = equal;
                 }
+        };
+        if (a.k <= 8) {
+            // round j of at most 8 can still look at 8 - j keys of a lane
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < a.k)
+                    round(j, 7 - j);
+        } else {
+            for (int j = 0; j < a.k; ++j)
+                round(j, V);
         }
+        if constexpr (W == 32)
+            nth[0] = __popc(__match_any_sync(kAll, __float_as_uint(got[0] + 0.0f)) &
+                            __match_any_sync(kAll, from[0]) & ((1u << lane) - 1u));
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < kSlots; ++q)
-            if (got[q] != 0) {
+            if (got[q] != -INFINITY) {
                 int32_t left = nth[q];
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    if (keys[from[q] * (V + kPad) + v] == got[q]) {
+                    if (keys[from[q] * kStride + v] == got[q]) {
                         if (left == 0)
                             mine[q] = from[q] * V + v;
                         --left;
@@ -347,7 +412,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
             }
     } else {
         for (int j = 0; j < a.k; ++j) {
-            uint32_t best = 0;
+            float best = -INFINITY;
             int32_t at = 0;
 #pragma unroll
             for (int v = 0; v < V; ++v)
@@ -355,59 +420,54 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
                     best = key[v];
                     at = e0 + v;
                 }
-            const uint32_t most = row_max<W>(best);
+            const float most = row_max<W>(best);
             const int32_t e = __shfl_sync(kAll, at, __ffs(__ballot_sync(kAll, best == most)) - 1);
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if (most != 0 && e == e0 + v)
-                    key[v] = 0;
+                if (e == e0 + v)
+                    key[v] = -INFINITY;
             if (j == lane)
-                mine[0] = most != 0 ? e : -1;
+                mine[0] = most != -INFINITY ? e : -1;
         }
     }
 
     // weights, from the selected logits (just read: in L1)
     float w[kSlots];
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q)
+        w[q] = mine[q] >= 0 ? Elem<T>::up(x_row[mine[q]]) : -INFINITY;
     if (a.renorm && !SIGMOID) {
         // the selection's own maximum, so that it never underflows as a whole
-        uint32_t most = 0;
+        float most = -INFINITY;
 #pragma unroll
-        for (int s = 0; s < kSlots; ++s) {
-            w[s] = mine[s] >= 0 ? Elem<T>::up(x_row[mine[s]]) : -INFINITY;
-            most = max(most, mine[s] >= 0 ? ordered(w[s]) : 0u);
-        }
-        top = unordered(row_max<W>(most));
-#pragma unroll
-        for (int s = 0; s < kSlots; ++s)
-            w[s] = mine[s] >= 0 ? expf(w[s] - top) : 0.0f;
-    } else {
-#pragma unroll
-        for (int s = 0; s < kSlots; ++s) {
-            w[s] = 0.0f;
-            if (mine[s] >= 0) {
-                const float f = Elem<T>::up(x_row[mine[s]]);
-                w[s] = SIGMOID ? sigmoid(f) : expf(f - top);
-            }
-        }
+        for (int q = 0; q < kSlots; ++q)
+            most = fmaxf(most, w[q]);
+        top = row_max<W>(most);
     }
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q)
+        if (mine[q] < 0)
+            w[q] = 0.0f;
+        else
+            w[q] = SIGMOID ? sigmoid(w[q]) : expf(w[q] - top);
     if (a.renorm) {
         total = 0.0f;
 #pragma unroll
-        for (int s = 0; s < kSlots; ++s)
-            total += w[s];
+        for (int q = 0; q < kSlots; ++q)
+            total += w[q];
         total = row_sum<W>(total);
     }
     if (!live)
         return;
     const bool divide = a.renorm || !SIGMOID;
 #pragma unroll
-    for (int s = 0; s < kSlots; ++s) {
-        const int j = lane + s * W;
+    for (int q = 0; q < kSlots; ++q) {
+        const int j = lane + q * W;
         if (j < a.k) {
-            float f = w[s];
+            float f = w[q];
             if (divide)   // nothing selected, or sigmoids that are all 0: weight 0
-                f = mine[s] < 0 || total == 0.0f ? 0.0f : f / total;
-            a.idx[row * a.k + j] = mine[s];
+                f = mine[q] < 0 || total == 0.0f ? 0.0f : f / total;
+            a.idx[row * a.k + j] = mine[q];
             a.weights[row * a.k + j] = f * a.scale;
         }
     }
@@ -448,8 +508,10 @@ struct Chosen {
             x = Elem<T>::up(static_cast<const T *>(a.logits)[row * a.E + e]);
             on = !is_masked(x);
         }
-        if (!on)
+        if (!on) {
+            x = -INFINITY;
             g = 0.0f;
+        }
     }
 };
 
@@ -505,7 +567,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_sparse_kernel(con
             d = slope * c.g;
         }
     } else {
-        const float top = unordered(row_max<KW>(c.on ? ordered(c.x) : 0u));
+        const float top = row_max<KW>(c.x);
         float p = c.on ? expf(c.x - top) : 0.0f;
         const float total = row_sum<KW>(p);
         p = c.on ? p / total : 0.0f;
@@ -552,11 +614,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_dense_kernel(cons
         for (int i = 0; i < VE; ++i)
             x[v + i] = f[i];
     }
-    uint32_t most = 0;
+    float most = -INFINITY;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        most = max(most, is_masked(x[v]) ? 0u : ordered(x[v]));
-    const float top = unordered(row_max<W>(most));
+        most = fmaxf(most, x[v]);
+    const float top = row_max<W>(most);
     float total = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -612,6 +674,8 @@ cudaError_t route_shape(RouteArgs a, bool sigmoid, cudaStream_t stream)
     const uintptr_t vec = std::min<uintptr_t>(16, (V < 8 ? V : 8) * sizeof(T));
     a.wide = a.E % (V < 8 ? V : 8) == 0 && a.E * sizeof(T) % vec == 0 &&
              reinterpret_cast<uintptr_t>(a.logits) % vec == 0;
+    a.bias_wide = a.E % (V < 4 ? V : 4) == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
+    a.scored = a.bias != nullptr || (a.groups > 1 && a.group_top == 2);
     const int lanes = a.per_group % V == 0 ? a.per_group / V : 0;
     a.group_lanes = lanes > 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
     const int rows = kRouteWarps * (32 / W);
