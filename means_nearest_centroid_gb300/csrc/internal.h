@@ -177,14 +177,13 @@ cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *orde
                          int32_t *offsets, void *scratch, cudaStream_t stream);
 cudaError_t launch_lookup(const void *table, int dtype, int64_t K, int64_t D, const int32_t *idx,
                           const float *weights, int64_t N, int32_t k, float scale, void *out,
-                          cudaStream_t stream);
+                          int sms, cudaStream_t stream);
 cudaError_t launch_dweights(const void *dout, const void *table, int dtype, const int32_t *idx,
-                            int64_t M, int32_t k, int64_t K, int64_t D, float scale,
+                            int64_t N, int32_t k, int64_t K, int64_t D, float scale,
                             float *dweights, cudaStream_t stream);
 // The gradient of the table from the sorted ids (launch_lists with rows);
 // parts: 16-byte aligned workspace of lookup_grad_parts_bytes.
-size_t lookup_grad_parts_bytes(const void *dout, int dtype, const void *dtable, int grad_dtype,
-                               int64_t M, int64_t D, int sms);
+size_t lookup_grad_parts_bytes(int64_t M, int64_t D, int sms);
 cudaError_t launch_lookup_grad(const void *dout, int dtype, const float *weights, int64_t M,
                                int32_t k, int64_t K, int64_t D, float scale, int32_t skip,
                                bool accumulate, const int32_t *order, const int32_t *rows,

@@ -237,7 +237,11 @@ int kmassign_lookup(const void *table, int32_t dtype, int64_t K, int64_t D, cons
     const void *ptrs[4] = {table, idx, weights, out};
     if ((rc = check_device_ptrs(ptrs, 4)) != KMASSIGN_OK)
         return rc;
-    return done(kma::launch_lookup(table, dtype, K, D, idx, weights, N, k, scale, out,
+    cudaMemPool_t pool;
+    int sms;
+    if ((rc = kma::library_device(&pool, &sms)) != KMASSIGN_OK)
+        return rc;
+    return done(kma::launch_lookup(table, dtype, K, D, idx, weights, N, k, scale, out, sms,
                                    static_cast<cudaStream_t>(stream)));
 }
 
@@ -267,7 +271,7 @@ int kmassign_lookup_grad(const void *dout, int32_t dtype, const int32_t *idx, co
         return rc;
     const int64_t M = N * k;
     if (dweights != nullptr && N > 0 &&
-        kma::launch_dweights(dout, table, dtype, idx, M, k, K, D, scale, dweights, s) !=
+        kma::launch_dweights(dout, table, dtype, idx, N, k, K, D, scale, dweights, s) !=
             cudaSuccess)
         return KMASSIGN_ERR_CUDA;
     if (dtable == nullptr || (N == 0 && accumulate))
@@ -280,8 +284,7 @@ int kmassign_lookup_grad(const void *dout, int32_t dtype, const int32_t *idx, co
     const size_t ids = up16(static_cast<size_t>(M) * 4);
     const size_t offs = up16(static_cast<size_t>(K + 1) * 4);
     const size_t sort = up16(kma::lists_scratch_bytes(M, K));
-    const size_t parts =
-        kma::lookup_grad_parts_bytes(dout, dtype, dtable, grad_dtype, M, D, sms);
+    const size_t parts = kma::lookup_grad_parts_bytes(M, D, sms);
     Scratch scratch(2 * ids + offs + sort + parts, pool, s);
     if (!scratch.ok())
         return KMASSIGN_ERR_CUDA;

@@ -2,19 +2,25 @@
 // that they name, each group in ascending order (a stable sort), with ids
 // outside [0, K) left out; offsets[r] is where row r's group begins.
 //
-// A radix sort from the lowest digit up, of (row, position) pairs.  Each of up
-// to 152 blocks owns one contiguous share of the pairs, so the order within a
-// digit is: earlier blocks first, then the block's own items in order.
-//   count:    block b counts its items by the first digit -> H0[b][digit]
+// A radix sort of (row, position) pairs from the lowest digit up.  Each of up
+// to 304 blocks owns one contiguous share of the pairs, so the order within a
+// digit is: earlier blocks first, then the block's own items in order.  Per digit
+//   count:    block b counts its items -> H[b][digit];
 //   scatter:  block b sums H[b'][digit] over the blocks b' before it and over
-//             all blocks, scans the digits, ranks its items (a warp's equal
-//             digits by match, warps by a per-warp count in shared memory) and
-//             writes them; it also counts the next digit for the block that
-//             will own the written place (integer atomics: any order gives the
-//             same counts).
-// So a sort of P digits is 1 + P launches, and up to kOneBlockMax items are one
+//             all blocks, scans the digits, and takes its items in tiles: ranks
+//             them (a warp's equal digits by match, warps by their counts in
+//             shared memory), orders the tile by digit in shared memory, and
+//             writes it out in runs of consecutive places.
+// The two launches cost less than one whose blocks count the next digit for
+// each other with atomics (measured on 2^20 ids of 4,096 rows: 31 us a scatter
+// with atomics and without the ordered tile).  Up to kOneBlockMax items are one
 // launch of one block.  Nothing depends on timing: the result is unique.
+//
+// offsets are found by a search in the sorted rows within the row's last digit:
+// 32 ways at a step by a warp for each row, or, where there are many rows (whose
+// searches hide each other's latency), eight ways by a thread.
 #include "internal.h"
+#include "launch.cuh"
 
 #include <algorithm>
 
@@ -25,18 +31,14 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxDigitBits = 10;
-constexpr int kMaxBins = 1 << kMaxDigitBits;
-constexpr int kMaxBlocks = 152;
+constexpr int kMaxBlocks = 304;           // two on each SM
 constexpr int64_t kOneBlockMax = 4096;
 constexpr int64_t kOneOffsetsMax = 8192;   // rows whose offsets the one block finds itself
-constexpr int kOneThreads = 1024;
-constexpr int kOneWarps = kOneThreads / 32;
-constexpr int kOneItems = static_cast<int>(kOneBlockMax) / kOneThreads;
-constexpr int kOneBits = 6;   // digit of the one-block sort
+constexpr int kOneBits = 8;                // digit of the one-block sort
 constexpr int kOneBins = 1 << kOneBits;
 
 // Exclusive scan over the block of one value per thread; *total: the sum.
-// warp_sums: blockDim.x / 32 + 1 values.
+// warp_sums: WARPS + 1 values.
 template <int WARPS>
 __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t *warp_sums, int32_t *total)
 {
@@ -75,14 +77,14 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t *warp_sums, int
 
 // Rank of the lane's item among the items of its digit seen so far by this
 // warp; `counts` (the warp's own bins) takes the new ones.  d < 0: no item.
-__device__ __forceinline__ int32_t warp_rank(int32_t d, int32_t *counts, int lane)
+__device__ __forceinline__ int32_t warp_rank(int32_t d, uint16_t *counts, int lane)
 {
     const uint32_t same = __match_any_sync(kAll, d);
     const uint32_t below = same & ((1u << lane) - 1u);
     int32_t base = 0;
     if (d >= 0 && below == 0) {
         base = counts[d];
-        counts[d] = base + __popc(same);
+        counts[d] = static_cast<uint16_t>(base + __popc(same));
     }
     base = __shfl_sync(kAll, base, __ffs(same) - 1);
     __syncwarp();
@@ -90,96 +92,107 @@ __device__ __forceinline__ int32_t warp_rank(int32_t d, int32_t *counts, int lan
 }
 
 struct SortArgs {
-    const int32_t *idx;     // first pass: the rows, position = index
-    const int2 *in;         // later passes: (row, position)
-    int2 *out;              // all but the last pass
-    int32_t *order;         // last pass
-    int32_t *rows;          // last pass, or nullptr: the rows in sorted order
-    int32_t *offsets;       // last pass of a one-digit sort, else nullptr
-    const int32_t *hist;    // H[block][bins] of this digit
-    int32_t *next_hist;     // of the next digit, or nullptr
-    int32_t *total;         // valid ids: written by the first pass, read by later ones
+    const int32_t *rows_in;   // first pass: idx, and the position is the index
+    const int32_t *pos_in;
+    int32_t *rows_out;        // last pass: may be nullptr
+    int32_t *pos_out;
+    int32_t *offsets;         // of a one-digit sort, else nullptr
+    int32_t *hist;            // H[block][bins] of this digit
+    int32_t *total;           // number of valid ids: set by the first pass
+    int32_t *starts;          // last pass: [bins + 1] where each digit's items start, or nullptr
     int64_t M;
-    int64_t share;          // items per block
+    int64_t share;            // items per block
     int32_t K;
-    int32_t shift, bins;    // this digit: (row >> shift) & (bins - 1)
-    int32_t next_shift, next_bins;
+    int32_t shift, bins;      // this digit: (row >> shift) & (bins - 1)
     int32_t blocks;
+    bool last;
 };
 
-// H[b][d] of the first digit; the later digits' counts are zeroed.
-__global__ void __launch_bounds__(kThreads)
-    lists_count_kernel(const int32_t *__restrict__ idx, int64_t M, int64_t share, int32_t K,
-                       int32_t bins, int32_t *__restrict__ hist, int32_t *__restrict__ later,
-                       int64_t n_later)
+template <bool FIRST>
+__global__ void __launch_bounds__(kThreads) lists_count_kernel(const SortArgs a)
 {
-    __shared__ int32_t h[kMaxBins];
-    for (int d = threadIdx.x; d < bins; d += kThreads)
-        h[d] = 0;
-    for (int64_t d = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; d < n_later;
-         d += static_cast<int64_t>(gridDim.x) * kThreads)
-        later[d] = 0;
+    extern __shared__ int32_t smem[];
+    let_next_start();
+    for (int d = threadIdx.x; d < a.bins; d += kThreads)
+        smem[d] = 0;
     __syncthreads();
-    const int64_t begin = static_cast<int64_t>(blockIdx.x) * share;
-    const int64_t end = min(M, begin + share);
+    wait_for_previous();
+    const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.share;
+    const int64_t end = min(FIRST ? a.M : static_cast<int64_t>(*a.total), begin + a.share);
+#pragma unroll 4
     for (int64_t i = begin + threadIdx.x; i < end; i += kThreads) {
-        const int32_t r = __ldg(idx + i);
-        if (r >= 0 && r < K)
-            atomicAdd(h + (r & (bins - 1)), 1);
+        const int32_t r = a.rows_in[i];
+        if (!FIRST || (r >= 0 && r < a.K))
+            atomicAdd(smem + ((r >> a.shift) & (a.bins - 1)), 1);
     }
     __syncthreads();
-    for (int d = threadIdx.x; d < bins; d += kThreads)
-        hist[static_cast<int64_t>(blockIdx.x) * bins + d] = h[d];
+    for (int d = threadIdx.x; d < a.bins; d += kThreads)
+        a.hist[static_cast<int64_t>(blockIdx.x) * a.bins + d] = smem[d];
+}
+
+// Shared memory of a scatter block: the places of each digit, its start in
+// the tile, the tile's pairs, the warps' counts.
+size_t scatter_smem(int bins, int items)
+{
+    return static_cast<size_t>(bins) * 8 + static_cast<size_t>(kThreads) * items * 8 +
+           static_cast<size_t>(kWarps) * bins * 2;
 }
 
 template <int ITEMS, bool FIRST>
 __global__ void __launch_bounds__(kThreads) lists_scatter_kernel(const SortArgs a)
 {
     extern __shared__ int32_t smem[];
-    int32_t *base = smem;                    // [bins] next place of each digit, this block
-    int32_t *counts = smem + a.bins;         // [kWarps][bins] of one tile
+    constexpr int kTile = kThreads * ITEMS;
+    int32_t *place = smem;                // [bins] next place of each digit, this block
+    int32_t *start = place + a.bins;      // [bins] its first item in the ordered tile
+    int32_t *t_row = start + a.bins;      // [kTile]
+    int32_t *t_pos = t_row + kTile;       // [kTile]
+    uint16_t *counts = reinterpret_cast<uint16_t *>(t_pos + kTile);   // [kWarps][bins]
     __shared__ int32_t warp_sums[kWarps + 1];
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
+    let_next_start();
+    for (int d = threadIdx.x; d < 2 * a.bins; d += kThreads)
+        smem[d] = 0;
+    __syncthreads();
+    wait_for_previous();
 
     // places: all smaller digits, then this digit in earlier blocks; the
     // threads share out the blocks' counts of a digit (integer sums)
-    int32_t *all = counts, *before = counts + a.bins;
-    for (int d = threadIdx.x; d < 2 * a.bins; d += kThreads)
-        counts[d] = 0;
-    __syncthreads();
     const int lanes = max(1, kThreads / a.bins);   // threads per digit
     for (int t = threadIdx.x; t < a.bins * lanes; t += kThreads) {
         const int d = t & (a.bins - 1);
         int32_t n_all = 0, n_before = 0;
 #pragma unroll 8
         for (int b = t / a.bins; b < a.blocks; b += lanes) {
-            const int32_t n = __ldg(a.hist + static_cast<int64_t>(b) * a.bins + d);
+            const int32_t n = a.hist[static_cast<int64_t>(b) * a.bins + d];
             n_all += n;
             n_before += b < static_cast<int>(blockIdx.x) ? n : 0;
         }
-        atomicAdd(all + d, n_all);
-        atomicAdd(before + d, n_before);
+        atomicAdd(start + d, n_all);
+        atomicAdd(place + d, n_before);
     }
     __syncthreads();
-    int32_t carry = 0;
+    int32_t total = 0;
     for (int d0 = 0; d0 < a.bins; d0 += kThreads) {
         const int d = d0 + threadIdx.x;
         int32_t sum;
         const int32_t first =
-            carry + block_scan<kWarps>(d < a.bins ? all[d] : 0, warp_sums, &sum);
-        carry += sum;
+            total + block_scan<kWarps>(d < a.bins ? start[d] : 0, warp_sums, &sum);
+        total += sum;
         if (d < a.bins) {
-            base[d] = first + before[d];
+            place[d] += first;
             if (a.offsets != nullptr && blockIdx.x == 0 && d < a.K)
                 a.offsets[d] = first;
+            if (a.starts != nullptr && blockIdx.x == 0)
+                a.starts[d] = first;
         }
     }
-    __syncthreads();   // counts is reused below
-    const int32_t total = carry;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-        if (FIRST && a.total != nullptr)
+        if (FIRST)
             *a.total = total;
+        if (a.starts != nullptr)
+            a.starts[a.bins] = total;
         if (a.offsets != nullptr)
             a.offsets[a.K] = total;
     }
@@ -187,10 +200,10 @@ __global__ void __launch_bounds__(kThreads) lists_scatter_kernel(const SortArgs 
     const int64_t limit = FIRST ? a.M : total;
     const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.share;
     const int64_t end = min(limit, begin + a.share);
-    for (int64_t t0 = begin; t0 < end; t0 += kThreads * ITEMS) {
-        for (int c = threadIdx.x; c < kWarps * a.bins; c += kThreads)
-            counts[c] = 0;
-        __syncthreads();
+    for (int64_t t0 = begin; t0 < end; t0 += kTile) {
+        uint32_t *words = reinterpret_cast<uint32_t *>(counts);
+        for (int c = threadIdx.x; c < (kWarps * a.bins) >> 1; c += kThreads)
+            words[c] = 0;
         int32_t row[ITEMS], pos[ITEMS], rank[ITEMS];
         const int64_t w0 = t0 + static_cast<int64_t>(warp) * (32 * ITEMS) + lane;
 #pragma unroll
@@ -199,146 +212,156 @@ __global__ void __launch_bounds__(kThreads) lists_scatter_kernel(const SortArgs 
             row[u] = -1;
             pos[u] = static_cast<int32_t>(i);
             if (i < end) {
-                if constexpr (FIRST) {
-                    const int32_t r = __ldg(a.idx + i);
-                    row[u] = r >= 0 && r < a.K ? r : -1;
-                } else {
-                    const int2 rp = __ldg(a.in + i);
-                    row[u] = rp.x;
-                    pos[u] = rp.y;
-                }
+                const int32_t r = a.rows_in[i];
+                row[u] = !FIRST || (r >= 0 && r < a.K) ? r : -1;
+                if (!FIRST)
+                    pos[u] = a.pos_in[i];
             }
         }
+        __syncthreads();
 #pragma unroll
         for (int u = 0; u < ITEMS; ++u) {
             const int32_t d = row[u] < 0 ? -1 : (row[u] >> a.shift) & (a.bins - 1);
             rank[u] = warp_rank(d, counts + warp * a.bins, lane);
         }
         __syncthreads();
-        // per digit: the warps' starts
-        for (int d = threadIdx.x; d < a.bins; d += kThreads) {
-            int32_t run = base[d];
+        // per digit: where its items, and each warp's of them, start in the ordered tile
+        int32_t in_tile = 0;
+        for (int d0 = 0; d0 < a.bins; d0 += kThreads) {
+            const int d = d0 + threadIdx.x;
+            int32_t n = 0;
+            if (d < a.bins)
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const int32_t n = counts[w * a.bins + d];
-                counts[w * a.bins + d] = run;
-                run += n;
-            }
-            base[d] = run;
+                for (int w = 0; w < kWarps; ++w) {
+                    const uint16_t c = counts[w * a.bins + d];
+                    counts[w * a.bins + d] = static_cast<uint16_t>(n);
+                    n += c;
+                }
+            int32_t sum;
+            const int32_t first = in_tile + block_scan<kWarps>(n, warp_sums, &sum);
+            in_tile += sum;
+            if (d < a.bins)
+                start[d] = first;
         }
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < ITEMS; ++u)
             if (row[u] >= 0) {
                 const int32_t d = (row[u] >> a.shift) & (a.bins - 1);
-                const int32_t to = counts[warp * a.bins + d] + rank[u];
-                if (a.next_hist != nullptr) {
-                    a.out[to] = make_int2(row[u], pos[u]);
-                    const uint32_t owner = static_cast<uint32_t>(to) / static_cast<uint32_t>(a.share);
-                    atomicAdd(a.next_hist + static_cast<int64_t>(owner) * a.next_bins +
-                                  ((row[u] >> a.next_shift) & (a.next_bins - 1)),
-                              1);
-                } else {
-                    a.order[to] = pos[u];
-                    if (a.rows != nullptr)
-                        a.rows[to] = row[u];
-                }
+                const int to = start[d] + counts[warp * a.bins + d] + rank[u];
+                t_row[to] = row[u];
+                t_pos[to] = pos[u];
             }
+        __syncthreads();
+        for (int t = threadIdx.x; t < in_tile; t += kThreads) {
+            const int32_t r = t_row[t];
+            const int32_t d = (r >> a.shift) & (a.bins - 1);
+            const int64_t to = place[d] + (t - start[d]);
+            a.pos_out[to] = t_pos[t];
+            if (a.rows_out != nullptr)
+                a.rows_out[to] = r;
+        }
+        __syncthreads();
+        for (int d = threadIdx.x; d < a.bins; d += kThreads)
+            place[d] += (d + 1 < a.bins ? start[d + 1] : in_tile) - start[d];
         __syncthreads();
     }
     // places that no valid id takes
-    if (a.next_hist == nullptr)
+    if (a.last)
         for (int64_t i = max(begin, static_cast<int64_t>(total)) + threadIdx.x;
              i < min(a.M, begin + a.share); i += kThreads)
-            a.order[i] = -1;
+            a.pos_out[i] = -1;
 }
 
-// Up to kOneBlockMax items: every digit by one block, the pairs in shared
-// memory.  Ids outside [0, K) carry the row K, sort last and become -1.
-__global__ void __launch_bounds__(kOneThreads)
+// Up to THREADS * ITEMS items: every digit by one block, the pairs in shared
+// memory.  The first digit's pass drops ids outside [0, K).
+template <int THREADS, int ITEMS>
+__global__ void __launch_bounds__(THREADS)
     lists_one_block_kernel(const int32_t *__restrict__ idx, int32_t M, int32_t K, int32_t bits,
                            int32_t *__restrict__ order, int32_t *__restrict__ rows,
                            int32_t *__restrict__ offsets, int32_t *__restrict__ total)
 {
-    __shared__ int32_t s_row[kOneBlockMax];
-    __shared__ uint16_t s_pos[kOneBlockMax];
-    __shared__ int32_t counts[kOneWarps][kOneBins];
-    __shared__ int32_t warp_sums[kOneWarps + 1];
+    constexpr int kW = THREADS / 32;
+    constexpr int kMax = THREADS * ITEMS;
+    static_assert(THREADS >= kOneBins, "a thread per digit");
+    __shared__ int32_t s_row[kMax];
+    __shared__ uint16_t s_pos[kMax];
+    __shared__ uint16_t counts[kW][kOneBins];
+    __shared__ int32_t warp_sums[kW + 1];
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
-    const int items = (M + kOneThreads - 1) / kOneThreads;   // per thread, <= kOneItems
-    int32_t row[kOneItems], pos[kOneItems], rank[kOneItems];
+    let_next_start();
+    wait_for_previous();
+    int32_t n = M;   // items of this pass
+    for (int shift = 0; shift == 0 || shift < bits; shift += kOneBits) {
+        const int items = (n + THREADS - 1) / THREADS;   // per thread, <= ITEMS
+        for (int c = threadIdx.x; c < kW * kOneBins / 2; c += THREADS)
+            reinterpret_cast<uint32_t *>(&counts[0][0])[c] = 0;
+        int32_t row[ITEMS], pos[ITEMS], rank[ITEMS];
 #pragma unroll
-    for (int u = 0; u < kOneItems; ++u) {
-        const int i = warp * (32 * items) + u * 32 + lane;
-        const bool in = u < items && i < M;
-        pos[u] = i;
-        row[u] = -1;
-        if (in) {
-            const int32_t r = __ldg(idx + i);
-            row[u] = r >= 0 && r < K ? r : K;
+        for (int u = 0; u < ITEMS; ++u) {
+            const int i = warp * (32 * items) + u * 32 + lane;
+            row[u] = -1;
+            pos[u] = i;
+            if (u < items && i < n) {
+                if (shift == 0) {
+                    const int32_t r = __ldg(idx + i);
+                    row[u] = r >= 0 && r < K ? r : -1;
+                } else {
+                    row[u] = s_row[i];
+                    pos[u] = s_pos[i];
+                }
+            }
         }
-    }
-    for (int shift = 0; shift < bits; shift += kOneBits) {
-        for (int c = threadIdx.x; c < kOneWarps * kOneBins; c += kOneThreads)
-            (&counts[0][0])[c] = 0;
         __syncthreads();
 #pragma unroll
-        for (int u = 0; u < kOneItems; ++u)
-            if (u < items) {
-                const int32_t d = row[u] < 0 ? -1 : (row[u] >> shift) & (kOneBins - 1);
-                rank[u] = warp_rank(d, counts[warp], lane);
-            }
+        for (int u = 0; u < ITEMS; ++u)
+            if (u < items)
+                rank[u] = warp_rank(row[u] < 0 ? -1 : (row[u] >> shift) & (kOneBins - 1),
+                                    counts[warp], lane);
         __syncthreads();
-        int32_t all = 0;
+        int32_t mine = 0;
         if (threadIdx.x < kOneBins)
 #pragma unroll
-            for (int w = 0; w < kOneWarps; ++w)
-                all += counts[w][threadIdx.x];
-        int32_t sum;
-        int32_t run = block_scan<kOneWarps>(all, warp_sums, &sum);
-        if (threadIdx.x < kOneBins)
+            for (int w = 0; w < kW; ++w)
+                mine += counts[w][threadIdx.x];
+        int32_t run = block_scan<kW>(mine, warp_sums, &n);
+        if (threadIdx.x < kOneBins) {
+            if (bits <= kOneBits && offsets != nullptr && threadIdx.x < K)
+                offsets[threadIdx.x] = run;
 #pragma unroll
-            for (int w = 0; w < kOneWarps; ++w) {
-                const int32_t n = counts[w][threadIdx.x];
-                counts[w][threadIdx.x] = run;
-                run += n;
+            for (int w = 0; w < kW; ++w) {
+                const int32_t c = counts[w][threadIdx.x];
+                counts[w][threadIdx.x] = static_cast<uint16_t>(run);
+                run += c;
             }
+        }
         __syncthreads();
 #pragma unroll
-        for (int u = 0; u < kOneItems; ++u)
+        for (int u = 0; u < ITEMS; ++u)
             if (u < items && row[u] >= 0) {
                 const int to = counts[warp][(row[u] >> shift) & (kOneBins - 1)] + rank[u];
                 s_row[to] = row[u];
                 s_pos[to] = static_cast<uint16_t>(pos[u]);
             }
         __syncthreads();
-#pragma unroll
-        for (int u = 0; u < kOneItems; ++u) {
-            const int i = warp * (32 * items) + u * 32 + lane;
-            if (u < items && i < M) {
-                row[u] = s_row[i];
-                pos[u] = s_pos[i];
-            }
-        }
-        __syncthreads();
     }
-#pragma unroll
-    for (int u = 0; u < kOneItems; ++u) {
-        const int i = warp * (32 * items) + u * 32 + lane;
-        if (u < items && i < M) {
-            order[i] = row[u] < K ? pos[u] : -1;
-            if (rows != nullptr)
-                rows[i] = row[u];
-            s_row[i] = row[u];
-        }
+    for (int i = threadIdx.x; i < M; i += THREADS) {
+        order[i] = i < n ? s_pos[i] : -1;
+        if (rows != nullptr && i < n)
+            rows[i] = s_row[i];
     }
-    __syncthreads();
-    // offsets[r]: the first place whose row is at least r (K <= kOneOffsetsMax;
-    // else only their number, for the offsets' own launch)
-    const int32_t most = offsets != nullptr ? K : threadIdx.x == 0 ? K : -1;
-    for (int32_t r = offsets != nullptr ? threadIdx.x : K; r <= most; r += kOneThreads) {
-        int lo = 0, hi = M;
+    if (total != nullptr && threadIdx.x == 0)
+        *total = n;
+    if (offsets == nullptr)
+        return;
+    if (threadIdx.x == 0)
+        offsets[K] = n;
+    if (bits <= kOneBits)
+        return;
+    // K <= kOneOffsetsMax: the first place whose row is at least r
+    for (int r = threadIdx.x; r < K; r += THREADS) {
+        int lo = 0, hi = n;
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (s_row[mid] < r)
@@ -346,48 +369,97 @@ __global__ void __launch_bounds__(kOneThreads)
             else
                 hi = mid;
         }
-        if (offsets != nullptr)
-            offsets[r] = lo;
-        else
-            *total = lo;
-        if (r == K)
-            break;   // no step past the largest row
+        offsets[r] = lo;
     }
 }
 
-// offsets[r] for r in [0, K] by bisection in the sorted rows.
+// offsets[r] for r in [0, K]: the number of sorted rows below r.  starts: where
+// the rows with each value of r >> shift start (nullptr: only their number,
+// *total).
 __global__ void __launch_bounds__(256)
-    lists_offsets_kernel(const int32_t *__restrict__ rows, const int32_t *__restrict__ total,
-                         int32_t K, int32_t *__restrict__ offsets)
+    lists_offsets_kernel(const int32_t *rows, const int32_t *total, const int32_t *starts,
+                         int32_t shift, int32_t K, int32_t *__restrict__ offsets)
 {
+    let_next_start();
+    wait_for_previous();
     const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (r > K)
         return;
-    int32_t lo = 0, hi = *total;
-    while (lo < hi) {
-        const int32_t mid = lo + ((hi - lo) >> 1);
-        if (__ldg(rows + mid) < r)
-            lo = mid + 1;
-        else
-            hi = mid;
+    // the answer is in [lo, lo + n]
+    int64_t lo = 0, n;
+    if (starts != nullptr && r < K) {
+        lo = starts[r >> shift];
+        n = starts[(r >> shift) + 1] - lo;
+    } else {
+        n = *total;
     }
-    offsets[r] = lo;
+    while (n > 0) {
+        // seven probes cut the range into eight; count those below r
+        const int64_t step = (n + 7) >> 3;
+        int below = 0;
+#pragma unroll
+        for (int q = 1; q < 8; ++q) {
+            const int64_t at = q * step - 1;
+            below += at < n && rows[lo + at] < r;
+        }
+        lo += below * step;
+        n -= below * step;
+        if (below < 7)
+            n = min(step - 1, n);
+    }
+    offsets[r] = static_cast<int32_t>(lo);
+}
+
+__global__ void __launch_bounds__(256)
+    lists_offsets_warp_kernel(const int32_t *rows, const int32_t *total, const int32_t *starts,
+                              int32_t shift, int32_t K, int32_t *__restrict__ offsets)
+{
+    let_next_start();
+    wait_for_previous();
+    const int lane = threadIdx.x & 31;
+    const int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    if (r > K)
+        return;
+    int64_t lo = 0, n;
+    if (starts != nullptr && r < K) {
+        lo = starts[r >> shift];
+        n = starts[(r >> shift) + 1] - lo;
+    } else {
+        n = *total;
+    }
+    while (n > 0) {
+        const int64_t step = (n + 31) >> 5;
+        const int64_t at = (lane + 1) * step - 1;
+        const int below = __popc(__ballot_sync(kAll, at < n && rows[lo + at] < r));
+        lo += below * step;
+        n -= below * step;
+        if (below < 32)
+            n = min(step - 1, n);
+    }
+    if (lane == 0)
+        offsets[r] = static_cast<int32_t>(lo);
 }
 
 struct SortPlan {
     int passes;
     int bits[4], shift[4];
-    int items;      // per thread and tile: 2 or 8
+    int items;      // per thread and tile: 2, 4 or 8
     int blocks;
     int64_t share;
 };
 
-SortPlan sort_plan(int64_t M, int64_t K)
+int row_bits(int64_t K)
 {
-    SortPlan p{};
     int bits = 0;
     while ((int64_t(1) << bits) < K)
         ++bits;
+    return bits;
+}
+
+SortPlan sort_plan(int64_t M, int64_t K)
+{
+    SortPlan p{};
+    const int bits = row_bits(K);
     p.passes = std::max(1, (bits + kMaxDigitBits - 1) / kMaxDigitBits);
     int at = 0;
     for (int i = 0; i < p.passes; ++i) {
@@ -395,7 +467,11 @@ SortPlan sort_plan(int64_t M, int64_t K)
         p.shift[i] = at;
         at += p.bits[i];
     }
-    p.items = M <= int64_t(kMaxBlocks) * kThreads * 2 ? 2 : 8;
+    // the smallest tiles of which every block has one, else large ones in turn
+    p.items = 8;
+    for (int items = 4; items >= 2; items >>= 1)
+        if (M <= int64_t(kMaxBlocks) * kThreads * items)
+            p.items = items;
     const int64_t tile = int64_t(kThreads) * p.items;
     const int64_t tiles = (M + tile - 1) / tile;
     const int64_t per = (tiles + kMaxBlocks - 1) / kMaxBlocks;
@@ -406,30 +482,46 @@ SortPlan sort_plan(int64_t M, int64_t K)
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
-void launch_offsets(const int32_t *rows, const int32_t *total, int64_t K, int32_t *offsets,
-                    cudaStream_t stream)
+// Rows up to which a warp searches for each (4,097 rows in 2^20 places: 3 us
+// against 6; 131,073 rows in 2^14: 5 us by threads).
+constexpr int64_t kWarpSearchMax = 32768;
+
+cudaError_t launch_offsets(const int32_t *rows, const int32_t *total, const int32_t *starts,
+                           int32_t shift, int64_t K, int32_t *offsets, cudaStream_t stream)
 {
-    const int64_t blocks = (K + 1 + 255) / 256;
-    lists_offsets_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
-        rows, total, static_cast<int32_t>(K), offsets);
+    if (K <= kWarpSearchMax)
+        return launch_after(lists_offsets_warp_kernel, static_cast<unsigned>((K + 1 + 7) / 8), 256,
+                            0, stream, rows, total, starts, shift, K, offsets);
+    return launch_after(lists_offsets_kernel, static_cast<unsigned>((K + 1 + 255) / 256), 256, 0,
+                        stream, rows, total, starts, shift, K, offsets);
 }
 
 template <bool FIRST>
-void scatter(const SortArgs &a, int items, cudaStream_t stream)
+cudaError_t sort_pass(const SortArgs &a, int items, cudaStream_t stream)
 {
-    const size_t smem = static_cast<size_t>(kWarps + 1) * a.bins * 4;
-    if (items == 2)
-        lists_scatter_kernel<2, FIRST><<<a.blocks, kThreads, smem, stream>>>(a);
-    else
-        lists_scatter_kernel<8, FIRST><<<a.blocks, kThreads, smem, stream>>>(a);
+    const unsigned blocks = static_cast<unsigned>(a.blocks);
+    const cudaError_t e = launch_after(lists_count_kernel<FIRST>, blocks, kThreads,
+                                       static_cast<size_t>(a.bins) * 4, stream, a);
+    if (e != cudaSuccess)
+        return e;
+    const size_t smem = scatter_smem(a.bins, items);
+    switch (items) {
+    case 2:
+        return launch_after(lists_scatter_kernel<2, FIRST>, blocks, kThreads, smem, stream, a);
+    case 4:
+        return launch_after(lists_scatter_kernel<4, FIRST>, blocks, kThreads, smem, stream, a);
+    default:
+        return launch_after(lists_scatter_kernel<8, FIRST>, blocks, kThreads, smem, stream, a);
+    }
 }
 
 }  // namespace
 
 cudaError_t lists_prepare()
 {
-    const int smem = (kWarps + 1) * kMaxBins * 4;
+    const int smem = static_cast<int>(scatter_smem(1 << kMaxDigitBits, 8));
     for (auto *f : {lists_scatter_kernel<2, false>, lists_scatter_kernel<2, true>,
+                    lists_scatter_kernel<4, false>, lists_scatter_kernel<4, true>,
                     lists_scatter_kernel<8, false>, lists_scatter_kernel<8, true>}) {
         const cudaError_t e =
             cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -444,85 +536,80 @@ size_t lists_scratch_bytes(int64_t M, int64_t K)
     if (M <= kOneBlockMax)
         return K <= kOneOffsetsMax ? 0 : 16 + static_cast<size_t>(M) * 4;
     const SortPlan p = sort_plan(M, K);
-    size_t n = 16;   // total
+    // total, the digits' counts, two sets of pairs (the second set's rows may
+    // stand in for the sorted rows)
+    size_t n = 16;
     for (int i = 0; i < p.passes; ++i)
         n += up16((size_t(4) << p.bits[i]) * p.blocks);
-    if (p.passes > 1)
-        n += static_cast<size_t>(std::min(p.passes - 1, 2)) * up16(static_cast<size_t>(M) * 8) +
-             up16(static_cast<size_t>(M) * 4);
-    return n;
+    n += up16((size_t(4) << p.bits[p.passes - 1]) + 4);   // the last digit's starts
+    const size_t sets = p.passes == 1 ? 0 : p.passes == 2 ? 1 : 2;
+    return n + sets * 2 * up16(static_cast<size_t>(M) * 4) + up16(static_cast<size_t>(M) * 4);
 }
 
 cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *order, int32_t *rows,
                          int32_t *offsets, void *scratch, cudaStream_t stream)
 {
+    cudaError_t e = cudaSuccess;
     if (M <= kOneBlockMax) {
-        int bits = 0;
-        while ((int64_t(1) << bits) <= K)   // rows 0 to K
-            ++bits;
         const bool own = K <= kOneOffsetsMax;
-        int32_t *total = static_cast<int32_t *>(scratch);
+        int32_t *total = own ? nullptr : static_cast<int32_t *>(scratch);
         if (!own && rows == nullptr)
             rows = total + 4;
-        lists_one_block_kernel<<<1, kOneThreads, 0, stream>>>(
-            idx, static_cast<int32_t>(M), static_cast<int32_t>(K), bits, order, rows,
-            own ? offsets : nullptr, total);
-        if (!own)
-            launch_offsets(rows, total, K, offsets, stream);
-        return cudaGetLastError();
+        // one warp for every 128 items, at least eight
+        if (M <= 1024)
+            e = launch_after(lists_one_block_kernel<256, 4>, 1, 256, 0, stream, idx, M, K,
+                             row_bits(K), order, rows, own ? offsets : nullptr, total);
+        else
+            e = launch_after(lists_one_block_kernel<1024, 4>, 1, 1024, 0, stream, idx, M, K,
+                             row_bits(K), order, rows, own ? offsets : nullptr, total);
+        if (e == cudaSuccess && !own)
+            e = launch_offsets(rows, total, nullptr, 0, K, offsets, stream);
+        return e;
     }
     const SortPlan p = sort_plan(M, K);
+    const size_t ids = up16(static_cast<size_t>(M) * 4);
     uint8_t *at = static_cast<uint8_t *>(scratch);
     int32_t *total = reinterpret_cast<int32_t *>(at);
     at += 16;
     int32_t *hist[4] = {};
-    int64_t later = 0;   // counters of the later digits, one piece of memory
     for (int i = 0; i < p.passes; ++i) {
         hist[i] = reinterpret_cast<int32_t *>(at);
         at += up16((size_t(4) << p.bits[i]) * p.blocks);
-        if (i > 0)
-            later += up16((size_t(4) << p.bits[i]) * p.blocks) / 4;
     }
-    int2 *pairs[2] = {};
+    int32_t *starts = reinterpret_cast<int32_t *>(at);
+    at += up16((size_t(4) << p.bits[p.passes - 1]) + 4);
     int32_t *sorted = rows;
-    if (p.passes > 1) {
-        for (int i = 0; i < std::min(p.passes - 1, 2); ++i) {
-            pairs[i] = reinterpret_cast<int2 *>(at);
-            at += up16(static_cast<size_t>(M) * 8);
+    if (sorted == nullptr && p.passes > 1)
+        sorted = reinterpret_cast<int32_t *>(at);   // searched for the offsets
+    at += ids;
+    int32_t *set[2][2] = {};   // rows, positions
+    for (int i = 0; i < std::min(p.passes - 1, 2); ++i)
+        for (int j = 0; j < 2; ++j) {
+            set[i][j] = reinterpret_cast<int32_t *>(at);
+            at += ids;
         }
-        if (sorted == nullptr)
-            sorted = reinterpret_cast<int32_t *>(at);
-    }
-    lists_count_kernel<<<p.blocks, kThreads, 0, stream>>>(
-        idx, M, p.share, static_cast<int32_t>(K), 1 << p.bits[0], hist[0], hist[1], later);
-    for (int i = 0; i < p.passes; ++i) {
-        const bool last = i == p.passes - 1;
+    for (int i = 0; i < p.passes && e == cudaSuccess; ++i) {
         SortArgs a{};
-        a.idx = idx;
-        a.in = i > 0 ? pairs[(i - 1) & 1] : nullptr;
-        a.out = last ? nullptr : pairs[i & 1];
-        a.order = order;
-        a.rows = sorted;
+        a.last = i == p.passes - 1;
+        a.rows_in = i == 0 ? idx : set[(i - 1) & 1][0];
+        a.pos_in = i == 0 ? nullptr : set[(i - 1) & 1][1];
+        a.rows_out = a.last ? sorted : set[i & 1][0];
+        a.pos_out = a.last ? order : set[i & 1][1];
         a.offsets = p.passes == 1 ? offsets : nullptr;
         a.hist = hist[i];
-        a.next_hist = last ? nullptr : hist[i + 1];
         a.total = total;
+        a.starts = a.last ? starts : nullptr;
         a.M = M;
         a.share = p.share;
         a.K = static_cast<int32_t>(K);
         a.shift = p.shift[i];
         a.bins = 1 << p.bits[i];
-        a.next_shift = last ? 0 : p.shift[i + 1];
-        a.next_bins = last ? 1 : 1 << p.bits[i + 1];
         a.blocks = p.blocks;
-        if (i == 0)
-            scatter<true>(a, p.items, stream);
-        else
-            scatter<false>(a, p.items, stream);
+        e = i == 0 ? sort_pass<true>(a, p.items, stream) : sort_pass<false>(a, p.items, stream);
     }
-    if (p.passes > 1)
-        launch_offsets(sorted, total, K, offsets, stream);
-    return cudaGetLastError();
+    if (e == cudaSuccess && p.passes > 1)
+        e = launch_offsets(sorted, total, starts, p.shift[p.passes - 1], K, offsets, stream);
+    return e;
 }
 
 }  // namespace kma

@@ -7,16 +7,19 @@
 // output is rounded once.
 //
 // The gradient of the table sorts the ids by row first (lists.cu).  The sorted
-// places are then cut into chunks of a fixed length; a warp sums one slice of
-// columns over one chunk in registers and writes a row as soon as its last
-// place is passed.  A row that continues past a chunk's end leaves its parts in
-// a workspace, and a second launch adds those in chunk order.  Every row of the
-// result is written once, by one warp, and the order of every sum follows from
-// the sizes alone: the bits do not change from run to run.
+// places are then cut into chunks of a fixed length; a group of lanes sums one
+// slice of columns over one chunk in registers and writes a row as soon as its
+// last place is passed.  A row that continues past a chunk's end leaves its
+// parts in a workspace, and a second launch adds those in chunk order.  Every
+// row of the result is written once, by one group, and the order of every sum
+// follows from the sizes alone: the bits do not change from run to run.
 #include "internal.h"
+#include "launch.cuh"
 #include "vec.cuh"
 
 #include <algorithm>
+#include <initializer_list>
+#include <utility>
 
 namespace kma {
 namespace {
@@ -27,82 +30,223 @@ constexpr int kWarps = kThreads / 32;
 
 // ---- lookup ---------------------------------------------------------------
 
-// One thread per VE columns of one output row.
-template <typename T, int VE>
-__global__ void __launch_bounds__(kThreads)
-    lookup_kernel(const T *__restrict__ table, const int32_t *__restrict__ idx,
-                  const float *__restrict__ weights, int64_t N, int32_t k, int32_t K, int32_t D,
-                  float scale, T *__restrict__ out)
+struct LookupArgs {
+    const void *table;
+    const int32_t *idx;
+    const float *weights;
+    void *out;
+    int64_t N;
+    int32_t k, K, D;
+    int32_t vecs;          // vectors per row
+    int32_t rows;          // rows of a block side by side
+    uint32_t magic;        // t / vecs == t * magic >> 16 for t < 256
+    bool ids_wide;         // four ids (and weights) can be loaded at once
+    float scale;
+};
+
+// A block takes rows side by side where several fit its threads, else one and
+// a piece of 256 vectors of it (blockIdx.y); the thread's vector and row.
+__device__ __forceinline__ bool lookup_place(const LookupArgs &a, int &row, int &vec)
 {
-    const int32_t vecs = D / VE;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (t >= N * vecs)
+    row = static_cast<int>((threadIdx.x * a.magic) >> 16);
+    vec = static_cast<int>(threadIdx.x) - row * a.vecs;
+    if (a.vecs > kThreads) {
+        row = 0;
+        vec = static_cast<int>(blockIdx.y) * kThreads + threadIdx.x;
+    }
+    return row < a.rows && vec < a.vecs;
+}
+
+// One id a point: a copy, U points a thread in flight.  Bound by HBM.
+template <typename T, int VE, int U>
+__global__ void __launch_bounds__(kThreads) lookup_one_kernel(const LookupArgs a)
+{
+    int r0, vec;
+    if (!lookup_place(a, r0, vec))
         return;
-    const int64_t i = t / vecs;
-    const int64_t col = (t - i * vecs) * VE;
-    float acc[VE] = {};
-    for (int32_t j0 = 0; j0 < k; j0 += 8) {
-        int32_t r[8];
-        Raw<T, VE> q[8];
+    const T *table = static_cast<const T *>(a.table) + static_cast<int64_t>(vec) * VE;
+    T *out = static_cast<T *>(a.out) + static_cast<int64_t>(vec) * VE;
+    int64_t i[U];
+    int32_t r[U];
+    Raw<T, VE> q[U];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            r[u] = j0 + u < k ? __ldg(idx + i * k + j0 + u) : -1;
-            if (r[u] >= K)
-                r[u] = -1;
+    for (int u = 0; u < U; ++u) {
+        i[u] = (static_cast<int64_t>(blockIdx.x) * U + u) * a.rows + r0;
+        r[u] = i[u] < a.N ? __ldg(a.idx + i[u]) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (r[u] >= 0 && r[u] < a.K)
+            q[u] = load_raw<T, VE>(table + static_cast<int64_t>(r[u]) * a.D);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (i[u] < a.N) {
+            float acc[VE] = {};
+            if (r[u] >= 0 && r[u] < a.K)
+                fma_raw<T, VE>(acc, q[u], a.weights != nullptr ? __ldg(a.weights + i[u]) : 1.0f);
+#pragma unroll
+            for (int v = 0; v < VE; ++v)
+                acc[v] *= a.scale;
+            store_raw<T, VE>(out + i[u] * a.D, narrow<T, VE>(acc));
+        }
+}
+
+// Several ids a point, J rows in flight a thread.  Tables that fit L2 bound it
+// by L2 and by issue: eight elements cost one load, eight widenings and four
+// packed multiply-adds.
+template <typename T, int VE, int J>
+__global__ void __launch_bounds__(kThreads) lookup_many_kernel(const LookupArgs a)
+{
+    int r0, vec;
+    if (!lookup_place(a, r0, vec))
+        return;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * a.rows + r0;
+    if (i >= a.N)
+        return;
+    const T *table = static_cast<const T *>(a.table) + static_cast<int64_t>(vec) * VE;
+    const int32_t *idx = a.idx + i * a.k;
+    const float *weights = a.weights != nullptr ? a.weights + i * a.k : nullptr;
+    float acc[VE] = {};
+    for (int32_t j0 = 0; j0 < a.k; j0 += J) {
+        int32_t r[J];
+        float w[J];
+        if (a.ids_wide) {
+#pragma unroll
+            for (int u = 0; u < J; u += 4) {
+                int4 v = make_int4(-1, -1, -1, -1);
+                float4 f = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+                if (j0 + u < a.k) {
+                    v = __ldg(reinterpret_cast<const int4 *>(idx + j0 + u));
+                    if (weights != nullptr)
+                        f = __ldg(reinterpret_cast<const float4 *>(weights + j0 + u));
+                }
+                r[u] = v.x, r[u + 1] = v.y, r[u + 2] = v.z, r[u + 3] = v.w;
+                w[u] = f.x, w[u + 1] = f.y, w[u + 2] = f.z, w[u + 3] = f.w;
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < J; ++u) {
+                r[u] = j0 + u < a.k ? __ldg(idx + j0 + u) : -1;
+                w[u] = weights != nullptr && j0 + u < a.k ? __ldg(weights + j0 + u) : 1.0f;
+            }
+        }
+        Raw<T, VE> q[J];
+#pragma unroll
+        for (int u = 0; u < J; ++u) {
+            if (static_cast<uint32_t>(r[u]) < static_cast<uint32_t>(a.K)) {
+                q[u] = load_raw<T, VE>(table + static_cast<int64_t>(r[u]) * a.D);
+            } else {   // adds nothing, whatever its weight
+                q[u] = Raw<T, VE>{};
+                w[u] = 0.0f;
+            }
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (r[u] >= 0)
-                q[u] = load_raw<T, VE>(table + static_cast<int64_t>(r[u]) * D + col);
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (r[u] >= 0) {
-                const float w = weights != nullptr ? __ldg(weights + i * k + j0 + u) : 1.0f;
-                float f[VE];
-                widen<T, VE>(q[u], f);
-#pragma unroll
-                for (int v = 0; v < VE; ++v)
-                    acc[v] = fmaf(w, f[v], acc[v]);
-            }
+        for (int u = 0; u < J; ++u)
+            fma_raw<T, VE>(acc, q[u], w[u]);
     }
 #pragma unroll
     for (int v = 0; v < VE; ++v)
-        acc[v] *= scale;
-    store_raw<T, VE>(out + i * D + col, narrow<T, VE>(acc));
+        acc[v] *= a.scale;
+    store_raw<T, VE>(static_cast<T *>(a.out) + i * a.D + static_cast<int64_t>(vec) * VE,
+                     narrow<T, VE>(acc));
 }
+
+// ---- groups of lanes over columns -------------------------------------------
+//
+// The gradients work in groups of LG lanes (8, 16 or 32, for rows of up to 64,
+// 128 or more columns), each lane holding 8 columns as NV vectors of VE, so
+// that narrow or oddly aligned rows cost the same bookkeeping per id as wide ones.
+
+constexpr int kLaneCols = 8;
+
+template <int VE, int LG>
+struct Columns {
+    static constexpr int kVectors = kLaneCols / VE;
+    static constexpr int kSlice = LG * kLaneCols;   // columns of a group
+    __device__ static __forceinline__ int at(int slice, int lane, int v)
+    {
+        return slice * kSlice + v * LG * VE + lane * VE;
+    }
+};
 
 // ---- gradient of the weights ----------------------------------------------
 
-// One warp per (point, id).
-template <typename T, int VE>
-__global__ void __launch_bounds__(kThreads)
-    dweights_kernel(const T *__restrict__ dout, const T *__restrict__ table,
-                    const int32_t *__restrict__ idx, int64_t M, int32_t k, int32_t K, int32_t D,
-                    float scale, float *__restrict__ dweights)
+struct DweightsArgs {
+    const void *dout, *table;
+    const int32_t *idx;
+    float *dweights;
+    int64_t N;
+    int32_t k, K, D;
+    float scale;
+};
+
+// A group of lanes per point: its gradient is held in registers while the rows
+// of its ids pass, eight in flight; the eight sums are added over the lanes
+// together, halving their number with the distance (9 exchanges for 32 lanes,
+// not 40).  Bound by the gather of N k rows from L2.
+template <typename T, int VE, int LG>
+__global__ void __launch_bounds__(kThreads) dweights_kernel(const DweightsArgs a)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t f = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (f >= M)
-        return;
-    const int32_t r = __ldg(idx + f);
-    float sum = 0.0f;
-    if (r >= 0 && r < K) {
-        const T *a = dout + f / k * D;
-        const T *b = table + static_cast<int64_t>(r) * D;
-        for (int c = lane * VE; c < D; c += 32 * VE) {
-            float p[VE], q[VE];
-            widen<T, VE>(load_raw<T, VE>(a + c), p);
-            widen<T, VE>(load_raw<T, VE>(b + c), q);
+    using C = Columns<VE, LG>;
+    constexpr int NV = C::kVectors;
+    const int lane = threadIdx.x & (LG - 1);
+    const int64_t any =
+        static_cast<int64_t>(blockIdx.x) * (kThreads / LG) + threadIdx.x / LG;
+    const bool live = any < a.N;
+    const int64_t i = live ? any : a.N - 1;
+    const T *dout = static_cast<const T *>(a.dout) + i * a.D;
+    const int slices = (a.D + C::kSlice - 1) / C::kSlice;
+    for (int32_t j0 = 0; j0 < a.k; j0 += 8) {
+        const T *row[8];
 #pragma unroll
-            for (int v = 0; v < VE; ++v)
-                sum = fmaf(p[v], q[v], sum);
+        for (int u = 0; u < 8; ++u) {
+            const int32_t r = j0 + u < a.k ? __ldg(a.idx + i * a.k + j0 + u) : -1;
+            row[u] = static_cast<uint32_t>(r) < static_cast<uint32_t>(a.K)
+                         ? static_cast<const T *>(a.table) + static_cast<int64_t>(r) * a.D
+                         : nullptr;
         }
-    }
+        float sum[8] = {};
+        for (int s = 0; s < slices; ++s) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        sum += __shfl_xor_sync(kAll, sum, off);
-    if (lane == 0)
-        dweights[f] = sum * scale;
+            for (int v = 0; v < NV; ++v) {
+                const int col = C::at(s, lane, v);
+                if (col < a.D) {
+                    float p[VE];
+                    widen<T, VE>(load_raw<T, VE>(dout + col), p);
+                    Raw<T, VE> q[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        q[u] = row[u] != nullptr ? load_raw<T, VE>(row[u] + col) : Raw<T, VE>{};
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        float f[VE];
+                        widen<T, VE>(q[u], f);
+#pragma unroll
+                        for (int e = 0; e < VE; ++e)
+                            sum[u] = fmaf(p[e], f[e], sum[u]);
+                    }
+                }
+            }
+        }
+        // after the step of distance d, a lane holds the sums whose bits its own bits picked
+        int j = 0;
+#pragma unroll
+        for (int half = 4, off = LG / 2; half > 0; half >>= 1, off >>= 1) {
+            const bool up = (lane & off) != 0;
+#pragma unroll
+            for (int u = 0; u < half; ++u) {
+                const float give = up ? sum[u] : sum[u + half];
+                const float keep = up ? sum[u + half] : sum[u];
+                sum[u] = keep + __shfl_xor_sync(kAll, give, off);
+            }
+            j += up ? half : 0;
+        }
+#pragma unroll
+        for (int off = LG / 16; off > 0; off >>= 1)
+            sum[0] += __shfl_xor_sync(kAll, sum[0], off);
+        if (live && (lane & (LG / 8 - 1)) == 0 && j0 + j < a.k)
+            a.dweights[i * a.k + j0 + j] = sum[0] * a.scale;
+    }
 }
 
 // ---- gradient of the table ------------------------------------------------
@@ -116,7 +260,7 @@ struct GradArgs {
     void *dtable;
     float *parts;              // [2][chunks][D]: a chunk's first and last row, unfinished
     int64_t chunks;
-    int32_t chunk;             // sorted places per chunk
+    int32_t chunk;             // sorted places per chunk, a multiple of 8
     int32_t slices;            // column slices of a row
     int64_t sum_blocks;        // blocks that sum; the others zero rows without ids
     int32_t k, K, D;
@@ -126,8 +270,7 @@ struct GradArgs {
 };
 
 template <typename G, int VE>
-__device__ __forceinline__ void put_row(const GradArgs &a, int32_t r, int col,
-                                        const float (&acc)[VE])
+__device__ __forceinline__ void put(const GradArgs &a, int32_t r, int col, const float (&acc)[VE])
 {
     G *p = static_cast<G *>(a.dtable) + static_cast<int64_t>(r) * a.D + col;
     float f[VE];
@@ -150,147 +293,179 @@ __device__ __forceinline__ void put_row(const GradArgs &a, int32_t r, int col,
     store_raw<G, VE>(p, narrow<G, VE>(f));
 }
 
-// T: type of dout, G: of dtable; a warp takes 32 * VE columns.
-template <typename T, typename G, int VE>
+// T: type of dout, G: of dtable.
+template <typename T, typename G, int VE, int LG>
 __global__ void __launch_bounds__(kThreads) segment_kernel(const GradArgs a)
 {
-    const int lane = threadIdx.x & 31;
+    using C = Columns<VE, LG>;
+    constexpr int NV = C::kVectors;
+    constexpr int U = sizeof(T) == 2 ? 8 : 4;   // rows in flight: 32 registers
+    let_next_start();
+    wait_for_previous();
     if (blockIdx.x >= a.sum_blocks) {
-        // rows that no id names
+        // rows that no id names, a warp each
+        const int lane = threadIdx.x & 31;
         const int64_t warps = (static_cast<int64_t>(gridDim.x) - a.sum_blocks) * kWarps;
         for (int64_t r = (static_cast<int64_t>(blockIdx.x) - a.sum_blocks) * kWarps +
                          (threadIdx.x >> 5);
              r < a.K; r += warps) {
-            if (__ldg(a.offsets + r) != __ldg(a.offsets + r + 1))
+            if (a.offsets[r] != a.offsets[r + 1])
                 continue;
             G *p = static_cast<G *>(a.dtable) + r * a.D;
-            const float zero[VE] = {};
+            const Raw<G, VE> zero{};
             for (int c = lane * VE; c < a.D; c += 32 * VE)
-                store_raw<G, VE>(p + c, narrow<G, VE>(zero));
+                store_raw<G, VE>(p + c, zero);
         }
         return;
     }
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & (LG - 1);
+    const int64_t unit =
+        static_cast<int64_t>(blockIdx.x) * (kThreads / LG) + threadIdx.x / LG;
     const int64_t chunk = unit / a.slices;
-    const int64_t total = __ldg(a.offsets + a.K);
+    const int slice = static_cast<int>(unit - chunk * a.slices);
+    const int64_t total = a.offsets[a.K];
     const int64_t begin = chunk * a.chunk;
-    if (chunk >= a.chunks || begin >= total)
-        return;
-    const int64_t end = min(total, begin + a.chunk);
-    const int col = (static_cast<int>(unit - chunk * a.slices) * 32 + lane) * VE;
-    const bool in = col < a.D;
-    const T *dout = static_cast<const T *>(a.dout) + (in ? col : 0);
+    const bool live = chunk < a.chunks && begin < total;   // else: no place of its own
+    const int64_t end = live ? min(total, begin + a.chunk) : begin;
+    const T *dout = static_cast<const T *>(a.dout);
     // the row at `begin` began in an earlier chunk / that at `end` goes on
-    const bool from_before = begin > 0 && __ldg(a.rows + begin - 1) == __ldg(a.rows + begin);
-    const bool goes_on = end < total && __ldg(a.rows + end - 1) == __ldg(a.rows + end);
+    const bool from_before = live && begin > 0 && a.rows[begin - 1] == a.rows[begin];
+    const bool goes_on = live && end < total && a.rows[end - 1] == a.rows[end];
 
-    float acc[VE] = {};
-    int32_t cur = __ldg(a.rows + begin);
+    float acc[NV][VE] = {};
+    int32_t cur = live ? a.rows[begin] : -1;
     bool first = true;   // cur is the row at `begin`
     auto part = [&](int which) {
-        if (in) {
-            float *p = a.parts + (which * a.chunks + chunk) * a.D + col;
-            store_raw<float, VE>(p, narrow<float, VE>(acc));
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int col = C::at(slice, lane, v);
+            if (col < a.D)
+                store_raw<float, VE>(a.parts + (which * a.chunks + chunk) * a.D + col,
+                                     narrow<float, VE>(acc[v]));
         }
     };
-    for (int64_t s0 = begin; s0 < end; s0 += 32) {
-        // a place per lane
-        const int64_t s = s0 + lane;
+    auto finish = [&]() {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int col = C::at(slice, lane, v);
+            if (col < a.D)
+                put<G, VE>(a, cur, col, acc[v]);
+        }
+    };
+    for (int32_t s0 = 0; s0 < a.chunk; s0 += LG) {
+        // a place per lane; the groups of a warp go through their chunks in step
+        const int64_t s = begin + s0 + lane;
         int32_t row = -1, point = 0;
         float w = 0.0f;
-        if (s < end) {
-            const int32_t f = __ldg(a.order + s);
-            row = __ldg(a.rows + s);
-            point = f / a.k;
+        if (s0 + lane < a.chunk && s < end) {
+            const int32_t f = a.order[s];
+            row = a.rows[s];
+            point = a.k == 1 ? f : f / a.k;
             w = a.weights != nullptr ? __ldg(a.weights + f) : 1.0f;
         }
-        const int n = static_cast<int>(min(static_cast<int64_t>(32), end - s0));
-        for (int u0 = 0; u0 < n; u0 += 8) {
-            Raw<T, VE> q[8];
+        const int n = min(LG, a.chunk - s0);
+        for (int u0 = 0; u0 < n; u0 += U) {
+            if (!__any_sync(kAll, row >= 0))
+                break;
+            Raw<T, VE> q[U][NV];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int32_t i = __shfl_sync(kAll, point, u0 + u);
-                if (u0 + u < n && in)
-                    q[u] = load_raw<T, VE>(dout + static_cast<int64_t>(i) * a.D);
+            for (int u = 0; u < U; ++u) {
+                const int32_t i = __shfl_sync(kAll, point, u0 + u, LG);
+                const int32_t r = __shfl_sync(kAll, row, u0 + u, LG);
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int col = C::at(slice, lane, v);
+                    if (r >= 0 && col < a.D)
+                        q[u][v] = load_raw<T, VE>(dout + static_cast<int64_t>(i) * a.D + col);
+                    else
+                        q[u][v] = Raw<T, VE>{};
+                }
             }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int32_t r = __shfl_sync(kAll, row, u0 + u);
-                const float wu = __shfl_sync(kAll, w, u0 + u);
-                if (u0 + u >= n)
-                    continue;
-                if (r != cur) {
+            for (int u = 0; u < U; ++u) {
+                const int32_t r = __shfl_sync(kAll, row, u0 + u, LG);
+                const float wu = __shfl_sync(kAll, w, u0 + u, LG);
+                if (r != cur && r >= 0) {
                     if (first && from_before)
                         part(0);
-                    else if (in)
-                        put_row<G, VE>(a, cur, col, acc);
+                    else
+                        finish();
                     first = false;
                     cur = r;
 #pragma unroll
-                    for (int v = 0; v < VE; ++v)
-                        acc[v] = 0.0f;
-                }
-                if (in) {
-                    float f[VE];
-                    widen<T, VE>(q[u], f);
+                    for (int v = 0; v < NV; ++v)
 #pragma unroll
-                    for (int v = 0; v < VE; ++v)
-                        acc[v] = fmaf(wu, f[v], acc[v]);
+                        for (int e = 0; e < VE; ++e)
+                            acc[v][e] = 0.0f;
                 }
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+                    fma_raw<T, VE>(acc[v], q[u][v], wu);
             }
         }
     }
+    if (!live)
+        return;
     if (first && from_before)
         part(0);
     else if (goes_on)
         part(1);
-    else if (in)
-        put_row<G, VE>(a, cur, col, acc);
+    else
+        finish();
 }
 
 // Rows that span chunks: the chunk in which such a row begins holds its first
 // part as its last row; the following chunks hold the others as their first.
-template <typename G, int VE>
+template <typename G, int VE, int LG>
 __global__ void __launch_bounds__(kThreads) join_kernel(const GradArgs a)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    using C = Columns<VE, LG>;
+    wait_for_previous();
+    const int lane = threadIdx.x & (LG - 1);
+    const int64_t unit =
+        static_cast<int64_t>(blockIdx.x) * (kThreads / LG) + threadIdx.x / LG;
     const int64_t chunk = unit / a.slices;
-    const int64_t total = __ldg(a.offsets + a.K);
+    const int slice = static_cast<int>(unit - chunk * a.slices);
+    const int64_t total = a.offsets[a.K];
     const int64_t begin = chunk * a.chunk;
     const int64_t end = begin + a.chunk;
     if (chunk >= a.chunks || end >= total)
         return;
-    const int32_t r = __ldg(a.rows + end - 1);
-    if (__ldg(a.rows + end) != r || __ldg(a.offsets + r) < begin)
+    const int32_t r = a.rows[end - 1];
+    if (a.rows[end] != r || a.offsets[r] < begin)
         return;   // ends here, or began in an earlier chunk
-    const int64_t last = (static_cast<int64_t>(__ldg(a.offsets + r + 1)) - 1) / a.chunk;
-    const int col = (static_cast<int>(unit - chunk * a.slices) * 32 + lane) * VE;
-    if (col >= a.D)
-        return;
-    float acc[VE];
-    widen<float, VE>(load_raw<float, VE>(a.parts + (a.chunks + chunk) * a.D + col), acc);
-    for (int64_t c0 = chunk + 1; c0 <= last; c0 += 8) {
-        Raw<float, VE> q[8];
+    const int64_t last = (static_cast<int64_t>(a.offsets[r + 1]) - 1) / a.chunk;
+#pragma unroll 1
+    for (int v = 0; v < C::kVectors; ++v) {
+        const int col = C::at(slice, lane, v);
+        if (col >= a.D)
+            return;
+        float acc[VE];
+        widen<float, VE>(load_raw<float, VE>(a.parts + (a.chunks + chunk) * a.D + col), acc);
+        for (int64_t c0 = chunk + 1; c0 <= last; c0 += 8) {
+            Raw<float, VE> q[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (c0 + u <= last)
-                q[u] = load_raw<float, VE>(a.parts + (c0 + u) * a.D + col);
+            for (int u = 0; u < 8; ++u)
+                if (c0 + u <= last)
+                    q[u] = load_raw<float, VE>(a.parts + (c0 + u) * a.D + col);
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (c0 + u <= last) {
-                float f[VE];
-                widen<float, VE>(q[u], f);
+            for (int u = 0; u < 8; ++u)
+                if (c0 + u <= last) {
+                    float f[VE];
+                    widen<float, VE>(q[u], f);
 #pragma unroll
-                for (int v = 0; v < VE; ++v)
-                    acc[v] += f[v];
-            }
+                    for (int e = 0; e < VE; ++e)
+                        acc[e] += f[e];
+                }
+        }
+        put<G, VE>(a, r, col, acc);
     }
-    put_row<G, VE>(a, r, col, acc);
 }
 
-// Elements per vector: the most, up to `most`, that divide D and that every
-// pointer's alignment allows for its type.
+// ---- choices --------------------------------------------------------------
+
+// Elements per vector: the most, up to 16 bytes of the input type, that
+// divide D and that every pointer's alignment allows for its type.
 int vector_elems(int64_t D, int most, std::initializer_list<std::pair<const void *, int>> ptrs)
 {
     for (int ve = most; ve > 1; ve >>= 1) {
@@ -305,71 +480,61 @@ int vector_elems(int64_t D, int most, std::initializer_list<std::pair<const void
     return 1;
 }
 
-template <typename T, int VE>
-cudaError_t lookup_launch(const void *table, const int32_t *idx, const float *weights, int64_t N,
-                          int32_t k, int64_t K, int64_t D, float scale, void *out,
-                          cudaStream_t stream)
+int most_elems(int dtype) { return 16 / dtype_bytes(dtype); }
+
+// Calls f with an integral constant of ve (8 only for 16-bit types).
+template <typename T, typename F>
+cudaError_t by_elems(int ve, F f)
 {
-    const int64_t blocks = (N * (D / VE) + kThreads - 1) / kThreads;
-    if (blocks > 0x7fffffff)
-        return cudaErrorInvalidValue;
-    lookup_kernel<T, VE><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
-        static_cast<const T *>(table), idx, weights, N, k, static_cast<int32_t>(K),
-        static_cast<int32_t>(D), scale, static_cast<T *>(out));
-    return cudaGetLastError();
+    if constexpr (sizeof(T) == 2)
+        if (ve == 8)
+            return f(std::integral_constant<int, 8>{});
+    if (ve >= 4)
+        return f(std::integral_constant<int, 4>{});
+    if (ve == 2)
+        return f(std::integral_constant<int, 2>{});
+    return f(std::integral_constant<int, 1>{});
 }
 
-template <typename T, int VE>
-cudaError_t dweights_launch(const void *dout, const void *table, const int32_t *idx, int64_t M,
-                            int32_t k, int64_t K, int64_t D, float scale, float *dweights,
-                            cudaStream_t stream)
+template <typename F>
+cudaError_t by_type(int dtype, F f)
 {
-    const int64_t blocks = (M + kWarps - 1) / kWarps;
-    dweights_kernel<T, VE><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
-        static_cast<const T *>(dout), static_cast<const T *>(table), idx, M, k,
-        static_cast<int32_t>(K), static_cast<int32_t>(D), scale, dweights);
-    return cudaGetLastError();
+    if (dtype == kFp32)
+        return f(float{});
+    if (dtype == kBf16)
+        return f(__nv_bfloat16{});
+    return f(__half{});
 }
 
-template <typename T, typename G, int VE>
-cudaError_t grad_launch(GradArgs a, int sms, cudaStream_t stream)
-{
-    a.sum_blocks = (a.chunks * a.slices + kWarps - 1) / kWarps;
-    int64_t zero_blocks = 0;
-    if (!a.accumulate)
-        zero_blocks = std::min<int64_t>((a.K + kWarps - 1) / kWarps, int64_t(sms) * 16);
-    segment_kernel<T, G, VE>
-        <<<static_cast<unsigned>(a.sum_blocks + zero_blocks), kThreads, 0, stream>>>(a);
-    if (a.chunks > 1)
-        join_kernel<G, VE><<<static_cast<unsigned>(a.sum_blocks), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
-}
+int lane_group(int64_t D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 
-// Sorted places per chunk: enough (chunk, slice) units for about 32 warps on
-// every SM, in steps of 8 places.
-int64_t chunk_places(int64_t M, int64_t slices, int sms)
+template <typename F>
+cudaError_t by_group(int64_t D, F f)
 {
-    const int64_t want = (M * slices + int64_t(sms) * 32 - 1) / (int64_t(sms) * 32);
-    return std::min<int64_t>(512, std::max<int64_t>(16, (want + 7) / 8 * 8));
-}
-
-template <typename T, typename G>
-cudaError_t grad_type(GradArgs &a, int ve, int sms, cudaStream_t stream)
-{
-    switch (ve) {
+    switch (lane_group(D)) {
     case 8:
-        if constexpr (sizeof(T) == 2)
-            return grad_launch<T, G, 8>(a, sms, stream);
-    case 4:
-        return grad_launch<T, G, 4>(a, sms, stream);
-    case 2:
-        return grad_launch<T, G, 2>(a, sms, stream);
+        return f(std::integral_constant<int, 8>{});
+    case 16:
+        return f(std::integral_constant<int, 16>{});
     default:
-        return grad_launch<T, G, 1>(a, sms, stream);
+        return f(std::integral_constant<int, 32>{});
     }
 }
 
-int most_elems(int dtype) { return 16 / dtype_bytes(dtype); }
+int64_t column_slices(int64_t D)
+{
+    const int64_t cols = lane_group(D) * kLaneCols;
+    return (D + cols - 1) / cols;
+}
+
+// Sorted places per chunk: enough (chunk, slice) units for 32 warps on every
+// SM, in steps of 8 places, at most 512.
+int64_t chunk_places(int64_t M, int64_t D, int sms)
+{
+    const int64_t groups = int64_t(sms) * 32 * (32 / lane_group(D));
+    const int64_t want = (M * column_slices(D) + groups - 1) / groups;
+    return std::min<int64_t>(512, std::max<int64_t>(16, (want + 7) / 8 * 8));
+}
 
 int grad_elems(const void *dout, int dtype, const void *dtable, int grad_dtype, int64_t D)
 {
@@ -377,64 +542,102 @@ int grad_elems(const void *dout, int dtype, const void *dtable, int grad_dtype, 
                         {{dout, dtype_bytes(dtype)}, {dtable, dtype_bytes(grad_dtype)}});
 }
 
-}  // namespace
+template <typename T, typename G>
+cudaError_t grad_launch(GradArgs a, int ve, int sms, cudaStream_t stream)
+{
+    return by_elems<T>(ve, [&](auto VE) {
+        return by_group(a.D, [&](auto LG) {
+            constexpr int kUnits = kThreads / decltype(LG)::value;
+            a.sum_blocks = (a.chunks * a.slices + kUnits - 1) / kUnits;
+            int64_t zero_blocks = 0;
+            if (!a.accumulate)
+                zero_blocks = std::min<int64_t>((a.K + kWarps - 1) / kWarps, int64_t(sms) * 16);
+            if (a.sum_blocks + zero_blocks > 0x7fffffff)
+                return cudaErrorInvalidValue;
+            cudaError_t e = launch_after(segment_kernel<T, G, decltype(VE)::value, decltype(LG)::value>,
+                                         static_cast<unsigned>(a.sum_blocks + zero_blocks),
+                                         kThreads, 0, stream, a);
+            if (e == cudaSuccess && a.chunks > 1)
+                e = launch_after(join_kernel<G, decltype(VE)::value, decltype(LG)::value>,
+                                 static_cast<unsigned>(a.sum_blocks), kThreads, 0, stream, a);
+            return e;
+        });
+    });
+}
 
-#define KMA_BY_VE(CALL, T)                                                                        \
-    switch (ve) {                                                                                 \
-    case 8:                                                                                       \
-        if constexpr (sizeof(T) == 2)                                                             \
-            return CALL(T, 8);                                                                    \
-    case 4:                                                                                       \
-        return CALL(T, 4);                                                                        \
-    case 2:                                                                                       \
-        return CALL(T, 2);                                                                        \
-    default:                                                                                      \
-        return CALL(T, 1);                                                                        \
-    }
+}  // namespace
 
 cudaError_t launch_lookup(const void *table, int dtype, int64_t K, int64_t D, const int32_t *idx,
                           const float *weights, int64_t N, int32_t k, float scale, void *out,
-                          cudaStream_t stream)
+                          int sms, cudaStream_t stream)
 {
     const int es = dtype_bytes(dtype);
     const int ve = vector_elems(D, most_elems(dtype), {{table, es}, {out, es}});
-#define KMA_CALL(T, VE)                                                                           \
-    (lookup_launch<T, VE>(table, idx, weights, N, k, K, D, scale, out, stream))
-    if (dtype == kFp32) {
-        KMA_BY_VE(KMA_CALL, float)
-    } else if (dtype == kBf16) {
-        KMA_BY_VE(KMA_CALL, __nv_bfloat16)
-    } else {
-        KMA_BY_VE(KMA_CALL, __half)
-    }
-#undef KMA_CALL
+    LookupArgs a{};
+    a.table = table;
+    a.idx = idx;
+    a.weights = weights;
+    a.out = out;
+    a.N = N;
+    a.k = k;
+    a.K = static_cast<int32_t>(K);
+    a.D = static_cast<int32_t>(D);
+    a.vecs = static_cast<int32_t>(D / ve);
+    a.rows = a.vecs <= kThreads ? kThreads / a.vecs : 1;
+    a.magic = (65536u + a.vecs - 1) / static_cast<uint32_t>(a.vecs);
+    a.ids_wide = k % 4 == 0 &&
+                 (reinterpret_cast<uintptr_t>(idx) | reinterpret_cast<uintptr_t>(weights)) % 16 == 0;
+    a.scale = scale;
+    const unsigned pieces = static_cast<unsigned>((a.vecs + kThreads - 1) / kThreads);
+    const int64_t blocks = (N + a.rows - 1) / a.rows;
+    // one id a point: four points a thread once that still gives every SM eight blocks
+    const bool four = blocks * pieces >= int64_t(sms) * 32;
+    return by_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        return by_elems<T>(ve, [&](auto VE) {
+            constexpr int kVe = decltype(VE)::value;
+            if (k > 1 && k <= 4)
+                lookup_many_kernel<T, kVe, 4>
+                    <<<dim3(static_cast<unsigned>(blocks), pieces), kThreads, 0, stream>>>(a);
+            else if (k > 1)
+                lookup_many_kernel<T, kVe, 8>
+                    <<<dim3(static_cast<unsigned>(blocks), pieces), kThreads, 0, stream>>>(a);
+            else if (four)
+                lookup_one_kernel<T, kVe, 4>
+                    <<<dim3(static_cast<unsigned>((blocks + 3) / 4), pieces), kThreads, 0,
+                       stream>>>(a);
+            else
+                lookup_one_kernel<T, kVe, 1>
+                    <<<dim3(static_cast<unsigned>(blocks), pieces), kThreads, 0, stream>>>(a);
+            return cudaGetLastError();
+        });
+    });
 }
 
 cudaError_t launch_dweights(const void *dout, const void *table, int dtype, const int32_t *idx,
-                            int64_t M, int32_t k, int64_t K, int64_t D, float scale,
+                            int64_t N, int32_t k, int64_t K, int64_t D, float scale,
                             float *dweights, cudaStream_t stream)
 {
     const int es = dtype_bytes(dtype);
     const int ve = vector_elems(D, most_elems(dtype), {{table, es}, {dout, es}});
-#define KMA_CALL(T, VE)                                                                           \
-    (dweights_launch<T, VE>(dout, table, idx, M, k, K, D, scale, dweights, stream))
-    if (dtype == kFp32) {
-        KMA_BY_VE(KMA_CALL, float)
-    } else if (dtype == kBf16) {
-        KMA_BY_VE(KMA_CALL, __nv_bfloat16)
-    } else {
-        KMA_BY_VE(KMA_CALL, __half)
-    }
-#undef KMA_CALL
+    DweightsArgs a{dout, table, idx, dweights, N, k, static_cast<int32_t>(K),
+                   static_cast<int32_t>(D), scale};
+    return by_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        return by_elems<T>(ve, [&](auto VE) {
+            return by_group(D, [&](auto LG) {
+                constexpr int kUnits = kThreads / decltype(LG)::value;
+                dweights_kernel<T, decltype(VE)::value, decltype(LG)::value>
+                    <<<static_cast<unsigned>((N + kUnits - 1) / kUnits), kThreads, 0, stream>>>(a);
+                return cudaGetLastError();
+            });
+        });
+    });
 }
-#undef KMA_BY_VE
 
-size_t lookup_grad_parts_bytes(const void *dout, int dtype, const void *dtable, int grad_dtype,
-                               int64_t M, int64_t D, int sms)
+size_t lookup_grad_parts_bytes(int64_t M, int64_t D, int sms)
 {
-    const int ve = grad_elems(dout, dtype, dtable, grad_dtype, D);
-    const int64_t slices = (D + 32 * ve - 1) / (32 * ve);
-    const int64_t places = chunk_places(M, slices, sms);
+    const int64_t places = chunk_places(M, D, sms);
     const int64_t chunks = (M + places - 1) / places;
     return static_cast<size_t>(2 * chunks) * D * 4;
 }
@@ -454,8 +657,8 @@ cudaError_t launch_lookup_grad(const void *dout, int dtype, const float *weights
     a.offsets = offsets;
     a.dtable = dtable;
     a.parts = parts;
-    a.slices = static_cast<int32_t>((D + 32 * ve - 1) / (32 * ve));
-    a.chunk = static_cast<int32_t>(chunk_places(M, a.slices, sms));
+    a.slices = static_cast<int32_t>(column_slices(D));
+    a.chunk = static_cast<int32_t>(chunk_places(M, D, sms));
     a.chunks = (M + a.chunk - 1) / a.chunk;
     a.k = k;
     a.K = static_cast<int32_t>(K);
@@ -463,13 +666,12 @@ cudaError_t launch_lookup_grad(const void *dout, int dtype, const float *weights
     a.skip = skip;
     a.scale = scale;
     a.accumulate = accumulate;
-    if (dtype == kFp32)
-        return grad_type<float, float>(a, ve, sms, stream);
-    if (dtype == kBf16)
-        return grad_dtype == kFp32 ? grad_type<__nv_bfloat16, float>(a, ve, sms, stream)
-                                   : grad_type<__nv_bfloat16, __nv_bfloat16>(a, ve, sms, stream);
-    return grad_dtype == kFp32 ? grad_type<__half, float>(a, ve, sms, stream)
-                               : grad_type<__half, __half>(a, ve, sms, stream);
+    return by_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        if (grad_dtype == kFp32)
+            return grad_launch<T, float>(a, ve, sms, stream);
+        return grad_launch<T, T>(a, ve, sms, stream);
+    });
 }
 
 }  // namespace kma

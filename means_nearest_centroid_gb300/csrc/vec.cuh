@@ -91,4 +91,23 @@ __device__ __forceinline__ void store_raw(T *p, const Raw<T, VE> &r)
     *reinterpret_cast<Raw<T, VE> *>(p) = r;
 }
 
+// acc += w * q, in fp32 (two products an instruction).
+template <typename T, int VE>
+__device__ __forceinline__ void fma_raw(float (&acc)[VE], const Raw<T, VE> &q, float w)
+{
+    float f[VE];
+    widen<T, VE>(q, f);
+    if constexpr (VE == 1) {
+        acc[0] = fmaf(w, f[0], acc[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VE; i += 2)
+            asm("{\n\t.reg .b64 a, b, c;\n\t"
+                "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%0, %1};\n\t"
+                "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+                : "+f"(acc[i]), "+f"(acc[i + 1])
+                : "f"(f[i]), "f"(f[i + 1]), "f"(w));
+    }
+}
+
 }  // namespace kma
