@@ -171,24 +171,29 @@ cudaError_t lists_prepare();
 // The stable sort of the positions [0, M) by row: order, the sorted rows (may
 // be NULL) and offsets[K + 1]; scratch (16-byte aligned) of
 // lists_scratch_bytes.  Places past offsets[K] hold -1 in order and nothing
-// in particular in rows.
+// in particular in rows.  zero_bytes (even) at zero are zeroed besides.
 size_t lists_scratch_bytes(int64_t M, int64_t K);
 cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *order, int32_t *rows,
-                         int32_t *offsets, void *scratch, cudaStream_t stream);
+                         int32_t *offsets, void *scratch, void *zero, size_t zero_bytes,
+                         cudaStream_t stream);
 cudaError_t launch_lookup(const void *table, int dtype, int64_t K, int64_t D, const int32_t *idx,
                           const float *weights, int64_t N, int32_t k, float scale, void *out,
                           int sms, cudaStream_t stream);
 cudaError_t launch_dweights(const void *dout, const void *table, int dtype, const int32_t *idx,
                             int64_t N, int32_t k, int64_t K, int64_t D, float scale,
-                            float *dweights, cudaStream_t stream);
+                            float *dweights, int sms, cudaStream_t stream);
 // The gradient of the table from the sorted ids (launch_lists with rows);
 // parts: 16-byte aligned workspace of lookup_grad_parts_bytes.
 size_t lookup_grad_parts_bytes(int64_t M, int64_t D, int sms);
-cudaError_t launch_lookup_grad(const void *dout, int dtype, const float *weights, int64_t M,
-                               int32_t k, int64_t K, int64_t D, float scale, int32_t skip,
-                               bool accumulate, const int32_t *order, const int32_t *rows,
-                               const int32_t *offsets, float *parts, void *dtable, int grad_dtype,
+cudaError_t launch_lookup_grad(const void *dout, int dtype, const int32_t *idx,
+                               const float *weights, const void *table, int64_t M, int32_t k,
+                               int64_t K, int64_t D, float scale, int32_t skip, bool accumulate,
+                               const int32_t *order, const int32_t *rows, const int32_t *offsets,
+                               float *parts, void *dtable, int grad_dtype, float *dweights,
                                int sms, cudaStream_t stream);
+// Whether launch_lookup_grad can form dweights (else NULL there, and
+// launch_dweights).
+bool dweights_with_dtable(int64_t D);
 // The norm over n tensors, and with `scale` their scaling into out (NULL: in
 // place); partial: workspace of clip_scratch_bytes.
 size_t clip_scratch_bytes(int32_t n, int sms);

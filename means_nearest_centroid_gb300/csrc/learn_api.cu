@@ -215,7 +215,7 @@ int kmassign_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *order, int
     Scratch scratch(kma::lists_scratch_bytes(M, K), pool, s);
     if (!scratch.ok())
         return KMASSIGN_ERR_CUDA;
-    rc = done(kma::launch_lists(idx, M, K, order, nullptr, offsets, scratch.get(), s));
+    rc = done(kma::launch_lists(idx, M, K, order, nullptr, offsets, scratch.get(), nullptr, 0, s));
     return scratch.release() ? rc : KMASSIGN_ERR_CUDA;
 }
 
@@ -270,16 +270,17 @@ int kmassign_lookup_grad(const void *dout, int32_t dtype, const int32_t *idx, co
     if ((rc = check_device_ptrs(ptrs, 6)) != KMASSIGN_OK)
         return rc;
     const int64_t M = N * k;
-    if (dweights != nullptr && N > 0 &&
-        kma::launch_dweights(dout, table, dtype, idx, N, k, K, D, scale, dweights, s) !=
-            cudaSuccess)
-        return KMASSIGN_ERR_CUDA;
-    if (dtable == nullptr || (N == 0 && accumulate))
-        return KMASSIGN_OK;
     cudaMemPool_t pool;
     int sms;
     if ((rc = kma::library_device(&pool, &sms)) != KMASSIGN_OK)
         return rc;
+    const bool both = dtable != nullptr && dweights != nullptr && kma::dweights_with_dtable(D);
+    if (dweights != nullptr && N > 0 && !both &&
+        kma::launch_dweights(dout, table, dtype, idx, N, k, K, D, scale, dweights, sms, s) !=
+            cudaSuccess)
+        return KMASSIGN_ERR_CUDA;
+    if (dtable == nullptr || (N == 0 && accumulate))
+        return KMASSIGN_OK;
     // one allocation: order, sorted rows, offsets, the sort's scratch, row parts
     const size_t ids = up16(static_cast<size_t>(M) * 4);
     const size_t offs = up16(static_cast<size_t>(K + 1) * 4);
@@ -293,12 +294,15 @@ int kmassign_lookup_grad(const void *dout, int32_t dtype, const int32_t *idx, co
     int32_t *rows = reinterpret_cast<int32_t *>(p + ids);
     int32_t *offsets = reinterpret_cast<int32_t *>(p + 2 * ids);
     cudaError_t e =
-        kma::launch_lists(idx, M, K, order, rows, offsets, p + 2 * ids + offs, s);
-    if (e == cudaSuccess)
-        e = kma::launch_lookup_grad(dout, dtype, weights, M, k, K, D, scale, padding,
+        kma::launch_lists(idx, M, K, order, rows, offsets, p + 2 * ids + offs,
+                          accumulate ? nullptr : dtable,
+                          accumulate ? 0 : static_cast<size_t>(K) * D * kma::dtype_bytes(grad_dtype),
+                          s);
+    if (e == cudaSuccess && M > 0)
+        e = kma::launch_lookup_grad(dout, dtype, idx, weights, table, M, k, K, D, scale, padding,
                                     accumulate != 0, order, rows, offsets,
                                     reinterpret_cast<float *>(p + 2 * ids + offs + sort), dtable,
-                                    grad_dtype, sms, s);
+                                    grad_dtype, both ? dweights : nullptr, sms, s);
     rc = done(e);
     return scratch.release() ? rc : KMASSIGN_ERR_CUDA;
 }

@@ -8,7 +8,7 @@
 //   count:    block b counts its items -> H[b][digit];
 //   scatter:  block b sums H[b'][digit] over the blocks b' before it and over
 //             all blocks, scans the digits, and takes its items in tiles: ranks
-//             them (a warp's equal digits by match, warps by their counts in
+//             them (a warp's equal digits by votes, warps by their counts in
 //             shared memory), orders the tile by digit in shared memory, and
 //             writes it out in runs of consecutive places.
 // The two launches cost less than one whose blocks count the next digit for
@@ -16,9 +16,8 @@
 // with atomics and without the ordered tile).  Up to kOneBlockMax items are one
 // launch of one block.  Nothing depends on timing: the result is unique.
 //
-// offsets are found by a search in the sorted rows within the row's last digit:
-// 32 ways at a step by a warp for each row, or, where there are many rows (whose
-// searches hide each other's latency), eight ways by a thread.
+// offsets are found by a search in the sorted rows within the row's last digit,
+// eight ways at a step: a third of bisection's dependent loads.
 #include "internal.h"
 #include "launch.cuh"
 
@@ -77,9 +76,17 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t *warp_sums, int
 
 // Rank of the lane's item among the items of its digit seen so far by this
 // warp; `counts` (the warp's own bins) takes the new ones.  d < 0: no item.
-__device__ __forceinline__ int32_t warp_rank(int32_t d, uint16_t *counts, int lane)
+// Equal digits are found bit by bit, by votes.
+__device__ __forceinline__ int32_t warp_rank(int32_t d, int bits, uint16_t *counts, int lane)
 {
-    const uint32_t same = __match_any_sync(kAll, d);
+    const uint32_t valid = __ballot_sync(kAll, d >= 0);
+    uint32_t same = d >= 0 ? valid : ~valid;
+#pragma unroll
+    for (int b = 0; b < kMaxDigitBits; ++b)
+        if (b < bits) {
+            const uint32_t ones = __ballot_sync(kAll, (d >> b) & 1);
+            same &= (d >> b) & 1 ? ones : ~ones;
+        }
     const uint32_t below = same & ((1u << lane) - 1u);
     int32_t base = 0;
     if (d >= 0 && below == 0) {
@@ -89,6 +96,37 @@ __device__ __forceinline__ int32_t warp_rank(int32_t d, uint16_t *counts, int la
     base = __shfl_sync(kAll, base, __ffs(same) - 1);
     __syncwarp();
     return base + __popc(below);
+}
+
+// Memory that the sort's scatter launches zero besides: blocks past a launch's
+// own write a share of it while those wait for their loads.  16 MiB a launch
+// (what it hides whole), more where that is not enough.
+struct Fill {
+    uint8_t *p;
+    int64_t bytes;     // 0: none
+    int32_t part, parts;
+    __host__ __device__ __forceinline__ bool any() const { return bytes > 0 && part < parts; }
+};
+
+__device__ __forceinline__ void fill_zero(const Fill &f, int64_t block, int64_t blocks)
+{
+    const int64_t head = min(f.bytes, static_cast<int64_t>(-reinterpret_cast<uintptr_t>(f.p) & 15));
+    uint4 *body = reinterpret_cast<uint4 *>(f.p + head);
+    const int64_t units = (f.bytes - head) >> 4;
+    const int64_t end = units * (f.part + 1) / f.parts;
+#pragma unroll 4
+    for (int64_t i = units * f.part / f.parts + block * blockDim.x + threadIdx.x; i < end;
+         i += blocks * blockDim.x)
+        body[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (f.part == 0 && block == 0) {   // the ends, fewer than 16 bytes each, of 2-byte elements
+        uint16_t *ends = reinterpret_cast<uint16_t *>(f.p);
+        const int t = static_cast<int>(threadIdx.x);
+        if (t < 8 && 2 * t < head)
+            ends[t] = 0;
+        const int64_t tail = head + units * 16 + 2 * t;
+        if (t < 8 && tail < f.bytes)
+            ends[tail >> 1] = 0;
+    }
 }
 
 struct SortArgs {
@@ -106,6 +144,7 @@ struct SortArgs {
     int32_t shift, bins;      // this digit: (row >> shift) & (bins - 1)
     int32_t blocks;
     bool last;
+    Fill fill;
 };
 
 template <bool FIRST>
@@ -152,6 +191,11 @@ __global__ void __launch_bounds__(kThreads) lists_scatter_kernel(const SortArgs 
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     let_next_start();
+    if (blockIdx.x >= a.blocks) {
+        wait_for_previous();
+        fill_zero(a.fill, blockIdx.x - a.blocks, gridDim.x - a.blocks);
+        return;
+    }
     for (int d = threadIdx.x; d < 2 * a.bins; d += kThreads)
         smem[d] = 0;
     __syncthreads();
@@ -159,18 +203,31 @@ __global__ void __launch_bounds__(kThreads) lists_scatter_kernel(const SortArgs 
 
     // places: all smaller digits, then this digit in earlier blocks; the
     // threads share out the blocks' counts of a digit (integer sums)
-    const int lanes = max(1, kThreads / a.bins);   // threads per digit
-    for (int t = threadIdx.x; t < a.bins * lanes; t += kThreads) {
-        const int d = t & (a.bins - 1);
-        int32_t n_all = 0, n_before = 0;
+    if (a.bins >= 4) {
+        // four digits a thread, so that a load covers 16 bytes
+        const int quads = a.bins >> 2;
+        const int lanes = kThreads / quads;   // at least 2
+        const int d = (threadIdx.x & (quads - 1)) << 2;
+        int4 all = make_int4(0, 0, 0, 0), before = all;
 #pragma unroll 8
-        for (int b = t / a.bins; b < a.blocks; b += lanes) {
-            const int32_t n = a.hist[static_cast<int64_t>(b) * a.bins + d];
-            n_all += n;
-            n_before += b < static_cast<int>(blockIdx.x) ? n : 0;
+        for (int b = threadIdx.x / quads; b < a.blocks; b += lanes) {
+            const int4 n = *reinterpret_cast<const int4 *>(a.hist + static_cast<int64_t>(b) * a.bins + d);
+            const int m = b < static_cast<int>(blockIdx.x) ? -1 : 0;
+            all.x += n.x, all.y += n.y, all.z += n.z, all.w += n.w;
+            before.x += n.x & m, before.y += n.y & m, before.z += n.z & m, before.w += n.w & m;
         }
-        atomicAdd(start + d, n_all);
-        atomicAdd(place + d, n_before);
+        atomicAdd(start + d, all.x), atomicAdd(start + d + 1, all.y);
+        atomicAdd(start + d + 2, all.z), atomicAdd(start + d + 3, all.w);
+        atomicAdd(place + d, before.x), atomicAdd(place + d + 1, before.y);
+        atomicAdd(place + d + 2, before.z), atomicAdd(place + d + 3, before.w);
+    } else {
+        for (int t = threadIdx.x; t < a.bins * a.blocks; t += kThreads) {
+            const int b = t / a.bins, d = t % a.bins;
+            const int32_t n = a.hist[t];
+            atomicAdd(start + d, n);
+            if (b < static_cast<int>(blockIdx.x))
+                atomicAdd(place + d, n);
+        }
     }
     __syncthreads();
     int32_t total = 0;
@@ -197,6 +254,7 @@ __global__ void __launch_bounds__(kThreads) lists_scatter_kernel(const SortArgs 
             a.offsets[a.K] = total;
     }
 
+    const int bits = 31 - __clz(a.bins);
     const int64_t limit = FIRST ? a.M : total;
     const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.share;
     const int64_t end = min(limit, begin + a.share);
@@ -222,7 +280,7 @@ __global__ void __launch_bounds__(kThreads) lists_scatter_kernel(const SortArgs 
 #pragma unroll
         for (int u = 0; u < ITEMS; ++u) {
             const int32_t d = row[u] < 0 ? -1 : (row[u] >> a.shift) & (a.bins - 1);
-            rank[u] = warp_rank(d, counts + warp * a.bins, lane);
+            rank[u] = warp_rank(d, bits, counts + warp * a.bins, lane);
         }
         __syncthreads();
         // per digit: where its items, and each warp's of them, start in the ordered tile
@@ -279,7 +337,7 @@ template <int THREADS, int ITEMS>
 __global__ void __launch_bounds__(THREADS)
     lists_one_block_kernel(const int32_t *__restrict__ idx, int32_t M, int32_t K, int32_t bits,
                            int32_t *__restrict__ order, int32_t *__restrict__ rows,
-                           int32_t *__restrict__ offsets, int32_t *__restrict__ total)
+                           int32_t *__restrict__ offsets, int32_t *__restrict__ total, Fill fill)
 {
     constexpr int kW = THREADS / 32;
     constexpr int kMax = THREADS * ITEMS;
@@ -292,6 +350,10 @@ __global__ void __launch_bounds__(THREADS)
     const int warp = threadIdx.x >> 5;
     let_next_start();
     wait_for_previous();
+    if (blockIdx.x > 0) {
+        fill_zero(fill, blockIdx.x - 1, gridDim.x - 1);
+        return;
+    }
     int32_t n = M;   // items of this pass
     for (int shift = 0; shift == 0 || shift < bits; shift += kOneBits) {
         const int items = (n + THREADS - 1) / THREADS;   // per thread, <= ITEMS
@@ -318,7 +380,7 @@ __global__ void __launch_bounds__(THREADS)
         for (int u = 0; u < ITEMS; ++u)
             if (u < items)
                 rank[u] = warp_rank(row[u] < 0 ? -1 : (row[u] >> shift) & (kOneBins - 1),
-                                    counts[warp], lane);
+                                    min(kOneBits, bits - shift), counts[warp], lane);
         __syncthreads();
         int32_t mine = 0;
         if (threadIdx.x < kOneBins)
@@ -376,68 +438,42 @@ __global__ void __launch_bounds__(THREADS)
 // offsets[r] for r in [0, K]: the number of sorted rows below r.  starts: where
 // the rows with each value of r >> shift start (nullptr: only their number,
 // *total).
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(128)
     lists_offsets_kernel(const int32_t *rows, const int32_t *total, const int32_t *starts,
                          int32_t shift, int32_t K, int32_t *__restrict__ offsets)
 {
     let_next_start();
     wait_for_previous();
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (r > K)
+    const uint32_t r = blockIdx.x * 128u + threadIdx.x;   // K < 2^31
+    if (r > static_cast<uint32_t>(K))
         return;
     // the answer is in [lo, lo + n]
-    int64_t lo = 0, n;
-    if (starts != nullptr && r < K) {
+    int32_t lo = 0, n;
+    if (starts != nullptr && r < static_cast<uint32_t>(K)) {
         lo = starts[r >> shift];
         n = starts[(r >> shift) + 1] - lo;
     } else {
         n = *total;
     }
+    if (r == static_cast<uint32_t>(K)) {
+        offsets[r] = n;
+        return;
+    }
     while (n > 0) {
         // seven probes cut the range into eight; count those below r
-        const int64_t step = (n + 7) >> 3;
-        int below = 0;
+        const int32_t step = (n >> 3) + ((n & 7) != 0);
+        int32_t below = 0;
 #pragma unroll
         for (int q = 1; q < 8; ++q) {
-            const int64_t at = q * step - 1;
-            below += at < n && rows[lo + at] < r;
+            const int32_t at = q * step - 1;
+            below += at < n && rows[lo + at] < static_cast<int32_t>(r);
         }
         lo += below * step;
         n -= below * step;
         if (below < 7)
             n = min(step - 1, n);
     }
-    offsets[r] = static_cast<int32_t>(lo);
-}
-
-__global__ void __launch_bounds__(256)
-    lists_offsets_warp_kernel(const int32_t *rows, const int32_t *total, const int32_t *starts,
-                              int32_t shift, int32_t K, int32_t *__restrict__ offsets)
-{
-    let_next_start();
-    wait_for_previous();
-    const int lane = threadIdx.x & 31;
-    const int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    if (r > K)
-        return;
-    int64_t lo = 0, n;
-    if (starts != nullptr && r < K) {
-        lo = starts[r >> shift];
-        n = starts[(r >> shift) + 1] - lo;
-    } else {
-        n = *total;
-    }
-    while (n > 0) {
-        const int64_t step = (n + 31) >> 5;
-        const int64_t at = (lane + 1) * step - 1;
-        const int below = __popc(__ballot_sync(kAll, at < n && rows[lo + at] < r));
-        lo += below * step;
-        n -= below * step;
-        if (below < 32)
-            n = min(step - 1, n);
-    }
-    if (lane == 0)
-        offsets[r] = static_cast<int32_t>(lo);
+    offsets[r] = lo;
 }
 
 struct SortPlan {
@@ -482,28 +518,37 @@ SortPlan sort_plan(int64_t M, int64_t K)
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
-// Rows up to which a warp searches for each (4,097 rows in 2^20 places: 3 us
-// against 6; 131,073 rows in 2^14: 5 us by threads).
-constexpr int64_t kWarpSearchMax = 32768;
+int32_t fill_parts(size_t bytes, int32_t launches)
+{
+    return static_cast<int32_t>(
+        std::min<size_t>((bytes + (size_t(16) << 20) - 1) >> 24, static_cast<size_t>(launches)));
+}
+
+// Blocks of `threads` threads that fill a share: 16 KiB or more each, at most
+// as many as the SMs hold.
+unsigned fill_blocks(const Fill &f, int threads)
+{
+    if (!f.any())
+        return 0;
+    return static_cast<unsigned>(
+        std::min<int64_t>(f.bytes / f.parts / 16384 + 1, kMaxBlocks * 1024 / threads));
+}
 
 cudaError_t launch_offsets(const int32_t *rows, const int32_t *total, const int32_t *starts,
                            int32_t shift, int64_t K, int32_t *offsets, cudaStream_t stream)
 {
-    if (K <= kWarpSearchMax)
-        return launch_after(lists_offsets_warp_kernel, static_cast<unsigned>((K + 1 + 7) / 8), 256,
-                            0, stream, rows, total, starts, shift, K, offsets);
-    return launch_after(lists_offsets_kernel, static_cast<unsigned>((K + 1 + 255) / 256), 256, 0,
-                        stream, rows, total, starts, shift, K, offsets);
+    return launch_after(lists_offsets_kernel, static_cast<unsigned>(K / 128 + 1), 128, 0, stream,
+                        rows, total, starts, shift, K, offsets);
 }
 
 template <bool FIRST>
-cudaError_t sort_pass(const SortArgs &a, int items, cudaStream_t stream)
+cudaError_t sort_pass(SortArgs &a, int items, cudaStream_t stream)
 {
-    const unsigned blocks = static_cast<unsigned>(a.blocks);
-    const cudaError_t e = launch_after(lists_count_kernel<FIRST>, blocks, kThreads,
-                                       static_cast<size_t>(a.bins) * 4, stream, a);
+    const cudaError_t e = launch_after(lists_count_kernel<FIRST>, static_cast<unsigned>(a.blocks),
+                                       kThreads, static_cast<size_t>(a.bins) * 4, stream, a);
     if (e != cudaSuccess)
         return e;
+    const unsigned blocks = static_cast<unsigned>(a.blocks) + fill_blocks(a.fill, kThreads);
     const size_t smem = scatter_smem(a.bins, items);
     switch (items) {
     case 2:
@@ -547,21 +592,26 @@ size_t lists_scratch_bytes(int64_t M, int64_t K)
 }
 
 cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *order, int32_t *rows,
-                         int32_t *offsets, void *scratch, cudaStream_t stream)
+                         int32_t *offsets, void *scratch, void *zero, size_t zero_bytes,
+                         cudaStream_t stream)
 {
     cudaError_t e = cudaSuccess;
+    Fill fill{static_cast<uint8_t *>(zero), static_cast<int64_t>(zero_bytes), 0, 1};
     if (M <= kOneBlockMax) {
         const bool own = K <= kOneOffsetsMax;
         int32_t *total = own ? nullptr : static_cast<int32_t *>(scratch);
         if (!own && rows == nullptr)
             rows = total + 4;
+        fill.parts = fill_parts(zero_bytes, 1);
         // one warp for every 128 items, at least eight
         if (M <= 1024)
-            e = launch_after(lists_one_block_kernel<256, 4>, 1, 256, 0, stream, idx, M, K,
-                             row_bits(K), order, rows, own ? offsets : nullptr, total);
+            e = launch_after(lists_one_block_kernel<256, 4>, 1 + fill_blocks(fill, 256), 256, 0,
+                             stream, idx, M, K, row_bits(K), order, rows,
+                             own ? offsets : nullptr, total, fill);
         else
-            e = launch_after(lists_one_block_kernel<1024, 4>, 1, 1024, 0, stream, idx, M, K,
-                             row_bits(K), order, rows, own ? offsets : nullptr, total);
+            e = launch_after(lists_one_block_kernel<1024, 4>, 1 + fill_blocks(fill, 1024), 1024, 0,
+                             stream, idx, M, K, row_bits(K), order, rows,
+                             own ? offsets : nullptr, total, fill);
         if (e == cudaSuccess && !own)
             e = launch_offsets(rows, total, nullptr, 0, K, offsets, stream);
         return e;
@@ -588,8 +638,11 @@ cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *orde
             set[i][j] = reinterpret_cast<int32_t *>(at);
             at += ids;
         }
+    fill.parts = fill_parts(zero_bytes, p.passes);
     for (int i = 0; i < p.passes && e == cudaSuccess; ++i) {
         SortArgs a{};
+        a.fill = fill;
+        a.fill.part = i;
         a.last = i == p.passes - 1;
         a.rows_in = i == 0 ? idx : set[(i - 1) & 1][0];
         a.pos_in = i == 0 ? nullptr : set[(i - 1) & 1][1];

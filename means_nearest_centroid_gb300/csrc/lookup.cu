@@ -11,8 +11,11 @@
 // slice of columns over one chunk in registers and writes a row as soon as its
 // last place is passed.  A row that continues past a chunk's end leaves its
 // parts in a workspace, and a second launch adds those in chunk order.  Every
-// row of the result is written once, by one group, and the order of every sum
-// follows from the sizes alone: the bits do not change from run to run.
+// row that ids name is written once, by one group, and the order of every sum
+// follows from the sizes alone: the bits do not change from run to run.  The
+// whole table is zeroed by the sort's launches, which leave HBM idle: for 131,072
+// rows of 2,048 (1.07 GB, 140 us) that hides the sort, where blocks that zeroed
+// the rows without ids afterwards took 250 us for the gradient of 16,384 tokens.
 #include "internal.h"
 #include "launch.cuh"
 #include "vec.cuh"
@@ -82,8 +85,13 @@ __global__ void __launch_bounds__(kThreads) lookup_one_kernel(const LookupArgs a
     for (int u = 0; u < U; ++u)
         if (i[u] < a.N) {
             float acc[VE] = {};
-            if (r[u] >= 0 && r[u] < a.K)
-                fma_raw<T, VE>(acc, q[u], a.weights != nullptr ? __ldg(a.weights + i[u]) : 1.0f);
+            if (r[u] >= 0 && r[u] < a.K) {
+                widen<T, VE>(q[u], acc);
+                const float w = a.weights != nullptr ? __ldg(a.weights + i[u]) : 1.0f;
+#pragma unroll
+                for (int v = 0; v < VE; ++v)
+                    acc[v] *= w;
+            }
 #pragma unroll
             for (int v = 0; v < VE; ++v)
                 acc[v] *= a.scale;
@@ -91,9 +99,11 @@ __global__ void __launch_bounds__(kThreads) lookup_one_kernel(const LookupArgs a
         }
 }
 
-// Several ids a point, J rows in flight a thread.  Tables that fit L2 bound it
-// by L2 and by issue: eight elements cost one load, eight widenings and four
-// packed multiply-adds.
+// Several ids a point, J rows in flight a thread.  Bound by the rows' way from
+// L2 (268 MB for 65,536 points of 8 ids in a table of 8 MB: 27 us, 10 TB/s).
+// Blocks that went through several points and read the next ids early, fewer
+// rows in flight at a higher occupancy, and rows copied asynchronously into
+// shared memory were 0 to 50% slower.
 template <typename T, int VE, int J>
 __global__ void __launch_bounds__(kThreads) lookup_many_kernel(const LookupArgs a)
 {
@@ -106,7 +116,8 @@ __global__ void __launch_bounds__(kThreads) lookup_many_kernel(const LookupArgs 
     const T *table = static_cast<const T *>(a.table) + static_cast<int64_t>(vec) * VE;
     const int32_t *idx = a.idx + i * a.k;
     const float *weights = a.weights != nullptr ? a.weights + i * a.k : nullptr;
-    float acc[VE] = {};
+    Sums<VE> acc;
+    acc.zero();
     for (int32_t j0 = 0; j0 < a.k; j0 += J) {
         int32_t r[J];
         float w[J];
@@ -144,11 +155,13 @@ __global__ void __launch_bounds__(kThreads) lookup_many_kernel(const LookupArgs 
         for (int u = 0; u < J; ++u)
             fma_raw<T, VE>(acc, q[u], w[u]);
     }
+    float f[VE];
+    acc.get(f);
 #pragma unroll
     for (int v = 0; v < VE; ++v)
-        acc[v] *= a.scale;
+        f[v] *= a.scale;
     store_raw<T, VE>(static_cast<T *>(a.out) + i * a.D + static_cast<int64_t>(vec) * VE,
-                     narrow<T, VE>(acc));
+                     narrow<T, VE>(f));
 }
 
 // ---- groups of lanes over columns -------------------------------------------
@@ -169,6 +182,32 @@ struct Columns {
     }
 };
 
+// Adds U values over a group's lanes together: after the step of distance d a
+// lane holds the values whose numbers' bits its own lane's bits picked, half as
+// many each time (for 8 values and 32 lanes 9 exchanges, not 40).  Returns the
+// number of the value that sum[0] then holds; lanes with lane % (LG / U) == 0
+// hold each once.
+template <int U, int LG>
+__device__ __forceinline__ int add_over_lanes(float (&sum)[U], int lane)
+{
+    int j = 0;
+#pragma unroll
+    for (int half = U / 2, off = LG / 2; half > 0; half >>= 1, off >>= 1) {
+        const bool up = (lane & off) != 0;
+#pragma unroll
+        for (int u = 0; u < half; ++u) {
+            const float give = up ? sum[u] : sum[u + half];
+            const float keep = up ? sum[u + half] : sum[u];
+            sum[u] = keep + __shfl_xor_sync(kAll, give, off);
+        }
+        j += up ? half : 0;
+    }
+#pragma unroll
+    for (int off = LG / U / 2; off > 0; off >>= 1)
+        sum[0] += __shfl_xor_sync(kAll, sum[0], off);
+    return j;
+}
+
 // ---- gradient of the weights ----------------------------------------------
 
 struct DweightsArgs {
@@ -180,72 +219,93 @@ struct DweightsArgs {
     float scale;
 };
 
-// A group of lanes per point: its gradient is held in registers while the rows
-// of its ids pass, eight in flight; the eight sums are added over the lanes
-// together, halving their number with the distance (9 exchanges for 32 lanes,
-// not 40).  Bound by the gather of N k rows from L2.
+// For rows of more than one slice, or without a gradient of the table.  A group
+// of lanes per point: its gradient is held in registers while the rows of its
+// ids pass, eight in flight.  Bound by the gather of N k rows from L2.
 template <typename T, int VE, int LG>
-__global__ void __launch_bounds__(kThreads) dweights_kernel(const DweightsArgs a)
+__global__ void __launch_bounds__(kThreads, 2) dweights_kernel(const DweightsArgs a)
 {
     using C = Columns<VE, LG>;
     constexpr int NV = C::kVectors;
+    constexpr int U = sizeof(T) == 2 ? 8 : 4;   // rows in flight
     const int lane = threadIdx.x & (LG - 1);
-    const int64_t any =
-        static_cast<int64_t>(blockIdx.x) * (kThreads / LG) + threadIdx.x / LG;
-    const bool live = any < a.N;
-    const int64_t i = live ? any : a.N - 1;
-    const T *dout = static_cast<const T *>(a.dout) + i * a.D;
+    const int64_t groups = static_cast<int64_t>(gridDim.x) * (kThreads / LG);
+    const T *table = static_cast<const T *>(a.table);
     const int slices = (a.D + C::kSlice - 1) / C::kSlice;
-    for (int32_t j0 = 0; j0 < a.k; j0 += 8) {
-        const T *row[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int32_t r = j0 + u < a.k ? __ldg(a.idx + i * a.k + j0 + u) : -1;
-            row[u] = static_cast<uint32_t>(r) < static_cast<uint32_t>(a.K)
-                         ? static_cast<const T *>(a.table) + static_cast<int64_t>(r) * a.D
-                         : nullptr;
+    int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / LG) + threadIdx.x / LG;
+    int32_t j0 = 0;
+    auto read = [&](int64_t at, int32_t j) {   // lane u: id u of the eight, -1 for none
+        const int32_t mine = j + (lane & 7);
+        const int32_t r = at < a.N && mine < a.k ? __ldg(a.idx + at * a.k + mine) : -1;
+        return static_cast<uint32_t>(r) < static_cast<uint32_t>(a.K) ? r : -1;
+    };
+    int32_t next = read(i, 0);
+    // the groups of a warp go through as many points each, the last ones idle
+    while (__any_sync(kAll, i < a.N)) {
+        const int32_t ids = next;
+        const int64_t at = i;
+        const int32_t at_j = j0;
+        j0 += 8;
+        if (j0 >= a.k) {
+            j0 = 0;
+            i += groups;
         }
-        float sum[8] = {};
+        next = read(i, j0);
+        const bool all = __all_sync(kAll, ids >= 0);
+        const T *dout = static_cast<const T *>(a.dout) + (at < a.N ? at : 0) * a.D;
+        Sums<2> two[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            two[u].zero();
         for (int s = 0; s < slices; ++s) {
+            int col[NV];
+            Sums<VE> p[NV];   // 0 past D, where column 0 is read instead
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const int col = C::at(s, lane, v);
-                if (col < a.D) {
-                    float p[VE];
-                    widen<T, VE>(load_raw<T, VE>(dout + col), p);
-                    Raw<T, VE> q[8];
+                const bool in = C::at(s, lane, v) < a.D;
+                col[v] = in ? C::at(s, lane, v) : 0;
+                float f[VE] = {};
+                if (in)
+                    widen<T, VE>(load_raw<T, VE>(dout + col[v]), f);
+                p[v].set(f);
+            }
 #pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        q[u] = row[u] != nullptr ? load_raw<T, VE>(row[u] + col) : Raw<T, VE>{};
+            for (int u0 = 0; u0 < 8; u0 += U) {
+                Raw<T, VE> q[U][NV];
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        float f[VE];
-                        widen<T, VE>(q[u], f);
+                for (int u = 0; u < U; ++u) {
+                    const int32_t r = __shfl_sync(kAll, ids, u0 + u, LG);
+                    const T *row = table + static_cast<int64_t>(r) * a.D;
+                    if (all || r >= 0) {
 #pragma unroll
-                        for (int e = 0; e < VE; ++e)
-                            sum[u] = fmaf(p[e], f[e], sum[u]);
+                        for (int v = 0; v < NV; ++v)
+                            q[u][v] = load_raw<T, VE>(row + col[v]);
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < NV; ++v)
+                            q[u][v] = Raw<T, VE>{};
                     }
                 }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int v = 0; v < NV; ++v)
+                        if (C::at(s, lane, v) < a.D)
+                            dot_raw<T, VE>(two[u0 + u], p[v], q[u][v]);
             }
         }
-        // after the step of distance d, a lane holds the sums whose bits its own bits picked
-        int j = 0;
+        float sum[8];
 #pragma unroll
-        for (int half = 4, off = LG / 2; half > 0; half >>= 1, off >>= 1) {
-            const bool up = (lane & off) != 0;
-#pragma unroll
-            for (int u = 0; u < half; ++u) {
-                const float give = up ? sum[u] : sum[u + half];
-                const float keep = up ? sum[u + half] : sum[u];
-                sum[u] = keep + __shfl_xor_sync(kAll, give, off);
-            }
-            j += up ? half : 0;
+        for (int u = 0; u < 8; ++u) {
+            float f[2];
+            two[u].get(f);
+            sum[u] = f[0] + f[1];
         }
-#pragma unroll
-        for (int off = LG / 16; off > 0; off >>= 1)
-            sum[0] += __shfl_xor_sync(kAll, sum[0], off);
-        if (live && (lane & (LG / 8 - 1)) == 0 && j0 + j < a.k)
-            a.dweights[i * a.k + j0 + j] = sum[0] * a.scale;
+        const int j = add_over_lanes<8, LG>(sum, lane);
+        // an id of no row counts 0, whatever dout holds
+        const bool there = __shfl_sync(kAll, ids, j, LG) >= 0;
+        if (at < a.N && (lane & (LG / 8 - 1)) == 0 && at_j + j < a.k)
+            a.dweights[at * a.k + at_j + j] = there ? sum[0] * a.scale : 0.0f;
     }
 }
 
@@ -254,15 +314,18 @@ __global__ void __launch_bounds__(kThreads) dweights_kernel(const DweightsArgs a
 struct GradArgs {
     const void *dout;
     const float *weights;      // or nullptr
+    const int32_t *idx;        // of the points, for dweights
+    const void *table;
+    float *dweights;           // formed on the way, or nullptr
     const int32_t *order;      // sorted places -> flat (point, id) positions
     const int32_t *rows;       // the rows in sorted order
     const int32_t *offsets;    // [K + 1]
     void *dtable;
     float *parts;              // [2][chunks][D]: a chunk's first and last row, unfinished
+    int64_t M;                 // ids
     int64_t chunks;
     int32_t chunk;             // sorted places per chunk, a multiple of 8
     int32_t slices;            // column slices of a row
-    int64_t sum_blocks;        // blocks that sum; the others zero rows without ids
     int32_t k, K, D;
     int32_t skip;              // a row that takes no gradient, or -1
     float scale;
@@ -293,30 +356,24 @@ __device__ __forceinline__ void put(const GradArgs &a, int32_t r, int col, const
     store_raw<G, VE>(p, narrow<G, VE>(f));
 }
 
-// T: type of dout, G: of dtable.
-template <typename T, typename G, int VE, int LG>
-__global__ void __launch_bounds__(kThreads) segment_kernel(const GradArgs a)
+// T: type of dout, G: of dtable.  DW (one slice): a place's weight's gradient is
+// formed on the way, from the row of the table that its group holds meanwhile;
+// the four sums of a batch are added over the lanes together.
+template <typename T, typename G, int VE, int LG, bool DW>
+__global__ void __launch_bounds__(kThreads, VE == 1 ? 2 : 3) segment_kernel(const GradArgs a)
 {
     using C = Columns<VE, LG>;
     constexpr int NV = C::kVectors;
-    constexpr int U = sizeof(T) == 2 ? 8 : 4;   // rows in flight: 32 registers
+    constexpr int U = 4;   // rows in flight
     let_next_start();
     wait_for_previous();
-    if (blockIdx.x >= a.sum_blocks) {
-        // rows that no id names, a warp each
-        const int lane = threadIdx.x & 31;
-        const int64_t warps = (static_cast<int64_t>(gridDim.x) - a.sum_blocks) * kWarps;
-        for (int64_t r = (static_cast<int64_t>(blockIdx.x) - a.sum_blocks) * kWarps +
-                         (threadIdx.x >> 5);
-             r < a.K; r += warps) {
-            if (a.offsets[r] != a.offsets[r + 1])
-                continue;
-            G *p = static_cast<G *>(a.dtable) + r * a.D;
-            const Raw<G, VE> zero{};
-            for (int c = lane * VE; c < a.D; c += 32 * VE)
-                store_raw<G, VE>(p + c, zero);
-        }
-        return;
+    if constexpr (DW) {
+        // ids of no row, which are not among the sorted places
+        const int64_t threads = static_cast<int64_t>(gridDim.x) * kThreads;
+        for (int64_t f = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; f < a.M;
+             f += threads)
+            if (static_cast<uint32_t>(__ldg(a.idx + f)) >= static_cast<uint32_t>(a.K))
+                a.dweights[f] = 0.0f;
     }
     const int lane = threadIdx.x & (LG - 1);
     const int64_t unit =
@@ -332,86 +389,117 @@ __global__ void __launch_bounds__(kThreads) segment_kernel(const GradArgs a)
     const bool from_before = live && begin > 0 && a.rows[begin - 1] == a.rows[begin];
     const bool goes_on = live && end < total && a.rows[end - 1] == a.rows[end];
 
-    float acc[NV][VE] = {};
+    int col[NV];   // past D: column 0, whose sums are not kept
+    Sums<VE> acc[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        col[v] = C::at(slice, lane, v) < a.D ? C::at(slice, lane, v) : 0;
+        acc[v].zero();
+    }
     int32_t cur = live ? a.rows[begin] : -1;
     bool first = true;   // cur is the row at `begin`
-    auto part = [&](int which) {
+    Sums<VE> t_row[DW ? NV : 1];   // the table's row cur, 0 past D
+    auto read_row = [&]() {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int col = C::at(slice, lane, v);
-            if (col < a.D)
-                store_raw<float, VE>(a.parts + (which * a.chunks + chunk) * a.D + col,
-                                     narrow<float, VE>(acc[v]));
+        for (int v = 0; v < (DW ? NV : 0); ++v) {
+            float f[VE] = {};
+            if (C::at(slice, lane, v) < a.D)
+                widen<T, VE>(load_raw<T, VE>(static_cast<const T *>(a.table) +
+                                             static_cast<int64_t>(cur) * a.D + col[v]),
+                             f);
+            t_row[v].set(f);
         }
     };
-    auto finish = [&]() {
+    if (DW && live)
+        read_row();
+    // the row summed so far: written, or left as the chunk's first (0) or last (1) part
+    auto finish = [&](int which) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int col = C::at(slice, lane, v);
-            if (col < a.D)
-                put<G, VE>(a, cur, col, acc[v]);
+            float f[VE];
+            acc[v].get(f);
+            if (C::at(slice, lane, v) < a.D) {
+                if (which < 0)
+                    put<G, VE>(a, cur, col[v], f);
+                else
+                    store_raw<float, VE>(a.parts + (which * a.chunks + chunk) * a.D + col[v],
+                                         narrow<float, VE>(f));
+            }
         }
     };
     for (int32_t s0 = 0; s0 < a.chunk; s0 += LG) {
         // a place per lane; the groups of a warp go through their chunks in step
         const int64_t s = begin + s0 + lane;
-        int32_t row = -1, point = 0;
+        int32_t row = -1, point = 0, f = -1;
         float w = 0.0f;
         if (s0 + lane < a.chunk && s < end) {
-            const int32_t f = a.order[s];
+            f = a.order[s];
             row = a.rows[s];
             point = a.k == 1 ? f : f / a.k;
             w = a.weights != nullptr ? __ldg(a.weights + f) : 1.0f;
         }
         const int n = min(LG, a.chunk - s0);
         for (int u0 = 0; u0 < n; u0 += U) {
-            if (!__any_sync(kAll, row >= 0))
+            // every group of the warp has U places here, or some have fewer, or none any
+            const bool whole = __all_sync(kAll, begin + s0 + u0 + U <= end);
+            if (!whole && !__any_sync(kAll, begin + s0 + u0 < end))
                 break;
             Raw<T, VE> q[U][NV];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int32_t i = __shfl_sync(kAll, point, u0 + u, LG);
-                const int32_t r = __shfl_sync(kAll, row, u0 + u, LG);
+                const T *p = dout + static_cast<int64_t>(__shfl_sync(kAll, point, u0 + u, LG)) * a.D;
+                if (whole || begin + s0 + u0 + u < end) {
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    const int col = C::at(slice, lane, v);
-                    if (r >= 0 && col < a.D)
-                        q[u][v] = load_raw<T, VE>(dout + static_cast<int64_t>(i) * a.D + col);
-                    else
+                    for (int v = 0; v < NV; ++v)
+                        q[u][v] = load_raw<T, VE>(p + col[v]);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < NV; ++v)
                         q[u][v] = Raw<T, VE>{};
                 }
             }
+            Sums<2> two[DW ? U : 1];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int32_t r = __shfl_sync(kAll, row, u0 + u, LG);
                 const float wu = __shfl_sync(kAll, w, u0 + u, LG);
                 if (r != cur && r >= 0) {
-                    if (first && from_before)
-                        part(0);
-                    else
-                        finish();
+                    finish(first && from_before ? 0 : -1);
                     first = false;
                     cur = r;
 #pragma unroll
                     for (int v = 0; v < NV; ++v)
-#pragma unroll
-                        for (int e = 0; e < VE; ++e)
-                            acc[v][e] = 0.0f;
+                        acc[v].zero();
+                    if constexpr (DW)
+                        read_row();
                 }
+                if constexpr (DW)
+                    two[u].zero();
 #pragma unroll
-                for (int v = 0; v < NV; ++v)
+                for (int v = 0; v < NV; ++v) {
                     fma_raw<T, VE>(acc[v], q[u][v], wu);
+                    if constexpr (DW)
+                        if (C::at(slice, lane, v) < a.D)
+                            dot_raw<T, VE>(two[u], t_row[v], q[u][v]);
+                }
+            }
+            if constexpr (DW) {
+                float sum[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float h[2];
+                    two[u].get(h);
+                    sum[u] = h[0] + h[1];
+                }
+                const int j = add_over_lanes<U, LG>(sum, lane);
+                const int32_t to = __shfl_sync(kAll, f, u0 + j, LG);
+                if (to >= 0 && (lane & (LG / U - 1)) == 0)
+                    a.dweights[to] = sum[0] * a.scale;
             }
         }
     }
-    if (!live)
-        return;
-    if (first && from_before)
-        part(0);
-    else if (goes_on)
-        part(1);
-    else
-        finish();
+    if (live)
+        finish(first && from_before ? 0 : goes_on ? 1 : -1);
 }
 
 // Rows that span chunks: the chunk in which such a row begins holds its first
@@ -527,39 +615,34 @@ int64_t column_slices(int64_t D)
     return (D + cols - 1) / cols;
 }
 
-// Sorted places per chunk: enough (chunk, slice) units for 32 warps on every
-// SM, in steps of 8 places, at most 512.
+// Sorted places per chunk: enough (chunk, slice) units for the 24 warps that an
+// SM holds, in steps of 8 places, at most 512.
 int64_t chunk_places(int64_t M, int64_t D, int sms)
 {
-    const int64_t groups = int64_t(sms) * 32 * (32 / lane_group(D));
+    const int64_t groups = int64_t(sms) * 24 * (32 / lane_group(D));
     const int64_t want = (M * column_slices(D) + groups - 1) / groups;
     return std::min<int64_t>(512, std::max<int64_t>(16, (want + 7) / 8 * 8));
 }
 
-int grad_elems(const void *dout, int dtype, const void *dtable, int grad_dtype, int64_t D)
-{
-    return vector_elems(D, most_elems(dtype),
-                        {{dout, dtype_bytes(dtype)}, {dtable, dtype_bytes(grad_dtype)}});
-}
-
 template <typename T, typename G>
-cudaError_t grad_launch(GradArgs a, int ve, int sms, cudaStream_t stream)
+cudaError_t grad_launch(const GradArgs &a, int ve, cudaStream_t stream)
 {
     return by_elems<T>(ve, [&](auto VE) {
         return by_group(a.D, [&](auto LG) {
             constexpr int kUnits = kThreads / decltype(LG)::value;
-            a.sum_blocks = (a.chunks * a.slices + kUnits - 1) / kUnits;
-            int64_t zero_blocks = 0;
-            if (!a.accumulate)
-                zero_blocks = std::min<int64_t>((a.K + kWarps - 1) / kWarps, int64_t(sms) * 16);
-            if (a.sum_blocks + zero_blocks > 0x7fffffff)
+            const int64_t want = (a.chunks * a.slices + kUnits - 1) / kUnits;
+            if (want > 0x7fffffff)
                 return cudaErrorInvalidValue;
-            cudaError_t e = launch_after(segment_kernel<T, G, decltype(VE)::value, decltype(LG)::value>,
-                                         static_cast<unsigned>(a.sum_blocks + zero_blocks),
-                                         kThreads, 0, stream, a);
+            const unsigned blocks = static_cast<unsigned>(want);
+            cudaError_t e =
+                a.dweights != nullptr
+                    ? launch_after(segment_kernel<T, G, decltype(VE)::value, decltype(LG)::value, true>,
+                                   blocks, kThreads, 0, stream, a)
+                    : launch_after(segment_kernel<T, G, decltype(VE)::value, decltype(LG)::value, false>,
+                                   blocks, kThreads, 0, stream, a);
             if (e == cudaSuccess && a.chunks > 1)
                 e = launch_after(join_kernel<G, decltype(VE)::value, decltype(LG)::value>,
-                                 static_cast<unsigned>(a.sum_blocks), kThreads, 0, stream, a);
+                                 blocks, kThreads, 0, stream, a);
             return e;
         });
     });
@@ -616,7 +699,7 @@ cudaError_t launch_lookup(const void *table, int dtype, int64_t K, int64_t D, co
 
 cudaError_t launch_dweights(const void *dout, const void *table, int dtype, const int32_t *idx,
                             int64_t N, int32_t k, int64_t K, int64_t D, float scale,
-                            float *dweights, cudaStream_t stream)
+                            float *dweights, int sms, cudaStream_t stream)
 {
     const int es = dtype_bytes(dtype);
     const int ve = vector_elems(D, most_elems(dtype), {{table, es}, {dout, es}});
@@ -627,8 +710,10 @@ cudaError_t launch_dweights(const void *dout, const void *table, int dtype, cons
         return by_elems<T>(ve, [&](auto VE) {
             return by_group(D, [&](auto LG) {
                 constexpr int kUnits = kThreads / decltype(LG)::value;
+                // the blocks that fit the SMs at once go through the points
+                const int64_t blocks = std::min<int64_t>((N + kUnits - 1) / kUnits, sms * 2);
                 dweights_kernel<T, decltype(VE)::value, decltype(LG)::value>
-                    <<<static_cast<unsigned>((N + kUnits - 1) / kUnits), kThreads, 0, stream>>>(a);
+                    <<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
                 return cudaGetLastError();
             });
         });
@@ -642,21 +727,32 @@ size_t lookup_grad_parts_bytes(int64_t M, int64_t D, int sms)
     return static_cast<size_t>(2 * chunks) * D * 4;
 }
 
-cudaError_t launch_lookup_grad(const void *dout, int dtype, const float *weights, int64_t M,
-                               int32_t k, int64_t K, int64_t D, float scale, int32_t skip,
-                               bool accumulate, const int32_t *order, const int32_t *rows,
-                               const int32_t *offsets, float *parts, void *dtable, int grad_dtype,
+bool dweights_with_dtable(int64_t D) { return column_slices(D) == 1; }
+
+cudaError_t launch_lookup_grad(const void *dout, int dtype, const int32_t *idx,
+                               const float *weights, const void *table, int64_t M, int32_t k,
+                               int64_t K, int64_t D, float scale, int32_t skip, bool accumulate,
+                               const int32_t *order, const int32_t *rows, const int32_t *offsets,
+                               float *parts, void *dtable, int grad_dtype, float *dweights,
                                int sms, cudaStream_t stream)
 {
-    const int ve = grad_elems(dout, dtype, dtable, grad_dtype, D);
+    const int ve = vector_elems(
+        D, most_elems(dtype),
+        {{dout, dtype_bytes(dtype)},
+         {dweights != nullptr ? table : nullptr, dtype_bytes(dtype)},
+         {dtable, dtype_bytes(grad_dtype)}});
     GradArgs a{};
     a.dout = dout;
     a.weights = weights;
+    a.idx = idx;
+    a.table = table;
+    a.dweights = dweights;
     a.order = order;
     a.rows = rows;
     a.offsets = offsets;
     a.dtable = dtable;
     a.parts = parts;
+    a.M = M;
     a.slices = static_cast<int32_t>(column_slices(D));
     a.chunk = static_cast<int32_t>(chunk_places(M, D, sms));
     a.chunks = (M + a.chunk - 1) / a.chunk;
@@ -669,8 +765,8 @@ cudaError_t launch_lookup_grad(const void *dout, int dtype, const float *weights
     return by_type(dtype, [&](auto t) {
         using T = decltype(t);
         if (grad_dtype == kFp32)
-            return grad_launch<T, float>(a, ve, sms, stream);
-        return grad_launch<T, T>(a, ve, sms, stream);
+            return grad_launch<T, float>(a, ve, stream);
+        return grad_launch<T, T>(a, ve, stream);
     });
 }
 

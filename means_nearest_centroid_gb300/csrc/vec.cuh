@@ -91,22 +91,77 @@ __device__ __forceinline__ void store_raw(T *p, const Raw<T, VE> &r)
     *reinterpret_cast<Raw<T, VE> *>(p) = r;
 }
 
-// acc += w * q, in fp32 (two products an instruction).
+// Sums of VE elements in fp32, held in pairs: two products an instruction.
+template <int VE>
+struct Sums {
+    static_assert(VE % 2 == 0, "pairs");
+    uint64_t p[VE / 2];
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i)
+            p[i] = 0;
+    }
+    __device__ __forceinline__ void set(const float (&f)[VE])
+    {
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i)
+            asm("mov.b64 %0, {%1, %2};" : "=l"(p[i]) : "f"(f[2 * i]), "f"(f[2 * i + 1]));
+    }
+    __device__ __forceinline__ void get(float (&f)[VE]) const
+    {
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i)
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(f[2 * i]), "=f"(f[2 * i + 1]) : "l"(p[i]));
+    }
+};
+template <>
+struct Sums<1> {
+    float p[1];
+    __device__ __forceinline__ void zero() { p[0] = 0.0f; }
+    __device__ __forceinline__ void set(const float (&f)[1]) { p[0] = f[0]; }
+    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = p[0]; }
+};
+
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void fma_pair(uint64_t &acc, uint64_t a, uint64_t b)
+{
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+
+// acc += w * q.
 template <typename T, int VE>
-__device__ __forceinline__ void fma_raw(float (&acc)[VE], const Raw<T, VE> &q, float w)
+__device__ __forceinline__ void fma_raw(Sums<VE> &acc, const Raw<T, VE> &q, float w)
 {
     float f[VE];
     widen<T, VE>(q, f);
     if constexpr (VE == 1) {
-        acc[0] = fmaf(w, f[0], acc[0]);
+        acc.p[0] = fmaf(w, f[0], acc.p[0]);
+    } else {
+        const uint64_t ww = pair(w, w);
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i)
+            fma_pair(acc.p[i], pair(f[2 * i], f[2 * i + 1]), ww);
+    }
+}
+
+// The sum of acc's two elements += <p, q>, p as pairs.
+template <typename T, int VE>
+__device__ __forceinline__ void dot_raw(Sums<2> &acc, const Sums<VE> &p, const Raw<T, VE> &q)
+{
+    float f[VE];
+    widen<T, VE>(q, f);
+    if constexpr (VE == 1) {
+        fma_pair(acc.p[0], pair(p.p[0], 0.0f), pair(f[0], 0.0f));
     } else {
 #pragma unroll
-        for (int i = 0; i < VE; i += 2)
-            asm("{\n\t.reg .b64 a, b, c;\n\t"
-                "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%0, %1};\n\t"
-                "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
-                : "+f"(acc[i]), "+f"(acc[i + 1])
-                : "f"(f[i]), "f"(f[i + 1]), "f"(w));
+        for (int i = 0; i < VE / 2; ++i)
+            fma_pair(acc.p[0], p.p[i], pair(f[2 * i], f[2 * i + 1]));
     }
 }
 
