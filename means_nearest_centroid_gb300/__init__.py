@@ -13,6 +13,7 @@ the shared library is missing, every call raises.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -598,13 +599,19 @@ def kmassign_lookup_grad(dout, idx, K: int, weights=None, table=None, scale: flo
     return dtable, dweights
 
 
+def _pointers(tensors):
+    """A C array of the tensors' device pointers (keep it while it is used)."""
+    return array.array("Q", [t.data_ptr() for t in tensors])
+
+
 def _tensor_arrays(tensors, name):
     """Pointers, sizes and type codes of a list of tensors, as C arrays."""
-    codes = [_need_float(t, name) for t in tensors]
-    n = len(codes)
-    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors])
-    sizes = (ctypes.c_int64 * n)(*[t.numel() for t in tensors])
-    return ptrs, sizes, (ctypes.c_int32 * n)(*codes), n
+    codes = array.array("i", [_need_float(t, name) for t in tensors])
+    return _pointers(tensors), array.array("q", [t.numel() for t in tensors]), codes
+
+
+def _address(a):
+    return a.buffer_info()[0]
 
 
 def _norm_out(tensors, norm):
@@ -620,9 +627,10 @@ def _norm_out(tensors, norm):
 def kmassign_grad_norm(tensors, norm=None, stream=None):
     """The 2-norm over all elements of a list of tensors, an fp32 scalar on the GPU."""
     tensors = list(tensors)
-    ptrs, sizes, codes, n = _tensor_arrays(tensors, "tensors")
+    ptrs, sizes, codes = _tensor_arrays(tensors, "tensors")
     norm = _norm_out(tensors, norm)
-    rc = library().kmassign_grad_norm(ptrs, sizes, codes, n, norm.data_ptr(),
+    rc = library().kmassign_grad_norm(_address(ptrs), _address(sizes), _address(codes),
+                                      len(tensors), norm.data_ptr(),
                                       _stream_ptr(stream, norm.device))
     _check(rc, "kmassign_grad_norm")
     return norm
@@ -636,20 +644,23 @@ def kmassign_clip(grads, max_norm: float, out=None, norm=None, stream=None):
     shapes and types.
     """
     grads = list(grads)
-    ptrs, sizes, codes, n = _tensor_arrays(grads, "grads")
+    ptrs, sizes, codes = _tensor_arrays(grads, "grads")
     outs = None
     if out is not None:
         out = list(out)
-        if len(out) != n:
+        if len(out) != len(grads):
             raise ValueError("out must hold one tensor per gradient")
         for g, o in zip(grads, out):
-            _need_cuda(o, "out", g.dtype)
+            if not (isinstance(o, torch.Tensor) and o.is_cuda and o.dtype is g.dtype
+                    and o.is_contiguous()):
+                _need_cuda(o, "out", g.dtype)
             if o.shape != g.shape:
                 raise ValueError("out must have the gradients' shapes")
-        outs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
+        outs = _pointers(out)
     norm = _norm_out(grads, norm)
-    rc = library().kmassign_clip(ptrs, outs, sizes, codes, n, float(max_norm), norm.data_ptr(),
-                                 _stream_ptr(stream, norm.device))
+    rc = library().kmassign_clip(_address(ptrs), None if outs is None else _address(outs),
+                                 _address(sizes), _address(codes), len(grads), float(max_norm),
+                                 norm.data_ptr(), _stream_ptr(stream, norm.device))
     _check(rc, "kmassign_clip")
     return norm
 

@@ -9,6 +9,7 @@
 // (gradients beyond 1e15 or below 1e-15), its squares are taken again in fp64,
 // so the norm is right over the whole range of the types.
 #include "internal.h"
+#include "launch.cuh"
 #include "vec.cuh"
 
 #include <algorithm>
@@ -21,33 +22,46 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kVecs = 4;                                // 16-byte vectors per thread and chunk
 constexpr int64_t kChunkBytes = int64_t(kThreads) * kVecs * 16;
-constexpr int kMaxTensors = 256;                        // per launch (kernel parameters)
+// Tensors of a launch, in its parameters: a short list costs the host 0.7 us a
+// launch less than a long one.
+constexpr int kShortList = 24;
+constexpr int kLongList = 256;
 
+template <int MAX>
 struct TensorList {
-    const void *src[kMaxTensors];
-    void *dst[kMaxTensors];
-    int64_t size[kMaxTensors];          // elements
-    int64_t first_chunk[kMaxTensors + 1];
-    uint8_t dtype[kMaxTensors];
-    uint8_t wide[kMaxTensors];          // src and dst 16-byte aligned
+    const void *src[MAX];
+    void *dst[MAX];
+    int64_t size[MAX];          // elements
+    int64_t first_chunk[MAX + 1];
+    uint8_t dtype[MAX];
+    uint8_t wide[MAX];          // src and dst 16-byte aligned
     int32_t n;
 };
 
-__device__ __forceinline__ double block_sum(double v)
+// Sum over lane 0 .. 31 in lane 0.
+__device__ __forceinline__ double warp_sum(double v)
 {
-    __shared__ double s[kWarps];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
         v += __shfl_down_sync(kAll, v, off);
-    if ((threadIdx.x & 31) == 0)
-        s[threadIdx.x >> 5] = v;
+    return v;
+}
+
+// Sum over the block in thread 0.  The SM adds two fp64 numbers a clock, so one
+// warp adds what the others hand it (a few hundred clocks; all warps reducing
+// by shuffles, and then each adding the warps' sums, took 5,000).
+__device__ __forceinline__ double block_sum(double v)
+{
+    __shared__ double s[kThreads];
+    s[threadIdx.x] = v;
     __syncthreads();
+    if (threadIdx.x >= 32)
+        return 0.0;
     double t = 0.0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
-        t += s[w];
-    __syncthreads();
-    return t;
+        t += s[w * 32 + threadIdx.x];
+    return warp_sum(t);
 }
 
 // Sum of squares of n values held in registers.
@@ -73,7 +87,8 @@ __device__ __forceinline__ double squares(const float (&f)[N])
 }
 
 // The tensor that chunk c belongs to.
-__device__ __forceinline__ int tensor_of(const TensorList &l, int64_t c)
+template <int MAX>
+__device__ __forceinline__ int tensor_of(const TensorList<MAX> &l, int64_t c)
 {
     int lo = 0, hi = l.n - 1;
     while (lo < hi) {
@@ -175,9 +190,12 @@ __device__ __forceinline__ int64_t share_begin(int64_t chunks, int64_t b, int64_
     return chunks * b / blocks;
 }
 
+template <int MAX>
 __global__ void __launch_bounds__(kThreads)
-    squares_kernel(const __grid_constant__ TensorList l, double *__restrict__ partial)
+    squares_kernel(const __grid_constant__ TensorList<MAX> l, double *__restrict__ partial)
 {
+    let_next_start();
+    wait_for_previous();
     const int64_t chunks = l.first_chunk[l.n];
     const int64_t c1 = share_begin(chunks, blockIdx.x + 1, gridDim.x);
     int64_t c = share_begin(chunks, blockIdx.x, gridDim.x);
@@ -206,31 +224,56 @@ __global__ void __launch_bounds__(kThreads)
         partial[blockIdx.x] = s;
 }
 
-__device__ __forceinline__ float norm_of(const double *__restrict__ partial, int32_t n)
+// sqrt of a sum of squares: an fp32 root of the sum scaled by a power of 4 into
+// [1, 4), within an fp32 ulp over the range of fp64 (an fp64 root costs the
+// scaling kernel half a microsecond).
+__device__ __forceinline__ float root(double total)
 {
-    double v = 0.0;
-    for (int i = threadIdx.x; i < n; i += kThreads)
-        v += __ldg(partial + i);
-    return static_cast<float>(sqrt(block_sum(v)));
+    if (!(total > 0.0) || total > 1e300)
+        return static_cast<float>(sqrt(total));   // 0, inf, NaN
+    const int half = (((__double2hiint(total) >> 20) & 0x7ff) - 1023) >> 1;
+    const double scale = __hiloint2double((1023 - 2 * half) << 20, 0);
+    return scalbnf(sqrtf(static_cast<float>(total * scale)), half);
 }
 
-__global__ void __launch_bounds__(kThreads)
-    norm_kernel(const double *__restrict__ partial, int32_t n, float *__restrict__ norm)
+// The norm from all partial sums, by one warp; in lane 0.
+__device__ __forceinline__ float norm_of(const double *partial, int32_t n)
 {
+    double v = 0.0;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < n; i += 32)
+        v += partial[i];
+    return root(warp_sum(v));
+}
+
+__global__ void __launch_bounds__(32)
+    norm_kernel(const double *partial, int32_t n, float *__restrict__ norm)
+{
+    wait_for_previous();
     const float f = norm_of(partial, n);
     if (threadIdx.x == 0)
         *norm = f;
 }
 
+template <int MAX>
 __global__ void __launch_bounds__(kThreads)
-    scale_kernel(const __grid_constant__ TensorList l, const double *__restrict__ partial,
+    scale_kernel(const __grid_constant__ TensorList<MAX> l, const double *partial,
                  int32_t partials, float max_norm, bool in_place, float *__restrict__ norm)
 {
-    const float f = norm_of(partial, partials);
-    if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0)
-        *norm = f;
-    const float ratio = max_norm / (f + 1e-6f);
-    const float coef = ratio >= 1.0f ? 1.0f : ratio;   // a NaN norm gives NaN
+    let_next_start();
+    wait_for_previous();
+    __shared__ float s_coef;
+    if (threadIdx.x < 32) {
+        const float f = norm_of(partial, partials);
+        if (threadIdx.x == 0) {
+            const float ratio = max_norm / (f + 1e-6f);
+            s_coef = ratio >= 1.0f ? 1.0f : ratio;   // a NaN norm gives NaN
+            if (norm != nullptr && blockIdx.x == 0)
+                *norm = f;
+        }
+    }
+    __syncthreads();
+    const float coef = s_coef;
     if (in_place && coef == 1.0f)
         return;
     const int64_t chunks = l.first_chunk[l.n];
@@ -263,15 +306,16 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-// Tensors [first, first + l->n) of the call that have elements; returns the
-// index after the last one taken.
+// The next tensors of the call that have elements, from `first` on; returns
+// the index after the last one taken.
+template <int MAX>
 int32_t fill_list(const void *const *src, void *const *dst, const int64_t *sizes,
-                  const int32_t *dtypes, int32_t n, int32_t first, TensorList *l)
+                  const int32_t *dtypes, int32_t n, int32_t first, TensorList<MAX> *l)
 {
     l->n = 0;
     l->first_chunk[0] = 0;
     int32_t i = first;
-    for (; i < n && l->n < kMaxTensors; ++i) {
+    for (; i < n && l->n < MAX; ++i) {
         if (sizes[i] == 0)
             continue;
         const int32_t t = l->n++;
@@ -287,46 +331,56 @@ int32_t fill_list(const void *const *src, void *const *dst, const int64_t *sizes
     return i;
 }
 
-unsigned list_blocks(const TensorList &l, int sms)
+template <int MAX>
+cudaError_t clip_lists(const void *const *grads, void *const *out, const int64_t *sizes,
+                       const int32_t *dtypes, int32_t n, bool scale, float max_norm, float *norm,
+                       double *partial, int sms, cudaStream_t stream)
 {
-    return static_cast<unsigned>(std::min<int64_t>(l.first_chunk[l.n], int64_t(sms) * 4));
+    auto blocks_of = [&](const TensorList<MAX> &l) {
+        return static_cast<unsigned>(std::min<int64_t>(l.first_chunk[l.n], int64_t(sms) * 4));
+    };
+    TensorList<MAX> l;
+    cudaError_t e = cudaSuccess;
+    int32_t partials = 0, lists = 0;
+    for (int32_t at = 0; at < n && e == cudaSuccess;) {
+        at = fill_list(grads, out, sizes, dtypes, n, at, &l);
+        if (l.n == 0)
+            break;
+        const unsigned blocks = blocks_of(l);
+        e = launch_after(squares_kernel<MAX>, blocks, kThreads, 0, stream, l, partial + partials);
+        partials += static_cast<int32_t>(blocks);
+        ++lists;
+    }
+    if (!scale || lists == 0)
+        return e != cudaSuccess
+                   ? e
+                   : launch_after(norm_kernel, 1, 32, 0, stream, partial, partials, norm);
+    for (int32_t at = 0, i = 0; i < lists && e == cudaSuccess; ++i) {
+        if (lists > 1)   // else l still holds the list
+            at = fill_list(grads, out, sizes, dtypes, n, at, &l);
+        e = launch_after(scale_kernel<MAX>, blocks_of(l), kThreads, 0, stream, l, partial, partials,
+                         max_norm, out == nullptr, i == 0 ? norm : nullptr);
+    }
+    return e;
 }
 
 }  // namespace
 
 size_t clip_scratch_bytes(int32_t n, int sms)
 {
-    const int64_t lists = (int64_t(n) + kMaxTensors - 1) / kMaxTensors;
-    return static_cast<size_t>(std::max<int64_t>(1, lists)) * sms * 4 * sizeof(double);
+    const int64_t lists = n <= kShortList ? 1 : (int64_t(n) + kLongList - 1) / kLongList;
+    return static_cast<size_t>(lists) * sms * 4 * sizeof(double);
 }
 
 cudaError_t launch_clip(const void *const *grads, void *const *out, const int64_t *sizes,
                         const int32_t *dtypes, int32_t n, bool scale, float max_norm, float *norm,
                         double *partial, int sms, cudaStream_t stream)
 {
-    TensorList l;
-    int32_t partials = 0;
-    for (int32_t at = 0; at < n;) {
-        at = fill_list(grads, out, sizes, dtypes, n, at, &l);
-        if (l.n == 0)
-            break;
-        const unsigned blocks = list_blocks(l, sms);
-        squares_kernel<<<blocks, kThreads, 0, stream>>>(l, partial + partials);
-        partials += static_cast<int32_t>(blocks);
-    }
-    bool wrote = false;
-    if (scale)
-        for (int32_t at = 0; at < n;) {
-            at = fill_list(grads, out, sizes, dtypes, n, at, &l);
-            if (l.n == 0)
-                break;
-            scale_kernel<<<list_blocks(l, sms), kThreads, 0, stream>>>(
-                l, partial, partials, max_norm, out == nullptr, wrote ? nullptr : norm);
-            wrote = true;
-        }
-    if (!wrote && norm != nullptr)
-        norm_kernel<<<1, kThreads, 0, stream>>>(partial, partials, norm);
-    return cudaGetLastError();
+    if (n <= kShortList)
+        return clip_lists<kShortList>(grads, out, sizes, dtypes, n, scale, max_norm, norm, partial,
+                                      sms, stream);
+    return clip_lists<kLongList>(grads, out, sizes, dtypes, n, scale, max_norm, norm, partial, sms,
+                                 stream);
 }
 
 }  // namespace kma
