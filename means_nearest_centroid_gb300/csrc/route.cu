@@ -82,6 +82,7 @@ struct RouteArgs {
     int32_t groups, topk_groups, group_top;
     int32_t per_group;      // E / groups
     int32_t group_lanes;    // lanes per group where each lane's experts are of one group, else 0
+    int32_t group_shift;    // its logarithm
     uint32_t group_magic;   // e / per_group == e * group_magic >> 20 for e < 1024
     bool renorm;
     bool wide;              // every lane's experts can be loaded as one vector
@@ -90,33 +91,22 @@ struct RouteArgs {
     float scale;
 };
 
-// Compare-exchange towards descending order, and the smallest networks of 2, 4
-// and 8 values.
-__device__ __forceinline__ void down(float &a, float &b)
-{
-    const float hi = fmaxf(a, b);
-    b = fminf(a, b);
-    a = hi;
-}
+// Descending order by Batcher's odd-even merge network (1968): 19, 63 and 191
+// compare-exchanges for 8, 16 and 32 values.
 template <int V>
 __device__ __forceinline__ void sort_down(float (&s)[V])
 {
-    static_assert(V == 1 || V == 2 || V == 4 || V == 8, "sizes with a network");
-    if constexpr (V == 2) {
-        down(s[0], s[1]);
-    } else if constexpr (V == 4) {
-        down(s[0], s[1]), down(s[2], s[3]);
-        down(s[0], s[2]), down(s[1], s[3]);
-        down(s[1], s[2]);
-    } else if constexpr (V == 8) {
-        down(s[0], s[1]), down(s[2], s[3]), down(s[4], s[5]), down(s[6], s[7]);
-        down(s[0], s[2]), down(s[1], s[3]), down(s[4], s[6]), down(s[5], s[7]);
-        down(s[1], s[2]), down(s[5], s[6]), down(s[0], s[4]), down(s[3], s[7]);
-        down(s[1], s[5]), down(s[2], s[6]);
-        down(s[1], s[4]), down(s[3], s[6]);
-        down(s[2], s[4]), down(s[3], s[5]);
-        down(s[3], s[4]);
-    }
+#pragma unroll
+    for (int p = 1; p < V; p *= 2)
+#pragma unroll
+        for (int k = p; k > 0; k /= 2)
+#pragma unroll
+            for (int i = 0; i + k < V; ++i)
+                if (i >= k % p && ((i - k % p) & k) == 0 && i / (2 * p) == (i + k) / (2 * p)) {
+                    const float hi = fmaxf(s[i], s[i + k]);
+                    s[i + k] = fminf(s[i], s[i + k]);
+                    s[i] = hi;
+                }
 }
 
 // The best two of a group's keys, held by several lanes.
@@ -140,28 +130,67 @@ struct Best2 {
     }
 };
 
+// A row's logits into its W lanes, V experts each: one vector where rows are
+// aligned to it, else element by element across the lanes (coalesced) and
+// through shared memory (W rows of STRIDE floats).
+template <typename T, int W, int V, int STRIDE>
+__device__ __forceinline__ void load_row(float (&x)[V], const T *row, int E, bool wide, int lane,
+                                         float *shared)
+{
+    constexpr int VE = V < 8 ? V : 8;
+    const int e0 = lane * V;
+    if (wide) {
+#pragma unroll
+        for (int v = 0; v < V; v += VE) {
+            float f[VE];
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                f[i] = -INFINITY;
+            if (e0 + v < E)
+                widen<T, VE>(load_raw<T, VE>(row + e0 + v), f);
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                x[v + i] = f[i];
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = v * W + lane;
+            x[v] = e < E ? Elem<T>::up(row[e]) : -INFINITY;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = v * W + lane;
+            shared[e / V * STRIDE + e % V] = x[v];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            x[v] = shared[lane * STRIDE + v];
+        __syncwarp();
+    }
+}
+
 // One row per W lanes; lane l of them holds the V experts from l V on, so
 // that of equal keys the lowest lane's come first.  A key of -inf is never
 // selected.  What bounds the kernel is issue: the logits are read once, but a
 // score costs an exponential and a reciprocal, and the selection has to order
-// k of E keys.  So each lane sorts its V <= 8 keys once (a network of minima
-// and maxima, without indices), and each of the k rounds takes the maximum
-// over the lanes' heads and advances the list of the lowest lane that holds
-// it; which expert a key belonged to is found once at the end, round j's by
-// lane j, from a copy of the keys in shared memory (equal keys of a lane leave
-// it in consecutive rounds: the how-manieth is counted).  Lists of 16 and 32
-// keys (E > 256) are not sorted: each round finds their maximum again.
+// k of E keys.  So each lane sorts its V keys once (a network of minima and
+// maxima, without indices), and each of the k rounds takes the maximum over
+// the lanes' heads and advances the list of the lowest lane that holds it;
+// which expert a key belonged to is found once at the end, round j's by lane j,
+// from a copy of the keys in shared memory (equal keys of a lane leave it in
+// consecutive rounds: the how-manieth is counted).
 template <typename T, int W, int V, bool SIGMOID, bool GROUPS>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs a)
 {
     constexpr int kRows = 32 / W;           // rows per warp
     constexpr int kSlots = 32 / W;          // selections a lane can hold (k <= 32)
-    constexpr bool kSorted = V <= 8;
     constexpr int kPad = V >= 4 ? 4 : 1;    // words after each lane's keys, against bank conflicts
     constexpr int kStride = V + kPad;
-    constexpr bool kStore = kSorted || GROUPS;
-    __shared__ alignas(16) float s_key[kStore ? kRouteWarps * kRows : 1][kStore ? W * kStride : 4];
+    __shared__ alignas(16) float s_key[kRouteWarps * kRows][W * kStride];
     __shared__ float s_group[GROUPS ? kRouteWarps * kRows : 1][GROUPS ? 32 : 1];
+    __shared__ int2 s_round[kRouteWarps * kRows][32];
     const int lane = threadIdx.x & (W - 1);
     const int local = threadIdx.x / W;
     const int64_t row_any = static_cast<int64_t>(blockIdx.x) * (kRouteWarps * kRows) + local;
@@ -170,31 +199,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
     const T *x_row = static_cast<const T *>(a.logits) + row * a.E;
     const int e0 = lane * V;
 
+    float *keys = s_key[local];
     float x[V];
-    if (a.wide) {
-        constexpr int VE = V < 8 ? V : 8;
-#pragma unroll
-        for (int v = 0; v < V; v += VE) {
-            float f[VE];
-#pragma unroll
-            for (int i = 0; i < VE; ++i)
-                f[i] = -INFINITY;
-            if (e0 + v < a.E)
-                widen<T, VE>(load_raw<T, VE>(x_row + e0 + v), f);
-#pragma unroll
-            for (int i = 0; i < VE; ++i)
-                x[v + i] = f[i];
-        }
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            x[v] = e0 + v < a.E ? Elem<T>::up(x_row[e0 + v]) : -INFINITY;
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        x[v] = fmaxf(x[v], -INFINITY);   // NaN is masked as -inf is
+    load_row<T, W, V, kStride>(x, x_row, a.E, a.wide, lane, keys);
 
-    // scores (softmax: exp(x - max), normalised by `total`)
+    // scores (softmax: exp(x - max), normalised by `total`); what stands in the
+    // places of masked experts is not used
     float part[V];
     float top = 0.0f, total = 1.0f;
     if constexpr (SIGMOID) {
@@ -202,7 +212,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
             float most = 1.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                part[v] = 1.0f + (x[v] == -INFINITY ? 0.0f : expf(-x[v]));
+                const float t = expf(-x[v]);   // formed for all: no branch
+                part[v] = 1.0f + (is_masked(x[v]) ? 0.0f : t);
                 most = fmaxf(most, part[v]);
             }
             if (__any_sync(kAll, most > 0x1p125f)) {
@@ -214,9 +225,6 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
                 for (int v = 0; v < V; ++v)
                     part[v] = reciprocal(part[v]);
             }
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                part[v] = x[v] == -INFINITY ? 0.0f : part[v];
         }
     } else if (a.scored || !a.renorm) {
         float most = -INFINITY;
@@ -227,7 +235,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
         total = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            part[v] = x[v] == -INFINITY ? 0.0f : expf(x[v] - top);
+            const float t = expf(x[v] - top);
+            part[v] = is_masked(x[v]) ? 0.0f : t;
             total += part[v];
         }
         total = row_sum<W>(total);
@@ -255,15 +264,21 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const float f = (SIGMOID ? part[v] : part[v] / total) + b[v];
-            key[v] = x[v] == -INFINITY ? -INFINITY : fmaxf(f, -INFINITY);
+            key[v] = is_masked(x[v]) ? -INFINITY : fmaxf(f, -INFINITY);
         }
     } else {
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            key[v] = x[v];
+            key[v] = fmaxf(x[v], -INFINITY);   // NaN is masked as -inf is
     }
 
-    float *keys = s_key[kStore ? local : 0];
+    // the lane's keys in descending order
+    float sorted[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        sorted[v] = key[v];
+    sort_down<V>(sorted);
+
     if constexpr (GROUPS) {
         float *of_group = s_group[local];
         const bool by_key = a.bias != nullptr || a.group_top == 1;
@@ -271,14 +286,21 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
             // a lane's experts are of one group: its lanes join theirs directly, then share
             // out the comparisons with the other groups
             Best2 b;
+            if (!by_key) {
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                b.add(by_key ? key[v] : key[v] == -INFINITY ? -INFINITY : part[v]);
-            for (int off = a.group_lanes >> 1; off > 0; off >>= 1)
-                b.join(off);
+                for (int v = 0; v < V; ++v)
+                    b.add(key[v] == -INFINITY ? -INFINITY : part[v]);
+            } else {
+                b.first = sorted[0];
+                b.second = V > 1 ? sorted[V > 1 ? 1 : 0] : -INFINITY;
+            }
+#pragma unroll
+            for (int off = 1; off < W; off <<= 1)
+                if (off < a.group_lanes)
+                    b.join(off);
             const float own = b.key(a.group_top);
             const int part_of = lane & (a.group_lanes - 1);
-            const int g = lane / a.group_lanes;
+            const int g = lane >> a.group_shift;
             if (part_of == 0 && g < a.groups)
                 of_group[g] = own;
             __syncwarp();
@@ -287,11 +309,14 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
                 const float f = of_group[h];
                 ahead += f > own || (f == own && h < g);
             }
-            for (int off = a.group_lanes >> 1; off > 0; off >>= 1)
-                ahead += __shfl_xor_sync(kAll, ahead, off);
+#pragma unroll
+            for (int off = 1; off < W; off <<= 1)
+                if (off < a.group_lanes)
+                    ahead += __shfl_xor_sync(kAll, ahead, off);
+            const bool stays = ahead < a.topk_groups;
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                key[v] = ahead < a.topk_groups ? key[v] : -INFINITY;
+                sorted[v] = stays ? sorted[v] : -INFINITY;
         } else {
 #pragma unroll
             for (int v = 0; v < V; ++v)
@@ -337,6 +362,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
                 if (((stays >> (g & 31)) & 1u) == 0)
                     key[v] = -INFINITY;
             }
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                sorted[v] = key[v];
+            sort_down<V>(sorted);
             __syncwarp();
         }
     }
@@ -345,90 +374,80 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
 #pragma unroll
     for (int q = 0; q < kSlots; ++q)
         mine[q] = -1;
-    if constexpr (kSorted) {
-        float s[V];
+    // Every key, to find the selected ones in, and each round's key and the lane that gave it
+    int2 *rounds = s_round[local];
+    if constexpr (V >= 4) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            s[v] = key[v];
-            keys[lane * kStride + v] = key[v];
-        }
-        sort_down<V>(s);
-        // round j's key, the lane it came from, and how many equal ones that lane gave before
-        float got[kSlots];
-        int32_t from[kSlots], nth[kSlots];
-#pragma unroll
-        for (int q = 0; q < kSlots; ++q) {
-            got[q] = -INFINITY;
-            from[q] = nth[q] = 0;
-        }
-        float last_key = 0.0f;
-        int32_t last_lane = -1, equal = 0;
-        auto round = [&](int j, int shift) {
-            const float most = row_max<W>(s[0]);
-            const uint32_t holds = __ballot_sync(kAll, s[0] == most) >> (threadIdx.x & (32 - W));
-            const int32_t winner = __ffs(holds) - 1;   // its row's lanes come first in holds
-            if constexpr (W < 32) {
-                equal = most == last_key && winner == last_lane ? equal + 1 : 0;
-                last_key = most;
-                last_lane = winner;
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (v < shift)
-                    s[v] = lane != winner ? s[v] : v + 1 < V ? s[v + 1] : -INFINITY;
-#pragma unroll
-            for (int q = 0; q < kSlots; ++q)
-                if (j == lane + q * W) {
-                    got[q] = most;
-                    from[q] = winner;
-                    nth[q] = equal;
-                }
-        };
-        if (a.k <= 8) {
-            // round j of at most 8 can still look at 8 - j keys of a lane
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < a.k)
-                    round(j, 7 - j);
-        } else {
-            for (int j = 0; j < a.k; ++j)
-                round(j, V);
-        }
-        if constexpr (W == 32)
-            nth[0] = __popc(__match_any_sync(kAll, __float_as_uint(got[0] + 0.0f)) &
-                            __match_any_sync(kAll, from[0]) & ((1u << lane) - 1u));
-        __syncwarp();
-#pragma unroll
-        for (int q = 0; q < kSlots; ++q)
-            if (got[q] != -INFINITY) {
-                int32_t left = nth[q];
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (keys[from[q] * kStride + v] == got[q]) {
-                        if (left == 0)
-                            mine[q] = from[q] * V + v;
-                        --left;
-                    }
-            }
+        for (int v = 0; v < V; v += 4)
+            *reinterpret_cast<float4 *>(keys + lane * kStride + v) =
+                make_float4(key[v], key[v + 1], key[v + 2], key[v + 3]);
     } else {
-        for (int j = 0; j < a.k; ++j) {
-            float best = -INFINITY;
-            int32_t at = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            keys[lane * kStride + v] = key[v];
+    }
+    auto round = [&](int j, int shift) {
+        const float most = row_max<W>(sorted[0]);
+        const uint32_t holds =
+            __ballot_sync(kAll, sorted[0] == most) >> (threadIdx.x & (32 - W));
+        const bool gives = lane == __ffs(holds) - 1;   // its row's lanes come first in holds
+        if (gives)
+            rounds[j] = make_int2(__float_as_int(most), lane);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (v < shift)
+                sorted[v] = !gives ? sorted[v] : v + 1 < V ? sorted[v + 1] : -INFINITY;
+    };
+    // round j of k can still look at k - j keys of a lane
+    if (a.k <= 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < a.k)
+                round(j, 7 - j);
+    } else if (V > 8 && a.k <= 16) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (j < a.k)
+                round(j, 15 - j);
+    } else {
+        for (int j = 0; j < a.k; ++j)
+            round(j, V);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) {
+        const int j = lane + q * W;
+        if (q * W >= a.k || j >= a.k)
+            continue;
+        const int2 r = rounds[j];
+        const float got = __int_as_float(r.x);
+        if (got == -INFINITY)
+            continue;
+        uint32_t equal = 0;   // the lane's keys equal to it
+        float own[V];
+        if constexpr (V >= 4) {
+#pragma unroll
+            for (int v = 0; v < V; v += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(keys + r.y * kStride + v);
+                own[v] = f.x, own[v + 1] = f.y, own[v + 2] = f.z, own[v + 3] = f.w;
+            }
+        } else {
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if (key[v] > best) {
-                    best = key[v];
-                    at = e0 + v;
-                }
-            const float most = row_max<W>(best);
-            const int32_t e = __shfl_sync(kAll, at, __ffs(__ballot_sync(kAll, best == most)) - 1);
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (e == e0 + v)
-                    key[v] = -INFINITY;
-            if (j == lane)
-                mine[0] = most != -INFINITY ? e : -1;
+                own[v] = keys[r.y * kStride + v];
         }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            equal |= own[v] == got ? 1u << v : 0u;
+        // equal keys of a lane leave it in consecutive rounds
+        if ((equal & (equal - 1)) != 0)
+            for (int i = j - 1; i >= 0; --i) {
+                const int2 before = rounds[i];
+                if (__int_as_float(before.x) != got || before.y != r.y)
+                    break;
+                equal &= equal - 1;
+            }
+        mine[q] = r.y * V + __ffs(equal) - 1;
     }
 
     // weights, from the selected logits (just read: in L1)
@@ -586,6 +605,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_dense_kernel(cons
     constexpr int kRows = 32 / W;
     constexpr int kSlots = 32 / W;
     constexpr int VE = V < 8 ? V : 8;
+    constexpr int kStride = V + (V >= 4 ? 4 : 1);
+    __shared__ alignas(16) float s_row[kRouteWarps * kRows][W * kStride];
+    float *stage = s_row[threadIdx.x / W];
     const int lane = threadIdx.x & (W - 1);
     const int64_t row_any =
         static_cast<int64_t>(blockIdx.x) * (kRouteWarps * kRows) + threadIdx.x / W;
@@ -595,25 +617,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_dense_kernel(cons
     T *out = static_cast<T *>(a.dlogits) + row * a.E;
     const int e0 = lane * V;
     float x[V];
-#pragma unroll
-    for (int v = 0; v < V; v += VE) {
-        float f[VE];
-#pragma unroll
-        for (int i = 0; i < VE; ++i)
-            f[i] = -INFINITY;
-        if (a.wide) {
-            if (e0 + v < a.E)
-                widen<T, VE>(load_raw<T, VE>(x_row + e0 + v), f);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VE; ++i)
-                if (e0 + v + i < a.E)
-                    f[i] = Elem<T>::up(x_row[e0 + v + i]);
-        }
-#pragma unroll
-        for (int i = 0; i < VE; ++i)
-            x[v + i] = f[i];
-    }
+    load_row<T, W, V, kStride>(x, x_row, a.E, a.wide, lane, stage);
     float most = -INFINITY;
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -641,24 +645,31 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_dense_kernel(cons
         }
     }
     mean = row_sum<W>(mean);
-    if (live) {
-        // a row without a single unmasked expert has total 0 and x 0
-        const float share = total == 0.0f ? 0.0f : mean / total;
+    // a row without a single unmasked expert has total 0 and x 0
+    const float share = total == 0.0f ? 0.0f : mean / total;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        x[v] = -x[v] * share * a.scale;
+    if (a.wide) {
 #pragma unroll
         for (int v = 0; v < V; v += VE) {
             float f[VE];
 #pragma unroll
             for (int i = 0; i < VE; ++i)
-                f[i] = -x[v + i] * share * a.scale;
-            if (a.wide) {
-                if (e0 + v < a.E)
-                    store_raw<T, VE>(out + e0 + v, narrow<T, VE>(f));
-            } else {
+                f[i] = x[v + i];
+            if (live && e0 + v < a.E)
+                store_raw<T, VE>(out + e0 + v, narrow<T, VE>(f));
+        }
+    } else {   // back through shared memory, so that the stores are coalesced
 #pragma unroll
-                for (int i = 0; i < VE; ++i)
-                    if (e0 + v + i < a.E)
-                        out[e0 + v + i] = Elem<T>::down(f[i]);
-            }
+        for (int v = 0; v < V; ++v)
+            stage[lane * kStride + v] = x[v];
+        __syncwarp();
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int i = v * W + lane;
+            if (live && i < a.E)
+                out[i] = Elem<T>::down(stage[i / V * kStride + i % V]);
         }
     }
     __syncwarp();
@@ -678,6 +689,8 @@ cudaError_t route_shape(RouteArgs a, bool sigmoid, cudaStream_t stream)
     a.scored = a.bias != nullptr || (a.groups > 1 && a.group_top == 2);
     const int lanes = a.per_group % V == 0 ? a.per_group / V : 0;
     a.group_lanes = lanes > 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+    while ((1 << a.group_shift) < a.group_lanes)
+        ++a.group_shift;
     const int rows = kRouteWarps * (32 / W);
     const unsigned blocks = static_cast<unsigned>((a.N + rows - 1) / rows);
     if (sigmoid) {
