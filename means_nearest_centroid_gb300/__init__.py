@@ -123,6 +123,8 @@ def _declare(lib):
 def library(path: str | None = None):
     """The loaded libkmassign (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or library_path()
@@ -407,7 +409,7 @@ def _need_float(t, name) -> int:
 
 
 def _need_shape(t, name, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:   # a torch.Size is a tuple
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
