@@ -601,15 +601,16 @@ def kmassign_lookup_grad(dout, idx, K: int, weights=None, table=None, scale: flo
     return dtable, dweights
 
 
-def _pointers(tensors):
-    """A C array of the tensors' device pointers (keep it while it is used)."""
-    return array.array("Q", [t.data_ptr() for t in tensors])
-
-
 def _tensor_arrays(tensors, name):
     """Pointers, sizes and type codes of a list of tensors, as C arrays."""
-    codes = array.array("i", [_need_float(t, name) for t in tensors])
-    return _pointers(tensors), array.array("q", [t.numel() for t in tensors]), codes
+    try:   # the common case in few steps a tensor; the detail only on failure
+        codes = [_DTYPES[t.dtype] for t in tensors if t.is_cuda and t.is_contiguous()]
+    except (AttributeError, KeyError):
+        codes = []
+    if len(codes) != len(tensors):
+        codes = [_need_float(t, name) for t in tensors]
+    return (array.array("Q", [t.data_ptr() for t in tensors]),
+            array.array("q", [t.numel() for t in tensors]), array.array("i", codes))
 
 
 def _address(a):
@@ -643,7 +644,7 @@ def kmassign_clip(grads, max_norm: float, out=None, norm=None, stream=None):
 
     Each gradient (fp32, bf16 or fp16) is multiplied by min(1, max_norm /
     (norm + 1e-6)): in place, or into ``out``, a list of tensors of the same
-    shapes and types.
+    sizes and types.
     """
     grads = list(grads)
     ptrs, sizes, codes = _tensor_arrays(grads, "grads")
@@ -652,13 +653,11 @@ def kmassign_clip(grads, max_norm: float, out=None, norm=None, stream=None):
         out = list(out)
         if len(out) != len(grads):
             raise ValueError("out must hold one tensor per gradient")
-        for g, o in zip(grads, out):
-            if not (isinstance(o, torch.Tensor) and o.is_cuda and o.dtype is g.dtype
-                    and o.is_contiguous()):
-                _need_cuda(o, "out", g.dtype)
-            if o.shape != g.shape:
-                raise ValueError("out must have the gradients' shapes")
-        outs = _pointers(out)
+        outs, out_sizes, out_codes = _tensor_arrays(out, "out")
+        if out_codes != codes:
+            raise TypeError("out must have the gradients' types")
+        if out_sizes != sizes:
+            raise ValueError("out must have the gradients' sizes")
     norm = _norm_out(grads, norm)
     rc = library().kmassign_clip(_address(ptrs), None if outs is None else _address(outs),
                                  _address(sizes), _address(codes), len(grads), float(max_norm),

@@ -29,7 +29,6 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 
 // ---- lookup ---------------------------------------------------------------
 
@@ -39,11 +38,10 @@ struct LookupArgs {
     const float *weights;
     void *out;
     int64_t N;
-    int32_t k, K, D;
+    int32_t K, D;
     int32_t vecs;          // vectors per row
     int32_t rows;          // rows of a block side by side
     uint32_t magic;        // t / vecs == t * magic >> 16 for t < 256
-    bool ids_wide;         // four ids (and weights) can be loaded at once
     float scale;
 };
 
@@ -99,74 +97,72 @@ __global__ void __launch_bounds__(kThreads) lookup_one_kernel(const LookupArgs a
         }
 }
 
-// Several ids a point, J rows in flight a thread.  Bound by the rows' way from
-// L2 (268 MB for 65,536 points of 8 ids in a table of 8 MB: 27 us, 10 TB/s).
-// Blocks that went through several points and read the next ids early, fewer
-// rows in flight at a higher occupancy, and rows copied asynchronously into
-// shared memory were 0 to 50% slower.
-template <typename T, int VE, int J>
-__global__ void __launch_bounds__(kThreads) lookup_many_kernel(const LookupArgs a)
+// The same for rows of an odd number of 2-byte elements, or at odd offsets: a
+// thread writes an aligned 16-byte vector of its output row (at the row's ends
+// some elements of one), gathered from aligned words of the table's row; where
+// the two rows' offsets differ by an odd number of elements, words are joined in
+// pairs.  16,384 rows of 2,047 bf16: 39 us (2,048: 23); an element a thread 56,
+// a word of two elements a thread 66.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) lookup_odd_kernel(const LookupArgs a)
 {
+    static_assert(sizeof(T) == 2, "two elements a word");
+    constexpr int VE = 8;
     int r0, vec;
     if (!lookup_place(a, r0, vec))
         return;
     const int64_t i = static_cast<int64_t>(blockIdx.x) * a.rows + r0;
     if (i >= a.N)
         return;
-    const T *table = static_cast<const T *>(a.table) + static_cast<int64_t>(vec) * VE;
-    const int32_t *idx = a.idx + i * a.k;
-    const float *weights = a.weights != nullptr ? a.weights + i * a.k : nullptr;
-    Sums<VE> acc;
-    acc.zero();
-    for (int32_t j0 = 0; j0 < a.k; j0 += J) {
-        int32_t r[J];
-        float w[J];
-        if (a.ids_wide) {
+    T *out = static_cast<T *>(a.out) + i * a.D;
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(out) & 15) / 2;
+    const int e0 = vec * VE - off, begin = max(e0, 0), end = min(e0 + VE, a.D);
+    if (begin >= end)
+        return;
+    const int32_t r = __ldg(a.idx + i);
+    const bool there = static_cast<uint32_t>(r) < static_cast<uint32_t>(a.K);
+    const float w = there && a.weights != nullptr ? __ldg(a.weights + i) : 1.0f;
+    const T *table = static_cast<const T *>(a.table);
+    const T *row = table + static_cast<int64_t>(there ? r : 0) * a.D;
+    const T *from = row + e0;
+    const bool odd = (reinterpret_cast<uintptr_t>(from) & 3) != 0;
+    // an odd start reads one element more at either end, which has to be the table's
+    if (end - begin < VE ||
+        (odd && (from == table || from + VE == table + static_cast<int64_t>(a.K) * a.D))) {
+        for (int e = begin; e < end; ++e)
+            out[e] = Elem<T>::down(there ? Elem<T>::up(row[e]) * w * a.scale : 0.0f);
+        return;
+    }
+    uint32_t q[4] = {0u, 0u, 0u, 0u};
+    if (there) {
+        if (!odd) {
 #pragma unroll
-            for (int u = 0; u < J; u += 4) {
-                int4 v = make_int4(-1, -1, -1, -1);
-                float4 f = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-                if (j0 + u < a.k) {
-                    v = __ldg(reinterpret_cast<const int4 *>(idx + j0 + u));
-                    if (weights != nullptr)
-                        f = __ldg(reinterpret_cast<const float4 *>(weights + j0 + u));
-                }
-                r[u] = v.x, r[u + 1] = v.y, r[u + 2] = v.z, r[u + 3] = v.w;
-                w[u] = f.x, w[u + 1] = f.y, w[u + 2] = f.z, w[u + 3] = f.w;
-            }
+            for (int u = 0; u < 4; ++u)
+                q[u] = __ldg(reinterpret_cast<const uint32_t *>(from) + u);
         } else {
+            const uint32_t *words = reinterpret_cast<const uint32_t *>(from - 1);
+            uint32_t p[5];
 #pragma unroll
-            for (int u = 0; u < J; ++u) {
-                r[u] = j0 + u < a.k ? __ldg(idx + j0 + u) : -1;
-                w[u] = weights != nullptr && j0 + u < a.k ? __ldg(weights + j0 + u) : 1.0f;
-            }
+            for (int u = 0; u < 5; ++u)
+                p[u] = __ldg(words + u);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                q[u] = __funnelshift_r(p[u], p[u + 1], 16);
         }
-        Raw<T, VE> q[J];
-#pragma unroll
-        for (int u = 0; u < J; ++u) {
-            if (static_cast<uint32_t>(r[u]) < static_cast<uint32_t>(a.K)) {
-                q[u] = load_raw<T, VE>(table + static_cast<int64_t>(r[u]) * a.D);
-            } else {   // adds nothing, whatever its weight
-                q[u] = Raw<T, VE>{};
-                w[u] = 0.0f;
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < J; ++u)
-            fma_raw<T, VE>(acc, q[u], w[u]);
     }
     float f[VE];
-    acc.get(f);
+    Raw<T, VE> raw;
+    memcpy(&raw, q, 16);
+    widen<T, VE>(raw, f);
 #pragma unroll
     for (int v = 0; v < VE; ++v)
-        f[v] *= a.scale;
-    store_raw<T, VE>(static_cast<T *>(a.out) + i * a.D + static_cast<int64_t>(vec) * VE,
-                     narrow<T, VE>(f));
+        f[v] = f[v] * w * a.scale;
+    store_raw<T, VE>(out + e0, narrow<T, VE>(f));
 }
 
 // ---- groups of lanes over columns -------------------------------------------
 //
-// The gradients work in groups of LG lanes (8, 16 or 32, for rows of up to 64,
+// What sums rows works in groups of LG lanes (8, 16 or 32, for rows of up to 64,
 // 128 or more columns), each lane holding 8 columns as NV vectors of VE, so
 // that narrow or oddly aligned rows cost the same bookkeeping per id as wide ones.
 
@@ -181,6 +177,92 @@ struct Columns {
         return slice * kSlice + v * LG * VE + lane * VE;
     }
 };
+
+// ---- lookup of several ids --------------------------------------------------
+
+struct GatherArgs {
+    const void *table;
+    const int32_t *idx;
+    const float *weights;
+    void *out;
+    int64_t N;
+    int32_t k, K, D;
+    int32_t slices;
+    float scale;
+};
+
+// A group of lanes per point and slice of columns; lane u reads id u of eight,
+// U rows are in flight.  Bound by the rows' way from L2 (268 MB for 65,536
+// points of 8 ids in a table of 8 MB: 27 us, 10 TB/s).  Groups that went
+// through several points and read the next ids early, and rows copied
+// asynchronously into shared memory, were 0 to 50% slower.
+template <typename T, int VE, int LG, int U>
+__global__ void __launch_bounds__(kThreads) lookup_many_kernel(const GatherArgs a)
+{
+    using C = Columns<VE, LG>;
+    constexpr int NV = C::kVectors;
+    const int lane = threadIdx.x & (LG - 1);
+    const int64_t unit =
+        static_cast<int64_t>(blockIdx.x) * (kThreads / LG) + threadIdx.x / LG;
+    const bool live = unit < a.N * a.slices;
+    const int64_t i = live ? unit / a.slices : a.N - 1;
+    const int slice = live ? static_cast<int>(unit - i * a.slices) : 0;
+    const T *table = static_cast<const T *>(a.table);
+    int col[NV];   // past D: column 0, whose sums are not kept
+    Sums<VE> acc[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        col[v] = C::at(slice, lane, v) < a.D ? C::at(slice, lane, v) : 0;
+        acc[v].zero();
+    }
+    for (int32_t j0 = 0; j0 < a.k; j0 += 8) {
+        const int32_t j = j0 + (lane & 7);
+        int32_t r = -1;
+        float w = 0.0f;   // an id of no row adds nothing, whatever its weight
+        if (j < a.k) {
+            r = __ldg(a.idx + i * a.k + j);
+            if (static_cast<uint32_t>(r) >= static_cast<uint32_t>(a.K))
+                r = -1;
+            else
+                w = a.weights != nullptr ? __ldg(a.weights + i * a.k + j) : 1.0f;
+        }
+#pragma unroll
+        for (int u0 = 0; u0 < 8; u0 += U) {
+            if (j0 + u0 >= a.k)
+                break;
+            Raw<T, VE> q[U][NV];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int32_t ru = __shfl_sync(kAll, r, u0 + u, LG);
+                const T *row = table + static_cast<int64_t>(ru) * a.D;
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    q[u][v] = Raw<T, VE>{};
+                    if (ru >= 0)
+                        q[u][v] = load_raw<T, VE>(row + col[v]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float wu = __shfl_sync(kAll, w, u0 + u, LG);
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+                    fma_raw<T, VE>(acc[v], q[u][v], wu);
+            }
+        }
+    }
+    T *out = static_cast<T *>(a.out) + i * a.D;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+        if (live && C::at(slice, lane, v) < a.D) {
+            float f[VE];
+            acc[v].get(f);
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+                f[e] *= a.scale;
+            store_raw<T, VE>(out + col[v], narrow<T, VE>(f));
+        }
+}
 
 // Adds U values over a group's lanes together: after the step of distance d a
 // lane holds the values whose numbers' bits its own lane's bits picked, half as
@@ -656,42 +738,74 @@ cudaError_t launch_lookup(const void *table, int dtype, int64_t K, int64_t D, co
 {
     const int es = dtype_bytes(dtype);
     const int ve = vector_elems(D, most_elems(dtype), {{table, es}, {out, es}});
+    if (k > 1) {
+        GatherArgs a{};
+        a.table = table;
+        a.idx = idx;
+        a.weights = weights;
+        a.out = out;
+        a.N = N;
+        a.k = k;
+        a.K = static_cast<int32_t>(K);
+        a.D = static_cast<int32_t>(D);
+        a.slices = static_cast<int32_t>(column_slices(D));
+        a.scale = scale;
+        return by_type(dtype, [&](auto t) {
+            using T = decltype(t);
+            return by_elems<T>(ve, [&](auto VE) {
+                return by_group(D, [&](auto LG) {
+                    constexpr int kUnits = kThreads / decltype(LG)::value;
+                    const int64_t blocks = (N * a.slices + kUnits - 1) / kUnits;
+                    if (blocks > 0x7fffffff)
+                        return cudaErrorInvalidValue;
+                    // rows in flight: as many as ids, within the registers
+                    constexpr int kMost = decltype(VE)::value * sizeof(T) >= 8 ? 8 : 4;
+                    const unsigned grid = static_cast<unsigned>(blocks);
+                    if (k <= 2)
+                        lookup_many_kernel<T, decltype(VE)::value, decltype(LG)::value, 2>
+                            <<<grid, kThreads, 0, stream>>>(a);
+                    else if (k <= 4)
+                        lookup_many_kernel<T, decltype(VE)::value, decltype(LG)::value, 4>
+                            <<<grid, kThreads, 0, stream>>>(a);
+                    else
+                        lookup_many_kernel<T, decltype(VE)::value, decltype(LG)::value, kMost>
+                            <<<grid, kThreads, 0, stream>>>(a);
+                    return cudaGetLastError();
+                });
+            });
+        });
+    }
     LookupArgs a{};
     a.table = table;
     a.idx = idx;
     a.weights = weights;
     a.out = out;
     a.N = N;
-    a.k = k;
     a.K = static_cast<int32_t>(K);
     a.D = static_cast<int32_t>(D);
-    a.vecs = static_cast<int32_t>(D / ve);
+    const bool odd = ve * es == 2 && D >= 32;   // shorter rows: an element a thread
+    a.vecs = static_cast<int32_t>(odd ? (D + 7) / 8 + 1 : D / ve);
     a.rows = a.vecs <= kThreads ? kThreads / a.vecs : 1;
     a.magic = (65536u + a.vecs - 1) / static_cast<uint32_t>(a.vecs);
-    a.ids_wide = k % 4 == 0 &&
-                 (reinterpret_cast<uintptr_t>(idx) | reinterpret_cast<uintptr_t>(weights)) % 16 == 0;
     a.scale = scale;
     const unsigned pieces = static_cast<unsigned>((a.vecs + kThreads - 1) / kThreads);
     const int64_t blocks = (N + a.rows - 1) / a.rows;
-    // one id a point: four points a thread once that still gives every SM eight blocks
+    // four points a thread once that still gives every SM eight blocks
     const bool four = blocks * pieces >= int64_t(sms) * 32;
     return by_type(dtype, [&](auto t) {
         using T = decltype(t);
+        const dim3 fours(static_cast<unsigned>((blocks + 3) / 4), pieces);
+        const dim3 ones(static_cast<unsigned>(blocks), pieces);
+        if constexpr (sizeof(T) == 2)
+            if (odd) {
+                lookup_odd_kernel<T><<<ones, kThreads, 0, stream>>>(a);
+                return cudaGetLastError();
+            }
         return by_elems<T>(ve, [&](auto VE) {
-            constexpr int kVe = decltype(VE)::value;
-            if (k > 1 && k <= 4)
-                lookup_many_kernel<T, kVe, 4>
-                    <<<dim3(static_cast<unsigned>(blocks), pieces), kThreads, 0, stream>>>(a);
-            else if (k > 1)
-                lookup_many_kernel<T, kVe, 8>
-                    <<<dim3(static_cast<unsigned>(blocks), pieces), kThreads, 0, stream>>>(a);
-            else if (four)
-                lookup_one_kernel<T, kVe, 4>
-                    <<<dim3(static_cast<unsigned>((blocks + 3) / 4), pieces), kThreads, 0,
-                       stream>>>(a);
+            if (four)
+                lookup_one_kernel<T, decltype(VE)::value, 4><<<fours, kThreads, 0, stream>>>(a);
             else
-                lookup_one_kernel<T, kVe, 1>
-                    <<<dim3(static_cast<unsigned>(blocks), pieces), kThreads, 0, stream>>>(a);
+                lookup_one_kernel<T, decltype(VE)::value, 1><<<ones, kThreads, 0, stream>>>(a);
             return cudaGetLastError();
         });
     });
