@@ -82,11 +82,13 @@ __device__ __forceinline__ int32_t warp_rank(int32_t d, int bits, uint16_t *coun
     const uint32_t valid = __ballot_sync(kAll, d >= 0);
     uint32_t same = d >= 0 ? valid : ~valid;
 #pragma unroll
-    for (int b = 0; b < kMaxDigitBits; ++b)
-        if (b < bits) {
-            const uint32_t ones = __ballot_sync(kAll, (d >> b) & 1);
-            same &= (d >> b) & 1 ? ones : ~ones;
-        }
+    for (int b = 0; b < kMaxDigitBits; ++b) {
+        if (b >= bits)
+            break;
+        const bool one = (d & (1 << b)) != 0;
+        const uint32_t ones = __ballot_sync(kAll, one);
+        same &= one ? ones : ~ones;
+    }
     const uint32_t below = same & ((1u << lane) - 1u);
     int32_t base = 0;
     if (d >= 0 && below == 0) {
@@ -298,8 +300,10 @@ __global__ void __launch_bounds__(kThreads) lists_scatter_kernel(const SortArgs 
             int32_t sum;
             const int32_t first = in_tile + block_scan<kWarps>(n, warp_sums, &sum);
             in_tile += sum;
-            if (d < a.bins)
+            if (d < a.bins) {
                 start[d] = first;
+                place[d] -= first;   // so that an item's place is this plus its number in the tile
+            }
         }
         __syncthreads();
 #pragma unroll
@@ -311,17 +315,18 @@ __global__ void __launch_bounds__(kThreads) lists_scatter_kernel(const SortArgs 
                 t_pos[to] = pos[u];
             }
         __syncthreads();
+#pragma unroll 4
         for (int t = threadIdx.x; t < in_tile; t += kThreads) {
             const int32_t r = t_row[t];
-            const int32_t d = (r >> a.shift) & (a.bins - 1);
-            const int64_t to = place[d] + (t - start[d]);
+            const uint32_t to = place[(r >> a.shift) & (a.bins - 1)] + t;
             a.pos_out[to] = t_pos[t];
             if (a.rows_out != nullptr)
                 a.rows_out[to] = r;
         }
         __syncthreads();
+        // place: past this tile's items of the digit, no longer less its start
         for (int d = threadIdx.x; d < a.bins; d += kThreads)
-            place[d] += (d + 1 < a.bins ? start[d + 1] : in_tile) - start[d];
+            place[d] += d + 1 < a.bins ? start[d + 1] : in_tile;
         __syncthreads();
     }
     // places that no valid id takes

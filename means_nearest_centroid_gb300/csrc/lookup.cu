@@ -701,6 +701,8 @@ int64_t column_slices(int64_t D)
 // SM holds, in steps of 8 places, at most 512.
 int64_t chunk_places(int64_t M, int64_t D, int sms)
 {
+    if (M <= 32)
+        return 32;   // one chunk: no row spans two, and no second launch
     const int64_t groups = int64_t(sms) * 24 * (32 / lane_group(D));
     const int64_t want = (M * column_slices(D) + groups - 1) / groups;
     return std::min<int64_t>(512, std::max<int64_t>(16, (want + 7) / 8 * 8));

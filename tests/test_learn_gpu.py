@@ -712,3 +712,95 @@ def test_soft_codes_example_learns(dev):
     losses, used = m.train(steps=40)
     assert losses[-1] < 0.5 * losses[0]
     assert m.train(steps=3)[0] == losses[:3]   # the same bits again
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", [31, 33, 47, 129, 2047])
+@pytest.mark.parametrize("shift", [0, 1, 3])
+def test_lookup_odd_rows_at_the_table_s_ends(dev, D, shift, dtype):
+    """Odd rows are gathered word by word; the first and the last row's words end with the table,
+    whose neighbours in memory hold NaN."""
+    K = 5
+    buf = torch.full((K * D + 16,), NAN, dtype=dtype)
+    buf[shift: shift + K * D] = torch.randn(K * D, generator=torch.Generator().manual_seed(D)).to(dtype)
+    bd = buf.to(dev)
+    T = bd[shift: shift + K * D].view(K, D)
+    ids = torch.tensor([0, K - 1, 2, 0, K - 1, -1, K], dtype=torch.int32, device=dev)
+    w = torch.tensor([1.0, 2.0, 0.5, -1.0, 1.0, NAN, NAN], device=dev)
+    out = km.kmassign_lookup(T, ids, weights=w)
+    want = T[ids[:5].long()].float() * w[:5, None]
+    assert torch.equal(out[:5], want.to(dtype)) and (out[5:] == 0).all()
+
+
+def test_in_a_captured_graph(dev):
+    """The calls, their temporaries included, run from a captured graph with new inputs."""
+    N, E, k, D = 600, 64, 4, 48
+    g = torch.Generator().manual_seed(0)
+    X = torch.randn(N, E, generator=g).to(dev)
+    T = torch.randn(E, D, generator=g).to(torch.bfloat16).to(dev)
+    dY = torch.randn(N, D, generator=g).to(torch.bfloat16).to(dev)
+
+    def step():
+        idx, w = km.kmassign_route(X, k, score="sigmoid", groups=8, topk_groups=3)
+        Y = km.kmassign_lookup(T, idx, weights=w)
+        dT, dw = km.kmassign_lookup_grad(dY, idx, E, weights=w, table=T)
+        dX = km.kmassign_route_grad(X, idx, dw, score="sigmoid")
+        order, offsets = km.kmassign_lists(idx, E)
+        norm = km.kmassign_clip([dT, dX], 1.0)
+        return [idx, w, Y, dT, dw, dX, order, offsets, norm]
+    side = torch.cuda.Stream(dev)
+    with torch.cuda.stream(side):
+        step()                               # first calls set the device up
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        outs = step()
+    for seed in (1, 2):
+        X.copy_(torch.randn(N, E, generator=torch.Generator().manual_seed(seed)))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M", [3000, 100_000])
+def test_lists_and_gradient_with_very_many_rows(dev, M):
+    """30 million rows: three digits of a sort, most rows empty."""
+    K = 30_000_000
+    ids = np.random.default_rng(M).integers(0, K, M).astype(np.int32)
+    check_lists(dev, ids, K)
+    dout = torch.randint(-4, 5, (M, 1), generator=torch.Generator().manual_seed(1)).float()
+    dt, _ = km.kmassign_lookup_grad(dout.to(dev), torch.from_numpy(ids).to(dev), K)
+    want = np.zeros(K)
+    np.add.at(want, ids, f64(dout)[:, 0])
+    assert np.array_equal(f64(dt)[:, 0], want)
+
+
+def test_clip_more_than_2_31_elements(dev):
+    n = 2 ** 31 + 100_003
+    g = torch.full((n,), 0.5, dtype=torch.bfloat16, device=dev)
+    g[-1] = 3.0
+    norm = km.kmassign_clip([g], 100.0)
+    want = np.sqrt(0.25 * (n - 1) + 9.0)
+    assert abs(norm.item() - want) <= 40 * U * want
+    c = 100.0 / want
+    for i in (0, 2 ** 31 - 1, 2 ** 31, n - 2, n - 1):
+        ref = (3.0 if i == n - 1 else 0.5) * c
+        assert abs(g[i].item() - ref) <= (48 * U + 2.0 ** -8) * ref
+
+
+def test_sigmoid_weights_are_the_quotient_s_bits(dev):
+    """Weights of single experts over all magnitudes: 1 / (1 + exp(-x)), each step rounded once;
+    and the same bits where the selection forms its keys (a zero bias orders by the scores)."""
+    x = torch.cat([torch.linspace(-110, 110, 400_001), torch.randn(100_000) * 3]).to(dev)
+    idx, w = km.kmassign_route(x[:, None].contiguous(), 1, score="sigmoid", renorm=False)
+    t = torch.exp(-x)                      # CUDA's expf
+    want = (1.0 / (1.0 + t).double()).float()
+    assert torch.equal(w[:, 0], want)
+    # rows of 8 neighbours: descending scores, ties to the lower index
+    rows = x[: 400_000].view(-1, 8).contiguous()
+    idx, w = km.kmassign_route(rows, 8, score="sigmoid", bias=torch.zeros(8, device=dev), renorm=False)
+    s = want[: 400_000].view(-1, 8)
+    value, order = s.sort(dim=1, descending=True, stable=True)
+    assert torch.equal(idx.long(), order) and torch.equal(w, value)
