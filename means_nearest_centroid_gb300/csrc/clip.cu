@@ -8,6 +8,11 @@
 // fp64; where such a sum leaves the range in which fp32 squares are sound
 // (gradients beyond 1e15 or below 1e-15), its squares are taken again in fp64,
 // so the norm is right over the whole range of the types.
+//
+// Bound by HBM, which the data crosses three times (nothing can be written before
+// the last square is known, and little of a large model's gradients stays in
+// L2): 294 M fp32 elements take 540 us, 6.5 TB/s of those 3.5 GB; ten tensors of
+// 1.8 MB in all take 10 us, two launches' latency.
 #include "internal.h"
 #include "launch.cuh"
 #include "vec.cuh"

@@ -58,7 +58,8 @@ __device__ __forceinline__ bool lookup_place(const LookupArgs &a, int &row, int 
     return row < a.rows && vec < a.vecs;
 }
 
-// One id a point: a copy, U points a thread in flight.  Bound by HBM.
+// One id a point: a copy, U points a thread in flight.  Bound by HBM: 16,384
+// rows of 2,048 bf16 take 22.7 us, 5.9 TB/s (floor 20).
 template <typename T, int VE, int U>
 __global__ void __launch_bounds__(kThreads) lookup_one_kernel(const LookupArgs a)
 {
@@ -440,7 +441,13 @@ __device__ __forceinline__ void put(const GradArgs &a, int32_t r, int col, const
 
 // T: type of dout, G: of dtable.  DW (one slice): a place's weight's gradient is
 // formed on the way, from the row of the table that its group holds meanwhile;
-// the four sums of a batch are added over the lanes together.
+// the four sums of a batch are added over the lanes together.  For 30,011 points
+// of 8 ids, 250 columns of bf16 and 16,384 rows it takes 40 us: the gathered
+// rows come from L2 (131 MB), but 106 warp instructions each (rows at 4-byte
+// boundaries need four loads) keep the issue slots 60% busy at the 24 warps that
+// 80 registers allow; the two gathers in kernels of their own took 57 us.  Eight
+// rows in flight at 16 warps, or chunks for 16, 32 or 48 warps, were 1 to 10%
+// slower on six shapes.
 template <typename T, typename G, int VE, int LG, bool DW>
 __global__ void __launch_bounds__(kThreads, VE == 1 ? 2 : 3) segment_kernel(const GradArgs a)
 {
@@ -586,6 +593,7 @@ __global__ void __launch_bounds__(kThreads, VE == 1 ? 2 : 3) segment_kernel(cons
 
 // Rows that span chunks: the chunk in which such a row begins holds its first
 // part as its last row; the following chunks hold the others as their first.
+// 6 us after the sums above: the latency of four dependent loads.
 template <typename G, int VE, int LG>
 __global__ void __launch_bounds__(kThreads) join_kernel(const GradArgs a)
 {

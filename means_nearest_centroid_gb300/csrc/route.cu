@@ -63,8 +63,8 @@ __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-
 // 1 / y correctly rounded for 1 <= y <= 2^125: one Newton step with fused
 // multiply-adds from the hardware's approximation, which is within one ulp
 // (Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990; over all 2^23 significands
-// it gave the quotient's bits on GB300).
+// processor", 1990; on GB300 it gave the quotient's bits for all 2^23
+// significands).
 __device__ __forceinline__ float reciprocal(float y)
 {
     float r;
@@ -180,7 +180,11 @@ __device__ __forceinline__ void load_row(float (&x)[V], const T *row, int E, boo
 // the lanes' heads and advances the list of the lowest lane that holds it;
 // which expert a key belonged to is found once at the end, round j's by lane j,
 // from a copy of the keys in shared memory (equal keys of a lane leave it in
-// consecutive rounds: the how-manieth is counted).
+// consecutive rounds: the how-manieth is counted).  Measured for 65,536 rows of
+// 256 fp32 logits, k = 8, sigmoid, bias, 4 of 8 groups: 45.5 us, 1.6 TB/s (the
+// bytes' floor is 10.6 us): 676 warp instructions a row, issue slots 83% busy.
+// Rounds over unsorted keys took 94 us; two rows a warp (16 keys a lane) 43 us
+// here, but 12% more without bias and groups.
 template <typename T, int W, int V, bool SIGMOID, bool GROUPS>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs a)
 {
@@ -556,7 +560,9 @@ __device__ __forceinline__ void zero_span(T *p, int n, int lane)
 // Gradients on the selected experts only (sigmoid, renormalised softmax): a
 // warp zeroes 32 / KW rows with wide stores, which wait for nothing, and forms
 // the selected elements meanwhile, lane j of a row's KW lanes selection j;
-// they are written over the zeros behind a warp barrier.
+// they are written over the zeros behind a warp barrier.  65,536 x 256 fp32,
+// k = 8: 16.7 us; the 8 logits of a row lie in as many 64-byte DRAM accesses, so
+// with them 115 MB move, 6.9 TB/s.  One row a warp, zeroed after the reads: 22.7.
 template <typename T, int KW, bool SIGMOID>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_sparse_kernel(const RouteGradArgs a)
 {
@@ -598,7 +604,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_sparse_kernel(con
 }
 
 // The softmax over all experts: a gradient on each of them.  Lanes and experts
-// as in route_kernel; the row is read once.
+// as in route_kernel; the row is read once.  30,011 x 72 bf16, k = 6: 7.2 us, of
+// which the 10 MB are 1.5: the rest is the latency of a row read, reduced twice
+// and written, by 12 blocks an SM.
 template <typename T, int W, int V>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_dense_kernel(const RouteGradArgs a)
 {
