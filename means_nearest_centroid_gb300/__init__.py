@@ -413,6 +413,13 @@ def _need_shape(t, name, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _stream_of(stream, t) -> int:
+    """The cudaStream_t to launch on: ``stream``, else the current one of t's device."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return _stream_ptr(stream, t.device)
+
+
 def _score_code(score) -> int:
     code = _SCORES.get(score)
     if code is None:
@@ -470,8 +477,9 @@ def kmassign_route(logits, k: int, score: str = "softmax", bias=None, groups: in
     rc = library().kmassign_route(
         logits.data_ptr(), dtype, N, E, k, _score_code(score), _ptr(bias), groups,
         groups if topk_groups is None else int(topk_groups), int(group_top), int(bool(renorm)),
-        float(scale), idx.data_ptr(), weights.data_ptr(), _stream_ptr(stream, logits.device))
-    _check(rc, "kmassign_route")
+        float(scale), idx.data_ptr(), weights.data_ptr(), _stream_of(stream, logits))
+    if rc:
+        _check(rc, "kmassign_route")
     return idx, weights
 
 
@@ -498,8 +506,9 @@ def kmassign_route_grad(logits, idx, dweights, score: str = "softmax", renorm: b
     rc = library().kmassign_route_grad(
         logits.data_ptr(), dtype, N, E, k, _score_code(score), int(bool(renorm)), float(scale),
         idx.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(),
-        _stream_ptr(stream, logits.device))
-    _check(rc, "kmassign_route_grad")
+        _stream_of(stream, logits))
+    if rc:
+        _check(rc, "kmassign_route_grad")
     return dlogits
 
 
@@ -523,8 +532,9 @@ def kmassign_lists(idx, K: int, order=None, offsets=None, stream=None):
         _need_cuda(offsets, "offsets", torch.int32)
         _need_shape(offsets, "offsets", (K + 1,))
     rc = library().kmassign_lists(idx.data_ptr(), M, K, order.data_ptr(), offsets.data_ptr(),
-                                  _stream_ptr(stream, idx.device))
-    _check(rc, "kmassign_lists")
+                                  _stream_of(stream, idx))
+    if rc:
+        _check(rc, "kmassign_lists")
     return order, offsets
 
 
@@ -548,8 +558,9 @@ def kmassign_lookup(table, idx, weights=None, scale: float = 1.0, out=None, stre
         _need_shape(out, "out", (N, D))
     rc = library().kmassign_lookup(table.data_ptr(), dtype, K, D, idx.data_ptr(), _ptr(weights),
                                    N, k, float(scale), out.data_ptr(),
-                                   _stream_ptr(stream, table.device))
-    _check(rc, "kmassign_lookup")
+                                   _stream_of(stream, table))
+    if rc:
+        _check(rc, "kmassign_lookup")
     return out
 
 
@@ -596,8 +607,9 @@ def kmassign_lookup_grad(dout, idx, K: int, weights=None, table=None, scale: flo
         dout.data_ptr(), code, idx.data_ptr(), _ptr(weights),
         table.data_ptr() if weights is not None else None, N, k, K, D, float(scale), int(padding),
         int(bool(accumulate)), dtable.data_ptr(), grad, _ptr(dweights),
-        _stream_ptr(stream, dout.device))
-    _check(rc, "kmassign_lookup_grad")
+        _stream_of(stream, dout))
+    if rc:
+        _check(rc, "kmassign_lookup_grad")
     return dtable, dweights
 
 
@@ -634,8 +646,9 @@ def kmassign_grad_norm(tensors, norm=None, stream=None):
     norm = _norm_out(tensors, norm)
     rc = library().kmassign_grad_norm(_address(ptrs), _address(sizes), _address(codes),
                                       len(tensors), norm.data_ptr(),
-                                      _stream_ptr(stream, norm.device))
-    _check(rc, "kmassign_grad_norm")
+                                      _stream_of(stream, norm))
+    if rc:
+        _check(rc, "kmassign_grad_norm")
     return norm
 
 
@@ -661,8 +674,9 @@ def kmassign_clip(grads, max_norm: float, out=None, norm=None, stream=None):
     norm = _norm_out(grads, norm)
     rc = library().kmassign_clip(_address(ptrs), None if outs is None else _address(outs),
                                  _address(sizes), _address(codes), len(grads), float(max_norm),
-                                 norm.data_ptr(), _stream_ptr(stream, norm.device))
-    _check(rc, "kmassign_clip")
+                                 norm.data_ptr(), _stream_of(stream, norm))
+    if rc:
+        _check(rc, "kmassign_clip")
     return norm
 
 
