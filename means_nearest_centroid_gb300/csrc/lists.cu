@@ -17,13 +17,17 @@
 // start while the one before it ends.  2^20 ids of 4,096 rows take 32 us in five
 // launches, of which the ids' and lists' 8.4 MB are 1.3: every scatter block's
 // chain of loads, votes, scans and barriers (issue slots 47% busy) bounds it, not
-// memory.  Up to kOneBlockMax items are one launch of one block (512 ids of 256
-// rows: 3 us).  Nothing depends on timing: the result is unique.
+// memory.  Up to kClusterMax items are one launch of a cluster of eight blocks that
+// exchange counts and pairs through each other's shared memory, and up to
+// kOneBlockMax one of one block (512 ids of 256 rows: 3 us).  Nothing depends on
+// timing: the result is unique.
 //
 // offsets are found by a search in the sorted rows within the row's last digit,
 // eight ways at a step: a third of bisection's dependent loads.
 #include "internal.h"
 #include "launch.cuh"
+
+#include <cooperative_groups.h>
 
 #include <algorithm>
 
@@ -38,6 +42,11 @@ constexpr int kMaxBlocks = 304;           // two on each SM
 constexpr int64_t kOneBlockMax = 4096;
 constexpr int64_t kOneOffsetsMax = 8192;   // rows whose offsets the one block finds itself
 constexpr int kOneBits = 8;                // digit of the one-block sort
+constexpr int kClusterBlocks = 8;
+constexpr int kClusterThreads = 1024;
+constexpr int kClusterItems = 2;           // a thread
+constexpr int64_t kClusterMax = int64_t(kClusterBlocks) * kClusterThreads * kClusterItems;
+constexpr unsigned kClusterFill = 120;     // blocks besides: clusters that run at once with the first
 constexpr int kOneBins = 1 << kOneBits;
 
 // Exclusive scan over the block of one value per thread; *total: the sum.
@@ -444,6 +453,144 @@ __global__ void __launch_bounds__(THREADS)
     }
 }
 
+// ---- up to kClusterMax items: one cluster ------------------------------------
+
+struct ClusterArgs {
+    const int32_t *idx;
+    int32_t *order;
+    int32_t *rows;       // or nullptr
+    int32_t *offsets;    // of a one-digit sort, else nullptr
+    int32_t *starts;     // of the last of several digits, else nullptr
+    int32_t *total;
+    int32_t M, K;
+    int32_t passes;
+    int32_t bits[4], shift[4];
+    Fill fill;
+};
+
+// Shared memory of a block: its share of the pairs, the warps' counts, and the
+// digits' counts and places.
+constexpr int kClusterSmem = kClusterThreads * kClusterItems * 8 +
+                             (kClusterThreads / 32) * (2 << kMaxDigitBits) + (8 << kMaxDigitBits);
+
+// Block b owns the places [b share, (b + 1) share) of every pass; a thread holds
+// two of its block's pairs in registers while they are placed.  Two cluster
+// barriers a digit: after the first the blocks read each other's counts (and all
+// have read their pairs), after the second the pairs are in their places.
+// Clusters after the first fill.  16,384 ids of 131,072 rows take 15 us (with the
+// search for the offsets) where the launches of the larger sorts took 22 to 24;
+// with four pairs a thread 30,000 ids of 16,384 rows took 19 for 22, but the
+// gradients that zero a table besides got 3 us slower.
+__global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kClusterThreads)
+    lists_cluster_kernel(const ClusterArgs a)
+{
+    namespace cg = cooperative_groups;
+    constexpr int kW = kClusterThreads / 32;
+    constexpr int ITEMS = kClusterItems;
+    constexpr int kShare = kClusterThreads * ITEMS;
+    constexpr int kBins = 1 << kMaxDigitBits;
+    extern __shared__ __align__(16) uint8_t cluster_smem[];
+    int2 *pairs = reinterpret_cast<int2 *>(cluster_smem);                        // [kShare] row, position
+    uint16_t *counts = reinterpret_cast<uint16_t *>(pairs + kShare);     // [kW][bins]
+    int32_t *hist = reinterpret_cast<int32_t *>(counts + kW * kBins);    // [bins] of this block
+    int32_t *place = hist + kBins;                                       // [bins]
+    __shared__ int32_t warp_sums[kW + 1];
+    let_next_start();
+    wait_for_previous();
+    if (blockIdx.x >= kClusterBlocks) {
+        fill_zero(a.fill, blockIdx.x - kClusterBlocks, gridDim.x - kClusterBlocks);
+        return;
+    }
+    cg::cluster_group cluster = cg::this_cluster();
+    const int block = static_cast<int>(blockIdx.x);
+    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
+    int2 item[ITEMS];
+    int32_t rank[ITEMS];
+    int n = a.M;   // pairs of this pass
+    for (int pass = 0; pass < a.passes; ++pass) {
+        const int bits = a.bits[pass], shift = a.shift[pass], bins = 1 << bits;
+        for (int c = threadIdx.x; c < kW * bins / 2; c += kClusterThreads)
+            reinterpret_cast<uint32_t *>(counts)[c] = 0;
+        const int mine = min(kShare, max(0, n - block * kShare));
+#pragma unroll
+        for (int u = 0; u < ITEMS; ++u) {
+            const int i = warp * (32 * ITEMS) + u * 32 + lane;
+            item[u] = make_int2(-1, block * kShare + i);
+            if (i < mine) {
+                if (pass > 0) {
+                    item[u] = pairs[i];
+                } else {
+                    const int32_t r = __ldg(a.idx + block * kShare + i);
+                    if (r >= 0 && r < a.K)
+                        item[u].x = r;
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < ITEMS; ++u)
+            rank[u] = warp_rank(item[u].x < 0 ? -1 : (item[u].x >> shift) & (bins - 1), bits,
+                                counts + warp * bins, lane);
+        __syncthreads();
+        const int d = threadIdx.x;   // a digit a thread
+        if (d < bins) {
+            int32_t run = 0;
+#pragma unroll
+            for (int w = 0; w < kW; ++w) {
+                const uint16_t c = counts[w * bins + d];
+                counts[w * bins + d] = static_cast<uint16_t>(run);
+                run += c;
+            }
+            hist[d] = run;
+        }
+        cluster.sync();
+        int32_t all = 0, before = 0;
+        if (d < bins)
+#pragma unroll
+            for (int b = 0; b < kClusterBlocks; ++b) {
+                const int32_t c = cluster.map_shared_rank(hist, b)[d];
+                all += c;
+                before += b < block ? c : 0;
+            }
+        const int32_t first = block_scan<kW>(all, warp_sums, &n);
+        if (d < bins) {
+            place[d] = first + before;
+            if (block == 0 && a.offsets != nullptr && d < a.K)
+                a.offsets[d] = first;
+            if (block == 0 && a.starts != nullptr && pass == a.passes - 1)
+                a.starts[d] = first;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < ITEMS; ++u)
+            if (item[u].x >= 0) {
+                const int32_t e = (item[u].x >> shift) & (bins - 1);
+                const int to = place[e] + counts[warp * bins + e] + rank[u];
+                cluster.map_shared_rank(pairs, to / kShare)[to % kShare] = item[u];
+            }
+        cluster.sync();
+    }
+    if (block == 0 && threadIdx.x == 0) {
+        *a.total = n;
+        if (a.offsets != nullptr)
+            a.offsets[a.K] = n;
+        if (a.starts != nullptr)
+            a.starts[1 << a.bits[a.passes - 1]] = n;
+    }
+    for (int i = threadIdx.x; i < kShare; i += kClusterThreads) {
+        const int p = block * kShare + i;
+        if (p < n) {
+            const int2 rp = pairs[i];
+            a.order[p] = rp.y;
+            if (a.rows != nullptr)
+                a.rows[p] = rp.x;
+        } else if (p < a.M) {
+            a.order[p] = -1;
+        }
+    }
+}
+
 // offsets[r] for r in [0, K]: the number of sorted rows below r.  starts: where
 // the rows with each value of r >> shift start (nullptr: only their number,
 // *total).
@@ -487,7 +634,7 @@ __global__ void __launch_bounds__(128)
 
 struct SortPlan {
     int passes;
-    int bits[4], shift[4];
+    int32_t bits[4], shift[4];
     int items;      // per thread and tile: 2, 4 or 8
     int blocks;
     int64_t share;
@@ -501,17 +648,24 @@ int row_bits(int64_t K)
     return bits;
 }
 
+// The digits of a row id, as many bits each as evenly as they divide.
+int digits(int64_t K, int most, int32_t *bits, int32_t *shift)
+{
+    const int all = row_bits(K);
+    const int passes = std::max(1, (all + most - 1) / most);
+    int at = 0;
+    for (int i = 0; i < passes; ++i) {
+        bits[i] = (all - at + (passes - i) - 1) / (passes - i);
+        shift[i] = at;
+        at += bits[i];
+    }
+    return passes;
+}
+
 SortPlan sort_plan(int64_t M, int64_t K)
 {
     SortPlan p{};
-    const int bits = row_bits(K);
-    p.passes = std::max(1, (bits + kMaxDigitBits - 1) / kMaxDigitBits);
-    int at = 0;
-    for (int i = 0; i < p.passes; ++i) {
-        p.bits[i] = (bits - at + (p.passes - i) - 1) / (p.passes - i);
-        p.shift[i] = at;
-        at += p.bits[i];
-    }
+    p.passes = digits(K, kMaxDigitBits, p.bits, p.shift);
     // the smallest tiles of which every block has one, else large ones in turn
     p.items = 8;
     for (int items = 4; items >= 2; items >>= 1)
@@ -582,13 +736,16 @@ cudaError_t lists_prepare()
         if (e != cudaSuccess)
             return e;
     }
-    return cudaSuccess;
+    return cudaFuncSetAttribute(lists_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kClusterSmem);
 }
 
 size_t lists_scratch_bytes(int64_t M, int64_t K)
 {
     if (M <= kOneBlockMax)
         return K <= kOneOffsetsMax ? 0 : 16 + static_cast<size_t>(M) * 4;
+    if (M <= kClusterMax)   // total, the last digit's starts, the sorted rows
+        return 16 + up16((size_t(4) << kMaxDigitBits) + 4) + up16(static_cast<size_t>(M) * 4);
     const SortPlan p = sort_plan(M, K);
     // total, the digits' counts, two sets of pairs (the second set's rows may
     // stand in for the sorted rows)
@@ -623,6 +780,35 @@ cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *orde
                              own ? offsets : nullptr, total, fill);
         if (e == cudaSuccess && !own)
             e = launch_offsets(rows, total, nullptr, 0, K, offsets, stream);
+        return e;
+    }
+    if (M <= kClusterMax) {
+        ClusterArgs a{};
+        a.passes = digits(K, kMaxDigitBits, a.bits, a.shift);
+        a.idx = idx;
+        a.order = order;
+        uint8_t *at = static_cast<uint8_t *>(scratch);
+        a.total = reinterpret_cast<int32_t *>(at);
+        if (a.passes == 1) {
+            a.offsets = offsets;
+            a.rows = rows;
+        } else {
+            a.starts = reinterpret_cast<int32_t *>(at + 16);
+            a.rows = rows != nullptr
+                         ? rows
+                         : reinterpret_cast<int32_t *>(at + 16 + up16((size_t(4) << kMaxDigitBits) + 4));
+        }
+        a.M = static_cast<int32_t>(M);
+        a.K = static_cast<int32_t>(K);
+        fill.parts = fill_parts(zero_bytes, 1);
+        a.fill = fill;
+        const unsigned blocks =
+            kClusterBlocks +
+            (std::min(fill_blocks(fill, kClusterThreads), kClusterFill) + kClusterBlocks - 1) /
+                kClusterBlocks * kClusterBlocks;
+        e = launch_after(lists_cluster_kernel, blocks, kClusterThreads, kClusterSmem, stream, a);
+        if (e == cudaSuccess && a.passes > 1)
+            e = launch_offsets(a.rows, a.total, a.starts, a.shift[a.passes - 1], K, offsets, stream);
         return e;
     }
     const SortPlan p = sort_plan(M, K);

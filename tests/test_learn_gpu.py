@@ -804,3 +804,28 @@ def test_sigmoid_weights_are_the_quotient_s_bits(dev):
     s = want[: 400_000].view(-1, 8)
     value, order = s.sort(dim=1, descending=True, stable=True)
     assert torch.equal(idx.long(), order) and torch.equal(w, value)
+
+
+@pytest.mark.parametrize("M", [4097, 5000, 8191, 12_288, 16_383, 16_384, 16_385])
+@pytest.mark.parametrize("K", [1, 2, 700, 1024, 1025, 200_000, 3_000_000])
+def test_lists_around_the_cluster_s_sizes(dev, M, K):
+    """Up to 16,384 ids one cluster sorts; shares of its blocks that end early, ids left out."""
+    g = np.random.default_rng(M * 7 + K)
+    check_lists(dev, np.where(g.random(M) < 0.3, K // 2, g.integers(-1, K + 1, M)).astype(np.int32), K)
+    check_lists(dev, np.where(g.random(M) < 0.999, -1, g.integers(0, K, M)).astype(np.int32), K)
+
+
+@pytest.mark.parametrize("N,K,D", [(5000, 20_000, 33), (16_384, 9000, 130), (16_385, 9000, 130), (4097, 60_001, 7)])
+def test_lookup_grad_zeroes_the_whole_table(dev, N, K, D):
+    """The zeros that the sort writes besides reach every element, whatever the table's ends."""
+    for kind in (torch.float32, torch.bfloat16):
+        for shift in (0, 1, 3):
+            buf = torch.full((K * D + 8,), 7.0, dtype=kind, device=dev)
+            out = buf[shift: shift + K * D].view(K, D)
+            ids = torch.full((N,), K // 3, dtype=torch.int32, device=dev)
+            dout = torch.ones(N, D, dtype=torch.bfloat16, device=dev)
+            km.kmassign_lookup_grad(dout, ids, K, dtable=out)
+            want = float(torch.tensor(float(N)).to(kind))
+            assert (out[K // 3] == want).all()
+            assert (out[: K // 3] == 0).all() and (out[K // 3 + 1:] == 0).all()
+            assert (buf[:shift] == 7).all() and (buf[shift + K * D:] == 7).all()
