@@ -39,7 +39,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxDigitBits = 10;
 constexpr int kMaxBlocks = 304;           // two on each SM
-constexpr int64_t kOneBlockMax = 4096;
+constexpr int64_t kOneBlockMax = 2048;     // 3,000 ids: 14.5 us a call by one block, 12.2 by eight; 1,100: 14.1, 15.7
 constexpr int64_t kOneOffsetsMax = 8192;   // rows whose offsets the one block finds itself
 constexpr int kOneBits = 8;                // digit of the one-block sort
 constexpr int kClusterBlocks = 8;
@@ -769,13 +769,12 @@ cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *orde
         if (!own && rows == nullptr)
             rows = total + 4;
         fill.parts = fill_parts(zero_bytes, 1);
-        // one warp for every 128 items, at least eight
         if (M <= 1024)
             e = launch_after(lists_one_block_kernel<256, 4>, 1 + fill_blocks(fill, 256), 256, 0,
                              stream, idx, M, K, row_bits(K), order, rows,
                              own ? offsets : nullptr, total, fill);
         else
-            e = launch_after(lists_one_block_kernel<1024, 4>, 1 + fill_blocks(fill, 1024), 1024, 0,
+            e = launch_after(lists_one_block_kernel<1024, 2>, 1 + fill_blocks(fill, 1024), 1024, 0,
                              stream, idx, M, K, row_bits(K), order, rows,
                              own ? offsets : nullptr, total, fill);
         if (e == cudaSuccess && !own)

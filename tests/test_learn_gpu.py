@@ -806,7 +806,7 @@ def test_sigmoid_weights_are_the_quotient_s_bits(dev):
     assert torch.equal(idx.long(), order) and torch.equal(w, value)
 
 
-@pytest.mark.parametrize("M", [4097, 5000, 8191, 12_288, 16_383, 16_384, 16_385])
+@pytest.mark.parametrize("M", [2047, 2048, 2049, 4097, 5000, 8191, 12_288, 16_383, 16_384, 16_385])
 @pytest.mark.parametrize("K", [1, 2, 700, 1024, 1025, 200_000, 3_000_000])
 def test_lists_around_the_cluster_s_sizes(dev, M, K):
     """Up to 16,384 ids one cluster sorts; shares of its blocks that end early, ids left out."""
