@@ -169,13 +169,13 @@ cudaError_t launch_route_grad(const void *logits, int dtype, int64_t N, int64_t 
 // Shared-memory attributes of the sort's kernels, once per device.
 cudaError_t lists_prepare();
 // The stable sort of the positions [0, M) by row: order, the sorted rows (may
-// be NULL) and offsets[K + 1]; scratch (16-byte aligned) of
-// lists_scratch_bytes.  Places past offsets[K] hold -1 in order and nothing
+// be NULL), offsets[K + 1] and the number of valid ids, total (either may be
+// NULL, not both); scratch (16-byte aligned) of lists_scratch_bytes.  Places past offsets[K] hold -1 in order and nothing
 // in particular in rows.  zero_bytes (even) at zero are zeroed besides.
 size_t lists_scratch_bytes(int64_t M, int64_t K);
 cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *order, int32_t *rows,
-                         int32_t *offsets, void *scratch, void *zero, size_t zero_bytes,
-                         cudaStream_t stream);
+                         int32_t *offsets, int32_t *total, void *scratch, void *zero,
+                         size_t zero_bytes, cudaStream_t stream);
 cudaError_t launch_lookup(const void *table, int dtype, int64_t K, int64_t D, const int32_t *idx,
                           const float *weights, int64_t N, int32_t k, float scale, void *out,
                           int sms, cudaStream_t stream);
@@ -188,7 +188,7 @@ size_t lookup_grad_parts_bytes(int64_t M, int64_t D, int sms);
 cudaError_t launch_lookup_grad(const void *dout, int dtype, const int32_t *idx,
                                const float *weights, const void *table, int64_t M, int32_t k,
                                int64_t K, int64_t D, float scale, int32_t skip, bool accumulate,
-                               const int32_t *order, const int32_t *rows, const int32_t *offsets,
+                               const int32_t *order, const int32_t *rows, const int32_t *total,
                                float *parts, void *dtable, int grad_dtype, float *dweights,
                                int sms, cudaStream_t stream);
 // Whether launch_lookup_grad can form dweights (else NULL there, and

@@ -215,7 +215,7 @@ int kmassign_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *order, int
     Scratch scratch(kma::lists_scratch_bytes(M, K), pool, s);
     if (!scratch.ok())
         return KMASSIGN_ERR_CUDA;
-    rc = done(kma::launch_lists(idx, M, K, order, nullptr, offsets, scratch.get(), nullptr, 0, s));
+    rc = done(kma::launch_lists(idx, M, K, order, nullptr, offsets, nullptr, scratch.get(), nullptr, 0, s));
     return scratch.release() ? rc : KMASSIGN_ERR_CUDA;
 }
 
@@ -281,28 +281,25 @@ int kmassign_lookup_grad(const void *dout, int32_t dtype, const int32_t *idx, co
         return KMASSIGN_ERR_CUDA;
     if (dtable == nullptr || (N == 0 && accumulate))
         return KMASSIGN_OK;
-    // one allocation: order, sorted rows, offsets, the sort's scratch, row parts
+    // one allocation: order, sorted rows, their number, the sort's scratch, row parts
     const size_t ids = up16(static_cast<size_t>(M) * 4);
-    const size_t offs = up16(static_cast<size_t>(K + 1) * 4);
     const size_t sort = up16(kma::lists_scratch_bytes(M, K));
-    const size_t parts = kma::lookup_grad_parts_bytes(M, D, sms);
-    Scratch scratch(2 * ids + offs + sort + parts, pool, s);
+    Scratch scratch(2 * ids + 16 + sort + kma::lookup_grad_parts_bytes(M, D, sms), pool, s);
     if (!scratch.ok())
         return KMASSIGN_ERR_CUDA;
     uint8_t *p = scratch.get();
     int32_t *order = reinterpret_cast<int32_t *>(p);
     int32_t *rows = reinterpret_cast<int32_t *>(p + ids);
-    int32_t *offsets = reinterpret_cast<int32_t *>(p + 2 * ids);
-    cudaError_t e =
-        kma::launch_lists(idx, M, K, order, rows, offsets, p + 2 * ids + offs,
-                          accumulate ? nullptr : dtable,
-                          accumulate ? 0 : static_cast<size_t>(K) * D * kma::dtype_bytes(grad_dtype),
-                          s);
+    int32_t *total = reinterpret_cast<int32_t *>(p + 2 * ids);
+    p += 2 * ids + 16;
+    cudaError_t e = kma::launch_lists(
+        idx, M, K, order, rows, nullptr, total, p, accumulate ? nullptr : dtable,
+        accumulate ? 0 : static_cast<size_t>(K) * D * kma::dtype_bytes(grad_dtype), s);
     if (e == cudaSuccess && M > 0)
         e = kma::launch_lookup_grad(dout, dtype, idx, weights, table, M, k, K, D, scale, padding,
-                                    accumulate != 0, order, rows, offsets,
-                                    reinterpret_cast<float *>(p + 2 * ids + offs + sort), dtable,
-                                    grad_dtype, both ? dweights : nullptr, sms, s);
+                                    accumulate != 0, order, rows, total,
+                                    reinterpret_cast<float *>(p + sort), dtable, grad_dtype,
+                                    both ? dweights : nullptr, sms, s);
     rc = done(e);
     return scratch.release() ? rc : KMASSIGN_ERR_CUDA;
 }

@@ -758,26 +758,28 @@ size_t lists_scratch_bytes(int64_t M, int64_t K)
 }
 
 cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *order, int32_t *rows,
-                         int32_t *offsets, void *scratch, void *zero, size_t zero_bytes,
-                         cudaStream_t stream)
+                         int32_t *offsets, int32_t *total, void *scratch, void *zero,
+                         size_t zero_bytes, cudaStream_t stream)
 {
     cudaError_t e = cudaSuccess;
     Fill fill{static_cast<uint8_t *>(zero), static_cast<int64_t>(zero_bytes), 0, 1};
     if (M <= kOneBlockMax) {
-        const bool own = K <= kOneOffsetsMax;
-        int32_t *total = own ? nullptr : static_cast<int32_t *>(scratch);
-        if (!own && rows == nullptr)
-            rows = total + 4;
+        const bool search = offsets != nullptr && K > kOneOffsetsMax;   // in a launch of its own
+        int32_t *own = search ? nullptr : offsets;
+        if (search && total == nullptr)
+            total = static_cast<int32_t *>(scratch);
+        if (search && rows == nullptr)
+            rows = static_cast<int32_t *>(scratch) + 4;
         fill.parts = fill_parts(zero_bytes, 1);
         if (M <= 1024)
             e = launch_after(lists_one_block_kernel<256, 4>, 1 + fill_blocks(fill, 256), 256, 0,
                              stream, idx, M, K, row_bits(K), order, rows,
-                             own ? offsets : nullptr, total, fill);
+                             own, total, fill);
         else
             e = launch_after(lists_one_block_kernel<1024, 2>, 1 + fill_blocks(fill, 1024), 1024, 0,
                              stream, idx, M, K, row_bits(K), order, rows,
-                             own ? offsets : nullptr, total, fill);
-        if (e == cudaSuccess && !own)
+                             own, total, fill);
+        if (e == cudaSuccess && search)
             e = launch_offsets(rows, total, nullptr, 0, K, offsets, stream);
         return e;
     }
@@ -787,8 +789,8 @@ cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *orde
         a.idx = idx;
         a.order = order;
         uint8_t *at = static_cast<uint8_t *>(scratch);
-        a.total = reinterpret_cast<int32_t *>(at);
-        if (a.passes == 1) {
+        a.total = total != nullptr ? total : reinterpret_cast<int32_t *>(at);
+        if (a.passes == 1 || offsets == nullptr) {
             a.offsets = offsets;
             a.rows = rows;
         } else {
@@ -806,14 +808,15 @@ cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *orde
             (std::min(fill_blocks(fill, kClusterThreads), kClusterFill) + kClusterBlocks - 1) /
                 kClusterBlocks * kClusterBlocks;
         e = launch_after(lists_cluster_kernel, blocks, kClusterThreads, kClusterSmem, stream, a);
-        if (e == cudaSuccess && a.passes > 1)
+        if (e == cudaSuccess && a.starts != nullptr)
             e = launch_offsets(a.rows, a.total, a.starts, a.shift[a.passes - 1], K, offsets, stream);
         return e;
     }
     const SortPlan p = sort_plan(M, K);
     const size_t ids = up16(static_cast<size_t>(M) * 4);
     uint8_t *at = static_cast<uint8_t *>(scratch);
-    int32_t *total = reinterpret_cast<int32_t *>(at);
+    if (total == nullptr)
+        total = reinterpret_cast<int32_t *>(at);
     at += 16;
     int32_t *hist[4] = {};
     for (int i = 0; i < p.passes; ++i) {
@@ -823,7 +826,7 @@ cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *orde
     int32_t *starts = reinterpret_cast<int32_t *>(at);
     at += up16((size_t(4) << p.bits[p.passes - 1]) + 4);
     int32_t *sorted = rows;
-    if (sorted == nullptr && p.passes > 1)
+    if (sorted == nullptr && p.passes > 1 && offsets != nullptr)
         sorted = reinterpret_cast<int32_t *>(at);   // searched for the offsets
     at += ids;
     int32_t *set[2][2] = {};   // rows, positions
@@ -854,7 +857,7 @@ cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *orde
         a.blocks = p.blocks;
         e = i == 0 ? sort_pass<true>(a, p.items, stream) : sort_pass<false>(a, p.items, stream);
     }
-    if (e == cudaSuccess && p.passes > 1)
+    if (e == cudaSuccess && p.passes > 1 && offsets != nullptr)
         e = launch_offsets(sorted, total, starts, p.shift[p.passes - 1], K, offsets, stream);
     return e;
 }

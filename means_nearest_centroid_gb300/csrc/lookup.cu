@@ -402,7 +402,7 @@ struct GradArgs {
     float *dweights;           // formed on the way, or nullptr
     const int32_t *order;      // sorted places -> flat (point, id) positions
     const int32_t *rows;       // the rows in sorted order
-    const int32_t *offsets;    // [K + 1]
+    const int32_t *total;      // sorted places
     void *dtable;
     float *parts;              // [2][chunks][D]: a chunk's first and last row, unfinished
     int64_t M;                 // ids
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, VE == 1 ? 2 : 3) segment_kernel(cons
         static_cast<int64_t>(blockIdx.x) * (kThreads / LG) + threadIdx.x / LG;
     const int64_t chunk = unit / a.slices;
     const int slice = static_cast<int>(unit - chunk * a.slices);
-    const int64_t total = a.offsets[a.K];
+    const int64_t total = *a.total;
     const int64_t begin = chunk * a.chunk;
     const bool live = chunk < a.chunks && begin < total;   // else: no place of its own
     const int64_t end = live ? min(total, begin + a.chunk) : begin;
@@ -604,15 +604,25 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const GradArgs a)
         static_cast<int64_t>(blockIdx.x) * (kThreads / LG) + threadIdx.x / LG;
     const int64_t chunk = unit / a.slices;
     const int slice = static_cast<int>(unit - chunk * a.slices);
-    const int64_t total = a.offsets[a.K];
+    const int64_t total = *a.total;
     const int64_t begin = chunk * a.chunk;
     const int64_t end = begin + a.chunk;
     if (chunk >= a.chunks || end >= total)
         return;
     const int32_t r = a.rows[end - 1];
-    if (a.rows[end] != r || a.offsets[r] < begin)
+    if (a.rows[end] != r || (begin > 0 && a.rows[begin] == r && a.rows[begin - 1] == r))
         return;   // ends here, or began in an earlier chunk
-    const int64_t last = (static_cast<int64_t>(a.offsets[r + 1]) - 1) / a.chunk;
+    // the last chunk that begins with the row: its lanes look at as many chunks at a time
+    const uint32_t group = LG == 32 ? kAll : ((1u << LG) - 1u) << (threadIdx.x & (32 - LG));
+    int64_t last = chunk + 1;
+    for (;;) {
+        const int64_t c = last + 1 + lane;
+        const bool on = c < a.chunks && c * a.chunk < total && a.rows[c * a.chunk] == r;
+        const int ahead = __popc(__ballot_sync(group, on) & group);
+        last += ahead;   // the rows are sorted: those that are on come first
+        if (ahead < LG)
+            break;
+    }
 #pragma unroll 1
     for (int v = 0; v < C::kVectors; ++v) {
         const int col = C::at(slice, lane, v);
@@ -856,7 +866,7 @@ bool dweights_with_dtable(int64_t D) { return column_slices(D) == 1; }
 cudaError_t launch_lookup_grad(const void *dout, int dtype, const int32_t *idx,
                                const float *weights, const void *table, int64_t M, int32_t k,
                                int64_t K, int64_t D, float scale, int32_t skip, bool accumulate,
-                               const int32_t *order, const int32_t *rows, const int32_t *offsets,
+                               const int32_t *order, const int32_t *rows, const int32_t *total,
                                float *parts, void *dtable, int grad_dtype, float *dweights,
                                int sms, cudaStream_t stream)
 {
@@ -873,7 +883,7 @@ cudaError_t launch_lookup_grad(const void *dout, int dtype, const int32_t *idx,
     a.dweights = dweights;
     a.order = order;
     a.rows = rows;
-    a.offsets = offsets;
+    a.total = total;
     a.dtable = dtable;
     a.parts = parts;
     a.M = M;
