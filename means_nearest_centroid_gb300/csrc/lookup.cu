@@ -177,6 +177,19 @@ struct Columns {
     {
         return slice * kSlice + v * LG * VE + lane * VE;
     }
+    // A lane's vectors of a row, from its first one on (fixed distances, so that a row costs
+    // one address); zeros past D, or where the row is not there.
+    template <typename T>
+    __device__ static __forceinline__ void read(Raw<T, VE> (&q)[kVectors], const T *first,
+                                                const bool (&in)[kVectors], bool there)
+    {
+#pragma unroll
+        for (int v = 0; v < kVectors; ++v) {
+            q[v] = Raw<T, VE>{};
+            if (there && in[v])
+                q[v] = load_raw<T, VE>(first + v * LG * VE);
+        }
+    }
 };
 
 // ---- lookup of several ids --------------------------------------------------
@@ -209,11 +222,12 @@ __global__ void __launch_bounds__(kThreads) lookup_many_kernel(const GatherArgs 
     const int64_t i = live ? unit / a.slices : a.N - 1;
     const int slice = live ? static_cast<int>(unit - i * a.slices) : 0;
     const T *table = static_cast<const T *>(a.table);
-    int col[NV];   // past D: column 0, whose sums are not kept
+    const int col = C::at(slice, lane, 0);
+    bool in[NV];
     Sums<VE> acc[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        col[v] = C::at(slice, lane, v) < a.D ? C::at(slice, lane, v) : 0;
+        in[v] = C::at(slice, lane, v) < a.D;
         acc[v].zero();
     }
     for (int32_t j0 = 0; j0 < a.k; j0 += 8) {
@@ -235,13 +249,7 @@ __global__ void __launch_bounds__(kThreads) lookup_many_kernel(const GatherArgs 
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int32_t ru = __shfl_sync(kAll, r, u0 + u, LG);
-                const T *row = table + static_cast<int64_t>(ru) * a.D;
-#pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    q[u][v] = Raw<T, VE>{};
-                    if (ru >= 0)
-                        q[u][v] = load_raw<T, VE>(row + col[v]);
-                }
+                C::template read<T>(q[u], table + static_cast<int64_t>(ru) * a.D + col, in, ru >= 0);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -252,16 +260,16 @@ __global__ void __launch_bounds__(kThreads) lookup_many_kernel(const GatherArgs 
             }
         }
     }
-    T *out = static_cast<T *>(a.out) + i * a.D;
+    T *out = static_cast<T *>(a.out) + i * a.D + col;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
-        if (live && C::at(slice, lane, v) < a.D) {
+        if (live && in[v]) {
             float f[VE];
             acc[v].get(f);
 #pragma unroll
             for (int e = 0; e < VE; ++e)
                 f[e] *= a.scale;
-            store_raw<T, VE>(out + col[v], narrow<T, VE>(f));
+            store_raw<T, VE>(out + v * LG * VE, narrow<T, VE>(f));
         }
 }
 
@@ -334,22 +342,24 @@ __global__ void __launch_bounds__(kThreads, 2) dweights_kernel(const DweightsArg
             i += groups;
         }
         next = read(i, j0);
-        const bool all = __all_sync(kAll, ids >= 0);
         const T *dout = static_cast<const T *>(a.dout) + (at < a.N ? at : 0) * a.D;
         Sums<2> two[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u)
             two[u].zero();
         for (int s = 0; s < slices; ++s) {
-            int col[NV];
-            Sums<VE> p[NV];   // 0 past D, where column 0 is read instead
+            const int col = C::at(s, lane, 0);
+            bool in[NV];
+            Sums<VE> p[NV];
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                in[v] = C::at(s, lane, v) < a.D;
+            Raw<T, VE> d[NV];
+            C::template read<T>(d, dout + col, in, true);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const bool in = C::at(s, lane, v) < a.D;
-                col[v] = in ? C::at(s, lane, v) : 0;
-                float f[VE] = {};
-                if (in)
-                    widen<T, VE>(load_raw<T, VE>(dout + col[v]), f);
+                float f[VE];
+                widen<T, VE>(d[v], f);
                 p[v].set(f);
             }
 #pragma unroll
@@ -358,23 +368,14 @@ __global__ void __launch_bounds__(kThreads, 2) dweights_kernel(const DweightsArg
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int32_t r = __shfl_sync(kAll, ids, u0 + u, LG);
-                    const T *row = table + static_cast<int64_t>(r) * a.D;
-                    if (all || r >= 0) {
-#pragma unroll
-                        for (int v = 0; v < NV; ++v)
-                            q[u][v] = load_raw<T, VE>(row + col[v]);
-                    } else {
-#pragma unroll
-                        for (int v = 0; v < NV; ++v)
-                            q[u][v] = Raw<T, VE>{};
-                    }
+                    C::template read<T>(q[u], table + static_cast<int64_t>(r) * a.D + col, in,
+                                        r >= 0);
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int v = 0; v < NV; ++v)
-                        if (C::at(s, lane, v) < a.D)
-                            dot_raw<T, VE>(two[u0 + u], p[v], q[u][v]);
+                        dot_raw<T, VE>(two[u0 + u], p[v], q[u][v]);
             }
         }
         float sum[8];
@@ -478,25 +479,28 @@ __global__ void __launch_bounds__(kThreads, VE == 1 ? 2 : 3) segment_kernel(cons
     const bool from_before = live && begin > 0 && a.rows[begin - 1] == a.rows[begin];
     const bool goes_on = live && end < total && a.rows[end - 1] == a.rows[end];
 
-    int col[NV];   // past D: column 0, whose sums are not kept
+    const int col = C::at(slice, lane, 0);
+    bool in[NV];
     Sums<VE> acc[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        col[v] = C::at(slice, lane, v) < a.D ? C::at(slice, lane, v) : 0;
+        in[v] = C::at(slice, lane, v) < a.D;
         acc[v].zero();
     }
     int32_t cur = live ? a.rows[begin] : -1;
     bool first = true;   // cur is the row at `begin`
     Sums<VE> t_row[DW ? NV : 1];   // the table's row cur, 0 past D
     auto read_row = [&]() {
+        if constexpr (DW) {
+            Raw<T, VE> t[NV];
+            C::template read<T>(
+                t, static_cast<const T *>(a.table) + static_cast<int64_t>(cur) * a.D + col, in, true);
 #pragma unroll
-        for (int v = 0; v < (DW ? NV : 0); ++v) {
-            float f[VE] = {};
-            if (C::at(slice, lane, v) < a.D)
-                widen<T, VE>(load_raw<T, VE>(static_cast<const T *>(a.table) +
-                                             static_cast<int64_t>(cur) * a.D + col[v]),
-                             f);
-            t_row[v].set(f);
+            for (int v = 0; v < NV; ++v) {
+                float f[VE];
+                widen<T, VE>(t[v], f);
+                t_row[v].set(f);
+            }
         }
     };
     if (DW && live)
@@ -507,12 +511,13 @@ __global__ void __launch_bounds__(kThreads, VE == 1 ? 2 : 3) segment_kernel(cons
         for (int v = 0; v < NV; ++v) {
             float f[VE];
             acc[v].get(f);
-            if (C::at(slice, lane, v) < a.D) {
+            if (in[v]) {
                 if (which < 0)
-                    put<G, VE>(a, cur, col[v], f);
+                    put<G, VE>(a, cur, col + v * LG * VE, f);
                 else
-                    store_raw<float, VE>(a.parts + (which * a.chunks + chunk) * a.D + col[v],
-                                         narrow<float, VE>(f));
+                    store_raw<float, VE>(
+                        a.parts + (which * a.chunks + chunk) * a.D + col + v * LG * VE,
+                        narrow<float, VE>(f));
             }
         }
     };
@@ -536,16 +541,9 @@ __global__ void __launch_bounds__(kThreads, VE == 1 ? 2 : 3) segment_kernel(cons
             Raw<T, VE> q[U][NV];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const T *p = dout + static_cast<int64_t>(__shfl_sync(kAll, point, u0 + u, LG)) * a.D;
-                if (whole || begin + s0 + u0 + u < end) {
-#pragma unroll
-                    for (int v = 0; v < NV; ++v)
-                        q[u][v] = load_raw<T, VE>(p + col[v]);
-                } else {
-#pragma unroll
-                    for (int v = 0; v < NV; ++v)
-                        q[u][v] = Raw<T, VE>{};
-                }
+                const int32_t i = __shfl_sync(kAll, point, u0 + u, LG);
+                C::template read<T>(q[u], dout + static_cast<int64_t>(i) * a.D + col, in,
+                                    whole || begin + s0 + u0 + u < end);
             }
             Sums<2> two[DW ? U : 1];
 #pragma unroll
@@ -568,8 +566,7 @@ __global__ void __launch_bounds__(kThreads, VE == 1 ? 2 : 3) segment_kernel(cons
                 for (int v = 0; v < NV; ++v) {
                     fma_raw<T, VE>(acc[v], q[u][v], wu);
                     if constexpr (DW)
-                        if (C::at(slice, lane, v) < a.D)
-                            dot_raw<T, VE>(two[u], t_row[v], q[u][v]);
+                        dot_raw<T, VE>(two[u], t_row[v], q[u][v]);
                 }
             }
             if constexpr (DW) {
