@@ -14,8 +14,9 @@
 // row that ids name is written once, by one group, and the order of every sum
 // follows from the sizes alone: the bits do not change from run to run.  The
 // whole table is zeroed by the sort's launches, which leave HBM idle: for 131,072
-// rows of 2,048 (1.07 GB, 140 us) that hides the sort, where blocks that zeroed
-// the rows without ids afterwards took 250 us for the gradient of 16,384 tokens.
+// rows of 2,048 (1.07 GB, 140 us) that hides the sort: the gradient of 16,384
+// tokens takes 191 us, where blocks that zeroed the rows without ids after the
+// same sort took 42 us longer.
 #include "internal.h"
 #include "launch.cuh"
 #include "vec.cuh"
@@ -207,9 +208,10 @@ struct GatherArgs {
 
 // A group of lanes per point and slice of columns; lane u reads id u of eight,
 // U rows are in flight.  Bound by the rows' way from L2 (268 MB for 65,536
-// points of 8 ids in a table of 8 MB: 27 us, 10 TB/s).  Groups that went
-// through several points and read the next ids early, and rows copied
-// asynchronously into shared memory, were 0 to 50% slower.
+// points of 8 ids in a table of 8 MB: 27 us, 10 TB/s); 20,011 points of 7 ids and
+// 255 columns, at 2-byte boundaries, 16.5 with the call.  Groups that went through several
+// points and read the next ids early, and rows copied asynchronously into shared
+// memory, were 0 to 50% slower.
 template <typename T, int VE, int LG, int U>
 __global__ void __launch_bounds__(kThreads) lookup_many_kernel(const GatherArgs a)
 {
@@ -443,12 +445,13 @@ __device__ __forceinline__ void put(const GradArgs &a, int32_t r, int col, const
 // T: type of dout, G: of dtable.  DW (one slice): a place's weight's gradient is
 // formed on the way, from the row of the table that its group holds meanwhile;
 // the four sums of a batch are added over the lanes together.  For 30,011 points
-// of 8 ids, 250 columns of bf16 and 16,384 rows it takes 40 us: the gathered
-// rows come from L2 (131 MB), but 106 warp instructions each (rows at 4-byte
-// boundaries need four loads) keep the issue slots 60% busy at the 24 warps that
-// 80 registers allow; the two gathers in kernels of their own took 57 us.  Eight
-// rows in flight at 16 warps, or chunks for 16, 32 or 48 warps, were 1 to 10%
-// slower on six shapes.
+// of 8 ids, 250 columns of bf16 and 16,384 rows it takes 32 us: the gathered
+// rows come from L2 (131 MB), at 84 warp instructions each, and the 24 warps that
+// 80 registers allow wait for them.  An address per vector instead of one per row
+// cost 23 instructions more (40 us); the two gathers in kernels of their own 57 us
+// on that footing.  Whole gradients of nine shapes: eight rows in flight at 16
+// warps 7% faster to 7% slower (58.7 to 60.7 us here), 32 warps of 64 registers up
+// to 16% slower (68), chunks for 48 warps up to 7%.
 template <typename T, typename G, int VE, int LG, bool DW>
 __global__ void __launch_bounds__(kThreads, VE == 1 ? 2 : 3) segment_kernel(const GradArgs a)
 {
@@ -589,8 +592,9 @@ __global__ void __launch_bounds__(kThreads, VE == 1 ? 2 : 3) segment_kernel(cons
 }
 
 // Rows that span chunks: the chunk in which such a row begins holds its first
-// part as its last row; the following chunks hold the others as their first.
-// 6 us after the sums above: the latency of four dependent loads.
+// part as its last row; the following chunks hold the others as their first,
+// the last of them found from the sorted rows at the chunks' starts.  A few us
+// after the sums above, of dependent loads.
 template <typename G, int VE, int LG>
 __global__ void __launch_bounds__(kThreads) join_kernel(const GradArgs a)
 {
