@@ -451,7 +451,8 @@ __device__ __forceinline__ void put(const GradArgs &a, int32_t r, int col, const
 // cost 23 instructions more (40 us); the two gathers in kernels of their own 57 us
 // on that footing.  Whole gradients of nine shapes: eight rows in flight at 16
 // warps 7% faster to 7% slower (58.7 to 60.7 us here), 32 warps of 64 registers up
-// to 16% slower (68), chunks for 48 warps up to 7%.
+// to 16% slower (68), chunks for 48 warps up to 7%, ids and table rows read ahead
+// of their use 0 to 5%.
 template <typename T, typename G, int VE, int LG, bool DW>
 __global__ void __launch_bounds__(kThreads, VE == 1 ? 2 : 3) segment_kernel(const GradArgs a)
 {
