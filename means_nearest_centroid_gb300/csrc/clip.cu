@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // The next tensors of the call that have elements, from `first` on; returns
-// the index after the last one taken.
+// the index of the next one that has, or n.
 template <int MAX>
 int32_t fill_list(const void *const *src, void *const *dst, const int64_t *sizes,
                   const int32_t *dtypes, int32_t n, int32_t first, TensorList<MAX> *l)
@@ -333,6 +333,8 @@ int32_t fill_list(const void *const *src, void *const *dst, const int64_t *sizes
         const int64_t bytes = sizes[i] * dtype_bytes(dtypes[i]);
         l->first_chunk[t + 1] = l->first_chunk[t] + (bytes + kChunkBytes - 1) / kChunkBytes;
     }
+    while (i < n && sizes[i] == 0)   // so that no list of a call but its first can be empty
+        ++i;
     return i;
 }
 

@@ -1,0 +1,29 @@
+"""Learned assignments on the GPU at the edges of what the entry points accept.
+
+Tolerances and helpers are those of test_learn_gpu."""
+
+import pytest
+import torch
+
+import means_nearest_centroid_gb300 as km
+from test_learn_gpu import NAN, check_clip, dev, make_grads  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- clipping -------------------------------------------------------------------
+
+@pytest.mark.parametrize("max_norm", [0.5, 1e9])
+@pytest.mark.parametrize("full,empty", [(256, 1), (256, 300), (512, 3), (24, 1), (25, 400), (257, 255)])
+def test_clip_with_empty_tensors_at_the_end(dev, full, empty, max_norm):  # noqa: F811
+    """A launch takes up to 256 tensors; what follows the last one that has elements takes none."""
+    for shapes in ([(5,)] * full + [(0,)] * empty, [(0,)] * empty + [(5,)] * full,
+                   [(5,)] * (full // 2) + [(0,)] * empty + [(5,)] * (full - full // 2) + [(0,)]):
+        grads = make_grads(shapes, full)
+        gd = [g.to(dev) for g in grads]
+        outs = [torch.full_like(g, NAN) for g in gd]
+        norm = km.kmassign_clip(gd, max_norm, out=outs)
+        check_clip(grads, outs, norm, max_norm)
+        assert torch.equal(km.kmassign_grad_norm(gd), norm)
+        assert torch.equal(km.kmassign_clip(gd, max_norm), norm)     # in place
+        assert all(torch.equal(a, b) for a, b in zip(gd, outs))
