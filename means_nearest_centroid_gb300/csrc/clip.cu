@@ -3,7 +3,9 @@
 //
 // Two launches: every block sums the squares of its share of the chunks into
 // one partial, then every block of the second launch adds all partials (in the
-// same order, so in the same bits) and scales its share.  Squares are summed in
+// same order, so in the same bits) and scales its share.  More tensors than one
+// launch takes are as many launches of each, with one between that adds the
+// partials, once.  Squares are summed in
 // fp32 over the 64 bytes that a thread loads at a time and from there on in
 // fp64; where such a sum leaves the range in which fp32 squares are sound
 // (gradients beyond 1e15 or below 1e-15), its squares are taken again in fp64,
@@ -260,20 +262,21 @@ __global__ void __launch_bounds__(32)
         *norm = f;
 }
 
+// partials 0: *norm holds the norm; else it is formed here, and written.
 template <int MAX>
 __global__ void __launch_bounds__(kThreads)
     scale_kernel(const __grid_constant__ TensorList<MAX> l, const double *partial,
-                 int32_t partials, float max_norm, bool in_place, float *__restrict__ norm)
+                 int32_t partials, float max_norm, bool in_place, float *norm)
 {
     let_next_start();
     wait_for_previous();
     __shared__ float s_coef;
     if (threadIdx.x < 32) {
-        const float f = norm_of(partial, partials);
+        const float f = partials == 0 ? *norm : norm_of(partial, partials);
         if (threadIdx.x == 0) {
             const float ratio = max_norm / (f + 1e-6f);
             s_coef = ratio >= 1.0f ? 1.0f : ratio;   // a NaN norm gives NaN
-            if (norm != nullptr && blockIdx.x == 0)
+            if (partials != 0 && blockIdx.x == 0)
                 *norm = f;
         }
     }
@@ -358,15 +361,17 @@ cudaError_t clip_lists(const void *const *grads, void *const *out, const int64_t
         partials += static_cast<int32_t>(blocks);
         ++lists;
     }
-    if (!scale || lists == 0)
-        return e != cudaSuccess
-                   ? e
-                   : launch_after(norm_kernel, 1, 32, 0, stream, partial, partials, norm);
+    if (e == cudaSuccess && (!scale || lists != 1)) {
+        e = launch_after(norm_kernel, 1, 32, 0, stream, partial, partials, norm);
+        partials = 0;
+    }
+    if (!scale)
+        return e;
     for (int32_t at = 0, i = 0; i < lists && e == cudaSuccess; ++i) {
         if (lists > 1)   // else l still holds the list
             at = fill_list(grads, out, sizes, dtypes, n, at, &l);
         e = launch_after(scale_kernel<MAX>, blocks_of(l), kThreads, 0, stream, l, partial, partials,
-                         max_norm, out == nullptr, i == 0 ? norm : nullptr);
+                         max_norm, out == nullptr, norm);
     }
     return e;
 }

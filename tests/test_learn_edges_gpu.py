@@ -27,3 +27,31 @@ def test_clip_with_empty_tensors_at_the_end(dev, full, empty, max_norm):  # noqa
         assert torch.equal(km.kmassign_grad_norm(gd), norm)
         assert torch.equal(km.kmassign_clip(gd, max_norm), norm)     # in place
         assert all(torch.equal(a, b) for a, b in zip(gd, outs))
+
+
+def clip_time(grads):
+    """GPU time of one clipping in place, in ms: the launches wait in the stream until the host
+    has made them all."""
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(600_000_000)
+    start.record()
+    km.kmassign_clip(grads, 1.0)
+    end.record()
+    assert not start.query()              # the GPU has not begun: the span holds no host time
+    torch.cuda.synchronize()
+    return start.elapsed_time(end)
+
+
+def test_clip_of_many_tensors_takes_time_in_proportion(dev):  # noqa: F811
+    """8 times the tensors take 8 times as long (twice that is allowed), not 64 times: the norm's
+    partial sums are added once, not by every block of every launch."""
+    flat = torch.randn(32_768 * 5, generator=torch.Generator().manual_seed(0)).to(dev)
+    grads = list(flat.split(5))
+    keep = flat.clone()
+    assert abs(km.kmassign_grad_norm(grads).item() - km.kmassign_grad_norm([flat]).item()) < 1e-3
+    few, many = (min(clip_time(g) for _ in range(3)) for g in (grads[:4096], grads))
+    assert many < 16 * few, (few, many)
+    flat.copy_(keep)
+    norm = km.kmassign_clip(grads, 1.0)
+    check_clip([keep.cpu()], [flat.cpu()], norm, 1.0)
