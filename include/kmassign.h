@@ -396,7 +396,9 @@ enum kmassign_score { KMASSIGN_SOFTMAX = 0, KMASSIGN_SIGMOID = 1 };
  *            (sum of the row's selected s); 0 at idx -1, and where a sigmoid
  *            row's sum is 0.  The renormalised softmax is taken over the
  *            selection, so it does not underflow.  A +inf logit makes the
- *            softmax weights of its row NaN, as the formula does
+ *            softmax weights of its row NaN, as the formula does (its expert
+ *            and its group come first; with a bias every key of the row is
+ *            NaN, and none is selected)
  * N = 0 launches nothing.  Errors: N, E or N * k out of range
  * KMASSIGN_ERR_SHAPE; k, groups, a flag, a type or a non-finite scale
  * KMASSIGN_ERR_ARG.

@@ -109,6 +109,15 @@ __device__ __forceinline__ void sort_down(float (&s)[V])
                 }
 }
 
+// What an expert with key x counts in its group's sum of scores.  A softmax with
+// a +inf logit is NaN there, which maxima pass over: the logit itself, so that
+// its group comes first.
+template <bool SIGMOID>
+__device__ __forceinline__ float group_score(float x, float part)
+{
+    return x == -INFINITY || (!SIGMOID && x == INFINITY) ? x : part;
+}
+
 // The best two of a group's keys, held by several lanes.
 struct Best2 {
     float first = -INFINITY, second = -INFINITY;
@@ -293,7 +302,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
             if (!by_key) {
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    b.add(key[v] == -INFINITY ? -INFINITY : part[v]);
+                    b.add(group_score<SIGMOID>(key[v], part[v]));
             } else {
                 b.first = sorted[0];
                 b.second = V > 1 ? sorted[V > 1 ? 1 : 0] : -INFINITY;
@@ -324,9 +333,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
         } else {
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                keys[lane * kStride + v] = by_key                ? key[v]
-                                           : key[v] == -INFINITY ? -INFINITY
-                                                                 : part[v];
+                keys[lane * kStride + v] =
+                    by_key ? key[v] : group_score<SIGMOID>(key[v], part[v]);
             __syncwarp();
             // lanes_per lanes form one group's key, all groups in one round where they fit
             int lanes_per = W;

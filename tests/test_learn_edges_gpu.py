@@ -6,9 +6,42 @@ import pytest
 import torch
 
 import means_nearest_centroid_gb300 as km
-from test_learn_gpu import NAN, check_clip, dev, make_grads  # noqa: F401
+from test_learn_gpu import INF, NAN, check_clip, dev, make_grads  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+# ---- routing --------------------------------------------------------------------
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("top", [1, 2])
+@pytest.mark.parametrize("E,groups", [(64, 8), (256, 8), (96, 6), (30, 10), (8, 4)])
+def test_route_groups_with_an_infinite_logit(dev, E, groups, top, renorm):  # noqa: F811
+    """The group of a +inf logit comes first, wherever it lies, and the softmax weights of the row
+    are NaN; a sigmoid's score there is 1, which two experts of another group can beat."""
+    per = E // groups
+    X = torch.randn(5, E, generator=torch.Generator().manual_seed(E)).to(dev)
+    X[1, E - 1] = INF                       # the last group
+    X[2, per], X[2, E - 2] = INF, INF       # two groups
+    X[3] = -INF
+    X[3, E - per] = INF                     # nothing but it
+    idx, w = km.kmassign_route(X, 2, groups=groups, topk_groups=2, group_top=top, renorm=renorm)
+    assert idx[1, 0].item() == E - 1 and idx[2].tolist() == [per, E - 2]
+    assert idx[3].tolist() == [E - per, -1] and w[3, 1].item() == 0
+    assert torch.isnan(w[1:3]).all() and torch.isnan(w[3, 0])
+    rest = X[1].clone()                     # second: the best of the second group and the last one's others
+    rest[E - 1] = -INF
+    if top == 2:                            # all other groups' sums are 0: the lowest is the second
+        rest[per: E - per] = -INF
+    assert idx[1, 1].item() == rest.argmax().item()
+    for i in (0, 4):
+        one, _ = km.kmassign_route(X[i: i + 1], 2, groups=groups, topk_groups=2, group_top=top)
+        assert torch.equal(one[0], idx[i]) and torch.isfinite(w[i]).all()
+    Y = torch.full((1, E), -9.0, device=dev)
+    Y[0, E - 1] = INF
+    Y[0, :2] = 0.5
+    idx, w = km.kmassign_route(Y, 1, score="sigmoid", groups=groups, topk_groups=1, group_top=top)
+    assert idx.item() == (0 if top == 2 else E - 1) and w.item() == 1.0
 
 
 # ---- clipping -------------------------------------------------------------------
