@@ -414,7 +414,8 @@ int kmassign_route(const void *logits, int32_t dtype, int64_t N, int64_t E, int3
  *   idx       int32 [N, k]: distinct experts in each row; ids outside [0, E)
  *             are skipped
  *   dweights  fp32 [N, k]; what stands at skipped ids is ignored
- *   dlogits   dtype [N, E], every element written (0 where there is none)
+ *   dlogits   dtype [N, E], every element written (0 where there is none, as
+ *             where a sigmoid is 0 in the weights: below x = -88.7)
  * logits, dtype, N, E, k (<= min(E, 32)), score, renorm, scale, errors: as in
  * kmassign_route.
  */

@@ -588,10 +588,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_sparse_kernel(con
     const Chosen<T> c(a, row, lane & (KW - 1), live);
     float d;
     if constexpr (SIGMOID) {
-        // s and s (1 - s) without cancellation, from t = exp(-|x|)
+        // s as the weights have it, 0 below x = -88.7 (and then without a slope); s (1 - s)
+        // without cancellation, from t = exp(-|x|)
         const float t = c.on ? expf(-fabsf(c.x)) : 0.0f;
-        const float s = c.on ? (c.x >= 0.0f ? 1.0f : t) / (1.0f + t) : 0.0f;
-        const float slope = t / ((1.0f + t) * (1.0f + t));
+        const float s = c.on ? sigmoid(c.x) : 0.0f;
+        const float slope = s > 0.0f ? t / ((1.0f + t) * (1.0f + t)) : 0.0f;
         if (a.renorm) {
             const float total = row_sum<KW>(s);
             const float mean = row_sum<KW>(s * c.g) / total;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import means_nearest_centroid_gb300 as km
-from test_learn_gpu import INF, NAN, check_clip, dev, make_grads  # noqa: F401
+from test_learn_gpu import INF, NAN, U, check_clip, dev, make_grads  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -42,6 +42,32 @@ def test_route_groups_with_an_infinite_logit(dev, E, groups, top, renorm):  # no
     Y[0, :2] = 0.5
     idx, w = km.kmassign_route(Y, 1, score="sigmoid", groups=groups, topk_groups=1, group_top=top)
     assert idx.item() == (0 if top == 2 else E - 1) and w.item() == 1.0
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("k", [3, 12, 20])
+def test_sigmoid_gradient_where_scores_underflow(dev, k, renorm):  # noqa: F811
+    """A sigmoid below x = -88.7 is 0 in the weights (1 / (1 + inf)), and a row of such scores has
+    weights 0: no gradient there, while the others' is what it is without that expert."""
+    N, E = 6, 32
+    gen = torch.Generator().manual_seed(k)
+    X = torch.full((N, E), -200.0)
+    X[:, :k] = torch.tensor([-90.0, -95.0, -100.0, -103.0, -120.0]).repeat(8)[torch.randperm(40, generator=gen)[:k]]
+    X[1:, 1] = torch.randn(N - 1, generator=gen)
+    X[2:, 2] = torch.randn(N - 2, generator=gen)
+    dw = torch.randn(N, k, generator=gen)
+    idx = torch.arange(k, dtype=torch.int32).repeat(N, 1)
+    d = km.kmassign_route_grad(X.to(dev), idx.to(dev), dw.to(dev), score="sigmoid", renorm=renorm).cpu()
+    s = 1 / (1 + torch.exp(-X.double()))
+    assert (d[0] == 0).all() and (d[X < -89] == 0).all()
+    if renorm:
+        assert (d[1].abs() <= 64 * U).all()     # the only score: its weight is 1
+        t = s[2:, 1] + s[2:, 2]
+        want = s[2:, 1] * s[2:, 2] * (1 - s[2:, 1]) / t ** 2 * (dw[2:, 1] - dw[2:, 2])
+        assert ((d[2:, 1] - want).abs() <= 64 * U * (want.abs() + 1)).all()
+    else:
+        want = (s * (1 - s))[2:, 1:3] * dw[2:, 1:3]
+        assert ((d[2:, 1:3] - want).abs() <= 64 * U).all()
 
 
 # ---- clipping -------------------------------------------------------------------
