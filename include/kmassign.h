@@ -411,8 +411,8 @@ int kmassign_route(const void *logits, int32_t dtype, int64_t N, int64_t E, int3
 /*
  * Gradient of kmassign_route's weights with respect to the logits, for the
  * choice idx it made (the choice itself has no gradient; the bias none).
- *   idx       int32 [N, k]: distinct experts in each row; ids outside [0, E)
- *             are skipped
+ *   idx       int32 [N, k]; ids outside [0, E) are skipped, an expert that a row
+ *             names more than once takes the sum over its places
  *   dweights  fp32 [N, k]; what stands at skipped ids is ignored
  *   dlogits   dtype [N, E], every element written (0 where there is none, as
  *             where a sigmoid is 0 in the weights: below x = -88.7)

@@ -487,8 +487,8 @@ def kmassign_route_grad(logits, idx, dweights, score: str = "softmax", renorm: b
                         scale: float = 1.0, dlogits=None, stream=None):
     """The gradient of the logits [N, E] (their type) from that of the weights.
 
-    ``idx`` (int32 [N, k], distinct in each row; ids outside [0, E) skipped) is
-    the choice ``kmassign_route`` made with the same ``score``, ``renorm`` and
+    ``idx`` (int32 [N, k]; ids outside [0, E) are skipped, an expert named more
+    than once in a row takes the sum over its places) is the choice ``kmassign_route`` made with the same ``score``, ``renorm`` and
     ``scale``; ``dweights`` is fp32 [N, k].
     """
     dtype = _need_float(logits, "logits")

@@ -607,8 +607,22 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_sparse_kernel(con
         p = c.on ? p / total : 0.0f;
         d = p * (c.g - row_sum<KW>(p * c.g));
     }
+    // an expert that a row names more than once: its first lane takes the sum
+    const uint32_t same =
+        __match_any_sync(kAll, c.on ? (lane / KW) << 16 | c.e : -1 - lane);
+    bool first = true;
+    if (__any_sync(kAll, (same & (same - 1)) != 0)) {
+        const uint32_t mine = same >> (lane & (32 - KW));   // of the row's lanes
+        first = (mine & ((1u << (lane & (KW - 1))) - 1u)) == 0;
+        float sum = 0.0f;
+        for (int j = 0; j < KW; ++j) {
+            const float f = __shfl_sync(kAll, d, j, KW);
+            sum += (mine >> j) & 1u ? f : 0.0f;
+        }
+        d = sum;
+    }
     __syncwarp();
-    if (c.on)
+    if (c.on && first)
         out[row * a.E + c.e] = Elem<T>::down(d * a.scale);
 }
 
@@ -687,6 +701,38 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_dense_kernel(cons
             const int i = v * W + lane;
             if (live && i < a.E)
                 out[i] = Elem<T>::down(stage[i / V * kStride + i % V]);
+        }
+    }
+    // an expert that a row names more than once: its first place takes the sum
+    bool look = a.k > W;   // more places than lanes: looked for among all of them
+    if (!look) {
+        const uint32_t same = __match_any_sync(
+            kAll, e[0] >= 0 ? static_cast<int>(threadIdx.x & 31) / W << 16 | e[0]
+                            : -1 - static_cast<int>(threadIdx.x & 31));
+        look = __any_sync(kAll, (same & (same - 1)) != 0);
+    }
+    if (look) {
+        float sum[kSlots] = {};
+        bool first[kSlots];
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s)
+            first[s] = true;
+#pragma unroll
+        for (int t = 0; t < kSlots; ++t)
+            for (int j = 0; j < min(W, a.k - t * W); ++j) {
+                const int32_t other = __shfl_sync(kAll, e[t], j, W);
+                const float f = __shfl_sync(kAll, g[t], j, W);
+#pragma unroll
+                for (int s = 0; s < kSlots; ++s)
+                    if (other == e[s]) {
+                        sum[s] += f;
+                        first[s] = first[s] && t * W + j >= s * W + lane;
+                    }
+            }
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s) {
+            g[s] = sum[s];
+            e[s] = first[s] ? e[s] : -1;
         }
     }
     __syncwarp();

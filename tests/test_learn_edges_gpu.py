@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import means_nearest_centroid_gb300 as km
-from test_learn_gpu import INF, NAN, U, check_clip, dev, make_grads  # noqa: F401
+from test_learn_gpu import INF, NAN, U, check_clip, dev, make_grads, weight_bound  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -68,6 +68,39 @@ def test_sigmoid_gradient_where_scores_underflow(dev, k, renorm):  # noqa: F811
     else:
         want = (s * (1 - s))[2:, 1:3] * dw[2:, 1:3]
         assert ((d[2:, 1:3] - want).abs() <= 64 * U).all()
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("N,E,k", [(9, 2, 2), (33, 5, 4), (40, 30, 12), (21, 64, 32), (18, 100, 8), (17, 128, 20),
+                                   (12, 200, 32), (7, 700, 9)])
+def test_route_grad_of_repeated_experts(dev, N, E, k, score, renorm):  # noqa: F811
+    """A row may name an expert twice: weights w_j = s_e(j) (/ sum_l s_e(l)) of each place, whose
+    gradients add up; bounds as in test_route_grad, and k more roundings of the sum."""
+    gen = torch.Generator().manual_seed(N)
+    X = torch.randn(N, E, generator=gen)
+    idx = torch.randint(-1, max(2, E // 3), (N, k), generator=gen).int()
+    idx[0] = E - 1                                     # one expert everywhere
+    dw = torch.randn(N, k, generator=gen)
+    d = km.kmassign_route_grad(X.to(dev), idx.to(dev), dw.to(dev), score=score, renorm=renorm, scale=1.5)
+    again = km.kmassign_route_grad(X.to(dev), idx.to(dev), dw.to(dev), score=score, renorm=renorm, scale=1.5)
+    assert torch.equal(d, again)
+    x = X.double().requires_grad_()
+    live = (idx >= 0).double()
+    # a renormalised softmax: the denominator over all experts cancels
+    s = torch.sigmoid(x) if score == "sigmoid" else torch.exp(x) if renorm else torch.softmax(x, 1)
+    w = s.gather(1, idx.clamp(min=0).long()) * live
+    if renorm:
+        w = w / w.sum(1, keepdim=True).clamp(min=1e-300)
+    (1.5 * w * dw.double()).sum().backward()
+    # magnitudes: of each place's own term and of what the others' share takes from it
+    amean = (w.detach() * dw.double().abs()).sum(1, keepdim=True)
+    size = torch.zeros(N, E, dtype=torch.float64).scatter_add_(
+        1, idx.clamp(min=0).long(), 1.5 * w.detach() * (dw.double().abs() + amean))
+    if score == "softmax" and not renorm:
+        size += 1.5 * s.detach() * amean
+    bound = (2 * weight_bound(x.detach().numpy(), k) + (k + 1) * U) * size.numpy() + 2 ** -120
+    assert ((d.cpu().double() - x.grad).abs().numpy() <= bound).all()
 
 
 # ---- clipping -------------------------------------------------------------------
