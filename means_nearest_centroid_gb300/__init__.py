@@ -161,6 +161,21 @@ def _stream_ptr(stream, device=None) -> int:
     return int(stream)
 
 
+def _new(shape, dtype, device, stream, make=torch.empty):
+    """An output of a call on ``stream`` (None: the current one), whose memory that stream owns.
+
+    The caching allocator hands out again at once what was freed on the current
+    stream, while work enqueued there may still read it; another stream must not
+    write there before that work is done (nor start before ``make`` has).
+    """
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -183,7 +198,7 @@ def kmassign_norms(C: torch.Tensor, out: torch.Tensor | None = None, stream=None
     _need_cuda(C, "C", torch.bfloat16)
     K, D = C.shape
     if out is None:
-        out = torch.empty(K, dtype=torch.float32, device=C.device)
+        out = _new(K, torch.float32, C.device, stream)
     _need_cuda(out, "out", torch.float32)
     _check(library().kmassign_norms(_ptr(C), K, D, _ptr(out), _stream_ptr(stream, C.device)),
            "kmassign_norms")
@@ -203,7 +218,7 @@ def kmassign_ex(X, C, cnorm=None, idx=None, minscore=None, ksplit: int = 0,
     if cnorm is not None:
         _need_cuda(cnorm, "cnorm", torch.float32)
     if idx is None:
-        idx = torch.empty(N, dtype=torch.int32, device=X.device)
+        idx = _new(N, torch.int32, X.device, stream)
     _need_cuda(idx, "idx", torch.int32)
     if minscore is not None:
         _need_cuda(minscore, "minscore", torch.float32)
@@ -225,7 +240,7 @@ def kmassign(X, C, cnorm=None, idx=None, minscore=None, stream=None):
     if cnorm is not None:
         _need_cuda(cnorm, "cnorm", torch.float32)
     if idx is None:
-        idx = torch.empty(N, dtype=torch.int32, device=X.device)
+        idx = _new(N, torch.int32, X.device, stream)
     _need_cuda(idx, "idx", torch.int32)
     if minscore is not None:
         _need_cuda(minscore, "minscore", torch.float32)
@@ -252,7 +267,7 @@ def kmassign_noalloc(X, C, cnorm=None, idx=None, minscore=None, stream=None):
     if cnorm is not None:
         _need_cuda(cnorm, "cnorm", torch.float32)
     if idx is None:
-        idx = torch.empty(N, dtype=torch.int32, device=X.device)
+        idx = _new(N, torch.int32, X.device, stream)
     _need_cuda(idx, "idx", torch.int32)
     if minscore is not None:
         _need_cuda(minscore, "minscore", torch.float32)
@@ -282,10 +297,10 @@ def kmassign_topk(X, C, k: int, cnorm=None, idx=None, score=None, distances: boo
         _need_cuda(cnorm, "cnorm", torch.float32)
     k = int(k)
     if idx is None:
-        idx = torch.empty((N, max(k, 0)), dtype=torch.int32, device=X.device)
+        idx = _new((N, max(k, 0)), torch.int32, X.device, stream)
     _need_cuda(idx, "idx", torch.int32)
     if score is None and (with_score or distances):
-        score = torch.empty((N, max(k, 0)), dtype=torch.float32, device=X.device)
+        score = _new((N, max(k, 0)), torch.float32, X.device, stream)
     if score is not None:
         _need_cuda(score, "score", torch.float32)
     lib = library()
@@ -341,9 +356,9 @@ def kmassign_update(X, idx, K: int, sums=None, counts=None, method: int = 0, str
     if idx.shape != (N,):
         raise ValueError("idx must hold one id per point")
     if sums is None:
-        sums = torch.zeros((K, D), dtype=torch.float32, device=X.device)
+        sums = _new((K, D), torch.float32, X.device, stream, torch.zeros)
     if counts is None:
-        counts = torch.zeros(K, dtype=torch.int32, device=X.device)
+        counts = _new(K, torch.int32, X.device, stream, torch.zeros)
     _need_cuda(sums, "sums", torch.float32)
     _need_cuda(counts, "counts", torch.int32)
     _check(library().kmassign_update_ex(_ptr(X), _ptr(idx), N, int(K), D, _ptr(sums),
@@ -360,7 +375,7 @@ def kmassign_centroids(sums, counts, C_old, C_new=None, means=None, stream=None)
     _need_cuda(C_old, "C_old", torch.bfloat16)
     K, D = C_old.shape
     if C_new is None:
-        C_new = torch.empty_like(C_old)
+        C_new = _new((K, D), torch.bfloat16, C_old.device, stream)
     _need_cuda(C_new, "C_new", torch.bfloat16)
     if means is not None:
         _need_cuda(means, "means", torch.float32)
@@ -380,7 +395,7 @@ def kmassign_lloyd(X, C, iters: int, idx=None, stream=None):
     N, D = X.shape
     K = C.shape[0]
     if idx is None:
-        idx = torch.empty(N, dtype=torch.int32, device=X.device)
+        idx = _new(N, torch.int32, X.device, stream)
     _need_cuda(idx, "idx", torch.int32)
     _check(library().kmassign_lloyd(_ptr(X), _ptr(C), N, K, D, int(iters), _ptr(idx),
                                     _stream_ptr(stream, X.device)), "kmassign_lloyd")
@@ -465,12 +480,12 @@ def kmassign_route(logits, k: int, score: str = "softmax", bias=None, groups: in
         _need_cuda(bias, "bias", torch.float32)
         _need_shape(bias, "bias", (E,))
     if idx is None:
-        idx = torch.empty((N, max(k, 0)), dtype=torch.int32, device=logits.device)
+        idx = _new((N, max(k, 0)), torch.int32, logits.device, stream)
     else:
         _need_cuda(idx, "idx", torch.int32)
         _need_shape(idx, "idx", (N, k))
     if weights is None:
-        weights = torch.empty((N, max(k, 0)), dtype=torch.float32, device=logits.device)
+        weights = _new((N, max(k, 0)), torch.float32, logits.device, stream)
     else:
         _need_cuda(weights, "weights", torch.float32)
         _need_shape(weights, "weights", (N, k))
@@ -499,7 +514,7 @@ def kmassign_route_grad(logits, idx, dweights, score: str = "softmax", renorm: b
     _need_cuda(dweights, "dweights", torch.float32)
     _need_shape(dweights, "dweights", (N, k))
     if dlogits is None:
-        dlogits = torch.empty_like(logits)
+        dlogits = _new((N, E), logits.dtype, logits.device, stream)
     else:
         _need_cuda(dlogits, "dlogits", logits.dtype)
         _need_shape(dlogits, "dlogits", (N, E))
@@ -522,12 +537,12 @@ def kmassign_lists(idx, K: int, order=None, offsets=None, stream=None):
     _need_cuda(idx, "idx", torch.int32)
     M, K = idx.numel(), int(K)
     if order is None:
-        order = torch.empty(M, dtype=torch.int32, device=idx.device)
+        order = _new(M, torch.int32, idx.device, stream)
     else:
         _need_cuda(order, "order", torch.int32)
         _need_shape(order, "order", (M,))
     if offsets is None:
-        offsets = torch.empty(max(K, 0) + 1, dtype=torch.int32, device=idx.device)
+        offsets = _new(max(K, 0) + 1, torch.int32, idx.device, stream)
     else:
         _need_cuda(offsets, "offsets", torch.int32)
         _need_shape(offsets, "offsets", (K + 1,))
@@ -552,7 +567,7 @@ def kmassign_lookup(table, idx, weights=None, scale: float = 1.0, out=None, stre
         _need_cuda(weights, "weights", torch.float32)
         _need_shape(weights, "weights", idx.shape)
     if out is None:
-        out = torch.empty((N, D), dtype=table.dtype, device=table.device)
+        out = _new((N, D), table.dtype, table.device, stream)
     else:
         _need_cuda(out, "out", table.dtype)
         _need_shape(out, "out", (N, D))
@@ -589,7 +604,7 @@ def kmassign_lookup_grad(dout, idx, K: int, weights=None, table=None, scale: flo
         _need_cuda(table, "table", dout.dtype)
         _need_shape(table, "table", (K, D))
         if dweights is None:
-            dweights = torch.empty(idx.shape, dtype=torch.float32, device=dout.device)
+            dweights = _new(idx.shape, torch.float32, dout.device, stream)
         else:
             _need_cuda(dweights, "dweights", torch.float32)
             _need_shape(dweights, "dweights", idx.shape)
@@ -598,7 +613,7 @@ def kmassign_lookup_grad(dout, idx, K: int, weights=None, table=None, scale: flo
     if dtable is None:
         if accumulate:
             raise ValueError("accumulate needs a given dtable")
-        dtable = torch.empty((max(K, 0), D), dtype=dtype or torch.float32, device=dout.device)
+        dtable = _new((max(K, 0), D), dtype or torch.float32, dout.device, stream)
     elif dtype is not None and dtable.dtype != dtype:
         raise TypeError(f"dtable must be {dtype}, got {dtable.dtype}")
     grad = _need_float(dtable, "dtable")
@@ -629,10 +644,10 @@ def _address(a):
     return a.buffer_info()[0]
 
 
-def _norm_out(tensors, norm):
+def _norm_out(tensors, norm, stream):
     if norm is None:
-        return torch.empty((), dtype=torch.float32,
-                           device=tensors[0].device if tensors else "cuda")
+        return _new((), torch.float32, tensors[0].device if tensors else torch.device("cuda"),
+                    stream)
     _need_cuda(norm, "norm", torch.float32)
     if norm.numel() != 1:
         raise ValueError("norm must hold one element")
@@ -643,7 +658,7 @@ def kmassign_grad_norm(tensors, norm=None, stream=None):
     """The 2-norm over all elements of a list of tensors, an fp32 scalar on the GPU."""
     tensors = list(tensors)
     ptrs, sizes, codes = _tensor_arrays(tensors, "tensors")
-    norm = _norm_out(tensors, norm)
+    norm = _norm_out(tensors, norm, stream)
     rc = library().kmassign_grad_norm(_address(ptrs), _address(sizes), _address(codes),
                                       len(tensors), norm.data_ptr(),
                                       _stream_of(stream, norm))
@@ -671,7 +686,7 @@ def kmassign_clip(grads, max_norm: float, out=None, norm=None, stream=None):
             raise TypeError("out must have the gradients' types")
         if out_sizes != sizes:
             raise ValueError("out must have the gradients' sizes")
-    norm = _norm_out(grads, norm)
+    norm = _norm_out(grads, norm, stream)
     rc = library().kmassign_clip(_address(ptrs), None if outs is None else _address(outs),
                                  _address(sizes), _address(codes), len(grads), float(max_norm),
                                  norm.data_ptr(), _stream_of(stream, norm))
@@ -711,7 +726,7 @@ def assign(X, C, cnorm=None, with_minscore: bool = False, stream=None):
     """Convenience: returns idx, or (idx, minscore) when ``with_minscore``."""
     ms = None
     if with_minscore:
-        ms = torch.empty(X.shape[0], dtype=torch.float32, device=X.device)
+        ms = _new(X.shape[0], torch.float32, X.device, stream)
     idx = kmassign(X, C, cnorm=cnorm, minscore=ms, stream=stream)
     return (idx, ms) if with_minscore else idx
 

@@ -147,3 +147,74 @@ def test_clip_of_many_tensors_takes_time_in_proportion(dev):  # noqa: F811
     flat.copy_(keep)
     norm = km.kmassign_clip(grads, 1.0)
     check_clip([keep.cpu()], [flat.cpu()], norm, 1.0)
+
+
+# ---- streams ----------------------------------------------------------------------
+
+def calls_with_large_outputs(dev):  # noqa: F811
+    """Calls whose outputs have 32 MiB each, by name."""
+    N, D, k = 1 << 14, 512, 8
+    rows = torch.zeros(N, D, device=dev)
+    ids = torch.zeros(N, dtype=torch.int32, device=dev)
+    logits = torch.zeros(1 << 20, k, device=dev)
+    many = torch.zeros(1 << 20, k, dtype=torch.int32, device=dev)
+    dw = torch.zeros(1 << 20, k, device=dev)
+    X = torch.zeros(1 << 20, 16, dtype=torch.bfloat16, device=dev)
+    return {
+        "route": lambda s: km.kmassign_route(logits, k, stream=s),
+        "route_grad": lambda s: [km.kmassign_route_grad(logits, many, dw, stream=s)],
+        "lists": lambda s: [km.kmassign_lists(many, 4, stream=s)[0]],
+        "lookup": lambda s: [km.kmassign_lookup(rows, ids, stream=s)],
+        "lookup_grad": lambda s: [km.kmassign_lookup_grad(rows, ids, N, stream=s)[0]],
+        "topk": lambda s: km.kmassign_topk(X, X[:64], k, stream=s),
+        "update": lambda s: [km.kmassign_update(X, ids.new_zeros(1 << 20), 1 << 19, stream=s)[0]],
+    }
+
+
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("name", ["route", "route_grad", "lists", "lookup", "lookup_grad", "topk", "update"])
+def test_outputs_of_a_call_on_another_stream_are_its_own(dev, name, handle):  # noqa: F811
+    """Memory freed on the current stream, behind work that still reads it, is not what a call on
+    another stream writes its outputs to."""
+    call = calls_with_large_outputs(dev)[name]
+    s = torch.cuda.Stream(dev)
+    torch.cuda.synchronize()
+    call(None)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    old = [torch.full((1 << 23,), 7.0, device=dev) for _ in range(4)]
+    places = {t.data_ptr() for t in old}
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    kept = [t.clone() for t in old]           # still to come when the call below is made
+    del old
+    outs = call(s.cuda_stream if handle else s)
+    s.synchronize()
+    assert all(t.numel() * t.element_size() == 1 << 25 for t in outs)
+    assert not places & {t.data_ptr() for t in outs}
+    torch.cuda.synchronize()
+    assert all((t == 7).all() for t in kept)
+
+
+def test_update_on_another_stream_starts_from_its_zeros(dev):  # noqa: F811
+    """The sums' zeros belong to the call's stream, not to the current one's queue."""
+    s = torch.cuda.Stream(dev)
+    X = torch.ones(3000, 64, dtype=torch.bfloat16, device=dev)
+    idx = torch.zeros(3000, dtype=torch.int32, device=dev)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    sums, counts = km.kmassign_update(X, idx, 5, stream=s)
+    s.synchronize()
+    with torch.cuda.stream(s):
+        got, n = sums.cpu(), counts.cpu()
+    torch.cuda.synchronize()
+    for t in (got, sums.cpu()):
+        assert (t[0] == 3000).all() and (t[1:] == 0).all()
+    assert n.tolist() == counts.tolist() == [3000, 0, 0, 0, 0]
+
+
+def test_default_stream_by_handle(dev):  # noqa: F811
+    X = torch.randn(100, 16, generator=torch.Generator().manual_seed(0)).to(dev)
+    idx, w = km.kmassign_route(X, 3, stream=0)
+    other, v = km.kmassign_route(X, 3)
+    assert torch.equal(idx, other) and torch.equal(w, v)
