@@ -403,6 +403,9 @@ def kmassign_lloyd(X, C, iters: int, idx=None, stream=None):
 
 
 # ---- learned assignments: routing, lookup, inverted lists, clipping ----------
+#
+# These calls are not recorded by autograd.  In grad mode they refuse inputs that
+# require grad (but for the bias, which the weights do not depend on).
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _SCORES = {"softmax": 0, "sigmoid": 1}
@@ -421,6 +424,16 @@ def _need_float(t, name) -> int:
     if t.dtype not in _DTYPES:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
     raise ValueError(f"{name} must be contiguous")
+
+
+def _need_detached(where, **inputs):
+    """Raises for inputs that require grad in grad mode: results are not part of autograd's graph."""
+    for name, t in inputs.items():
+        if t is not None and t.requires_grad:
+            raise RuntimeError(
+                f"{where}: {name} requires grad, and autograd would not see the result; call it "
+                "under torch.no_grad() or in a torch.autograd.Function (gradients: "
+                "kmassign_route_grad, kmassign_lookup_grad)")
 
 
 def _need_shape(t, name, shape):
@@ -475,6 +488,8 @@ def kmassign_route(logits, k: int, score: str = "softmax", bias=None, groups: in
     """
     dtype = _need_float(logits, "logits")
     N, E = _need_matrix(logits, "logits")
+    if torch.is_grad_enabled():
+        _need_detached("kmassign_route", logits=logits)
     k, groups = int(k), int(groups)
     if bias is not None:
         _need_cuda(bias, "bias", torch.float32)
@@ -513,6 +528,8 @@ def kmassign_route_grad(logits, idx, dweights, score: str = "softmax", renorm: b
     _need_shape(idx, "idx", (N, k))
     _need_cuda(dweights, "dweights", torch.float32)
     _need_shape(dweights, "dweights", (N, k))
+    if torch.is_grad_enabled():
+        _need_detached("kmassign_route_grad", logits=logits, dweights=dweights)
     if dlogits is None:
         dlogits = _new((N, E), logits.dtype, logits.device, stream)
     else:
@@ -566,6 +583,8 @@ def kmassign_lookup(table, idx, weights=None, scale: float = 1.0, out=None, stre
     if weights is not None:
         _need_cuda(weights, "weights", torch.float32)
         _need_shape(weights, "weights", idx.shape)
+    if torch.is_grad_enabled():
+        _need_detached("kmassign_lookup", table=table, weights=weights)
     if out is None:
         out = _new((N, D), table.dtype, table.device, stream)
     else:
@@ -596,6 +615,9 @@ def kmassign_lookup_grad(dout, idx, K: int, weights=None, table=None, scale: flo
     if rows != N:
         raise ValueError("idx must hold one row of ids per row of dout")
     K = int(K)
+    if torch.is_grad_enabled():
+        _need_detached("kmassign_lookup_grad", dout=dout, weights=weights,
+                       table=None if weights is None else table)
     if weights is not None:
         _need_cuda(weights, "weights", torch.float32)
         _need_shape(weights, "weights", idx.shape)
@@ -628,14 +650,18 @@ def kmassign_lookup_grad(dout, idx, K: int, weights=None, table=None, scale: flo
     return dtable, dweights
 
 
-def _tensor_arrays(tensors, name):
+def _tensor_arrays(tensors, where, name):
     """Pointers, sizes and type codes of a list of tensors, as C arrays."""
     try:   # the common case in few steps a tensor; the detail only on failure
-        codes = [_DTYPES[t.dtype] for t in tensors if t.is_cuda and t.is_contiguous()]
+        codes = [_DTYPES[t.dtype] for t in tensors
+                 if t.is_cuda and t.is_contiguous() and not t.requires_grad]
     except (AttributeError, KeyError):
         codes = []
     if len(codes) != len(tensors):
         codes = [_need_float(t, name) for t in tensors]
+        if torch.is_grad_enabled():
+            for t in tensors:
+                _need_detached(where, **{name: t})
     return (array.array("Q", [t.data_ptr() for t in tensors]),
             array.array("q", [t.numel() for t in tensors]), array.array("i", codes))
 
@@ -657,7 +683,7 @@ def _norm_out(tensors, norm, stream):
 def kmassign_grad_norm(tensors, norm=None, stream=None):
     """The 2-norm over all elements of a list of tensors, an fp32 scalar on the GPU."""
     tensors = list(tensors)
-    ptrs, sizes, codes = _tensor_arrays(tensors, "tensors")
+    ptrs, sizes, codes = _tensor_arrays(tensors, "kmassign_grad_norm", "tensors")
     norm = _norm_out(tensors, norm, stream)
     rc = library().kmassign_grad_norm(_address(ptrs), _address(sizes), _address(codes),
                                       len(tensors), norm.data_ptr(),
@@ -675,13 +701,13 @@ def kmassign_clip(grads, max_norm: float, out=None, norm=None, stream=None):
     sizes and types.
     """
     grads = list(grads)
-    ptrs, sizes, codes = _tensor_arrays(grads, "grads")
+    ptrs, sizes, codes = _tensor_arrays(grads, "kmassign_clip", "grads")
     outs = None
     if out is not None:
         out = list(out)
         if len(out) != len(grads):
             raise ValueError("out must hold one tensor per gradient")
-        outs, out_sizes, out_codes = _tensor_arrays(out, "out")
+        outs, out_sizes, out_codes = _tensor_arrays(out, "kmassign_clip", "out")
         if out_codes != codes:
             raise TypeError("out must have the gradients' types")
         if out_sizes != sizes:

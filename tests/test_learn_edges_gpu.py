@@ -218,3 +218,59 @@ def test_default_stream_by_handle(dev):  # noqa: F811
     idx, w = km.kmassign_route(X, 3, stream=0)
     other, v = km.kmassign_route(X, 3)
     assert torch.equal(idx, other) and torch.equal(w, v)
+
+
+# ---- autograd -----------------------------------------------------------------------
+
+def test_inputs_that_require_grad_are_refused_in_grad_mode(dev):  # noqa: F811
+    """No result is silently cut off from the graph: such inputs raise, but under no_grad and in
+    the forward and backward of an autograd function."""
+    x = torch.randn(8, 16, device=dev)
+    p = x.clone().requires_grad_()
+    i = torch.zeros(8, 2, dtype=torch.int32, device=dev)
+    w = torch.ones(8, 2, device=dev)
+    wp = w.clone().requires_grad_()
+    calls = [lambda: km.kmassign_route(p, 2), lambda: km.kmassign_route(p * 2, 2),
+             lambda: km.kmassign_route_grad(p, i, w), lambda: km.kmassign_route_grad(x, i, wp),
+             lambda: km.kmassign_lookup(p, i), lambda: km.kmassign_lookup(x, i, weights=wp),
+             lambda: km.kmassign_lookup_grad(p, i, 8),
+             lambda: km.kmassign_lookup_grad(x, i, 8, weights=wp, table=x),
+             lambda: km.kmassign_lookup_grad(x, i, 8, weights=w, table=p),
+             lambda: km.kmassign_grad_norm([x, p]), lambda: km.kmassign_clip([x, p], 1.0),
+             lambda: km.kmassign_clip([x], 1.0, out=[p])]
+    before = p.detach().clone()
+    for call in calls:
+        with pytest.raises(RuntimeError, match="requires grad"):
+            call()
+    assert torch.equal(p, before)
+    with torch.no_grad():
+        for call in calls:
+            call()
+    km.kmassign_route(x, 2, score="sigmoid", bias=torch.zeros(16, device=dev, requires_grad=True))
+
+
+def test_as_an_autograd_function(dev):  # noqa: F811
+    """The lookup and its gradient inside a torch.autograd.Function, against torch's own."""
+    class Lookup(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, table, idx, weights):
+            ctx.save_for_backward(table, idx, weights)
+            return km.kmassign_lookup(table, idx, weights=weights)
+
+        @staticmethod
+        def backward(ctx, dout):
+            table, idx, weights = ctx.saved_tensors
+            dtable, dw = km.kmassign_lookup_grad(dout, idx, table.shape[0], weights=weights, table=table)
+            return dtable, None, dw
+
+    gen = torch.Generator().manual_seed(0)
+    table = torch.randn(10, 6, generator=gen).to(dev).requires_grad_()
+    weights = torch.randn(30, 3, generator=gen).to(dev).requires_grad_()
+    idx = torch.randint(0, 10, (30, 3), generator=gen).int().to(dev)
+    c = torch.randn(30, 6, generator=gen).to(dev)
+    (Lookup.apply(table, idx, weights) * c).sum().backward()
+    t, v = table.detach().double().requires_grad_(), weights.detach().double().requires_grad_()
+    ((t[idx.long()] * v[..., None]).sum(1) * c.double()).sum().backward()
+    # at most 90 terms an element of magnitude below 20
+    assert (table.grad - t.grad).abs().max() <= 100 * U * 90 * 20
+    assert (weights.grad - v.grad).abs().max() <= 10 * U * 6 * 20
