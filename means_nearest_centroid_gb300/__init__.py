@@ -518,8 +518,9 @@ def kmassign_route_grad(logits, idx, dweights, score: str = "softmax", renorm: b
     """The gradient of the logits [N, E] (their type) from that of the weights.
 
     ``idx`` (int32 [N, k]; ids outside [0, E) are skipped, an expert named more
-    than once in a row takes the sum over its places) is the choice ``kmassign_route`` made with the same ``score``, ``renorm`` and
-    ``scale``; ``dweights`` is fp32 [N, k].
+    than once in a row takes the sum over its places) is the choice that
+    ``kmassign_route`` made with the same ``score``, ``renorm`` and ``scale``;
+    ``dweights`` is fp32 [N, k].
     """
     dtype = _need_float(logits, "logits")
     N, E = _need_matrix(logits, "logits")
@@ -615,9 +616,6 @@ def kmassign_lookup_grad(dout, idx, K: int, weights=None, table=None, scale: flo
     if rows != N:
         raise ValueError("idx must hold one row of ids per row of dout")
     K = int(K)
-    if torch.is_grad_enabled():
-        _need_detached("kmassign_lookup_grad", dout=dout, weights=weights,
-                       table=None if weights is None else table)
     if weights is not None:
         _need_cuda(weights, "weights", torch.float32)
         _need_shape(weights, "weights", idx.shape)
@@ -632,6 +630,9 @@ def kmassign_lookup_grad(dout, idx, K: int, weights=None, table=None, scale: flo
             _need_shape(dweights, "dweights", idx.shape)
     elif dweights is not None:
         raise ValueError("dweights needs weights")
+    if torch.is_grad_enabled():
+        _need_detached("kmassign_lookup_grad", dout=dout, weights=weights,
+                       table=None if weights is None else table)
     if dtable is None:
         if accumulate:
             raise ValueError("accumulate needs a given dtable")

@@ -239,6 +239,10 @@ def test_inputs_that_require_grad_are_refused_in_grad_mode(dev):  # noqa: F811
              lambda: km.kmassign_grad_norm([x, p]), lambda: km.kmassign_clip([x, p], 1.0),
              lambda: km.kmassign_clip([x], 1.0, out=[p])]
     before = p.detach().clone()
+    with pytest.raises(TypeError):           # what is no tensor is told as before
+        km.kmassign_lookup_grad(x, i, 8, weights=[1.0], table=x)
+    with pytest.raises(TypeError):
+        km.kmassign_lookup_grad(x, i, 8, weights=w, table=[1.0])
     for call in calls:
         with pytest.raises(RuntimeError, match="requires grad"):
             call()
