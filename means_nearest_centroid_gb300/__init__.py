@@ -436,6 +436,12 @@ def _need_detached(where, **inputs):
                 "kmassign_route_grad, kmassign_lookup_grad)")
 
 
+def _written(*tensors):
+    """Tells autograd that a call wrote to these tensors of the caller (None: to one of its own), as
+    torch's in-place operations do: a backward pass that has saved one raises."""
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
 def _need_shape(t, name, shape):
     if t.shape != shape:   # a torch.Size is a tuple
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -494,6 +500,7 @@ def kmassign_route(logits, k: int, score: str = "softmax", bias=None, groups: in
     if bias is not None:
         _need_cuda(bias, "bias", torch.float32)
         _need_shape(bias, "bias", (E,))
+    given = idx, weights
     if idx is None:
         idx = _new((N, max(k, 0)), torch.int32, logits.device, stream)
     else:
@@ -510,6 +517,8 @@ def kmassign_route(logits, k: int, score: str = "softmax", bias=None, groups: in
         float(scale), idx.data_ptr(), weights.data_ptr(), _stream_of(stream, logits))
     if rc:
         _check(rc, "kmassign_route")
+    if given != (None, None):
+        _written(*given)
     return idx, weights
 
 
@@ -531,7 +540,8 @@ def kmassign_route_grad(logits, idx, dweights, score: str = "softmax", renorm: b
     _need_shape(dweights, "dweights", (N, k))
     if torch.is_grad_enabled():
         _need_detached("kmassign_route_grad", logits=logits, dweights=dweights)
-    if dlogits is None:
+    given = dlogits is not None
+    if not given:
         dlogits = _new((N, E), logits.dtype, logits.device, stream)
     else:
         _need_cuda(dlogits, "dlogits", logits.dtype)
@@ -542,6 +552,8 @@ def kmassign_route_grad(logits, idx, dweights, score: str = "softmax", renorm: b
         _stream_of(stream, logits))
     if rc:
         _check(rc, "kmassign_route_grad")
+    if given:
+        _written(dlogits)
     return dlogits
 
 
@@ -554,6 +566,7 @@ def kmassign_lists(idx, K: int, order=None, offsets=None, stream=None):
     """
     _need_cuda(idx, "idx", torch.int32)
     M, K = idx.numel(), int(K)
+    given = order, offsets
     if order is None:
         order = _new(M, torch.int32, idx.device, stream)
     else:
@@ -568,6 +581,8 @@ def kmassign_lists(idx, K: int, order=None, offsets=None, stream=None):
                                   _stream_of(stream, idx))
     if rc:
         _check(rc, "kmassign_lists")
+    if given != (None, None):
+        _written(*given)
     return order, offsets
 
 
@@ -586,7 +601,8 @@ def kmassign_lookup(table, idx, weights=None, scale: float = 1.0, out=None, stre
         _need_shape(weights, "weights", idx.shape)
     if torch.is_grad_enabled():
         _need_detached("kmassign_lookup", table=table, weights=weights)
-    if out is None:
+    given = out is not None
+    if not given:
         out = _new((N, D), table.dtype, table.device, stream)
     else:
         _need_cuda(out, "out", table.dtype)
@@ -596,6 +612,8 @@ def kmassign_lookup(table, idx, weights=None, scale: float = 1.0, out=None, stre
                                    _stream_of(stream, table))
     if rc:
         _check(rc, "kmassign_lookup")
+    if given:
+        _written(out)
     return out
 
 
@@ -616,6 +634,7 @@ def kmassign_lookup_grad(dout, idx, K: int, weights=None, table=None, scale: flo
     if rows != N:
         raise ValueError("idx must hold one row of ids per row of dout")
     K = int(K)
+    given = dtable, dweights
     if weights is not None:
         _need_cuda(weights, "weights", torch.float32)
         _need_shape(weights, "weights", idx.shape)
@@ -648,6 +667,8 @@ def kmassign_lookup_grad(dout, idx, K: int, weights=None, table=None, scale: flo
         _stream_of(stream, dout))
     if rc:
         _check(rc, "kmassign_lookup_grad")
+    if given != (None, None):
+        _written(*given)
     return dtable, dweights
 
 
@@ -685,12 +706,15 @@ def kmassign_grad_norm(tensors, norm=None, stream=None):
     """The 2-norm over all elements of a list of tensors, an fp32 scalar on the GPU."""
     tensors = list(tensors)
     ptrs, sizes, codes = _tensor_arrays(tensors, "kmassign_grad_norm", "tensors")
+    given = norm is not None
     norm = _norm_out(tensors, norm, stream)
     rc = library().kmassign_grad_norm(_address(ptrs), _address(sizes), _address(codes),
                                       len(tensors), norm.data_ptr(),
                                       _stream_of(stream, norm))
     if rc:
         _check(rc, "kmassign_grad_norm")
+    if given:
+        _written(norm)
     return norm
 
 
@@ -713,12 +737,15 @@ def kmassign_clip(grads, max_norm: float, out=None, norm=None, stream=None):
             raise TypeError("out must have the gradients' types")
         if out_sizes != sizes:
             raise ValueError("out must have the gradients' sizes")
+    written = (grads if out is None else out) + ([] if norm is None else [norm])
     norm = _norm_out(grads, norm, stream)
     rc = library().kmassign_clip(_address(ptrs), None if outs is None else _address(outs),
                                  _address(sizes), _address(codes), len(grads), float(max_norm),
                                  norm.data_ptr(), _stream_of(stream, norm))
     if rc:
         _check(rc, "kmassign_clip")
+    if written:
+        _written(*written)
     return norm
 
 

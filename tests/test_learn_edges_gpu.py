@@ -278,3 +278,44 @@ def test_as_an_autograd_function(dev):  # noqa: F811
     # at most 90 terms an element of magnitude below 20
     assert (table.grad - t.grad).abs().max() <= 100 * U * 90 * 20
     assert (weights.grad - v.grad).abs().max() <= 10 * U * 6 * 20
+
+
+def test_writes_to_given_tensors_are_seen_by_autograd(dev):  # noqa: F811
+    """Every tensor of the caller that a call writes to counts a version, so that a backward pass
+    that has saved it raises; the inputs' versions stay."""
+    x, big = torch.randn(8, 16, device=dev), torch.randn(8, 16, device=dev)
+    i = torch.zeros(8, 2, dtype=torch.int32, device=dev)
+    w = torch.ones(8, 2, device=dev)
+
+    def f(*shape):
+        return torch.zeros(shape, device=dev)
+
+    def z(*shape):
+        return torch.zeros(shape, dtype=torch.int32, device=dev)
+    cases = [
+        (lambda o: km.kmassign_route(x, 2, idx=o[0], weights=o[1]), [z(8, 2), f(8, 2)]),
+        (lambda o: km.kmassign_route(x, 2, weights=o[0]), [f(8, 2)]),
+        (lambda o: km.kmassign_route_grad(x, i, w, dlogits=o[0]), [f(8, 16)]),
+        (lambda o: km.kmassign_lists(i, 4, order=o[0], offsets=o[1]), [z(16), z(5)]),
+        (lambda o: km.kmassign_lookup(x, i, out=o[0]), [f(8, 16)]),
+        (lambda o: km.kmassign_lookup_grad(x, i, 8, weights=w, table=big, dtable=o[0], dweights=o[1]),
+         [f(8, 16), f(8, 2)]),
+        (lambda o: km.kmassign_lookup_grad(x, i, 8, dtable=o[0], accumulate=True), [f(8, 16)]),
+        (lambda o: km.kmassign_grad_norm([x], norm=o[0]), [f()]),
+        (lambda o: km.kmassign_clip([o[0], o[1]], 1.0, norm=o[2]), [big.clone(), f(3), f()]),
+        (lambda o: km.kmassign_clip([x], 1.0, out=[o[0]]), [f(8, 16)]),
+    ]
+    for call, outs in cases:
+        versions = [o._version for o in outs]
+        call(outs)
+        assert all(o._version > v for o, v in zip(outs, versions))
+    assert x._version == i._version == w._version == 0
+    p = torch.randn(8, 16, device=dev, requires_grad=True)
+    y = (p * big).sum()
+    km.kmassign_clip([big], 1e-3)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        inner = torch.ones(8, 16, device=dev)
+        km.kmassign_clip([inner], 1.0)
+    km.kmassign_clip([inner], 1.0)
