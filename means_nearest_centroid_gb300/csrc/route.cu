@@ -12,6 +12,7 @@
 // rounded operation or one expf, in a fixed order, so that a row's choice does
 // not depend on the batch.
 #include "internal.h"
+#include "reciprocal.cuh"
 #include "vec.cuh"
 
 #include <algorithm>
@@ -59,18 +60,6 @@ __device__ __forceinline__ float row_sum(float v)
 __device__ __forceinline__ bool is_masked(float x) { return !(x > -INFINITY); }
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
-
-// 1 / y correctly rounded for 1 <= y <= 2^125: one Newton step with fused
-// multiply-adds from the hardware's approximation, which is within one ulp
-// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990; on GB300 it gave the quotient's bits for all 2^23
-// significands).
-__device__ __forceinline__ float reciprocal(float y)
-{
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
-    return fmaf(r, fmaf(-y, r, 1.0f), r);
-}
 
 struct RouteArgs {
     const void *logits;

@@ -2,10 +2,15 @@
 
 Tolerances and helpers are those of test_learn_gpu."""
 
+import ctypes
+import os
+import subprocess
+
 import pytest
 import torch
 
 import means_nearest_centroid_gb300 as km
+from means_nearest_centroid_gb300 import _build
 from test_learn_gpu import INF, NAN, U, check_clip, dev, make_grads, weight_bound  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -101,6 +106,47 @@ def test_route_grad_of_repeated_experts(dev, N, E, k, score, renorm):  # noqa: F
         size += 1.5 * s.detach() * amean
     bound = (2 * weight_bound(x.detach().numpy(), k) + (k + 1) * U) * size.numpy() + 2 ** -120
     assert ((d.cpu().double() - x.grad).abs().numpy() <= bound).all()
+
+
+def test_reciprocal_has_the_quotient_s_bits(dev, tmp_path):  # noqa: F811
+    """Routing's reciprocal against the division, for every significand and exponents of its range."""
+    lib = str(tmp_path / "libreciprocal_check.so")
+    source = os.path.join(os.path.dirname(os.path.abspath(__file__)), "reciprocal_check.cu")
+    subprocess.run([_build.nvcc(), *_build.NVCC_FLAGS, "-shared", "-I", _build.CSRC, source, "-o", lib], check=True)
+    check = ctypes.CDLL(lib).reciprocal_check
+    check.argtypes, check.restype = [ctypes.c_int, ctypes.c_void_p], ctypes.c_int
+    count = torch.zeros(1, dtype=torch.int32, device=dev)
+    torch.cuda.synchronize()
+    for e in [*range(0, 125, 31), 1, 2, 123]:
+        assert check(e, count.data_ptr()) == 0
+        torch.cuda.synchronize()
+        assert count.item() == 0, e
+
+
+@pytest.mark.parametrize("E", [8, 16, 64, 100])
+def test_choice_does_not_depend_on_the_batch(dev, E):  # noqa: F811
+    """Sigmoids near 1 take few values, so a last bit decides an order; a logit below -87 in a
+    warp has all its scores formed by divisions.  The same choice with and without it."""
+    N, k = 64, min(E, 32)
+    gen = torch.Generator().manual_seed(E)
+    X = 8 + 9 * torch.rand(N, E, generator=gen)
+    X[::3] = 4 * torch.randn(X[::3].shape, generator=gen)
+    bias = torch.zeros(E, device=dev)
+
+    def choice(x):
+        return km.kmassign_route(x.to(dev), k, score="sigmoid", bias=bias)
+    idx, w = choice(X)
+    low = X.clone()
+    low[1::2, 0] = -100.0                     # every second row: one at least in each warp
+    got, v = choice(low)
+    assert torch.equal(got[::2], idx[::2]) and torch.equal(v[::2], w[::2])
+    for i in (0, 2, 6, N - 2):
+        one, u = choice(X[i: i + 1])
+        assert torch.equal(one[0], idx[i]) and torch.equal(u[0], w[i])
+    # by the fp32 quotients themselves, with and without such a logit in the row
+    for x, chosen in ((X, idx), (low, got)):
+        s = (1.0 / (1.0 + torch.exp(-x.to(dev))).double()).float()
+        assert torch.equal(chosen.long(), s.sort(dim=1, descending=True, stable=True).indices[:, :k])
 
 
 # ---- clipping -------------------------------------------------------------------
