@@ -6,12 +6,14 @@ import ctypes
 import os
 import subprocess
 
+import numpy as np
 import pytest
 import torch
 
 import means_nearest_centroid_gb300 as km
 from means_nearest_centroid_gb300 import _build
-from test_learn_gpu import INF, NAN, U, check_clip, dev, make_grads, weight_bound  # noqa: F401
+from test_learn_gpu import (  # noqa: F401
+    INF, NAN, TYPES, U, check_clip, dev, f64, make_grads, make_logits, ref_choice, ref_keys, ref_weights, weight_bound)
 
 pytestmark = pytest.mark.gpu
 
@@ -106,6 +108,92 @@ def test_route_grad_of_repeated_experts(dev, N, E, k, score, renorm):  # noqa: F
         size += 1.5 * s.detach() * amean
     bound = (2 * weight_bound(x.detach().numpy(), k) + (k + 1) * U) * size.numpy() + 2 ** -120
     assert ((d.cpu().double() - x.grad).abs().numpy() <= bound).all()
+
+
+def selected_weight_bound(x, idx, scored):
+    """Relative bound of a row's weights, from its own selected logits: expf (2 ulp), the rounding
+    of x - max (relative |x - max| U), sums of E and of k terms, a division and two products."""
+    E, k = x.shape[1], idx.shape[1]
+    at = np.take_along_axis(x, np.maximum(idx, 0), 1)
+    top = np.max(np.where(np.isnan(x), -INF, x), 1, keepdims=True)
+    with np.errstate(invalid="ignore"):
+        away = np.where(idx >= 0, np.minimum(np.abs(at - top), 104.0), 0.0)
+    if scored == "sigmoid":
+        away = np.zeros_like(away)            # exp(-x) takes x as it is
+    return (2 * away + E / 8 + k + 12) * 2 * U
+
+
+@pytest.mark.parametrize("top", [1, 2])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("N,E,k,groups,topk", [(400, 256, 8, 8, 4), (300, 72, 6, 6, 3), (300, 16, 2, 4, 2),
+                                               (128, 512, 16, 16, 7), (40, 1024, 8, 16, 5), (200, 256, 8, 1, 1)])
+def test_route_with_bias_row_by_row(dev, N, E, k, groups, topk, score, top):  # noqa: F811
+    """The whole choice with a bias and groups: a row may differ from the 64-bit one only where its
+    own deciding group sums, or its own deciding keys, are closer than their fp32 error; in no row
+    is an expert named twice, out of range, masked or outside topk groups.  Keys: a score of at
+    most 1 and a bias below 1.1, each rounding at most 2 U of 2; a softmax's scores relatively
+    (2 |x - max| + E / 8 + 12) U of at most exp(x - max), so at most (2 / e + E / 8 + 12) U."""
+    gen = torch.Generator().manual_seed(E + k)
+    X = make_logits(N, E, torch.float32, N + 1)
+    bias = 0.2 * torch.randn(E, generator=gen)
+    bias.clamp_(-1.0, 1.0)
+    x, b = f64(X), f64(bias)
+    key, s = ref_keys(x, score, b, 1, 1, top)             # all groups' keys
+    per = E // groups
+    m = -np.sort(-key.reshape(N, groups, per), 2)[:, :, :top]
+    of_group = np.where(m[:, :, 0] == -INF, -INF, np.where(m == -INF, 0.0, m).sum(2))
+    tol = 2 * (2 / np.e + E / 8 + 12 + 4) * U             # of two keys' difference
+    idx, w = km.kmassign_route(X.to(dev), k, score=score, bias=bias.to(dev), groups=groups,
+                               topk_groups=topk, group_top=top, renorm=False)
+    got = idx.cpu().numpy()
+    differ = 0
+    for i in range(N):
+        mine = got[i][got[i] >= 0]
+        assert len(set(mine.tolist())) == len(mine) and (mine < E).all() and (key[i, mine] > -INF).all()
+        assert (got[i][len(mine):] == -1).all()           # free slots come last
+        chosen = set((mine // per).tolist())
+        assert len(chosen) <= topk
+        order = np.argsort(-of_group[i], kind="stable")
+        kept = set(order[:topk].tolist())
+        if groups > topk:
+            last, next_ = of_group[i, order[topk - 1]], of_group[i, order[topk]]
+            if next_ > -INF and last - next_ <= 2 * tol:  # a near-tie of groups: either side is right
+                edge = {g for g in range(groups) if abs(of_group[i, g] - last) <= 4 * tol}
+                assert chosen <= kept | edge
+                differ += 1
+                continue
+        allowed = np.where(np.isin(np.arange(E) // per, list(kept)), key[i], -INF)
+        want = ref_choice(allowed[None], k)[0]
+        assert np.array_equal(got[i] < 0, want < 0)
+        on = want >= 0
+        assert (np.abs(key[i, got[i][on]] - key[i, want[on]]) <= tol).all() and (allowed[mine] > -INF).all()
+    assert differ <= N // 20
+    ref = ref_weights(x, s, got, score, False, 1.0)
+    assert (np.abs(f64(w) - ref) <= selected_weight_bound(x, got, score) * ref + 2 ** -125).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("N,E,k", [(64, 8, 8), (40, 64, 6), (30, 200, 16), (65, 256, 8), (8, 1024, 32)])
+def test_route_weights_by_their_own_logits(dev, N, E, k, score, renorm, dtype):  # noqa: F811
+    """Weights to the bound of the logits that were selected, not of the lowest in the matrix."""
+    X = make_logits(N, E, dtype, seed=E)
+    x = f64(X)
+    idx, w = km.kmassign_route(X.to(dev), k, score=score, renorm=renorm, scale=2.5)
+    got = idx.cpu().numpy()
+    key, s = ref_keys(x, score, None, 1, 1, 2)
+    assert np.array_equal(got, ref_choice(key, k))
+    ref = ref_weights(x, s, got, score, renorm, 2.5)
+    assert (np.abs(f64(w) - ref) <= selected_weight_bound(x, got, score) * ref + 2 ** -125).all()
+
+
+def test_route_softmax_with_bias_and_an_infinite_logit(dev):  # noqa: F811
+    """Every score of the row is NaN, so every key is, and none is selected."""
+    X = torch.zeros(3, 12, device=dev)
+    X[1, 4] = INF
+    idx, w = km.kmassign_route(X, 2, bias=torch.zeros(12, device=dev))
+    assert idx.tolist() == [[0, 1], [-1, -1], [0, 1]] and w[1].tolist() == [0.0, 0.0]
 
 
 def test_reciprocal_has_the_quotient_s_bits(dev, tmp_path):  # noqa: F811
