@@ -108,10 +108,11 @@ def load_traffic(kernel_sha: str):
 
 
 # The sources assign_kernel is compiled from: a stored ncu traffic record is
-# reported only while these are unchanged.
+# reported only while these are unchanged.  (Of include/kmassign.h the kernels
+# take status codes only, which change no traffic.)
 ASSIGN_KERNEL_SOURCES = [os.path.join("means_nearest_centroid_gb300", "csrc", f)
-                         for f in ("assign.cu", "pipeline.cuh", "ptx.cuh", "internal.h")] + \
-                        [os.path.join("include", "kmassign.h")]
+                         for f in ("assign.cu", "pipeline.cuh", "ptx.cuh", "internal.h",
+                                   "norm_math.cuh")]
 
 
 def kernel_source_sha() -> str:

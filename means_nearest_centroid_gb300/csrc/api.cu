@@ -2,6 +2,7 @@
 // TMA descriptors and launches.  No arithmetic of the method lives here.
 #include "kmassign.h"
 #include "internal.h"
+#include "learn.h"
 
 #include <cudaTypedefs.h>
 

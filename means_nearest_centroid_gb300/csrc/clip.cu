@@ -15,8 +15,8 @@
 // the last square is known, and little of a large model's gradients stays in
 // L2): 294 M fp32 elements take 540 us, 6.5 TB/s of those 3.5 GB; ten tensors of
 // 1.8 MB in all take 10 us, two launches' latency.
-#include "internal.h"
 #include "launch.cuh"
+#include "learn.h"
 #include "vec.cuh"
 
 #include <algorithm>

@@ -2,7 +2,7 @@
 // clipping: argument checks, temporaries and launches.  No arithmetic of the
 // operators lives here.
 #include "kmassign.h"
-#include "internal.h"
+#include "learn.h"
 
 #include <algorithm>
 #include <cmath>

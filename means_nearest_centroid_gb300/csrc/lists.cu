@@ -24,8 +24,8 @@
 //
 // offsets are found by a search in the sorted rows within the row's last digit,
 // eight ways at a step: a third of bisection's dependent loads.
-#include "internal.h"
 #include "launch.cuh"
+#include "learn.h"
 
 #include <cooperative_groups.h>
 

@@ -17,8 +17,8 @@
 // rows of 2,048 (1.07 GB, 140 us) that hides the sort: the gradient of 16,384
 // tokens takes 191 us, where blocks that zeroed the rows without ids after the
 // same sort took 42 us longer.
-#include "internal.h"
 #include "launch.cuh"
+#include "learn.h"
 #include "vec.cuh"
 
 #include <algorithm>

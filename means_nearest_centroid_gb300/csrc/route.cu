@@ -11,7 +11,7 @@
 // equal keys the lower index comes first.  Each fp32 step is one correctly
 // rounded operation or one expf, in a fixed order, so that a row's choice does
 // not depend on the batch.
-#include "internal.h"
+#include "learn.h"
 #include "reciprocal.cuh"
 #include "vec.cuh"
 
