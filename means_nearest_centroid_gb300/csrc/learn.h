@@ -61,10 +61,10 @@ cudaError_t lists_prepare();
 // NULL, not both); scratch (16-byte aligned) of lists_scratch_bytes.  Places
 // past offsets[K] hold -1 in order and nothing in particular in rows.
 // zero_bytes (even) at zero are zeroed besides.
-size_t lists_scratch_bytes(int64_t M, int64_t K);
+size_t lists_scratch_bytes(int64_t M, int64_t K, int sms);
 cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *order, int32_t *rows,
                          int32_t *offsets, int32_t *total, void *scratch, void *zero,
-                         size_t zero_bytes, cudaStream_t stream);
+                         size_t zero_bytes, int sms, cudaStream_t stream);
 cudaError_t launch_lookup(const void *table, int dtype, int64_t K, int64_t D, const int32_t *idx,
                           const float *weights, int64_t N, int32_t k, float scale, void *out,
                           int sms, cudaStream_t stream);

@@ -212,10 +212,11 @@ int kmassign_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *order, int
     int sms;
     if ((rc = kma::library_device(&pool, &sms)) != KMASSIGN_OK)
         return rc;
-    Scratch scratch(kma::lists_scratch_bytes(M, K), pool, s);
+    Scratch scratch(kma::lists_scratch_bytes(M, K, sms), pool, s);
     if (!scratch.ok())
         return KMASSIGN_ERR_CUDA;
-    rc = done(kma::launch_lists(idx, M, K, order, nullptr, offsets, nullptr, scratch.get(), nullptr, 0, s));
+    rc = done(kma::launch_lists(idx, M, K, order, nullptr, offsets, nullptr, scratch.get(), nullptr,
+                                0, sms, s));
     return scratch.release() ? rc : KMASSIGN_ERR_CUDA;
 }
 
@@ -283,7 +284,7 @@ int kmassign_lookup_grad(const void *dout, int32_t dtype, const int32_t *idx, co
         return KMASSIGN_OK;
     // one allocation: order, sorted rows, their number, the sort's scratch, row parts
     const size_t ids = up16(static_cast<size_t>(M) * 4);
-    const size_t sort = up16(kma::lists_scratch_bytes(M, K));
+    const size_t sort = up16(kma::lists_scratch_bytes(M, K, sms));
     Scratch scratch(2 * ids + 16 + sort + kma::lookup_grad_parts_bytes(M, D, sms), pool, s);
     if (!scratch.ok())
         return KMASSIGN_ERR_CUDA;
@@ -294,7 +295,7 @@ int kmassign_lookup_grad(const void *dout, int32_t dtype, const int32_t *idx, co
     p += 2 * ids + 16;
     cudaError_t e = kma::launch_lists(
         idx, M, K, order, rows, nullptr, total, p, accumulate ? nullptr : dtable,
-        accumulate ? 0 : static_cast<size_t>(K) * D * kma::dtype_bytes(grad_dtype), s);
+        accumulate ? 0 : static_cast<size_t>(K) * D * kma::dtype_bytes(grad_dtype), sms, s);
     if (e == cudaSuccess && M > 0)
         e = kma::launch_lookup_grad(dout, dtype, idx, weights, table, M, k, K, D, scale, padding,
                                     accumulate != 0, order, rows, total,

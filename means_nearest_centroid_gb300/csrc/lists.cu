@@ -3,7 +3,7 @@
 // outside [0, K) left out; offsets[r] is where row r's group begins.
 //
 // A radix sort of (row, position) pairs from the lowest digit up.  Each of up
-// to 304 blocks owns one contiguous share of the pairs, so the order within a
+// to two blocks an SM owns one contiguous share of the pairs, so the order within a
 // digit is: earlier blocks first, then the block's own items in order.  Per digit
 //   count:    block b counts its items -> H[b][digit];
 //   scatter:  block b sums H[b'][digit] over the blocks b' before it and over
@@ -38,7 +38,7 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxDigitBits = 10;
-constexpr int kMaxBlocks = 304;           // two on each SM
+constexpr int kBlocksPerSm = 2;            // of kThreads
 constexpr int64_t kOneBlockMax = 2048;     // 3,000 ids: 14.5 us a call by one block, 12.2 by eight; 1,100: 14.1, 15.7
 constexpr int64_t kOneOffsetsMax = 8192;   // rows whose offsets the one block finds itself
 constexpr int kOneBits = 8;                // digit of the one-block sort
@@ -46,7 +46,6 @@ constexpr int kClusterBlocks = 8;
 constexpr int kClusterThreads = 1024;
 constexpr int kClusterItems = 2;           // a thread
 constexpr int64_t kClusterMax = int64_t(kClusterBlocks) * kClusterThreads * kClusterItems;
-constexpr unsigned kClusterFill = 120;     // blocks besides: clusters that run at once with the first
 constexpr int kOneBins = 1 << kOneBits;
 
 // Exclusive scan over the block of one value per thread; *total: the sum.
@@ -662,18 +661,19 @@ int digits(int64_t K, int most, int32_t *bits, int32_t *shift)
     return passes;
 }
 
-SortPlan sort_plan(int64_t M, int64_t K)
+SortPlan sort_plan(int64_t M, int64_t K, int sms)
 {
+    const int64_t most = int64_t(sms) * kBlocksPerSm;
     SortPlan p{};
     p.passes = digits(K, kMaxDigitBits, p.bits, p.shift);
     // the smallest tiles of which every block has one, else large ones in turn
     p.items = 8;
     for (int items = 4; items >= 2; items >>= 1)
-        if (M <= int64_t(kMaxBlocks) * kThreads * items)
+        if (M <= most * kThreads * items)
             p.items = items;
     const int64_t tile = int64_t(kThreads) * p.items;
     const int64_t tiles = (M + tile - 1) / tile;
-    const int64_t per = (tiles + kMaxBlocks - 1) / kMaxBlocks;
+    const int64_t per = (tiles + most - 1) / most;
     p.share = per * tile;
     p.blocks = static_cast<int>((M + p.share - 1) / p.share);
     return p;
@@ -689,12 +689,12 @@ int32_t fill_parts(size_t bytes, int32_t launches)
 
 // Blocks of `threads` threads that fill a share: 16 KiB or more each, at most
 // as many as the SMs hold.
-unsigned fill_blocks(const Fill &f, int threads)
+unsigned fill_blocks(const Fill &f, int threads, int sms)
 {
     if (!f.any())
         return 0;
     return static_cast<unsigned>(
-        std::min<int64_t>(f.bytes / f.parts / 16384 + 1, kMaxBlocks * 1024 / threads));
+        std::min<int64_t>(f.bytes / f.parts / 16384 + 1, int64_t(sms) * 2048 / threads));
 }
 
 cudaError_t launch_offsets(const int32_t *rows, const int32_t *total, const int32_t *starts,
@@ -705,13 +705,13 @@ cudaError_t launch_offsets(const int32_t *rows, const int32_t *total, const int3
 }
 
 template <bool FIRST>
-cudaError_t sort_pass(SortArgs &a, int items, cudaStream_t stream)
+cudaError_t sort_pass(SortArgs &a, int items, int sms, cudaStream_t stream)
 {
     const cudaError_t e = launch_after(lists_count_kernel<FIRST>, static_cast<unsigned>(a.blocks),
                                        kThreads, static_cast<size_t>(a.bins) * 4, stream, a);
     if (e != cudaSuccess)
         return e;
-    const unsigned blocks = static_cast<unsigned>(a.blocks) + fill_blocks(a.fill, kThreads);
+    const unsigned blocks = static_cast<unsigned>(a.blocks) + fill_blocks(a.fill, kThreads, sms);
     const size_t smem = scatter_smem(a.bins, items);
     switch (items) {
     case 2:
@@ -740,13 +740,13 @@ cudaError_t lists_prepare()
                                 kClusterSmem);
 }
 
-size_t lists_scratch_bytes(int64_t M, int64_t K)
+size_t lists_scratch_bytes(int64_t M, int64_t K, int sms)
 {
     if (M <= kOneBlockMax)
         return K <= kOneOffsetsMax ? 0 : 16 + static_cast<size_t>(M) * 4;
     if (M <= kClusterMax)   // total, the last digit's starts, the sorted rows
         return 16 + up16((size_t(4) << kMaxDigitBits) + 4) + up16(static_cast<size_t>(M) * 4);
-    const SortPlan p = sort_plan(M, K);
+    const SortPlan p = sort_plan(M, K, sms);
     // total, the digits' counts, two sets of pairs (the second set's rows may
     // stand in for the sorted rows)
     size_t n = 16;
@@ -759,7 +759,7 @@ size_t lists_scratch_bytes(int64_t M, int64_t K)
 
 cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *order, int32_t *rows,
                          int32_t *offsets, int32_t *total, void *scratch, void *zero,
-                         size_t zero_bytes, cudaStream_t stream)
+                         size_t zero_bytes, int sms, cudaStream_t stream)
 {
     cudaError_t e = cudaSuccess;
     Fill fill{static_cast<uint8_t *>(zero), static_cast<int64_t>(zero_bytes), 0, 1};
@@ -772,12 +772,12 @@ cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *orde
             rows = static_cast<int32_t *>(scratch) + 4;
         fill.parts = fill_parts(zero_bytes, 1);
         if (M <= 1024)
-            e = launch_after(lists_one_block_kernel<256, 4>, 1 + fill_blocks(fill, 256), 256, 0,
-                             stream, idx, M, K, row_bits(K), order, rows,
+            e = launch_after(lists_one_block_kernel<256, 4>, 1 + fill_blocks(fill, 256, sms), 256,
+                             0, stream, idx, M, K, row_bits(K), order, rows,
                              own, total, fill);
         else
-            e = launch_after(lists_one_block_kernel<1024, 2>, 1 + fill_blocks(fill, 1024), 1024, 0,
-                             stream, idx, M, K, row_bits(K), order, rows,
+            e = launch_after(lists_one_block_kernel<1024, 2>, 1 + fill_blocks(fill, 1024, sms), 1024,
+                             0, stream, idx, M, K, row_bits(K), order, rows,
                              own, total, fill);
         if (e == cudaSuccess && search)
             e = launch_offsets(rows, total, nullptr, 0, K, offsets, stream);
@@ -803,16 +803,20 @@ cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *orde
         a.K = static_cast<int32_t>(K);
         fill.parts = fill_parts(zero_bytes, 1);
         a.fill = fill;
+        // clusters that fill: on four fifths of the SMs (120 blocks of GB300's 152), so that they
+        // run at once with the one that sorts
+        const unsigned most = std::max<unsigned>(
+            kClusterBlocks, static_cast<unsigned>(sms) * 4 / 5 / kClusterBlocks * kClusterBlocks);
         const unsigned blocks =
             kClusterBlocks +
-            (std::min(fill_blocks(fill, kClusterThreads), kClusterFill) + kClusterBlocks - 1) /
+            (std::min(fill_blocks(fill, kClusterThreads, sms), most) + kClusterBlocks - 1) /
                 kClusterBlocks * kClusterBlocks;
         e = launch_after(lists_cluster_kernel, blocks, kClusterThreads, kClusterSmem, stream, a);
         if (e == cudaSuccess && a.starts != nullptr)
             e = launch_offsets(a.rows, a.total, a.starts, a.shift[a.passes - 1], K, offsets, stream);
         return e;
     }
-    const SortPlan p = sort_plan(M, K);
+    const SortPlan p = sort_plan(M, K, sms);
     const size_t ids = up16(static_cast<size_t>(M) * 4);
     uint8_t *at = static_cast<uint8_t *>(scratch);
     if (total == nullptr)
@@ -855,7 +859,8 @@ cudaError_t launch_lists(const int32_t *idx, int64_t M, int64_t K, int32_t *orde
         a.shift = p.shift[i];
         a.bins = 1 << p.bits[i];
         a.blocks = p.blocks;
-        e = i == 0 ? sort_pass<true>(a, p.items, stream) : sort_pass<false>(a, p.items, stream);
+        e = i == 0 ? sort_pass<true>(a, p.items, sms, stream)
+                   : sort_pass<false>(a, p.items, sms, stream);
     }
     if (e == cudaSuccess && p.passes > 1 && offsets != nullptr)
         e = launch_offsets(sorted, total, starts, p.shift[p.passes - 1], K, offsets, stream);
