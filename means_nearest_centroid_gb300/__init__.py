@@ -426,20 +426,18 @@ def _need_float(t, name) -> int:
     raise ValueError(f"{name} must be contiguous")
 
 
-def _need_detached(where, **inputs):
-    """Raises for inputs that require grad in grad mode: results are not part of autograd's graph."""
-    for name, t in inputs.items():
-        if t is not None and t.requires_grad:
-            raise RuntimeError(
-                f"{where}: {name} requires grad, and autograd would not see the result; call it "
-                "under torch.no_grad() or in a torch.autograd.Function (gradients: "
-                "kmassign_route_grad, kmassign_lookup_grad)")
+def _need_detached(where, name):
+    """In grad mode, raises for an input that requires grad: no result is part of autograd's graph."""
+    if torch.is_grad_enabled():
+        raise RuntimeError(
+            f"{where}: {name} requires grad, and autograd would not see the result; call it "
+            "under torch.no_grad() or in a torch.autograd.Function (gradients: "
+            "kmassign_route_grad, kmassign_lookup_grad)")
 
 
-def _written(*tensors):
-    """Tells autograd that a call wrote to these tensors of the caller (None: to one of its own), as
-    torch's in-place operations do: a backward pass that has saved one raises."""
-    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+# Tells autograd that a call wrote to these tensors of the caller, as torch's in-place operations
+# do: a backward pass that has saved one raises.
+_written = torch.autograd.graph.increment_version
 
 
 def _need_shape(t, name, shape):
@@ -494,8 +492,8 @@ def kmassign_route(logits, k: int, score: str = "softmax", bias=None, groups: in
     """
     dtype = _need_float(logits, "logits")
     N, E = _need_matrix(logits, "logits")
-    if torch.is_grad_enabled():
-        _need_detached("kmassign_route", logits=logits)
+    if logits.requires_grad:
+        _need_detached("kmassign_route", "logits")
     k, groups = int(k), int(groups)
     if bias is not None:
         _need_cuda(bias, "bias", torch.float32)
@@ -518,7 +516,7 @@ def kmassign_route(logits, k: int, score: str = "softmax", bias=None, groups: in
     if rc:
         _check(rc, "kmassign_route")
     if given != (None, None):
-        _written(*given)
+        _written([t for t in given if t is not None])
     return idx, weights
 
 
@@ -538,8 +536,8 @@ def kmassign_route_grad(logits, idx, dweights, score: str = "softmax", renorm: b
     _need_shape(idx, "idx", (N, k))
     _need_cuda(dweights, "dweights", torch.float32)
     _need_shape(dweights, "dweights", (N, k))
-    if torch.is_grad_enabled():
-        _need_detached("kmassign_route_grad", logits=logits, dweights=dweights)
+    if logits.requires_grad or dweights.requires_grad:
+        _need_detached("kmassign_route_grad", "logits or dweights")
     given = dlogits is not None
     if not given:
         dlogits = _new((N, E), logits.dtype, logits.device, stream)
@@ -553,7 +551,7 @@ def kmassign_route_grad(logits, idx, dweights, score: str = "softmax", renorm: b
     if rc:
         _check(rc, "kmassign_route_grad")
     if given:
-        _written(dlogits)
+        _written([dlogits])
     return dlogits
 
 
@@ -582,7 +580,7 @@ def kmassign_lists(idx, K: int, order=None, offsets=None, stream=None):
     if rc:
         _check(rc, "kmassign_lists")
     if given != (None, None):
-        _written(*given)
+        _written([t for t in given if t is not None])
     return order, offsets
 
 
@@ -599,8 +597,8 @@ def kmassign_lookup(table, idx, weights=None, scale: float = 1.0, out=None, stre
     if weights is not None:
         _need_cuda(weights, "weights", torch.float32)
         _need_shape(weights, "weights", idx.shape)
-    if torch.is_grad_enabled():
-        _need_detached("kmassign_lookup", table=table, weights=weights)
+    if table.requires_grad or (weights is not None and weights.requires_grad):
+        _need_detached("kmassign_lookup", "table or weights")
     given = out is not None
     if not given:
         out = _new((N, D), table.dtype, table.device, stream)
@@ -613,7 +611,7 @@ def kmassign_lookup(table, idx, weights=None, scale: float = 1.0, out=None, stre
     if rc:
         _check(rc, "kmassign_lookup")
     if given:
-        _written(out)
+        _written([out])
     return out
 
 
@@ -649,9 +647,9 @@ def kmassign_lookup_grad(dout, idx, K: int, weights=None, table=None, scale: flo
             _need_shape(dweights, "dweights", idx.shape)
     elif dweights is not None:
         raise ValueError("dweights needs weights")
-    if torch.is_grad_enabled():
-        _need_detached("kmassign_lookup_grad", dout=dout, weights=weights,
-                       table=None if weights is None else table)
+    if dout.requires_grad or (weights is not None and
+                              (weights.requires_grad or table.requires_grad)):
+        _need_detached("kmassign_lookup_grad", "dout, weights or table")
     if dtable is None:
         if accumulate:
             raise ValueError("accumulate needs a given dtable")
@@ -668,24 +666,43 @@ def kmassign_lookup_grad(dout, idx, K: int, weights=None, table=None, scale: flo
     if rc:
         _check(rc, "kmassign_lookup_grad")
     if given != (None, None):
-        _written(*given)
+        _written([t for t in given if t is not None])
     return dtable, dweights
 
 
+_contiguous, _pointer, _size = (torch.Tensor.is_contiguous, torch.Tensor.data_ptr,
+                                torch.Tensor.numel)
+
+
+def _need_floats(tensors, where, name):
+    """The kmassign_dtypes of a list of tensors; raises for one that cannot be taken."""
+    codes = [_need_float(t, name) for t in tensors]
+    if any(t.requires_grad for t in tensors):
+        _need_detached(where, f"one of {name}")
+    return codes
+
+
 def _tensor_arrays(tensors, where, name):
-    """Pointers, sizes and type codes of a list of tensors, as C arrays."""
+    """Pointers, sizes and type codes of a list of tensors, as C arrays.
+
+    Past the first tensor, which memory they are in is left to the library's own
+    check (``_check_tensors`` tells the detail).
+    """
     try:   # the common case in few steps a tensor; the detail only on failure
-        codes = [_DTYPES[t.dtype] for t in tensors
-                 if t.is_cuda and t.is_contiguous() and not t.requires_grad]
-    except (AttributeError, KeyError):
-        codes = []
-    if len(codes) != len(tensors):
-        codes = [_need_float(t, name) for t in tensors]
-        if torch.is_grad_enabled():
-            for t in tensors:
-                _need_detached(where, **{name: t})
-    return (array.array("Q", [t.data_ptr() for t in tensors]),
-            array.array("q", [t.numel() for t in tensors]), array.array("i", codes))
+        codes = [_DTYPES[t.dtype] for t in tensors if _contiguous(t) and not t.requires_grad]
+        plain = len(codes) == len(tensors) and (not tensors or tensors[0].is_cuda)
+    except (TypeError, KeyError):
+        plain = False
+    if not plain:
+        codes = _need_floats(tensors, where, name)
+    return (array.array("Q", list(map(_pointer, tensors))),
+            array.array("q", list(map(_size, tensors))), array.array("i", codes))
+
+
+def _check_tensors(code, where, **lists):
+    for name, tensors in lists.items():
+        _need_floats(tensors or (), where, name)
+    _check(code, where)
 
 
 def _address(a):
@@ -712,9 +729,9 @@ def kmassign_grad_norm(tensors, norm=None, stream=None):
                                       len(tensors), norm.data_ptr(),
                                       _stream_of(stream, norm))
     if rc:
-        _check(rc, "kmassign_grad_norm")
+        _check_tensors(rc, "kmassign_grad_norm", tensors=tensors)
     if given:
-        _written(norm)
+        _written([norm])
     return norm
 
 
@@ -737,15 +754,16 @@ def kmassign_clip(grads, max_norm: float, out=None, norm=None, stream=None):
             raise TypeError("out must have the gradients' types")
         if out_sizes != sizes:
             raise ValueError("out must have the gradients' sizes")
-    written = (grads if out is None else out) + ([] if norm is None else [norm])
+    given = norm is not None
     norm = _norm_out(grads, norm, stream)
     rc = library().kmassign_clip(_address(ptrs), None if outs is None else _address(outs),
                                  _address(sizes), _address(codes), len(grads), float(max_norm),
                                  norm.data_ptr(), _stream_of(stream, norm))
     if rc:
-        _check(rc, "kmassign_clip")
-    if written:
-        _written(*written)
+        _check_tensors(rc, "kmassign_clip", grads=grads, out=out)
+    _written(grads if out is None else out)
+    if given:
+        _written([norm])
     return norm
 
 

@@ -453,3 +453,18 @@ def test_writes_to_given_tensors_are_seen_by_autograd(dev):  # noqa: F811
         inner = torch.ones(8, 16, device=dev)
         km.kmassign_clip([inner], 1.0)
     km.kmassign_clip([inner], 1.0)
+
+
+def test_clip_tells_which_tensor_it_cannot_take(dev):  # noqa: F811
+    x = torch.randn(8, 16, device=dev)
+    for bad, error, text in ((torch.zeros(3), ValueError, "CUDA"), (x.T, ValueError, "contiguous"),
+                             (x.double(), TypeError, "float32"), ([1.0], TypeError, "Tensor")):
+        keep = x.clone()
+        for grads in ([x, bad], [bad, x], [x, x[:2], bad]):
+            with pytest.raises(error, match=text):
+                km.kmassign_clip(grads, 1e-3)
+            with pytest.raises(error, match=text):
+                km.kmassign_grad_norm(grads)
+            with pytest.raises((error, ValueError), match=f"{text}|sizes|one tensor"):
+                km.kmassign_clip([x] * len(grads), 1e-3, out=grads)
+        assert torch.equal(x, keep)
