@@ -596,17 +596,21 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_sparse_kernel(con
         p = c.on ? p / total : 0.0f;
         d = p * (c.g - row_sum<KW>(p * c.g));
     }
-    // an expert that a row names more than once: its first lane takes the sum
-    const uint32_t same =
-        __match_any_sync(kAll, c.on ? (lane / KW) << 16 | c.e : -1 - lane);
-    bool first = true;
-    if (__any_sync(kAll, (same & (same - 1)) != 0)) {
-        const uint32_t mine = same >> (lane & (32 - KW));   // of the row's lanes
-        first = (mine & ((1u << (lane & (KW - 1))) - 1u)) == 0;
+    // an expert that a row names more than once: its first lane takes the sum.  Each lane looks
+    // at the half of the others after it (a match over the lanes took 2 us more of 6)
+    const int32_t e = c.on ? c.e : -1;
+    bool again = false, first = true;
+#pragma unroll
+    for (int off = 1; off <= KW / 2; ++off)
+        again |= __shfl_sync(kAll, e, lane + off, KW) == e;
+    if (__any_sync(kAll, again && e >= 0)) {
         float sum = 0.0f;
         for (int j = 0; j < KW; ++j) {
             const float f = __shfl_sync(kAll, d, j, KW);
-            sum += (mine >> j) & 1u ? f : 0.0f;
+            if (__shfl_sync(kAll, e, j, KW) == e) {
+                sum += f;
+                first = first && j >= (lane & (KW - 1));
+            }
         }
         d = sum;
     }
@@ -616,9 +620,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_sparse_kernel(con
 }
 
 // The softmax over all experts: a gradient on each of them.  Lanes and experts
-// as in route_kernel; the row is read once.  30,011 x 72 bf16, k = 6: 7.2 us, of
-// which the 10 MB are 1.5: the rest is the latency of a row read, reduced twice
-// and written, by 12 blocks an SM.
+// as in route_kernel; the row is read once.  65,536 x 256 bf16, k = 8: 31 us, fp32
+// 35 (134 MB, 20 at HBM's rate); 30,011 x 72 bf16, k = 6: 9.3 us, of which the
+// 10 MB are 1.5.  The rest is latency: a row is read, reduced twice and written by
+// one warp, its selected experts marked and written again.  Finding experts named
+// twice by a match over the lanes took 39 us for 35, by shuffles 36.9; marking
+// before the reductions 37.2.
 template <typename T, int W, int V>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_dense_kernel(const RouteGradArgs a)
 {
@@ -692,15 +699,20 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_dense_kernel(cons
                 out[i] = Elem<T>::down(stage[i / V * kStride + i % V]);
         }
     }
-    // an expert that a row names more than once: its first place takes the sum
-    bool look = a.k > W;   // more places than lanes: looked for among all of them
-    if (!look) {
-        const uint32_t same = __match_any_sync(
-            kAll, e[0] >= 0 ? static_cast<int>(threadIdx.x & 31) / W << 16 | e[0]
-                            : -1 - static_cast<int>(threadIdx.x & 31));
-        look = __any_sync(kAll, (same & (same - 1)) != 0);
-    }
-    if (look) {
+    // an expert that a row names more than once: its first place takes the sum.  Every place
+    // marks its expert in shared memory; where another place's mark stands, there are two
+    __syncwarp();
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s)
+        if (e[s] >= 0)
+            stage[e[s]] = __int_as_float(s * W + lane);
+    __syncwarp();
+    bool again = false;
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s)
+        if (e[s] >= 0)
+            again |= __float_as_int(stage[e[s]]) != s * W + lane;
+    if (__any_sync(kAll, again)) {
         float sum[kSlots] = {};
         bool first[kSlots];
 #pragma unroll
