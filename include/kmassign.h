@@ -367,7 +367,12 @@ int kmassign_topk_ex(const void *X, const void *C, const float *cnorm, int64_t N
  * Every result is the same from run to run: no sum is formed by atomics on
  * floating values.  Outputs must not overlap inputs unless said so.
  */
-enum kmassign_dtype { KMASSIGN_FP32 = 0, KMASSIGN_BF16 = 1, KMASSIGN_FP16 = 2 };
+enum kmassign_dtype {
+    KMASSIGN_FP32 = 0,
+    KMASSIGN_BF16 = 1,
+    KMASSIGN_FP16 = 2,
+    KMASSIGN_E4M3 = 3   /* kmassign_experts' operands, kmassign_rmsnorm's output */
+};
 enum kmassign_score { KMASSIGN_SOFTMAX = 0, KMASSIGN_SIGMOID = 1 };
 
 /* Largest E kmassign_route accepts. */
@@ -487,6 +492,108 @@ int kmassign_grad_norm(const void *const *grads, const int64_t *sizes, const int
  */
 int kmassign_clip(const void *const *grads, void *const *out, const int64_t *sizes,
                   const int32_t *dtypes, int32_t n, float max_norm, float *norm, void *stream);
+
+/*
+ * ---- Experts behind a router ----------------------------------------------
+ * Products grouped by expert over the lists of kmassign_lists, in 16 or 8 bits,
+ * their gradients, and the root-mean-square norm in front of them.  The
+ * matrices of the products must be 16-byte aligned; F and D are multiples of 8
+ * (D of 16 in 8 bits), at most 65536.
+ */
+
+/* Largest E of the products. */
+#define KMASSIGN_EXPERTS_MAX 1024
+
+/*
+ * Products grouped by expert: for every position p, offsets[e] <= p <
+ * offsets[e + 1],
+ *     out[places[p]] = W[e] . X[rows[p] / slots]      (a row of F elements)
+ *   X         dtype [R, D]: KMASSIGN_BF16, _FP16, or _E4M3 with scales
+ *   W         dtype [E, F, D], 1 <= E <= KMASSIGN_EXPERTS_MAX
+ *   xscale    E4M3 only, fp32 [R, ceil(D / 128)]: X's values are code * scale,
+ *             one for each row and 128 columns
+ *   wscale    E4M3 only, fp32 [E, ceil(F / 128), ceil(D / 128)]: one for each
+ *             128 x 128 block of W[e]
+ *   offsets   int32 [E + 1], not descending, in [0, M] (kmassign_lists'); values
+ *             outside are clamped, lists that overlap give rows of either.  NULL
+ *             with E = 1: one list of all M positions (a plain product)
+ *   rows      int32 [M] or NULL (slots = 1, M <= R): position p takes row p.  With
+ *             kmassign_lists' order over ids [N, k] and slots = k the points'
+ *             own rows are taken.  An id that names no row gives a row of zeros
+ *   places    int32 [M] or NULL (M <= out_rows): position p goes to row p.  Ids
+ *             outside [0, out_rows) are not written, and rows that no position
+ *             names stay as they were; an id named twice holds either product
+ *   out       out_dtype [out_rows, F]: X's type or KMASSIGN_FP32; any of the three
+ *             types in 8 bits.  Without places the rows of positions of no list
+ *             (before offsets[0], from offsets[E] to M) are zeros; rows past M
+ *             stay as they were
+ * Products are summed in fp32 (the tensor cores' sums of 2,048 elements, in 8
+ * bits of one block of 128, added up rounded to nearest; in 8 bits each block's
+ * sum is multiplied by the fp32 product of its two scales) and rounded once.  A
+ * row's bits depend on neither the other rows nor the lists.
+ * M = 0 or out_rows = 0 writes nothing.  Errors: KMASSIGN_ERR_SHAPE also for E,
+ * slots, or M above R (without rows) or out_rows (without places), or R = 0 with
+ * places; F or D KMASSIGN_ERR_UNSUPPORTED_D; types KMASSIGN_ERR_ARG.
+ */
+int kmassign_experts(const void *X, int32_t dtype, int64_t R, int64_t D, const void *W, int64_t E,
+                     int64_t F, const float *xscale, const float *wscale, const int32_t *offsets,
+                     int64_t M, const int32_t *rows, int32_t slots, const int32_t *places,
+                     void *out, int32_t out_dtype, int64_t out_rows, void *stream);
+
+/*
+ * Gradients of kmassign_experts in 16 bits, dY_p = dout[places[p]]:
+ *     dX[r] = sum over p with rows[p] / slots == r of W[e]^T . dY_p
+ *     dW[e] = sum over p of list e of dY_p . X[rows[p] / slots]^T
+ *   dout   dtype [out_rows, F]
+ *   dX     dtype [R, D] or NULL, every row written (0 where no position names
+ *          it).  With rows each position's product is rounded to dtype before
+ *          the sum over positions (fp32, in the lists' order), as the forward
+ *          product of a row is
+ *   dW     dw_dtype [E, F, D] or NULL (not both), KMASSIGN_FP32 or dtype; zeros
+ *          for an expert without positions
+ * A position whose row or place does not exist adds nothing.  Everything else,
+ * and errors, as in kmassign_experts.
+ */
+int kmassign_experts_grad(const void *dout, int32_t dtype, int64_t out_rows, int64_t F,
+                          const void *X, int64_t R, int64_t D, const void *W, int64_t E,
+                          const int32_t *offsets, int64_t M, const int32_t *rows, int32_t slots,
+                          const int32_t *places, void *dX, void *dW, int32_t dw_dtype,
+                          void *stream);
+
+/*
+ * Root-mean-square norm of rows:
+ *     t = X + residual          (rounded to dtype, written to total; or t = X)
+ *     rstd = 1 / sqrt(mean over d of t^2 + eps),    y = t * rstd * weight
+ *   X, residual  dtype [N, D], 1 <= D <= 32768; residual may be NULL
+ *   weight       weight_dtype [D] (KMASSIGN_FP32 or dtype), or NULL: all 1
+ *   total        dtype [N, D], written with a residual (NULL without; may be X or
+ *                residual themselves)
+ *   out          y as dtype (may be X, or total), or as KMASSIGN_E4M3 codes with
+ *   scales       fp32 [N, ceil(D / 128)], written: the largest |y| of each 128
+ *                columns (at least 2^-100) / 448; code = e4m3(y / scale), to
+ *                nearest.  This is kmassign_experts' xscale
+ *   rstd         fp32 [N], written, or NULL
+ * Sums are fp32 (t^2 has to stay in fp32's range).  N = 0 launches nothing.
+ * Errors: D KMASSIGN_ERR_UNSUPPORTED_D; types, or eps negative or not finite
+ * KMASSIGN_ERR_ARG.
+ */
+int kmassign_rmsnorm(const void *X, int32_t dtype, int64_t N, int64_t D, const void *residual,
+                     const void *weight, int32_t weight_dtype, float eps, void *total, void *out,
+                     int32_t out_dtype, float *scales, float *rstd, void *stream);
+
+/*
+ * Gradients of kmassign_rmsnorm from that of y (of its output in dtype), with
+ * n = total * rstd and g = weight * dout:
+ *     dX = rstd * (g - n * mean over d of (g n)) + dtotal     (residual's too)
+ *     dweight[d] = sum over rows of dout * n
+ *   total    dtype [N, D]: t of the forward call; rstd fp32 [N], as it wrote it
+ *   dtotal   dtype [N, D] or NULL: the gradient that reaches t otherwise
+ *   dX       dtype [N, D], written (may be dout or dtotal)
+ *   dweight  fp32 [D], written, or NULL; fp32 sums in an order fixed by the sizes
+ */
+int kmassign_rmsnorm_grad(const void *dout, int32_t dtype, int64_t N, int64_t D, const void *total,
+                          const void *weight, int32_t weight_dtype, const float *rstd,
+                          const void *dtotal, void *dX, float *dweight, void *stream);
 
 /*
  * Bound, in nanoseconds of the GPU's global timer, on every pipeline wait in

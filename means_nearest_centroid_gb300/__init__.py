@@ -29,6 +29,7 @@ __all__ = [
     "kmassign_plan", "kmassign_plan_for", "kmassign_check", "kmassign_strerror", "assign", "norms", "assign_host",
     "kmassign_route", "kmassign_route_grad", "kmassign_lists", "kmassign_lookup",
     "kmassign_lookup_grad", "kmassign_grad_norm", "kmassign_clip",
+    "kmassign_experts", "kmassign_experts_grad", "kmassign_rmsnorm", "kmassign_rmsnorm_grad",
     "STATUS",
 ]
 
@@ -111,6 +112,16 @@ def _declare(lib):
     lib.kmassign_grad_norm.restype = i32
     lib.kmassign_clip.argtypes = [vp, vp, vp, vp, i32, f32, vp, vp]
     lib.kmassign_clip.restype = i32
+    lib.kmassign_experts.argtypes = [vp, i32, i64, i64, vp, i64, i64, vp, vp, vp, i64, vp, i32, vp,
+                                     vp, i32, i64, vp]
+    lib.kmassign_experts.restype = i32
+    lib.kmassign_experts_grad.argtypes = [vp, i32, i64, i64, vp, i64, i64, vp, i64, vp, i64, vp,
+                                          i32, vp, vp, vp, i32, vp]
+    lib.kmassign_experts_grad.restype = i32
+    lib.kmassign_rmsnorm.argtypes = [vp, i32, i64, i64, vp, vp, i32, f32, vp, vp, i32, vp, vp, vp]
+    lib.kmassign_rmsnorm.restype = i32
+    lib.kmassign_rmsnorm_grad.argtypes = [vp, i32, i64, i64, vp, vp, i32, vp, vp, vp, vp, vp]
+    lib.kmassign_rmsnorm_grad.restype = i32
     lib.kmassign_set_wait_timeout.argtypes = [ctypes.c_uint64]
     lib.kmassign_set_wait_timeout.restype = i32
     lib.kmassign_check.argtypes = [vp]
@@ -432,7 +443,8 @@ def _need_detached(where, name):
         raise RuntimeError(
             f"{where}: {name} requires grad, and autograd would not see the result; call it "
             "under torch.no_grad() or in a torch.autograd.Function (gradients: "
-            "kmassign_route_grad, kmassign_lookup_grad)")
+            "kmassign_route_grad, kmassign_lookup_grad, kmassign_experts_grad, "
+            "kmassign_rmsnorm_grad)")
 
 
 # Tells autograd that a call wrote to these tensors of the caller, as torch's in-place operations
@@ -765,6 +777,280 @@ def kmassign_clip(grads, max_norm: float, out=None, norm=None, stream=None):
     if given:
         _written([norm])
     return norm
+
+
+# ---- experts behind a router: grouped products, their gradients, the norm ------
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def _blocks(n) -> int:
+    """Blocks of 128 columns (or rows) that share a scale."""
+    return -(-n // 128)
+
+
+def _need_product_types(X, W, xscale, wscale):
+    """The kmassign_dtype of the operands; their scales' shapes are checked."""
+    if isinstance(X, torch.Tensor) and X.dtype == _E4M3:
+        _need_cuda(X, "X", _E4M3)
+        if xscale is None or wscale is None:
+            raise ValueError("8-bit operands need xscale and wscale")
+        _need_cuda(xscale, "xscale", torch.float32)
+        _need_cuda(wscale, "wscale", torch.float32)
+        code = 3
+    else:
+        code = _need_float(X, "X")
+        if code == 0:
+            raise TypeError("X must be bfloat16, float16 or float8_e4m3fn, got torch.float32")
+        if xscale is not None or wscale is not None:
+            raise ValueError("xscale and wscale belong to 8-bit operands")
+    _need_cuda(W, "W", X.dtype)
+    return code
+
+
+def _need_lists(X, W, offsets, rows, slots, places):
+    """R, D, E, F, M of a grouped product; the ids' types and sizes are checked."""
+    R, D = _need_matrix(X, "X")
+    if W.dim() != (2 if offsets is None else 3):
+        raise ValueError("W must have shape [E, F, D] with offsets and [F, D] without, got "
+                         f"{tuple(W.shape)}")
+    E, F = (1, W.shape[0]) if offsets is None else W.shape[:2]
+    if W.shape[-1] != D:
+        raise ValueError("X and W disagree on D")
+    if offsets is not None:
+        _need_cuda(offsets, "offsets", torch.int32)
+        _need_shape(offsets, "offsets", (E + 1,))
+    M = R
+    if rows is not None:
+        _need_cuda(rows, "rows", torch.int32)
+        M = rows.numel()
+    elif slots != 1:
+        raise ValueError("slots needs rows")
+    if places is not None:
+        _need_cuda(places, "places", torch.int32)
+        if rows is not None and places.numel() != M:
+            raise ValueError("rows and places must hold one id per position each")
+        M = places.numel()
+    return R, D, E, F, M
+
+
+def kmassign_experts(X, W, offsets=None, rows=None, slots: int = 1, places=None, xscale=None,
+                     wscale=None, dtype=None, out=None, stream=None):
+    """Products grouped by expert: out[places[p]] = W[e] X[rows[p] // slots] for p in list e.
+
+    ``X`` is [R, D] and ``W`` [E, F, D], bf16 or fp16, or float8_e4m3fn with
+    ``xscale`` (fp32 [R, ceil(D / 128)]) and ``wscale`` (fp32 [E, ceil(F /
+    128), ceil(D / 128)]).  ``offsets`` (int32 [E + 1], ``kmassign_lists``')
+    says which positions belong to which expert; without it ``W`` is [F, D]
+    and all positions take it.  ``rows`` and ``places`` are int32 [M] (of any
+    shape): ``rows=order, slots=k`` takes the points' rows in the lists' order,
+    ``places=order`` puts rows of the lists' order back to their slots.  Returns
+    out [M, F] in ``dtype``: X's type or fp32, in 8 bits bf16 (the default),
+    fp16 or fp32.  Rows of no list are zeros; with ``places`` rows that no
+    position names are zeros, or stay as they were in a given ``out``, which
+    may then have any number of rows.
+    """
+    code = _need_product_types(X, W, xscale, wscale)
+    slots = int(slots)
+    R, D, E, F, M = _need_lists(X, W, offsets, rows, slots, places)
+    if code == 3:
+        _need_shape(xscale, "xscale", (R, _blocks(D)))
+        _need_shape(wscale, "wscale", (*W.shape[:-2], _blocks(F), _blocks(D)))
+    if X.requires_grad or W.requires_grad:
+        _need_detached("kmassign_experts", "X or W")
+    given = out is not None
+    if not given:
+        out = _new((M, F), dtype or (torch.bfloat16 if code == 3 else X.dtype), X.device, stream,
+                   torch.empty if places is None else torch.zeros)
+    elif dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out must be {dtype}, got {out.dtype}")
+    out_code = _need_float(out, "out")
+    if code != 3 and out_code not in (0, code):
+        raise TypeError(f"out must be {X.dtype} or float32, got {out.dtype}")
+    out_rows, out_cols = _need_matrix(out, "out")
+    if out_cols != F or (places is None and out_rows != M):
+        raise ValueError(f"out must have shape {(M, F)}, got {tuple(out.shape)}")
+    rc = library().kmassign_experts(
+        X.data_ptr(), code, R, D, W.data_ptr(), E, F, _ptr(xscale), _ptr(wscale), _ptr(offsets), M,
+        _ptr(rows), slots, _ptr(places), out.data_ptr(), out_code, out_rows,
+        _stream_of(stream, X))
+    if rc:
+        _check(rc, "kmassign_experts")
+    if given:
+        _written([out])
+    return out
+
+
+def kmassign_experts_grad(dout, X, W, offsets=None, rows=None, slots: int = 1, places=None,
+                          dtype=None, dX=None, dW=None, need_x: bool = True, need_w: bool = True,
+                          stream=None):
+    """Gradients of ``kmassign_experts`` in 16 bits: (dX [R, D], dW of W's shape).
+
+    ``dout`` is [M, F] ([out's rows, F] with ``places``) in X's type, the other
+    arguments are the forward call's.  ``dX`` has X's type, ``dW`` is fp32 (the
+    default ``dtype``) or X's type; one that is not needed is None.
+    """
+    code = _need_product_types(X, W, None, None)
+    if code == 3:
+        raise TypeError("X must be bfloat16 or float16, got torch.float8_e4m3fn")
+    slots = int(slots)
+    R, D, E, F, M = _need_lists(X, W, offsets, rows, slots, places)
+    _need_cuda(dout, "dout", X.dtype)
+    out_rows, out_cols = _need_matrix(dout, "dout")
+    if out_cols != F or (places is None and out_rows != M):
+        raise ValueError(f"dout must have shape {(M, F)}, got {tuple(dout.shape)}")
+    if not (need_x or need_w):
+        raise ValueError("neither gradient is needed")
+    if dout.requires_grad or X.requires_grad or W.requires_grad:
+        _need_detached("kmassign_experts_grad", "dout, X or W")
+    given = dX, dW
+    if not need_x:
+        if dX is not None:
+            raise ValueError("dX is given but not needed")
+    elif dX is None:
+        dX = _new((R, D), X.dtype, X.device, stream)
+    else:
+        _need_cuda(dX, "dX", X.dtype)
+        _need_shape(dX, "dX", (R, D))
+    if not need_w:
+        if dW is not None:
+            raise ValueError("dW is given but not needed")
+    elif dW is None:
+        dW = _new(W.shape, dtype or torch.float32, X.device, stream)
+    else:
+        if dtype is not None and dW.dtype != dtype:
+            raise TypeError(f"dW must be {dtype}, got {dW.dtype}")
+        _need_shape(dW, "dW", W.shape)
+    dw_code = 0 if dW is None else _need_float(dW, "dW")
+    if dw_code not in (0, code):
+        raise TypeError(f"dW must be {X.dtype} or float32, got {dW.dtype}")
+    rc = library().kmassign_experts_grad(
+        dout.data_ptr(), code, out_rows, F, X.data_ptr(), R, D, W.data_ptr(), E, _ptr(offsets), M,
+        _ptr(rows), slots, _ptr(places), _ptr(dX), _ptr(dW), dw_code, _stream_of(stream, X))
+    if rc:
+        _check(rc, "kmassign_experts_grad")
+    if given != (None, None):
+        _written([t for t in given if t is not None])
+    return dX, dW
+
+
+def _need_norm_weight(weight, dtype, D) -> int:
+    """The kmassign_dtype of a norm's weight: fp32 or the rows' type."""
+    if weight is None:
+        return 0
+    code = _need_float(weight, "weight")
+    if code not in (0, _DTYPES[dtype]):
+        raise TypeError(f"weight must be {dtype} or float32, got {weight.dtype}")
+    _need_shape(weight, "weight", (D,))
+    return code
+
+
+def kmassign_rmsnorm(X, weight=None, residual=None, eps: float = 1e-6, dtype=None, out=None,
+                     scales=None, total=None, rstd=None, stream=None):
+    """Root-mean-square norm of rows: (out, scales, total, rstd).
+
+    ``X`` is fp32, bf16 or fp16 [N, D]; with ``residual`` (the same) the rows
+    are total = X + residual, rounded to that type, else total is ``X`` itself.
+    out = total * rstd * weight, rstd = 1 / sqrt(mean(total^2) + eps) (fp32
+    [N]); ``weight`` [D] is fp32 or of X's type, None for all 1.  ``dtype`` is
+    X's type (the default; scales is None) or float8_e4m3fn: out's values are
+    then code * scale with scales fp32 [N, ceil(D / 128)], as
+    ``kmassign_experts`` takes them.
+    """
+    code = _need_float(X, "X")
+    N, D = _need_matrix(X, "X")
+    wcode = _need_norm_weight(weight, X.dtype, D)
+    if residual is not None:
+        _need_cuda(residual, "residual", X.dtype)
+        _need_shape(residual, "residual", (N, D))
+    elif total is not None:
+        raise ValueError("total needs a residual")
+    if X.requires_grad or (weight is not None and weight.requires_grad) or (
+            residual is not None and residual.requires_grad):
+        _need_detached("kmassign_rmsnorm", "X, weight or residual")
+    given = [t for t in (out, scales, total, rstd) if t is not None]
+    if dtype is None:
+        dtype = X.dtype if out is None else out.dtype
+    if dtype not in (X.dtype, _E4M3):
+        raise TypeError(f"dtype must be {X.dtype} or float8_e4m3fn, got {dtype}")
+    if out is None:
+        out = _new((N, D), dtype, X.device, stream)
+    else:
+        _need_cuda(out, "out", dtype)
+        _need_shape(out, "out", (N, D))
+    if dtype == _E4M3:
+        if scales is None:
+            scales = _new((N, _blocks(D)), torch.float32, X.device, stream)
+        else:
+            _need_cuda(scales, "scales", torch.float32)
+            _need_shape(scales, "scales", (N, _blocks(D)))
+    elif scales is not None:
+        raise ValueError("scales belong to an 8-bit output")
+    if residual is not None:
+        if total is None:
+            total = _new((N, D), X.dtype, X.device, stream)
+        else:
+            _need_cuda(total, "total", X.dtype)
+            _need_shape(total, "total", (N, D))
+    if rstd is None:
+        rstd = _new((N,), torch.float32, X.device, stream)
+    else:
+        _need_cuda(rstd, "rstd", torch.float32)
+        _need_shape(rstd, "rstd", (N,))
+    rc = library().kmassign_rmsnorm(
+        X.data_ptr(), code, N, D, _ptr(residual), _ptr(weight), wcode, float(eps), _ptr(total),
+        out.data_ptr(), 3 if dtype == _E4M3 else code, _ptr(scales), rstd.data_ptr(),
+        _stream_of(stream, X))
+    if rc:
+        _check(rc, "kmassign_rmsnorm")
+    if given:
+        _written(given)
+    return out, scales, X if total is None else total, rstd
+
+
+def kmassign_rmsnorm_grad(dout, total, weight, rstd, dtotal=None, dX=None, dweight=None,
+                          stream=None):
+    """Gradients of ``kmassign_rmsnorm``: (dX [N, D], dweight fp32 [D] or None without a weight).
+
+    ``dout`` is the gradient of out in the rows' type, ``total`` and ``rstd``
+    what the forward call returned; ``dtotal`` (the rows' type), the gradient
+    that reaches total otherwise, is added.  dX is the gradient of X and of the
+    residual alike.
+    """
+    code = _need_float(total, "total")
+    N, D = _need_matrix(total, "total")
+    _need_cuda(dout, "dout", total.dtype)
+    _need_shape(dout, "dout", (N, D))
+    wcode = _need_norm_weight(weight, total.dtype, D)
+    _need_cuda(rstd, "rstd", torch.float32)
+    _need_shape(rstd, "rstd", (N,))
+    if dtotal is not None:
+        _need_cuda(dtotal, "dtotal", total.dtype)
+        _need_shape(dtotal, "dtotal", (N, D))
+    if any(t is not None and t.requires_grad for t in (dout, total, weight, rstd, dtotal)):
+        _need_detached("kmassign_rmsnorm_grad", "an input")
+    given = [t for t in (dX, dweight) if t is not None]
+    if dX is None:
+        dX = _new((N, D), total.dtype, total.device, stream)
+    else:
+        _need_cuda(dX, "dX", total.dtype)
+        _need_shape(dX, "dX", (N, D))
+    if weight is None:
+        if dweight is not None:
+            raise ValueError("dweight needs a weight")
+    elif dweight is None:
+        dweight = _new((D,), torch.float32, total.device, stream)
+    else:
+        _need_cuda(dweight, "dweight", torch.float32)
+        _need_shape(dweight, "dweight", (D,))
+    rc = library().kmassign_rmsnorm_grad(
+        dout.data_ptr(), code, N, D, total.data_ptr(), _ptr(weight), wcode, rstd.data_ptr(),
+        _ptr(dtotal), dX.data_ptr(), _ptr(dweight), _stream_of(stream, total))
+    if rc:
+        _check(rc, "kmassign_rmsnorm_grad")
+    if given:
+        _written(given)
+    return dX, dweight
 
 
 def kmassign_set_wait_timeout(ns: int) -> None:

@@ -20,7 +20,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libkmassign.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["api.cu", "assign.cu", "topk.cu", "aux_kernels.cu", "update.cu", "host_path.cu",
-           "route.cu", "lists.cu", "lookup.cu", "clip.cu", "learn_api.cu"]
+           "route.cu", "lists.cu", "lookup.cu", "clip.cu", "learn_api.cu",
+           "experts.cu", "rmsnorm.cu", "experts_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-Xcompiler", "-Wall", "-I", INCLUDE]

@@ -96,7 +96,8 @@ int current_device_info(DeviceInfo *out)
             for (int kb = 1; kb <= 4; ++kb)
                 if (kma::topk_prepare(kb, list, static_cast<size_t>(d.smem_optin)) != cudaSuccess)
                     return KMASSIGN_ERR_CUDA;
-        if (kma::lists_prepare() != cudaSuccess)
+        if (kma::lists_prepare() != cudaSuccess ||
+            kma::experts_prepare(static_cast<size_t>(d.smem_optin)) != cudaSuccess)
             return KMASSIGN_ERR_CUDA;
         cudaMemPoolProps props = {};
         props.allocType = cudaMemAllocationTypePinned;
@@ -588,6 +589,37 @@ int library_device(cudaMemPool_t *pool, int *sms)
         *sms = dev.sms;
     }
     return rc;
+}
+
+int library_smem(size_t *bytes)
+{
+    DeviceInfo dev;
+    const int rc = current_device_info(&dev);
+    if (rc == KMASSIGN_OK)
+        *bytes = static_cast<size_t>(dev.smem_optin);
+    return rc;
+}
+
+uint64_t wait_timeout_ns() { return g_wait_timeout_ns.load(); }
+
+bool encode_tiled(CUtensorMap *map, CUtensorMapDataType type, const void *ptr, int rank,
+                  const uint64_t *dims, const uint64_t *strides, const uint32_t *box)
+{
+    auto fn = encode_fn();
+    if (fn == nullptr || rank < 2 || rank > 3)
+        return false;
+    cuuint64_t d[3] = {}, st[2] = {};
+    cuuint32_t b[3] = {}, one[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+    }
+    for (int i = 0; i + 1 < rank; ++i)
+        st[i] = strides[i];
+    return fn(map, type, static_cast<cuuint32_t>(rank), const_cast<void *>(ptr), d, st, b, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int library_pool(cudaMemPool_t *pool)
@@ -1183,11 +1215,12 @@ int kmassign_check(void *stream)
 {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return KMASSIGN_ERR_CUDA;
-    int code = 0, code_topk = 0;
+    int code = 0, code_topk = 0, code_experts = 0;
     if (kma::status_read_and_clear(&code) != cudaSuccess ||
-        kma::topk_status_read_and_clear(&code_topk) != cudaSuccess)
+        kma::topk_status_read_and_clear(&code_topk) != cudaSuccess ||
+        kma::experts_status_read_and_clear(&code_experts) != cudaSuccess)
         return KMASSIGN_ERR_CUDA;
-    return code != 0 ? code : code_topk;
+    return code != 0 ? code : code_topk != 0 ? code_topk : code_experts;
 }
 
 const char *kmassign_strerror(int code)

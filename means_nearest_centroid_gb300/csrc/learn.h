@@ -16,6 +16,46 @@ int library_device(cudaMemPool_t *pool, int *sms);
 // which is made current; KMASSIGN_ERR_NOT_DEVICE otherwise.
 int check_device_ptrs(const void *const *ptrs, int n);
 
+// Largest dynamic shared memory of a block on the current device (library_device's), and the bound
+// on every pipeline wait.
+int library_smem(size_t *bytes);
+uint64_t wait_timeout_ns();
+
+// A tensor map of rank 2 or 3 (dims, innermost first; strides[i]: bytes from one index of dims[i + 1]
+// to the next), 128-byte swizzle, zeros outside; false if the driver refuses it.
+bool encode_tiled(CUtensorMap *map, CUtensorMapDataType type, const void *ptr, int rank,
+                  const uint64_t *dims, const uint64_t *strides, const uint32_t *box);
+
+// One stream-ordered allocation from the library's pool, released (in stream
+// order) when it goes out of scope.
+class Scratch {
+public:
+    Scratch(size_t bytes, cudaMemPool_t pool, cudaStream_t stream) : stream_(stream)
+    {
+        if (bytes > 0 && cudaMallocFromPoolAsync(&p_, bytes, pool, stream) != cudaSuccess) {
+            cudaGetLastError();
+            p_ = nullptr;
+            ok_ = false;
+        }
+    }
+    ~Scratch() { release(); }
+    bool ok() const { return ok_; }
+    uint8_t *get() const { return static_cast<uint8_t *>(p_); }
+    bool release()
+    {
+        void *p = p_;
+        p_ = nullptr;
+        return p == nullptr || cudaFreeAsync(p, stream_) == cudaSuccess;
+    }
+    Scratch(const Scratch &) = delete;
+    Scratch &operator=(const Scratch &) = delete;
+
+private:
+    cudaStream_t stream_;
+    void *p_ = nullptr;
+    bool ok_ = true;
+};
+
 // Puts back the calling thread's current device when an entry point returns
 // (check_device_ptrs makes the pointers' device current for the launches;
 // the caller's own notion of its current device must not change).
@@ -45,7 +85,8 @@ private:
 
 // Element types (the KMASSIGN_FP32, _BF16, _FP16 of kmassign.h).
 constexpr int kFp32 = 0, kBf16 = 1, kFp16 = 2;
-inline int dtype_bytes(int dtype) { return dtype == kFp32 ? 4 : 2; }
+constexpr int kE4m3 = 3;   // KMASSIGN_E4M3: the experts' products and the norm's output only
+__host__ __device__ inline int dtype_bytes(int dtype) { return dtype == kFp32 ? 4 : 2; }
 
 cudaError_t launch_route(const void *logits, int dtype, int64_t N, int64_t E, int32_t k,
                          bool sigmoid, const float *bias, int32_t groups, int32_t topk_groups,
@@ -89,5 +130,59 @@ size_t clip_scratch_bytes(int32_t n, int sms);
 cudaError_t launch_clip(const void *const *grads, void *const *out, const int64_t *sizes,
                         const int32_t *dtypes, int32_t n, bool scale, float max_norm, float *norm,
                         double *partial, int sms, cudaStream_t stream);
+
+// ---- products grouped by expert, root-mean-square norm ----------------------
+
+// The row that a list position stands for: ids[p] / slots, or p where ids is
+// NULL; none where that is outside [0, rows).
+struct RowMap {
+    const int32_t *ids;
+    int32_t slots, rows;
+};
+
+enum ExpertsKind { kForward, kRowsGrad, kWeightsGrad };
+
+struct ExpertsParams {
+    const int32_t *offsets;   // [E + 1]; NULL: one list of all M positions
+    int32_t E, M;
+    int32_t mdim;             // the outputs' contiguous extent (F; gradients: D)
+    int32_t ndim;             // weights' gradient: F
+    int32_t kblocks;          // 128-byte blocks of the contraction (not the weights' gradient)
+    RowMap a_rows;            // rows of X (weights' gradient)
+    RowMap b_rows;            // rows of the positions' operand
+    RowMap places;            // rows of the output (forward, rows' gradient)
+    bool zero_rest;           // rows of no list are written 0
+    void *out;
+    int32_t out_type;
+    const float *xscale, *wscale;   // 8 bits: [rows, kblocks], [E, fblocks, kblocks]
+    int32_t fblocks;
+    int32_t stages;           // set by launch_experts, like idesc
+    uint32_t idesc;
+    uint64_t timeout_ns;
+};
+
+// Shared-memory attributes, once per device.
+cudaError_t experts_prepare(size_t smem_optin);
+// Boxes of the operands' tensor maps (rows of 128 bytes): A as [E][F][D], 128
+// rows K-major (forward) or 64 MN-major, X 64 rows; B 32 rows (the weights'
+// gradient 64); one row where ids name the rows.
+constexpr uint32_t kExpertsBoxA = 128, kExpertsBoxMn = 64, kExpertsBoxB = 32;
+cudaError_t launch_experts(ExpertsKind kind, bool e8, int type, const CUtensorMap &a,
+                           const CUtensorMap &b, ExpertsParams p, int sms, size_t smem_optin,
+                           cudaStream_t stream);
+cudaError_t experts_status_read_and_clear(int *code);
+// row[p] = the row that map names for positions of a list, -1 for the others.
+cudaError_t launch_listed_rows(const int32_t *offsets, int32_t E, int32_t M, RowMap map,
+                               int32_t *row, cudaStream_t stream);
+
+cudaError_t launch_rmsnorm(const void *X, int dtype, int64_t N, int64_t D, const void *residual,
+                           const void *weight, int weight_dtype, float eps, void *total, void *out,
+                           int out_dtype, float *scales, float *rstd, int sms,
+                           cudaStream_t stream);
+size_t rmsnorm_grad_parts_bytes(int64_t N, int64_t D, int sms);
+cudaError_t launch_rmsnorm_grad(const void *dout, int dtype, int64_t N, int64_t D,
+                                const void *total, const void *weight, int weight_dtype,
+                                const float *rstd, const void *dtotal, void *dX, float *dweight,
+                                float *parts, int sms, cudaStream_t stream);
 
 }  // namespace kma

@@ -15,6 +15,7 @@ namespace {
 
 using kma::check_device_ptrs;
 using kma::DeviceRestore;
+using kma::Scratch;
 
 constexpr int64_t kLimit = int64_t(1) << 31;
 constexpr int64_t kMaxDim = 65536;        // D of a table
@@ -28,36 +29,6 @@ bool aligned(const void *p, uintptr_t a)
 bool known_type(int dtype) { return dtype >= KMASSIGN_FP32 && dtype <= KMASSIGN_FP16; }
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
-
-// One stream-ordered allocation from the library's pool, released (in stream
-// order) when it goes out of scope.
-class Scratch {
-public:
-    Scratch(size_t bytes, cudaMemPool_t pool, cudaStream_t stream) : stream_(stream)
-    {
-        if (bytes > 0 && cudaMallocFromPoolAsync(&p_, bytes, pool, stream) != cudaSuccess) {
-            cudaGetLastError();
-            p_ = nullptr;
-            ok_ = false;
-        }
-    }
-    ~Scratch() { release(); }
-    bool ok() const { return ok_; }
-    uint8_t *get() const { return static_cast<uint8_t *>(p_); }
-    bool release()
-    {
-        void *p = p_;
-        p_ = nullptr;
-        return p == nullptr || cudaFreeAsync(p, stream_) == cudaSuccess;
-    }
-    Scratch(const Scratch &) = delete;
-    Scratch &operator=(const Scratch &) = delete;
-
-private:
-    cudaStream_t stream_;
-    void *p_ = nullptr;
-    bool ok_ = true;
-};
 
 int done(cudaError_t e) { return e == cudaSuccess ? KMASSIGN_OK : KMASSIGN_ERR_CUDA; }
 

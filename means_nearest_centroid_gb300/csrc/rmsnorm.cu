@@ -1,0 +1,491 @@
+// rmsnorm.cu -- root-mean-square norm of rows, with the residual's addition in
+// front and an output in 8 bits behind, and its gradients:
+//   t = x + residual (rounded to the rows' type: what is kept is what is normed)
+//   rstd = 1 / sqrt(mean(t^2) + eps),   y = t rstd w
+//   8 bits: for each block of 128 columns scale = max |y| / 448, codes e4m3(y / scale)
+//   g = w dy,  dx = rstd (g - t rstd mean(g t rstd)) + dt,  dw = sum over rows of dy t rstd
+//
+// Both are bound by memory: every element crosses HBM once in each direction.
+// A row lives in the registers of one warp, or of the warps of one block where
+// it is longer or where rows are few, so it is read once for its statistics and
+// its output alike.  Sums are fp32.  A warp's piece of a row is a whole number
+// of 128-column blocks, so the scales need shuffles only.
+#include "learn.h"
+#include "vec.cuh"
+
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+namespace kma {
+
+namespace {
+
+constexpr float kTop = 448.0f;             // e4m3's largest number
+constexpr float kLeast = 7.8886091e-31f;   // 2^-100, under which a block's largest is taken as that
+
+// Column of a thread's vector j: `warps` warps share the row, each warp's
+// vectors go in groups that cover whole 128-column blocks.
+template <int VE>
+__device__ __forceinline__ int column(int j, int warps, int warp, int lane)
+{
+    constexpr int kGroup = VE >= 4 ? 1 : 4 / VE;
+    return (((j / kGroup) * warps + warp) * kGroup + j % kGroup) * 32 * VE + lane * VE;
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2)
+        v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+
+// The sum over the warps of a block (one row a block); slot: which half of the
+// buffer, alternating from call to call.
+__device__ __forceinline__ float block_sum(float v, float *buf, int warps, int slot)
+{
+    v = warp_sum(v);
+    if (warps == 1)
+        return v;
+    if ((threadIdx.x & 31) == 0)
+        buf[slot * 32 + (threadIdx.x >> 5)] = v;
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    return warp_sum(lane < warps ? buf[slot * 32 + lane] : 0.0f);
+}
+
+template <typename T, int VE>
+__device__ __forceinline__ void load_weight(const void *weight, bool fp32, int col, float (&w)[VE])
+{
+    if (weight == nullptr) {
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+            w[i] = 1.0f;
+    } else if (fp32) {
+        const float *p = static_cast<const float *>(weight) + col;
+        constexpr int kPart = VE < 4 ? VE : 4;
+#pragma unroll
+        for (int i = 0; i < VE; i += kPart) {
+            float f[kPart];
+            widen<float, kPart>(load_raw<float, kPart>(p + i), f);
+#pragma unroll
+            for (int k = 0; k < kPart; ++k)
+                w[i + k] = f[k];
+        }
+    } else {
+        widen<T, VE>(load_raw<T, VE>(static_cast<const T *>(weight) + col), w);
+    }
+}
+
+template <int VE>
+__device__ __forceinline__ void store_codes(uint8_t *p, const float (&v)[VE])
+{
+    if constexpr (VE == 1) {
+        *p = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
+    } else {
+        __nv_fp8x2_storage_t c[VE / 2];
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i)
+            c[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE,
+                                            __NV_E4M3);
+        typename RawOf<VE>::type r;
+        memcpy(&r, c, sizeof(r));
+        *reinterpret_cast<typename RawOf<VE>::type *>(p) = r;
+    }
+}
+
+struct NormArgs {
+    const void *x, *residual, *weight;
+    bool weight_fp32;
+    int64_t N;
+    int32_t D;
+    float eps;
+    void *total, *out;
+    float *scales, *rstd;
+};
+
+// NV vectors of VE elements a thread.  warps == 1: a warp a row, four rows a
+// block; else one row a block.
+template <typename T, bool CODES, int VE, int NV>
+__global__ void __launch_bounds__(512) rmsnorm_kernel(const NormArgs a, int warps)
+{
+    __shared__ float buf[32];
+    const int lane = threadIdx.x & 31;
+    const int warp = warps == 1 ? 0 : threadIdx.x >> 5;
+    const int64_t row =
+        warps == 1 ? blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5)
+                   : blockIdx.x;
+    if (row >= a.N)
+        return;   // whole warps; with several warps a row, never
+    const int64_t at = row * a.D;
+    float t[NV][VE];
+    float ss = 0.0f;
+    Raw<T, VE> rx[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int col = column<VE>(j, warps, warp, lane);
+        if (col < a.D)
+            rx[j] = load_raw<T, VE>(static_cast<const T *>(a.x) + at + col);
+    }
+    if (a.residual != nullptr) {
+        Raw<T, VE> rr[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = column<VE>(j, warps, warp, lane);
+            if (col < a.D)
+                rr[j] = load_raw<T, VE>(static_cast<const T *>(a.residual) + at + col);
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = column<VE>(j, warps, warp, lane);
+            if (col < a.D) {
+                float u[VE], v[VE];
+                widen<T, VE>(rx[j], u);
+                widen<T, VE>(rr[j], v);
+#pragma unroll
+                for (int i = 0; i < VE; ++i)
+                    u[i] += v[i];
+                rx[j] = narrow<T, VE>(u);
+                store_raw<T, VE>(static_cast<T *>(a.total) + at + col, rx[j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int col = column<VE>(j, warps, warp, lane);
+        if (col < a.D) {
+            widen<T, VE>(rx[j], t[j]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                t[j][i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+            ss = fmaf(t[j][i], t[j][i], ss);
+    }
+    ss = block_sum(ss, buf, warps, 0);
+    const float rstd = __frcp_rn(__fsqrt_rn(ss / static_cast<float>(a.D) + a.eps));
+    if (a.rstd != nullptr && lane == 0 && warp == 0)
+        a.rstd[row] = rstd;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int col = column<VE>(j, warps, warp, lane);
+        if (col < a.D) {
+            float w[VE];
+            load_weight<T, VE>(a.weight, a.weight_fp32, col, w);
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                t[j][i] = t[j][i] * rstd * w[i];
+            if (!CODES)
+                store_raw<T, VE>(static_cast<T *>(a.out) + at + col, narrow<T, VE>(t[j]));
+        }
+    }
+    if constexpr (CODES) {
+        constexpr int kGroup = VE >= 4 ? 1 : 4 / VE;    // vectors of a block
+        constexpr int kLanes = VE >= 4 ? 128 / VE : 32;   // lanes that share it
+        const int blocks = (a.D + 127) / 128;
+#pragma unroll
+        for (int j = 0; j < NV; j += kGroup) {
+            float top = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k)
+#pragma unroll
+                for (int i = 0; i < VE; ++i)
+                    top = fmaxf(top, fabsf(t[j + k][i]));
+#pragma unroll
+            for (int d = kLanes / 2; d > 0; d /= 2)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float scale = fmaxf(top, kLeast) / kTop;
+            const float inverse = 1.0f / scale;
+            const int first = column<VE>(j, warps, warp, lane);
+            if (lane % kLanes == 0 && first < a.D)
+                a.scales[row * blocks + first / 128] = scale;
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k) {
+                const int col = column<VE>(j + k, warps, warp, lane);
+                if (col < a.D) {
+                    float q[VE];
+#pragma unroll
+                    for (int i = 0; i < VE; ++i)
+                        q[i] = t[j + k][i] * inverse;
+                    store_codes<VE>(static_cast<uint8_t *>(a.out) + at + col, q);
+                }
+            }
+        }
+    }
+}
+
+struct NormGradArgs {
+    const void *dout, *total, *weight, *dtotal;
+    bool weight_fp32;
+    const float *rstd;
+    int64_t N;
+    int32_t D;
+    void *dx;
+    float *parts;   // [groups, D], or NULL
+};
+
+// A group of threads (a warp, or the block) takes rows in turn and keeps its
+// share of the weight's gradient in registers; one partial row a group.
+template <typename T, int VE, int NV>
+__global__ void __launch_bounds__(512) rmsnorm_grad_kernel(const NormGradArgs a, int warps,
+                                                           int groups)
+{
+    __shared__ float buf[64];
+    const int lane = threadIdx.x & 31;
+    const int warp = warps == 1 ? 0 : threadIdx.x >> 5;
+    const int group = warps == 1 ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    if (group >= groups)
+        return;   // whole warps
+    float dw[NV][VE];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+            dw[j][i] = 0.0f;
+    const float mean = 1.0f / static_cast<float>(a.D);
+    int slot = 0;
+    for (int64_t row = group; row < a.N; row += groups, slot ^= 1) {
+        const int64_t at = row * a.D;
+        const float rstd = __ldg(a.rstd + row);
+        Raw<T, VE> rd[NV], rt[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = column<VE>(j, warps, warp, lane);
+            if (col < a.D) {
+                rd[j] = load_raw<T, VE>(static_cast<const T *>(a.dout) + at + col);
+                rt[j] = load_raw<T, VE>(static_cast<const T *>(a.total) + at + col);
+            }
+        }
+        float dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = column<VE>(j, warps, warp, lane);
+            if (col < a.D) {
+                float d[VE], t[VE], w[VE];
+                widen<T, VE>(rd[j], d);
+                widen<T, VE>(rt[j], t);
+                load_weight<T, VE>(a.weight, a.weight_fp32, col, w);
+#pragma unroll
+                for (int i = 0; i < VE; ++i) {
+                    const float n = t[i] * rstd;
+                    dw[j][i] = fmaf(d[i], n, dw[j][i]);
+                    dot = fmaf(d[i] * w[i], n, dot);
+                }
+            }
+        }
+        const float c = block_sum(dot, buf, warps, slot) * mean;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = column<VE>(j, warps, warp, lane);
+            if (col < a.D) {
+                float d[VE], t[VE], w[VE], o[VE];
+                widen<T, VE>(rd[j], d);
+                widen<T, VE>(rt[j], t);
+                load_weight<T, VE>(a.weight, a.weight_fp32, col, w);
+#pragma unroll
+                for (int i = 0; i < VE; ++i)
+                    o[i] = (d[i] * w[i] - t[i] * rstd * c) * rstd;
+                if (a.dtotal != nullptr) {
+                    float r[VE];
+                    widen<T, VE>(load_raw<T, VE>(static_cast<const T *>(a.dtotal) + at + col), r);
+#pragma unroll
+                    for (int i = 0; i < VE; ++i)
+                        o[i] += r[i];
+                }
+                store_raw<T, VE>(static_cast<T *>(a.dx) + at + col, narrow<T, VE>(o));
+            }
+        }
+    }
+    if (a.parts != nullptr) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int col = column<VE>(j, warps, warp, lane);
+            if (col < a.D)
+                for (int i = 0; i < VE; ++i)
+                    a.parts[static_cast<int64_t>(group) * a.D + col + i] = dw[j][i];
+        }
+    }
+}
+
+// dweight[d] = the sum of the partial rows' column d: 32 columns a block, 32
+// warps a column, in an order fixed by the sizes.
+__global__ void __launch_bounds__(1024)
+    join_parts_kernel(const float *parts, int groups, int D, float *dweight)
+{
+    __shared__ float sums[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + lane;
+    float v = 0.0f;
+    if (col < D) {
+#pragma unroll 8
+        for (int g = warp; g < groups; g += 32)
+            v += parts[static_cast<int64_t>(g) * D + col];
+    }
+    sums[warp][lane] = v;
+    __syncthreads();
+    v = warp_sum(sums[lane][warp]);
+    const int out = blockIdx.x * 32 + warp;
+    if (lane == 0 && out < D)
+        dweight[out] = v;
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+int warps_for(int64_t D, int elems) { return static_cast<int>((D + 32 * elems - 1) / (32 * elems)); }
+
+// Vectors a thread: the row in one warp where rows are many, up to `most`
+// vectors; spread over up to 16 warps where they are few.
+template <int VE>
+int vectors_for(int64_t N, int64_t D, int least, int most, int sms)
+{
+    const int64_t few = 4 * static_cast<int64_t>(sms);
+    int nv = least;
+    while (nv < most && warps_for(D, VE * nv) > (N <= few ? 16 : 1))
+        nv *= VE == 1 ? 4 : 2;
+    return nv;
+}
+
+template <typename T, bool CODES, int VE, int NV>
+cudaError_t run_norm(const NormArgs &a, cudaStream_t s)
+{
+    const int warps = warps_for(a.D, VE * NV);
+    if (warps == 1)
+        rmsnorm_kernel<T, CODES, VE, NV>
+            <<<static_cast<unsigned>((a.N + 3) / 4), 128, 0, s>>>(a, 1);
+    else
+        rmsnorm_kernel<T, CODES, VE, NV>
+            <<<static_cast<unsigned>(a.N), 32 * warps, 0, s>>>(a, warps);
+    return cudaGetLastError();
+}
+
+template <typename T, bool CODES>
+cudaError_t norm_shape(const NormArgs &a, int sms, cudaStream_t s)
+{
+    constexpr int VE = 16 / sizeof(T);
+    const bool wide = a.D % VE == 0 && aligned16(a.x) && aligned16(a.residual) &&
+                      aligned16(a.weight) && aligned16(a.total) && aligned16(a.out);
+    if (!wide) {
+        switch (vectors_for<1>(a.N, a.D, 4, 64, sms)) {
+        case 4:
+            return run_norm<T, CODES, 1, 4>(a, s);
+        case 16:
+            return run_norm<T, CODES, 1, 16>(a, s);
+        default:
+            return run_norm<T, CODES, 1, 64>(a, s);
+        }
+    }
+    switch (vectors_for<VE>(a.N, a.D, 1, 64 / VE, sms)) {
+    case 1:
+        return run_norm<T, CODES, VE, 1>(a, s);
+    case 2:
+        return run_norm<T, CODES, VE, 2>(a, s);
+    case 4:
+        return run_norm<T, CODES, VE, 4>(a, s);
+    case 8:
+        return run_norm<T, CODES, VE, 8>(a, s);
+    default:
+        return run_norm<T, CODES, VE, 64 / VE>(a, s);
+    }
+}
+
+template <typename T>
+cudaError_t norm_type(const NormArgs &a, bool codes, int sms, cudaStream_t s)
+{
+    return codes ? norm_shape<T, true>(a, sms, s) : norm_shape<T, false>(a, sms, s);
+}
+
+// Row groups of the gradient: eight warps' worth of blocks an SM, fewer where
+// rows are few.
+int grad_groups(int64_t N, int sms)
+{
+    return static_cast<int>(std::min<int64_t>(N, 8 * static_cast<int64_t>(sms)));
+}
+
+template <typename T, int VE, int NV>
+cudaError_t run_grad(const NormGradArgs &a, int groups, cudaStream_t s)
+{
+    const int warps = warps_for(a.D, VE * NV);
+    if (warps == 1)
+        rmsnorm_grad_kernel<T, VE, NV><<<(groups + 3) / 4, 128, 0, s>>>(a, 1, groups);
+    else
+        rmsnorm_grad_kernel<T, VE, NV><<<groups, 32 * warps, 0, s>>>(a, warps, groups);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t grad_type(const NormGradArgs &a, int groups, int sms, cudaStream_t s)
+{
+    constexpr int VE = 16 / sizeof(T);
+    const bool wide = a.D % VE == 0 && aligned16(a.dout) && aligned16(a.total) &&
+                      aligned16(a.weight) && aligned16(a.dtotal) && aligned16(a.dx);
+    if (!wide) {
+        switch (vectors_for<1>(a.N, a.D, 4, 64, sms)) {
+        case 4:
+            return run_grad<T, 1, 4>(a, groups, s);
+        case 16:
+            return run_grad<T, 1, 16>(a, groups, s);
+        default:
+            return run_grad<T, 1, 64>(a, groups, s);
+        }
+    }
+    int nv = vectors_for<VE>(a.N, a.D, 1, 32 / VE, sms);
+    if (warps_for(a.D, VE * nv) > 16)
+        nv = 64 / VE;
+    switch (nv) {
+    case 1:
+        return run_grad<T, VE, 1>(a, groups, s);
+    case 2:
+        return run_grad<T, VE, 2>(a, groups, s);
+    case 4:
+        return run_grad<T, VE, 4>(a, groups, s);
+    case 8:
+        return run_grad<T, VE, 8>(a, groups, s);
+    default:
+        return run_grad<T, VE, 64 / VE>(a, groups, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm(const void *X, int dtype, int64_t N, int64_t D, const void *residual,
+                           const void *weight, int weight_dtype, float eps, void *total, void *out,
+                           int out_dtype, float *scales, float *rstd, int sms, cudaStream_t stream)
+{
+    const NormArgs a{X,   residual, weight, weight_dtype == kFp32, N, static_cast<int32_t>(D), eps,
+                     total, out,    scales, rstd};
+    const bool codes = out_dtype == kE4m3;
+    if (dtype == kFp32)
+        return norm_type<float>(a, codes, sms, stream);
+    if (dtype == kBf16)
+        return norm_type<__nv_bfloat16>(a, codes, sms, stream);
+    return norm_type<__half>(a, codes, sms, stream);
+}
+
+size_t rmsnorm_grad_parts_bytes(int64_t N, int64_t D, int sms)
+{
+    return static_cast<size_t>(grad_groups(N, sms)) * D * sizeof(float);
+}
+
+cudaError_t launch_rmsnorm_grad(const void *dout, int dtype, int64_t N, int64_t D,
+                                const void *total, const void *weight, int weight_dtype,
+                                const float *rstd, const void *dtotal, void *dX, float *dweight,
+                                float *parts, int sms, cudaStream_t stream)
+{
+    const int groups = grad_groups(N, sms);
+    const NormGradArgs a{dout, total, weight, dtotal, weight_dtype == kFp32,
+                         rstd, N,     static_cast<int32_t>(D), dX, dweight != nullptr ? parts : nullptr};
+    cudaError_t e = dtype == kFp32   ? grad_type<float>(a, groups, sms, stream)
+                    : dtype == kBf16 ? grad_type<__nv_bfloat16>(a, groups, sms, stream)
+                                     : grad_type<__half>(a, groups, sms, stream);
+    if (e == cudaSuccess && dweight != nullptr) {
+        join_parts_kernel<<<static_cast<unsigned>((D + 31) / 32), 1024, 0, stream>>>(
+            parts, groups, static_cast<int>(D), dweight);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+}  // namespace kma
