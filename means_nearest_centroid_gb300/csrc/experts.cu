@@ -39,8 +39,7 @@
 #include "experts_ptx.cuh"
 #include "learn.h"
 #include "pipeline.cuh"
-
-#include <cuda_fp16.h>
+#include "vec.cuh"
 
 #include <algorithm>
 
@@ -48,27 +47,31 @@ namespace kma {
 
 namespace {
 
-constexpr int kEpilogueWarps = 8;
-constexpr int kWarpA = 8, kWarpB = 9, kWarpMma = 10, kWarpScale = 11;
-constexpr int kThreads = 32 * 12;
+// A block: CW (8 or 16) warps of consumers, then one each for A, B, the MMAs
+// and the scales.  Registers a thread: the launch's (65,536 over the threads),
+// of which the last warpgroup gives up some for the consumers, who hold up to
+// 128 (8 warps) or 64 (16) sums.
+constexpr int threads_of(int CW) { return 32 * (CW + 4); }
+__host__ __device__ constexpr int consumer_regs(int CW) { return CW == 8 ? 208 : 104; }
+__host__ __device__ constexpr int other_regs(int CW) { return CW == 8 ? 80 : 64; }
+static_assert(2 * consumer_regs(8) + other_regs(8) <= 3 * 168, "the launch's registers");
+static_assert(4 * consumer_regs(16) + other_regs(16) <= 5 * 96, "the launch's registers");
 constexpr int kRowsA = 128;                        // rows of A a CTA holds
-constexpr int kMaxN = 256;                         // columns of a tile
-constexpr uint32_t kPartBytes = kRowsA * 128;      // one operand's k-block in a CTA
-constexpr uint32_t kStageBytes = 2 * kPartBytes;
+constexpr uint32_t kPartA = kRowsA * 128;          // A's k-block in a CTA
 constexpr uint32_t kAtomBytes = 64 * 128;          // MN-major: 64 elements by 64 rows
 constexpr int kScaleStages = 8;
-constexpr uint32_t kTmemColumns = 2 * kMaxN;       // two accumulators
+constexpr uint32_t kGroupBarrier = 1;              // named barriers of the consumers' groups
 // 16-bit k-blocks between two additions to registers: 2,048 elements.
 constexpr int kSegment = 32;
 
 // Barriers: full and empty of each stage, of the accumulators, of the scales;
-// one for each loader's k-blocks with missing rows; the last MMA's.
-constexpr int kMaxRing = 8;
+// one for each loader's k-blocks with missing rows; the issuers' last MMAs'.
+constexpr int kMaxRing = 10;
 constexpr int kFull = 0, kEmpty = kFull + kMaxRing;
 constexpr int kAccF = kEmpty + kMaxRing, kAccE = kAccF + 2;
 constexpr int kScF = kAccE + 2, kScE = kScF + kScaleStages;
 constexpr int kFix = kScE + kScaleStages, kLast = kFix + 2;
-constexpr int kBars = kLast + 1;
+constexpr int kBars = kLast + 2;
 
 struct Tile {
     int32_t e, m0, n0, n;      // expert; first row and column; columns (a multiple of 32)
@@ -76,24 +79,28 @@ struct Tile {
     int32_t kblocks;
 };
 
-// Shared memory behind the ring: scales, then the lists' starts, ends and the
+// Shared memory behind the ring: the consumers' staging and row numbers, scales, then the lists' starts, ends and the
 // tiles before each expert, then barriers.
 struct Layout {
-    uint32_t ring, scale, lists, bars, end;
+    uint32_t ring, staging, dst, scale, lists, bars, end;
 };
 
-__host__ __device__ inline Layout layout_of(int stages, int E, bool scaled)
+__host__ __device__ constexpr uint32_t stage_bytes(int NT) { return kPartA + NT / 2 * 128; }
+
+__host__ __device__ inline Layout layout_of(int NT, int stages, int E, bool scaled)
 {
     Layout l;
     l.ring = 0;
-    l.scale = stages * kStageBytes;
-    l.lists = l.scale + (scaled ? kScaleStages * kMaxN * 4u : 0u);
+    l.staging = stages * stage_bytes(NT);         // shared by the groups of consumers
+    l.dst = l.staging + 16384u;           // [group][tile parity][columns]
+    l.scale = l.dst + 2u * NT * 4u;
+    l.lists = l.scale + (scaled ? kScaleStages * NT * 4u : 0u);
     l.bars = (l.lists + 3u * static_cast<uint32_t>(E + 1) * 4u + 15u) / 16u * 16u;
     l.end = l.bars + kBars * 8u + 16u;
     return l;
 }
 
-template <ExpertsKind KIND>
+template <ExpertsKind KIND, int NT>
 struct Schedule {
     const ExpertsParams &p;
     const int32_t *begin, *end, *before;
@@ -105,7 +112,7 @@ struct Schedule {
         end = lists + (p.E + 1);
         before = lists + 2 * (p.E + 1);
         mblocks = (p.mdim + 2 * kRowsA - 1) / (2 * kRowsA);
-        nblocks = (p.ndim + kMaxN - 1) / kMaxN;
+        nblocks = (p.ndim + NT - 1) / NT;
         total = KIND == kWeightsGrad ? p.E * mblocks * nblocks : before[p.E] * mblocks;
     }
 
@@ -116,9 +123,9 @@ struct Schedule {
         w.m0 = (t - q * mblocks) * 2 * kRowsA;
         if (KIND == kWeightsGrad) {
             w.e = q / nblocks;
-            w.n0 = (q - w.e * nblocks) * kMaxN;
+            w.n0 = (q - w.e * nblocks) * NT;
             // whole atoms of 64 columns in each CTA
-            w.n = min(kMaxN, (p.ndim - w.n0 + 127) / 128 * 128);
+            w.n = min(NT, (p.ndim - w.n0 + 127) / 128 * 128);
             w.lo = begin[w.e];
             w.hi = end[w.e];
             w.kblocks = (w.hi - w.lo + 63) / 64;
@@ -135,7 +142,7 @@ struct Schedule {
         w.e = lo;
         w.lo = begin[lo];
         w.hi = end[lo];
-        // an expert's positions in even parts of at most 256, each a multiple of 32
+        // an expert's positions in even parts of at most NT, each a multiple of 32
         const int parts = before[lo + 1] - before[lo];
         w.n = ((w.hi - w.lo + parts - 1) / parts + 31) / 32 * 32;
         w.n0 = w.lo + (q - before[lo]) * w.n;
@@ -147,6 +154,7 @@ struct Schedule {
 // Starts, ends and tiles before each expert, by one warp.  What the offsets
 // hold is clamped to [0, M], an end to its start: no position is out of range,
 // whatever they are.
+template <int NT>
 __device__ void form_lists(const ExpertsParams &p, int32_t *lists, int lane)
 {
     int32_t *begin = lists, *end = lists + (p.E + 1), *before = lists + 2 * (p.E + 1);
@@ -160,7 +168,7 @@ __device__ void form_lists(const ExpertsParams &p, int32_t *lists, int lane)
             begin[e] = lo;
             end[e] = hi;
         }
-        const int tiles = (hi - lo + kMaxN - 1) / kMaxN;
+        const int tiles = (hi - lo + NT - 1) / NT;
         int sum = tiles;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -190,60 +198,121 @@ __device__ __forceinline__ int32_t row_of(const RowMap &m, int32_t at, int32_t h
     return row < m.rows ? row : -1;
 }
 
-template <int TYPE>
-struct Pack;
-template <>
-struct Pack<kBf16> {
-    static __device__ __forceinline__ uint32_t two(float a, float b)
-    {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t *>(&v);
-    }
-};
-template <>
-struct Pack<kFp16> {
-    static __device__ __forceinline__ uint32_t two(float a, float b)
-    {
-        const __half2 v = __floats2half2_rn(a, b);
-        return *reinterpret_cast<const uint32_t *>(&v);
-    }
-};
-
-// 32 columns of a warp's 32 rows: lane l holds element f of the columns' output
-// rows, whose index is at lane c for column c (-1: not stored).  Two lanes trade
-// so that each stores two neighbouring elements of one row: 64 bytes of a row
-// in a warp's store.
-template <int TYPE>
-__device__ __forceinline__ void store_columns(const float (&v)[32], void *out, int32_t dst,
-                                              int32_t f, int32_t mdim, int lane)
+// Weights' gradient: whether a position adds nothing.
+__device__ __forceinline__ bool missing(const ExpertsParams &p, int32_t at, int32_t hi)
 {
-    const bool odd = lane & 1;
-    uint8_t *const base = static_cast<uint8_t *>(out) + 2 * static_cast<int64_t>(f & ~1);
-#pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-        const float mine = odd ? v[c + 1] : v[c];
-        const float other = __shfl_xor_sync(0xffffffffu, odd ? v[c] : v[c + 1], 1);
-        const int32_t row = __shfl_sync(0xffffffffu, dst, c + (lane & 1));
-        if (row >= 0 && f < mdim)
-            *reinterpret_cast<uint32_t *>(base + 2 * static_cast<int64_t>(row) * mdim) =
-                odd ? Pack<TYPE>::two(other, mine) : Pack<TYPE>::two(mine, other);
-    }
-}
-template <>
-__device__ __forceinline__ void store_columns<kFp32>(const float (&v)[32], void *out, int32_t dst,
-                                                     int32_t f, int32_t mdim, int lane)
-{
-    float *const base = static_cast<float *>(out) + f;
-#pragma unroll
-    for (int c = 0; c < 32; ++c) {
-        const int32_t row = __shfl_sync(0xffffffffu, dst, c);
-        if (row >= 0 && f < mdim)
-            base[static_cast<int64_t>(row) * mdim] = v[c];
-    }
+    return row_of(p.from, at, hi) < 0 || row_of(p.placed, at, hi) < 0;
 }
 
-template <ExpertsKind KIND, bool E8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+// Waits for a stage's operands (a whole warp).  Where threads of either CTA may
+// have written them, the wait acquires at the cluster's scope.
+__device__ __forceinline__ bool wait_operands(uint32_t bar, uint32_t parity, bool threads_write,
+                                              volatile uint32_t *abort_flag, uint64_t limit_ns)
+{
+    if (!wait_warp(bar, parity, abort_flag, limit_ns))
+        return false;
+    if (threads_write)
+        mbar_acquire_cluster(bar, parity);   // complete already: returns at once
+    return true;
+}
+
+// A warp's sums: 32 rows (elements of an output row) by COLS columns (output
+// rows).  Lane l holds, for each half of 16 rows and each 8 columns, rows l / 4
+// and l / 4 + 8 of columns 2 (l % 4) and the next: v[0], v[1] and v[2], v[3].
+template <int COLS>
+struct Frags {
+    float v[COLS / 8][2][4];
+};
+
+// 8 x 8 16-bit matrices out of such fragments to shared memory, transposed:
+// lane l gives the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void store_matrices(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                               uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+template <typename O>
+__device__ __forceinline__ uint32_t pack_two(float a, float b)
+{
+    const O two[2] = {Elem<O>::down(a), Elem<O>::down(b)};
+    uint32_t r;
+    memcpy(&r, two, 4);
+    return r;
+}
+
+// A group's threads (four warps, 128 rows of the tile) turn their columns into
+// rows of the output by way of shared memory, some columns at a time: a column's
+// 128 elements stand together there, their 16-byte pieces at piece ^ (column %
+// 8) so that no two lanes meet in a bank, and are stored as one run of 256 bytes
+// (fp32: 512).  BYTES of staging hold one buffer, or two that take turns where
+// both hold 8 columns.
+// `dst`: the output rows of the group's columns; -1: none, -2 - row: a row of
+// zeros.
+template <typename O, int COLS, int BYTES>
+__device__ __forceinline__ void store_columns(const Frags<COLS> &sum, int cols, uint8_t *stage,
+                                              const int32_t *dst, void *out, int32_t m,
+                                              int32_t mdim, int group, int thread)
+{
+    constexpr int kColBytes = 128 * sizeof(O);
+    constexpr int kBuffers = BYTES >= 2 * 8 * kColBytes ? 2 : 1;
+    constexpr int kCols = BYTES / kBuffers / kColBytes < COLS ? BYTES / kBuffers / kColBytes : COLS;
+    constexpr int kLanes = kColBytes / 16;           // threads to a column
+    constexpr int kPerThread = 16 / sizeof(O);
+    static_assert(kCols % 8 == 0 && COLS % kCols == 0, "whole matrices");
+    // columns come in multiples of 32: the next tile starts with the other buffer
+    static_assert(kBuffers == 1 || 32 % (2 * kCols) == 0, "an even number of turns");
+    const int piece = thread % kLanes;
+    const int lane = thread & 31, q = thread >> 5;
+    const bool inside = m + piece * kPerThread < mdim;
+    O *const to = static_cast<O *>(out) + m + piece * kPerThread;
+#pragma unroll
+    for (int c = 0; c < COLS; c += kCols) {
+        if (c < cols) {
+            uint8_t *const buf = stage + (c / kCols % kBuffers) * (BYTES / kBuffers);
+            if (kBuffers == 1)
+                named_bar_sync(kGroupBarrier + group, 128);
+#pragma unroll
+            for (int j = 0; j < kCols / 8; ++j) {
+                const float(&v)[2][4] = sum.v[c / 8 + j];
+                if constexpr (sizeof(O) == 2) {
+                    const int col = 8 * j + (lane & 7);
+                    const int at = (4 * q + (lane >> 3)) ^ (lane & 7);
+                    store_matrices(smem_addr(buf) + col * kColBytes + 16 * at,
+                                   pack_two<O>(v[0][0], v[0][1]), pack_two<O>(v[0][2], v[0][3]),
+                                   pack_two<O>(v[1][0], v[1][1]), pack_two<O>(v[1][2], v[1][3]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int col = 8 * j + 2 * (lane & 3) + (i & 1);
+                        const int f = 32 * q + 16 * (i >> 2) + 8 * (i >> 1 & 1) + (lane >> 2);
+                        *reinterpret_cast<float *>(buf + col * kColBytes +
+                                                   16 * ((f >> 2) ^ (col & 7)) + 4 * (f & 3)) =
+                            v[i >> 2][i & 3];
+                    }
+                }
+            }
+            named_bar_sync(kGroupBarrier + group, 128);
+#pragma unroll
+            for (int i = 0; i < kCols; i += 128 / kLanes) {
+                const int col = i + thread / kLanes;
+                const int32_t d = dst[c + col];
+                uint4 v = *reinterpret_cast<const uint4 *>(buf + col * kColBytes +
+                                                           16 * (piece ^ (col & 7)));
+                if (d < -1)
+                    v = make_uint4(0, 0, 0, 0);
+                const int32_t row = d < -1 ? -2 - d : d;
+                if (row >= 0 && inside)
+                    *reinterpret_cast<uint4 *>(to + static_cast<int64_t>(row) * mdim) = v;
+            }
+        }
+    }
+}
+
+template <ExpertsKind KIND, bool E8, int NT, int CW>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
     experts_kernel(const __grid_constant__ CUtensorMap amap,
                    const __grid_constant__ CUtensorMap bmap, const ExpertsParams p)
 {
@@ -252,12 +321,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     constexpr bool kFixes = KIND == kWeightsGrad;   // loaders zero missing rows
     constexpr int kSeg = E8 ? 1 : kSegment;
     constexpr int kElems = E8 ? 128 : 64;           // elements of a k-block
+    constexpr bool kGathers = KIND == kForward && NT == 64;
+    constexpr uint32_t kStageBytes = stage_bytes(NT);
+    constexpr int kWarpA = CW, kWarpB = CW + 1, kWarpMma = CW + 2, kWarpScale = CW + 3;
+    // 8 bits: every k-block is a segment with an accumulator to hand over, which
+    // takes the issuing warp about as long again as its MMAs take.  So two warps
+    // issue, one for each accumulator, and one loader brings both operands.
+    constexpr bool kTwo = E8 && NT == 256;
+    constexpr int kGroupCols = NT / (CW / 4);       // columns of a group of consumers
+    constexpr uint32_t kStagingBytes = 16384 / (CW / 4);   // of a group
+    constexpr uint32_t kTmemColumns = 2 * NT;       // two accumulators
     constexpr uint16_t kBoth = 0x3;
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    const Layout lay = layout_of(p.stages, p.E, E8);
+    const Layout lay = layout_of(NT, p.stages, p.E, E8);
     uint8_t *const sbase = smem_raw + (base - raw);
     int32_t *const lists = reinterpret_cast<int32_t *>(sbase + lay.lists);
     float *const scales = reinterpret_cast<float *>(sbase + lay.scale);
@@ -267,29 +346,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto bar = [&](int i) -> uint32_t { return base + lay.bars + 8u * static_cast<uint32_t>(i); };
     auto lead_bar = [&](int i) -> uint32_t { return map_to_rank(bar(i), 0); };
     auto part_a = [&](uint32_t stage) { return base + stage * kStageBytes; };
-    auto part_b = [&](uint32_t stage) { return base + stage * kStageBytes + kPartBytes; };
+    auto part_b = [&](uint32_t stage) { return base + stage * kStageBytes + kPartA; };
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
+    const bool gathers = kGathers && p.b_rows.ids != nullptr;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxRing; ++s) {
-            // both loaders of the leader, or of both CTAs
-            mbar_init(bar(kFull + s), kFixes ? 4 : 2);
+            // the leader's loaders; both CTAs' where a loader may zero rows
+            mbar_init(bar(kFull + s), kFixes ? 4 : kTwo ? 1 : 2);
             mbar_init(bar(kEmpty + s), 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(bar(kAccF + a), 1);
-            mbar_init(bar(kAccE + a), 2 * kEpilogueWarps);
+            mbar_init(bar(kAccE + a), 2 * CW);
             mbar_init(bar(kFix + a), 1);
+            mbar_init(bar(kLast + a), 1);
         }
         for (int s = 0; s < kScaleStages; ++s) {
-            mbar_init(bar(kScF + s), 32);
-            mbar_init(bar(kScE + s), kEpilogueWarps);
+            mbar_init(bar(kScF + s), 1);
+            mbar_init(bar(kScE + s), CW);
         }
-        mbar_init(bar(kLast), 1);
         *abort_flag = 0u;
         fence_mbar_init();
     }
@@ -297,14 +377,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_alloc_pair(smem_addr(const_cast<uint32_t *>(tmem_slot)), kTmemColumns);
         tmem_relinquish_pair();
     } else if (warp == 1) {
-        form_lists(p, lists, lane);
+        form_lists<NT>(p, lists, lane);
     }
     tc_fence_before();
     __syncthreads();
     cluster_sync();   // both CTAs' barriers exist before any cross-CTA signal
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const Schedule<KIND> plan(p, lists);
+    const Schedule<KIND, NT> plan(p, lists);
     const int first = static_cast<int>(blockIdx.x >> 1);
     const int step = static_cast<int>(gridDim.x >> 1);
     const uint32_t stages = static_cast<uint32_t>(p.stages);
@@ -316,12 +396,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     };
 
-    if (warp == kWarpA || warp == kWarpB) {
+    if (warp >= CW) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(CW)));
+    if ((warp == kWarpA && !kTwo) || warp == kWarpB) {
         const bool is_a = warp == kWarpA;
         uint32_t stage = 0, phase = 0, fixes = 0;
         bool ok = true;
-        if (lane == 0)
-            tma_prefetch_desc(is_a ? &amap : &bmap);
         auto next_stage = [&]() {
             if (++stage == stages) {
                 stage = 0;
@@ -329,29 +409,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         };
         if constexpr (kFixes) {
-            // Rows of positions, 64 to a k-block, as atoms of 64 columns:
-            // lane l has the four rows 4 (l % 16) .. of atom l / 16.
-            const RowMap &map = is_a ? p.a_rows : p.b_rows;
+            // Rows of positions, 64 to a k-block, as atoms of 64 columns.
             const void *tmap = is_a ? &amap : &bmap;
-            const int four = 4 * (lane & 15), atom = lane >> 4;
+            const bool holes = p.holes != nullptr && *p.holes != 0;
             for (int t = first; ok && t < plan.total; t += step) {
                 const Tile w = plan.tile(t);
                 const int atoms = is_a ? 2 : w.n / 128;
                 const int x = (is_a ? w.m0 : w.n0) + static_cast<int>(rank) * 64 * atoms;
                 const uint32_t bytes = atoms * kAtomBytes;
                 for (int kb = 0; ok && kb < w.kblocks; ++kb, next_stage()) {
-                    const int at = w.lo + kb * 64 + four;
-                    int32_t row[4];
-                    uint32_t gone = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        row[i] = row_of(map, at + i, w.hi);
-                        if (row[i] < 0) {
-                            gone |= 1u << i;
-                            row[i] = 0;   // a row that exists; zeroed below
-                        }
-                    }
-                    const bool fix = __any_sync(0xffffffffu, gone != 0);
+                    const int at = w.lo + kb * 64;
+                    const bool fix = at + 64 > w.hi || holes;
                     if (!(ok = wait_warp(bar(kEmpty + stage), phase ^ 1u, abort_flag, p.timeout_ns)))
                         break;
                     const uint32_t dst = is_a ? part_a(stage) : part_b(stage);
@@ -364,33 +432,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             mbar_arrive_expect_tx(bar(kFull + stage), 2 * bytes);
                         else
                             mbar_arrive_cluster(full);
+                        const uint32_t done = fix ? map_to_rank(own_fix, rank) : full;
+                        for (int a = 0; a < atoms; ++a)
+                            tma_load_2d_pair(dst + a * kAtomBytes, tmap, done, x + 64 * a, at);
                     }
                     __syncwarp();
-                    const uint32_t done = fix ? map_to_rank(own_fix, rank) : full;
-                    if (map.ids != nullptr) {
-                        if (atom < atoms)
-                            tma_gather4_pair(dst + atom * kAtomBytes + four * 128, tmap, done,
-                                             x + 64 * atom, row);
-                    } else if (lane == 0) {
-                        for (int a = 0; a < atoms; ++a)
-                            tma_load_2d_pair(dst + a * kAtomBytes, tmap, done, x + 64 * a,
-                                             w.lo + kb * 64);
-                    }
                     if (fix) {
                         ok = wait_warp(own_fix, fixes & 1u, abort_flag, p.timeout_ns);
                         ++fixes;
                         if (!ok)
                             break;
+                        // lane l: whether positions l and 32 + l are missing
+                        const uint32_t gone[2] = {
+                            __ballot_sync(0xffffffffu, missing(p, at + lane, w.hi)),
+                            __ballot_sync(0xffffffffu, missing(p, at + 32 + lane, w.hi))};
                         // whole rows: the swizzle moves 16-byte pieces within a row
-                        if (atom < atoms) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (gone >> i & 1u)
-                                    for (int c = 0; c < 8; ++c)
-                                        st_shared_v4_u32(dst + atom * kAtomBytes + (four + i) * 128 +
-                                                             16 * c,
-                                                         0, 0, 0, 0);
-                        }
+                        for (int i = lane; i < 64 * 8; i += 32)
+                            if (gone[i >> 8] >> (i >> 3 & 31) & 1u)
+                                for (int a = 0; a < atoms; ++a)
+                                    st_shared_v4_u32(dst + a * kAtomBytes + 16 * i, 0, 0, 0, 0);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0)
@@ -401,6 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         } else if (is_a) {
             // The weights of the tile's 128 rows of this CTA.
             if (lane == 0) {
+                tma_prefetch_desc(&amap);
                 for (int t = first; ok && t < plan.total; t += step) {
                     const Tile w = plan.tile(t);
                     const int m = w.m0 + static_cast<int>(rank) * kRowsA;
@@ -408,7 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (!(ok = wait1(bar(kEmpty + stage), phase ^ 1u, abort_flag, p.timeout_ns)))
                             break;
                         if (leader)
-                            mbar_arrive_expect_tx(bar(kFull + stage), 2 * kPartBytes);
+                            mbar_arrive_expect_tx(bar(kFull + stage), 2 * kPartA);
                         const uint32_t full = lead_bar(kFull + stage);
                         if (kAMn) {
                             tma_load_3d_pair(part_a(stage), &amap, full, m, kb * 64, w.e);
@@ -422,23 +483,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         } else {
             // The positions' rows: this CTA's half of the tile's columns.
+            if (lane == 0)
+                tma_prefetch_desc(&bmap);
             for (int t = first; ok && t < plan.total; t += step) {
                 const Tile w = plan.tile(t);
                 const int half = w.n / 2;
                 const int at = w.n0 + static_cast<int>(rank) * half;
-                const bool gathers = p.b_rows.ids != nullptr;
                 const int boxes = (half + 31) / 32;
                 const uint32_t bytes = gathers ? half * 128 : boxes * 4096;
                 int32_t row[4];
+                if (kGathers) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)   // a column without a row: any row, not stored or zero
-                    row[i] = gathers ? max(row_of(p.b_rows, at + 4 * lane + i, w.hi), 0) : 0;
+                    for (int i = 0; i < 4; ++i)   // none: any row, the column is zero or not stored
+                        row[i] = gathers ? max(row_of(p.b_rows, at + 4 * lane + i, w.hi), 0) : 0;
+                }
                 for (int kb = 0; kb < w.kblocks; ++kb, next_stage()) {
                     if (!(ok = wait_warp(bar(kEmpty + stage), phase ^ 1u, abort_flag, p.timeout_ns)))
                         break;
                     if (leader && lane == 0)
-                        mbar_arrive_expect_tx(bar(kFull + stage), 2 * bytes);
+                        mbar_arrive_expect_tx(bar(kFull + stage), 2 * (bytes + (kTwo ? kPartA : 0)));
                     const uint32_t full = lead_bar(kFull + stage);
+                    if (kTwo && lane == 31)
+                        tma_load_3d_pair(part_a(stage), &amap, full, kb * kElems,
+                                         w.m0 + static_cast<int>(rank) * kRowsA, w.e);
                     if (gathers) {
                         if (4 * lane < half)
                             tma_gather4_pair(part_b(stage) + 512 * lane, &bmap, full, kb * kElems,
@@ -453,28 +520,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok && lane == 0)
             let_copies_land();
         __syncwarp();
-    } else if (warp == kWarpMma) {
+    } else if (warp == kWarpMma || (warp == kWarpA && kTwo)) {
         if (leader) {
+            const uint32_t me = kTwo && warp == kWarpA;
             uint32_t stage = 0, phase = 0, acc = 0;
             bool ok = true, issued = false;
+            auto next_stage = [&]() {
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            };
             for (int t = first; ok && t < plan.total; t += step) {
                 const Tile w = plan.tile(t);
                 const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
                 for (int k0 = 0; ok && k0 < w.kblocks; k0 += kSeg, ++acc) {
                     const uint32_t as = acc & 1u;
+                    if (kTwo && as != me) {
+                        next_stage();
+                        continue;
+                    }
                     if (!(ok = wait_warp(bar(kAccE + as), ((acc >> 1) & 1u) ^ 1u, abort_flag,
                                          p.timeout_ns)))
                         break;
                     tc_fence_after();
-                    const uint32_t d = tmem_base + as * kMaxN;
+                    const uint32_t d = tmem_base + as * NT;
                     const int k1 = min(k0 + kSeg, w.kblocks);
-                    for (int kb = k0; kb < k1; ++kb) {
-                        if (!(ok = wait_warp(bar(kFull + stage), phase, abort_flag, p.timeout_ns)))
+                    for (int kb = k0; kb < k1; ++kb, next_stage()) {
+                        if (!(ok = wait_operands(bar(kFull + stage), phase, kFixes, abort_flag,
+                                                 p.timeout_ns)))
                             break;
-                        if (kFixes) {
-                            fence_acquire_cluster();
-                            fence_proxy_async_smem();
-                        }
                         const uint64_t a = kAMn ? sw128_mnmajor_desc(part_a(stage), kAtomBytes)
                                                 : sw128_kmajor_desc(part_a(stage));
                         const uint64_t b = kBMn ? sw128_mnmajor_desc(part_b(stage), kAtomBytes)
@@ -496,18 +571,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                         __syncwarp();
                         issued = true;
-                        if (++stage == stages) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
                     }
                 }
             }
             if (issued) {
                 if (elect_one())
-                    mma_commit_pair(bar(kLast), 0x1);
+                    mma_commit_pair(bar(kLast + me), 0x1);
                 __syncwarp();
-                wait_warp(bar(kLast), 0u, abort_flag, kDrainLimitNs, false);
+                wait_warp(bar(kLast + me), 0u, abort_flag, kDrainLimitNs, false);
             }
         }
     } else if (warp == kWarpScale) {
@@ -521,63 +592,98 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int fb = min((w.m0 >> 7) + static_cast<int>(rank), p.fblocks - 1);
                 const float *ws =
                     p.wscale + (static_cast<int64_t>(w.e) * p.fblocks + fb) * w.kblocks;
-                const float *xs[8];
+                constexpr int kPer = NT / 32;   // columns a lane
+                int32_t row[kPer];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    xs[i] = p.xscale + static_cast<int64_t>(max(
-                                           row_of(p.b_rows, w.n0 + 32 * i + lane, w.hi), 0)) *
-                                           w.kblocks;
-                for (int kb = 0; kb < w.kblocks; ++kb, ++n) {
-                    const uint32_t s = n % kScaleStages;
-                    const float one = __ldg(ws + kb);
-                    float v[8];
+                for (int i = 0; i < kPer; ++i)
+                    row[i] = max(row_of(p.from, w.n0 + 32 * i + lane, w.hi), 0);
+                // Two k-blocks are loaded ahead: a load takes about as long as
+                // the tensor cores need for both.
+                float v[3][kPer], one[3];
+                auto load = [&](int kb, float (&to)[kPer], float &ws_kb) {
+                    if (kb < w.kblocks) {
+                        ws_kb = __ldg(ws + kb);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[i] = 32 * i < w.n ? __ldg(xs[i] + kb) * one : 0.0f;
-                    if (!(ok = wait_warp(bar(kScE + s), ((n / kScaleStages) & 1u) ^ 1u, abort_flag,
-                                         p.timeout_ns)))
-                        break;
+                        for (int i = 0; i < kPer; ++i)
+                            if (32 * i < w.n)
+                                to[i] = __ldg(p.xscale +
+                                              static_cast<int64_t>(row[i]) * w.kblocks + kb);
+                    }
+                };
+                load(0, v[0], one[0]);
+                load(1, v[1], one[1]);
+                // unrolled: a value that is moved is waited for
+                for (int k0 = 0; ok && k0 < w.kblocks; k0 += 3) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (32 * i < w.n)
-                            scales[s * kMaxN + 32 * i + lane] = v[i];
-                    mbar_arrive(bar(kScF + s));
+                    for (int j = 0; j < 3; ++j) {
+                        const int kb = k0 + j;
+                        if (kb >= w.kblocks)
+                            break;
+                        const uint32_t s = n % kScaleStages;
+                        load(kb + 2, v[(j + 2) % 3], one[(j + 2) % 3]);
+                        if (!(ok = wait_warp(bar(kScE + s), ((n / kScaleStages) & 1u) ^ 1u,
+                                             abort_flag, p.timeout_ns)))
+                            break;
+#pragma unroll
+                        for (int i = 0; i < kPer; ++i)
+                            if (32 * i < w.n)
+                                scales[s * NT + 32 * i + lane] = v[j][i] * one[j];
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(bar(kScF + s));
+                        ++n;
+                    }
                 }
             }
         }
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(consumer_regs(CW)));
         // Consumers: warp q of four holds 32 of the CTA's 128 rows, the two
-        // groups of four the lower and the upper 128 columns.
+        // groups of four the lower and the upper half of the columns.
         const int q = warp & 3, group = warp >> 2;
-        const int c0 = group * (kMaxN / 2);
+        const int c0 = group * kGroupCols;
         const uint32_t tmem_warp = tmem_base + (static_cast<uint32_t>(q) << 21) + c0;
         if (p.zero_rest) {
             // Rows of no list: before the first and behind the last.
             const int32_t lo = p.E > 0 ? lists[0] : 0, hi = lists[p.E + 1 + p.E - 1];
             const int32_t rest = p.M - (hi - lo);
             const int64_t units = static_cast<int64_t>(p.mdim) * dtype_bytes(p.out_type) / 16;
-            for (int64_t r = blockIdx.x * kEpilogueWarps + warp; r < rest;
-                 r += gridDim.x * kEpilogueWarps) {
+            for (int64_t r = blockIdx.x * CW + warp; r < rest;
+                 r += gridDim.x * CW) {
                 const int64_t row = r < lo ? r : r - lo + hi;
                 uint4 *out = static_cast<uint4 *>(p.out) + row * units;
                 for (int64_t i = lane; i < units; i += 32)
                     out[i] = make_uint4(0, 0, 0, 0);
             }
         }
-        uint32_t acc = 0, n = 0;
+        const int thread = threadIdx.x & 127;
+        uint8_t *const staging = sbase + lay.staging + group * kStagingBytes;
+        int32_t *const dsts = reinterpret_cast<int32_t *>(sbase + lay.dst) + group * 2 * kGroupCols;
+        uint32_t acc = 0, n = 0, used = 0;
         bool ok = true;
         for (int t = first; ok && t < plan.total; t += step) {
             const Tile w = plan.tile(t);
-            const int cols = min(max(w.n - c0, 0), kMaxN / 2);
-            float sum[4][32];
-            if (E8 || w.kblocks == 0) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        sum[c][i] = 0.0f;
+            const int cols = min(max(w.n - c0, 0), kGroupCols);
+            int32_t *const dst = dsts + kGroupCols * (used & 1u);
+            if (cols > 0 && thread < kGroupCols) {
+                const int32_t at = w.n0 + c0 + thread;   // this thread's column
+                int32_t d;
+                if (KIND == kWeightsGrad) {
+                    d = at < p.ndim ? w.e * p.ndim + at : -1;
+                } else {
+                    d = row_of(p.places, at, w.hi);
+                    if (d >= 0 && row_of(p.from, at, w.hi) < 0)
+                        d = -2 - d;
+                }
+                dst[thread] = d;
             }
-            for (int k0 = 0; k0 < w.kblocks; k0 += kSeg, ++acc) {
+            used += cols > 0;
+            Frags<kGroupCols> sum;
+#pragma unroll
+            for (int i = 0; i < kGroupCols; ++i)
+                sum.v[i / 8][i / 4 % 2][i % 4] = 0.0f;
+            for (int k0 = 0; k0 < w.kblocks; k0 += kSeg, ++acc, ++n) {
                 const uint32_t as = acc & 1u;
                 const uint32_t s = n % kScaleStages;
                 if (E8 && !(ok = wait_warp(bar(kScF + s), (n / kScaleStages) & 1u, abort_flag,
@@ -587,26 +693,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     break;
                 tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (32 * c < cols) {
-                        float v[32];
-                        tmem_ld_32x32b_x32(tmem_warp + as * kMaxN + 32 * c, v);
-                        tmem_wait_ld();
-                        if (E8) {
-                            const uint32_t sc =
-                                base + lay.scale + 4u * (s * kMaxN + c0 + 32 * c);
+                for (int c = 0; c < kGroupCols; c += 32) {
+                    if (c < cols) {
+                        float2 f[4];
+                        if constexpr (E8) {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 f = ld_shared_v4(sc + 4u * i);
-                                fma2(sum[c][i], sum[c][i + 1], v[i], v[i + 1], f.x, f.y, sum[c][i],
-                                     sum[c][i + 1]);
-                                fma2(sum[c][i + 2], sum[c][i + 3], v[i + 2], v[i + 3], f.z, f.w,
-                                     sum[c][i + 2], sum[c][i + 3]);
+                            for (int j = 0; j < 4; ++j)
+                                f[j] = *reinterpret_cast<const float2 *>(
+                                    scales + s * NT + c0 + c + 8 * j + 2 * (lane & 3));
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float v[16];
+                            tmem_ld_16x256b_x4(tmem_warp + (h << 20) + as * NT + c, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                float &to = sum.v[c / 8 + i / 4][h][i % 4];
+                                if constexpr (E8)
+                                    to = fmaf(v[i], i & 1 ? f[i / 4].y : f[i / 4].x, to);
+                                else
+                                    to += v[i];
                             }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                sum[c][i] = k0 == 0 ? v[i] : sum[c][i] + v[i];
                         }
                     }
                 }
@@ -617,37 +725,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (E8)
                         mbar_arrive(bar(kScE + s));
                 }
-                ++n;
             }
             if (!ok)
                 break;
-            const int32_t f = w.m0 + static_cast<int>(rank) * kRowsA + 32 * q + lane;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (32 * c >= cols)
-                    break;
-                const int32_t at = w.n0 + c0 + 32 * c + lane;   // this lane's column
-                int32_t dst;
-                if (KIND == kWeightsGrad) {
-                    dst = at < p.ndim ? w.e * p.ndim + at : -1;
-                } else {
-                    dst = row_of(p.places, at, w.hi);
-                    uint32_t gone = __ballot_sync(
-                        0xffffffffu, p.b_rows.ids != nullptr && row_of(p.b_rows, at, w.hi) < 0);
-                    if (gone != 0) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (gone >> i & 1u)
-                                sum[c][i] = 0.0f;
-                    }
-                }
-                if (p.out_type == kBf16)
-                    store_columns<kBf16>(sum[c], p.out, dst, f, p.mdim, lane);
-                else if (p.out_type == kFp16)
-                    store_columns<kFp16>(sum[c], p.out, dst, f, p.mdim, lane);
-                else
-                    store_columns<kFp32>(sum[c], p.out, dst, f, p.mdim, lane);
-            }
+            const int32_t m = w.m0 + static_cast<int>(rank) * kRowsA;
+            if (p.out_type == kBf16)
+                store_columns<__nv_bfloat16, kGroupCols, kStagingBytes>(sum, cols, staging, dst, p.out, m, p.mdim, group, thread);
+            else if (p.out_type == kFp16)
+                store_columns<__half, kGroupCols, kStagingBytes>(sum, cols, staging, dst, p.out, m, p.mdim, group, thread);
+            else
+                store_columns<float, kGroupCols, kStagingBytes>(sum, cols, staging, dst, p.out, m, p.mdim, group, thread);
         }
     }
 
@@ -669,20 +756,75 @@ __global__ void __launch_bounds__(256)
         row[at] = at < lo ? -1 : row_of(map, static_cast<int32_t>(at), hi);
 }
 
+// Rows in the lists' order: to[p] = the row that map names for position p,
+// zeros where there is none in map or in also (*holes is then set, if given).
+// A power of two of lanes a row, up to eight 16-byte pieces in flight a lane.
+__global__ void __launch_bounds__(256, 4)
+    gather_rows_kernel(const int32_t *offsets, int32_t E, int32_t M, RowMap map, RowMap also,
+                       const uint4 *from, int32_t units, int32_t lanes, uint4 *to, int32_t *holes)
+{
+    const int32_t lo = offsets == nullptr ? 0 : min(max(__ldg(offsets), 0), M);
+    const int32_t hi = offsets == nullptr ? M : min(max(__ldg(offsets + E), 0), M);
+    const int32_t mine = threadIdx.x & (lanes - 1);
+    const int32_t rows = 256 / lanes;
+    for (int64_t at = blockIdx.x * static_cast<int64_t>(rows) + threadIdx.x / lanes; at < M;
+         at += gridDim.x * static_cast<int64_t>(rows)) {
+        const int32_t p = static_cast<int32_t>(at);
+        int32_t row = -1;
+        if (p >= lo && p < hi) {
+            row = row_of(map, p, hi);
+            if (row_of(also, p, hi) < 0)
+                row = -1;
+            if (row < 0 && holes != nullptr && mine == 0)
+                *holes = 1;
+        }
+        const uint4 *const src = from + static_cast<int64_t>(row) * units;
+        uint4 *const dst = to + at * units;
+        int32_t u = mine;
+        if (row >= 0) {
+            for (; u + 7 * lanes < units; u += 8 * lanes) {
+                uint4 v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    v[k] = __ldg(src + u + k * lanes);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    dst[u + k * lanes] = v[k];
+            }
+        }
+        for (; u < units; u += lanes)
+            dst[u] = row >= 0 ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+    }
+}
+
 // Ring depth that fits beside the lists and scales.
-int stages_for(int E, bool scaled, size_t smem)
+int stages_for(int NT, int E, bool scaled, size_t smem)
 {
     for (int s = kMaxRing; s >= 2; --s)
-        if (1024u + layout_of(s, E, scaled).end <= smem)
+        if (1024u + layout_of(NT, s, E, scaled).end <= smem)
             return s;
     return 0;
 }
 
-template <ExpertsKind KIND, bool E8>
-cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const ExpertsParams &p, int grid,
-                   size_t smem, cudaStream_t stream)
+// Consumer warps of the wide tiles.
+constexpr int kWide = 8, kWideE8 = 16;
+
+template <ExpertsKind KIND, bool E8, int NT, int CW>
+cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, ExpertsParams p, int sms,
+                   size_t smem_optin, cudaStream_t stream)
 {
-    experts_kernel<KIND, E8><<<grid, kThreads, smem, stream>>>(a, b, p);
+    p.stages = stages_for(NT, p.E, E8, smem_optin);
+    if (p.stages == 0)
+        return cudaErrorInvalidConfiguration;
+    const size_t smem = 1024u + layout_of(NT, p.stages, p.E, E8).end;
+    // no more clusters than tiles there can be
+    const int64_t mblocks = (p.mdim + 2 * kRowsA - 1) / (2 * kRowsA);
+    const int64_t tiles = KIND == kWeightsGrad
+                              ? mblocks * ((p.ndim + NT - 1) / NT) * p.E
+                              : mblocks * (std::min<int64_t>(p.E, p.M) + p.M / NT);
+    const int grid =
+        2 * static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tiles, sms / 2)));
+    experts_kernel<KIND, E8, NT, CW><<<grid, threads_of(CW), smem, stream>>>(a, b, p);
     return cudaGetLastError();
 }
 
@@ -690,10 +832,13 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const ExpertsPara
 
 cudaError_t experts_prepare(size_t smem_optin)
 {
-    const void *kernels[4] = {
-        (const void *)experts_kernel<kForward, false>, (const void *)experts_kernel<kForward, true>,
-        (const void *)experts_kernel<kRowsGrad, false>,
-        (const void *)experts_kernel<kWeightsGrad, false>};
+    const void *kernels[] = {(const void *)experts_kernel<kForward, false, 64, 8>,
+                             (const void *)experts_kernel<kForward, false, 256, kWide>,
+                             (const void *)experts_kernel<kForward, true, 64, 8>,
+                             (const void *)experts_kernel<kForward, true, 256, kWideE8>,
+                             (const void *)experts_kernel<kRowsGrad, false, 64, 8>,
+                             (const void *)experts_kernel<kRowsGrad, false, 256, kWide>,
+                             (const void *)experts_kernel<kWeightsGrad, false, 256, kWide>};
     for (const void *k : kernels) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(smem_optin));
@@ -703,32 +848,27 @@ cudaError_t experts_prepare(size_t smem_optin)
     return cudaSuccess;
 }
 
+bool experts_few(int64_t M, int64_t E) { return M <= 32 * E; }
+
 cudaError_t launch_experts(ExpertsKind kind, bool e8, int type, const CUtensorMap &a,
                            const CUtensorMap &b, ExpertsParams p, int sms, size_t smem_optin,
                            cudaStream_t stream)
 {
-    p.stages = stages_for(p.E, e8, smem_optin);
-    if (p.stages == 0)
-        return cudaErrorInvalidConfiguration;
     p.idesc = idesc_base(e8 ? 0u : type == kBf16 ? 1u : 0u, kind != kForward, kind == kWeightsGrad,
                          2 * kRowsA);
-    const size_t smem = 1024u + layout_of(p.stages, p.E, e8).end;
-    // no more clusters than tiles there can be
-    const int64_t mblocks = (p.mdim + 2 * kRowsA - 1) / (2 * kRowsA);
-    const int64_t tiles =
-        kind == kWeightsGrad
-            ? mblocks * ((p.ndim + kMaxN - 1) / kMaxN) * p.E
-            : mblocks * (std::min<int64_t>(p.E, p.M) + p.M / kMaxN);
-    const int grid =
-        2 * static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tiles, sms / 2)));
+    const bool few = experts_few(p.M, p.E);
     switch (kind) {
     case kForward:
-        return e8 ? launch<kForward, true>(a, b, p, grid, smem, stream)
-                  : launch<kForward, false>(a, b, p, grid, smem, stream);
+        if (e8)
+            return few ? launch<kForward, true, 64, 8>(a, b, p, sms, smem_optin, stream)
+                       : launch<kForward, true, 256, kWideE8>(a, b, p, sms, smem_optin, stream);
+        return few ? launch<kForward, false, 64, 8>(a, b, p, sms, smem_optin, stream)
+                   : launch<kForward, false, 256, kWide>(a, b, p, sms, smem_optin, stream);
     case kRowsGrad:
-        return launch<kRowsGrad, false>(a, b, p, grid, smem, stream);
+        return few ? launch<kRowsGrad, false, 64, 8>(a, b, p, sms, smem_optin, stream)
+                   : launch<kRowsGrad, false, 256, kWide>(a, b, p, sms, smem_optin, stream);
     default:
-        return launch<kWeightsGrad, false>(a, b, p, grid, smem, stream);
+        return launch<kWeightsGrad, false, 256, kWide>(a, b, p, sms, smem_optin, stream);
     }
 }
 
@@ -737,6 +877,21 @@ cudaError_t launch_listed_rows(const int32_t *offsets, int32_t E, int32_t M, Row
 {
     const int blocks = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(M) + 255) / 256, 4096));
     listed_rows_kernel<<<blocks, 256, 0, stream>>>(offsets, E, M, map, row);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_gather_rows(const int32_t *offsets, int32_t E, int32_t M, RowMap map,
+                               RowMap also, const void *from, int64_t pitch, void *to,
+                               int32_t *holes, int sms, cudaStream_t stream)
+{
+    const int32_t units = static_cast<int32_t>(pitch / 16);
+    int32_t lanes = 32;
+    while (lanes > 1 && lanes / 2 >= units)
+        lanes /= 2;
+    const int64_t blocks = (static_cast<int64_t>(M) * lanes + 255) / 256;
+    gather_rows_kernel<<<static_cast<unsigned>(std::min<int64_t>(blocks, 16 * sms)), 256, 0,
+                         stream>>>(offsets, E, M, map, also, static_cast<const uint4 *>(from),
+                                   units, lanes, static_cast<uint4 *>(to), holes);
     return cudaGetLastError();
 }
 

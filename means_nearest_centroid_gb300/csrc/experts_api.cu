@@ -152,22 +152,41 @@ int kmassign_experts(const void *X, int32_t dtype, int64_t R, int64_t D, const v
         return done(cudaMemsetAsync(out, 0, static_cast<size_t>(M) * F * kma::dtype_bytes(out_dtype),
                                     st));
     }
+    // Many positions: their rows first come into the lists' order, by a pass of
+    // its own, and are then loaded in whole boxes.
+    const int64_t pitch = D * (e8 ? 1 : 2);
+    const bool few = kma::experts_few(M, E);
+    Scratch sorted(rows != nullptr && !few ? static_cast<size_t>(M * pitch) : 0, dev.pool, st);
+    if (!sorted.ok())
+        return KMASSIGN_ERR_CUDA;
+    const RowMap from = map_of(rows, slots, R);
+    const bool gathers = rows != nullptr && few;
     CUtensorMap a, b;
     if (!weights_map(&a, dtype, W, E, F, D, kma::kExpertsBoxA) ||
-        !rows_map(&b, dtype, X, R, D, rows != nullptr ? 1 : kma::kExpertsBoxB))
+        (sorted.get() != nullptr
+             ? !rows_map(&b, dtype, sorted.get(), M, D, kma::kExpertsBoxB)
+             : !rows_map(&b, dtype, X, R, D, gathers ? 1 : kma::kExpertsBoxB)))
         return KMASSIGN_ERR_CUDA;
     ExpertsParams p = params_of(s, offsets);
     p.mdim = static_cast<int32_t>(F);
-    p.kblocks = static_cast<int32_t>((D + (e8 ? 127 : 63)) / (e8 ? 128 : 64));
+    p.kblocks = static_cast<int32_t>((pitch + 127) / 128);
     p.fblocks = static_cast<int32_t>((F + 127) / 128);
-    p.b_rows = map_of(rows, slots, R);
+    p.b_rows = gathers ? from : map_of(nullptr, 1, M);
+    p.from = from;
     p.places = map_of(places, 1, out_rows);
     p.zero_rest = places == nullptr;
     p.out = out;
     p.out_type = out_dtype;
     p.xscale = xscale;
     p.wscale = wscale;
-    return done(kma::launch_experts(kma::kForward, e8, dtype, a, b, p, dev.sms, dev.smem, st));
+    cudaError_t e = cudaSuccess;
+    if (sorted.get() != nullptr)
+        e = kma::launch_gather_rows(offsets, p.E, p.M, from, map_of(nullptr, 1, M), X, pitch,
+                                    sorted.get(), nullptr, dev.sms, st);
+    if (e == cudaSuccess)
+        e = kma::launch_experts(kma::kForward, e8, dtype, a, b, p, dev.sms, dev.smem, st);
+    rc = done(e);
+    return sorted.release() ? rc : KMASSIGN_ERR_CUDA;
 }
 
 int kmassign_experts_grad(const void *dout, int32_t dtype, int64_t out_rows, int64_t F,
@@ -205,66 +224,90 @@ int kmassign_experts_grad(const void *dout, int32_t dtype, int64_t out_rows, int
             return KMASSIGN_ERR_CUDA;
         return dW == nullptr ? KMASSIGN_OK : done(cudaMemsetAsync(dW, 0, dw_bytes, st));
     }
-    if (dW != nullptr) {
-        CUtensorMap a, b;
-        if (!rows_map(&a, dtype, X, R, D, rows != nullptr ? 1 : kma::kExpertsBoxMn) ||
-            !rows_map(&b, dtype, dout, out_rows, F, places != nullptr ? 1 : kma::kExpertsBoxMn))
-            return KMASSIGN_ERR_CUDA;
-        ExpertsParams p = params_of(s, offsets);
-        p.mdim = static_cast<int32_t>(D);
-        p.ndim = static_cast<int32_t>(F);
-        p.a_rows = map_of(rows, slots, R);
-        p.b_rows = map_of(places, 1, out_rows);
-        p.out = dW;
-        p.out_type = dw_dtype;
-        if (kma::launch_experts(kma::kWeightsGrad, false, dtype, a, b, p, dev.sms, dev.smem, st) !=
-            cudaSuccess)
-            return KMASSIGN_ERR_CUDA;
-    }
-    if (dX == nullptr)
-        return KMASSIGN_OK;
-    // Without row ids position p's gradient is row p's.  With them the rows'
-    // gradients are formed position by position, in the rows' type, and summed
-    // by row like those of a lookup (sorted, no atomics).
-    const size_t ids = up16(static_cast<size_t>(M) * 4);
-    const size_t sort = rows == nullptr ? 0 : up16(kma::lists_scratch_bytes(M, R, dev.sms));
-    const size_t each = rows == nullptr ? 0 : up16(static_cast<size_t>(M) * D * 2);
-    const size_t parts = rows == nullptr ? 0 : up16(kma::lookup_grad_parts_bytes(M, D, dev.sms));
-    Scratch scratch(rows == nullptr ? 0 : 3 * ids + 16 + sort + each + parts, dev.pool, st);
+    // Rows that ids name come into the lists' order first.  Without row ids
+    // position p's gradient is row p's; with them the rows' gradients are formed
+    // position by position, in the rows' type, and summed by row like those of a
+    // lookup (sorted, no atomics).
+    const RowMap from = map_of(rows, slots, R), placed = map_of(places, 1, out_rows);
+    const bool sum = dX != nullptr && rows != nullptr;
+    const size_t ids = sum ? up16(static_cast<size_t>(M) * 4) : 0;
+    const size_t sort = sum ? up16(kma::lists_scratch_bytes(M, R, dev.sms)) : 0;
+    const size_t parts = sum ? up16(kma::lookup_grad_parts_bytes(M, D, dev.sms)) : 0;
+    // X's rows, and later the rows' gradients
+    const size_t each = rows != nullptr ? static_cast<size_t>(M) * D * 2 : 0;
+    const size_t dys = places != nullptr ? static_cast<size_t>(M) * F * 2 : 0;
+    const bool gathers = rows != nullptr || places != nullptr;
+    Scratch scratch(each + dys + (gathers ? 16 : 0) + 3 * ids + (sum ? 16 : 0) + sort + parts,
+                    dev.pool, st);
     if (!scratch.ok())
         return KMASSIGN_ERR_CUDA;
     uint8_t *q = scratch.get();
-    CUtensorMap a, b;
-    if (!weights_map(&a, dtype, W, E, F, D, kma::kExpertsBoxMn) ||
-        !rows_map(&b, dtype, dout, out_rows, F, places != nullptr ? 1 : kma::kExpertsBoxB))
-        return KMASSIGN_ERR_CUDA;
+    uint8_t *const by_position = q, *const dy_sorted = q + each;
+    q += each + dys;
+    int32_t *holes = nullptr;
+    const void *const dy = places != nullptr ? dy_sorted : dout;
+    const int64_t dy_rows = places != nullptr ? M : out_rows;
+    cudaError_t e = cudaSuccess;
+    if (gathers) {
+        holes = reinterpret_cast<int32_t *>(q);
+        q += 16;
+        if (dW != nullptr)
+            e = cudaMemsetAsync(holes, 0, 4, st);
+    }
+    if (e == cudaSuccess && places != nullptr)
+        e = kma::launch_gather_rows(offsets, static_cast<int32_t>(E), static_cast<int32_t>(M),
+                                    placed, from, dout, 2 * F, dy_sorted, holes, dev.sms, st);
     ExpertsParams p = params_of(s, offsets);
     p.mdim = static_cast<int32_t>(D);
-    p.kblocks = static_cast<int32_t>((F + 63) / 64);
-    p.b_rows = map_of(places, 1, out_rows);
-    p.places = map_of(nullptr, 1, M);
-    p.zero_rest = rows == nullptr;
-    p.out = rows == nullptr ? dX : q + 3 * ids + 16 + sort;
-    p.out_type = dtype;
-    cudaError_t e =
-        kma::launch_experts(kma::kRowsGrad, false, dtype, a, b, p, dev.sms, dev.smem, st);
-    if (e == cudaSuccess && rows == nullptr && R > M)
-        e = cudaMemsetAsync(static_cast<uint8_t *>(dX) + static_cast<size_t>(M) * D * 2, 0,
-                            static_cast<size_t>(R - M) * D * 2, st);
-    if (e == cudaSuccess && rows != nullptr) {
+    p.b_rows = p.places = map_of(nullptr, 1, M);
+    p.from = from;
+    p.placed = placed;
+    CUtensorMap a, b;
+    if (e == cudaSuccess && dW != nullptr) {
+        if (e == cudaSuccess && rows != nullptr)
+            e = kma::launch_gather_rows(offsets, p.E, p.M, from, placed, X, 2 * D, by_position,
+                                        holes, dev.sms, st);
+        if (!rows_map(&a, dtype, rows != nullptr ? by_position : X, rows != nullptr ? M : R, D,
+                      kma::kExpertsBoxMn) ||
+            !rows_map(&b, dtype, dy, dy_rows, F, kma::kExpertsBoxMn))
+            return KMASSIGN_ERR_CUDA;
+        p.holes = holes;
+        p.ndim = static_cast<int32_t>(F);
+        p.out = dW;
+        p.out_type = dw_dtype;
+        if (e == cudaSuccess)
+            e = kma::launch_experts(kma::kWeightsGrad, false, dtype, a, b, p, dev.sms, dev.smem, st);
+    }
+    if (e == cudaSuccess && dX != nullptr) {
+        if (!weights_map(&a, dtype, W, E, F, D, kma::kExpertsBoxMn) ||
+            !rows_map(&b, dtype, dy, dy_rows, F, kma::kExpertsBoxB))
+            return KMASSIGN_ERR_CUDA;
+        p.kblocks = static_cast<int32_t>((F + 63) / 64);
+        p.from = placed;
+        p.zero_rest = rows == nullptr;
+        p.out = rows == nullptr ? dX : by_position;
+        p.out_type = dtype;
+        e = kma::launch_experts(kma::kRowsGrad, false, dtype, a, b, p, dev.sms, dev.smem, st);
+        if (e == cudaSuccess && rows == nullptr && R > M)
+            e = cudaMemsetAsync(static_cast<uint8_t *>(dX) + static_cast<size_t>(M) * D * 2, 0,
+                                static_cast<size_t>(R - M) * D * 2, st);
+    }
+    if (e == cudaSuccess && sum) {
         int32_t *row = reinterpret_cast<int32_t *>(q);
         int32_t *order = reinterpret_cast<int32_t *>(q + ids);
         int32_t *sorted = reinterpret_cast<int32_t *>(q + 2 * ids);
         int32_t *total = reinterpret_cast<int32_t *>(q + 3 * ids);
-        e = kma::launch_listed_rows(offsets, p.E, p.M, map_of(rows, slots, R), row, st);
+        uint8_t *const space = q + 3 * ids + 16;
+        // a position whose place is missing has a gradient of zeros: it may be summed
+        e = kma::launch_listed_rows(offsets, p.E, p.M, from, row, st);
         if (e == cudaSuccess)
-            e = kma::launch_lists(row, M, R, order, sorted, nullptr, total, q + 3 * ids + 16, dX,
+            e = kma::launch_lists(row, M, R, order, sorted, nullptr, total, space, dX,
                                   static_cast<size_t>(R) * D * 2, dev.sms, st);
         if (e == cudaSuccess)
-            e = kma::launch_lookup_grad(p.out, dtype, row, nullptr, nullptr, M, 1, R, D, 1.0f, -1,
-                                        false, order, sorted, total,
-                                        reinterpret_cast<float *>(q + 3 * ids + 16 + sort + each),
-                                        dX, dtype, nullptr, dev.sms, st);
+            e = kma::launch_lookup_grad(by_position, dtype, row, nullptr, nullptr, M, 1, R, D, 1.0f,
+                                        -1, false, order, sorted, total,
+                                        reinterpret_cast<float *>(space + sort), dX, dtype, nullptr,
+                                        dev.sms, st);
     }
     rc = done(e);
     return scratch.release() ? rc : KMASSIGN_ERR_CUDA;

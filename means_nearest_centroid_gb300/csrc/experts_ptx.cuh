@@ -1,6 +1,6 @@
 // experts_ptx.cuh -- the PTX wrappers that the experts' products use besides
-// those of ptx.cuh: three-dimensional and gathering TMA loads, cluster-scope
-// arrivals and waits, transposed operand descriptors, 8-bit MMAs.
+// those of ptx.cuh: three-dimensional TMA loads, cluster-scope arrivals and waits,
+// transposed operand descriptors, 8-bit MMAs.
 #pragma once
 
 #include "ptx.cuh"
@@ -50,10 +50,14 @@ __device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_bar
                  : "memory");
 }
 
-// The waiting side of mbar_arrive_release_cluster.
-__device__ __forceinline__ void fence_acquire_cluster()
+// The waiting side of mbar_arrive_release_cluster, for a phase that is known
+// to be complete: orders what follows behind it at the cluster's scope.
+__device__ __forceinline__ void mbar_acquire_cluster(uint32_t bar, uint32_t parity)
 {
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(bar),
+                 "r"(parity)
+                 : "memory");
 }
 
 // MN-major operand tile, 128-byte swizzle: atoms of 64 16-bit elements along M
@@ -69,6 +73,24 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t 
     d |= static_cast<uint64_t>(1u) << 46;
     d |= static_cast<uint64_t>(2u) << 61;
     return d;
+}
+
+// 16 lanes x 32 consecutive 32-bit columns: for each 8 columns thread t gets
+// columns 2 (t % 4) and the next of lanes t / 4 and t / 4 + 8, in this order.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, float (&v)[16])
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        v[i] = __uint_as_float(r[i]);
 }
 
 // Pair MMA of 8-bit floating-point operands (K = 32), fp32 accumulate.

@@ -148,8 +148,11 @@ struct ExpertsParams {
     int32_t mdim;             // the outputs' contiguous extent (F; gradients: D)
     int32_t ndim;             // weights' gradient: F
     int32_t kblocks;          // 128-byte blocks of the contraction (not the weights' gradient)
-    RowMap a_rows;            // rows of X (weights' gradient)
-    RowMap b_rows;            // rows of the positions' operand
+    RowMap b_rows;            // rows of X, where the product gathers them itself (few positions)
+    RowMap from;              // rows of X (and of xscale), of dY for the rows' gradient: a
+                              // position without one has a product of zeros
+    RowMap placed;            // weights' gradient: rows of dY; a position that lacks either row
+    const int32_t *holes;     // adds nothing.  Whether there is one (NULL: none)
     RowMap places;            // rows of the output (forward, rows' gradient)
     bool zero_rest;           // rows of no list are written 0
     void *out;
@@ -165,8 +168,11 @@ struct ExpertsParams {
 cudaError_t experts_prepare(size_t smem_optin);
 // Boxes of the operands' tensor maps (rows of 128 bytes): A as [E][F][D], 128
 // rows K-major (forward) or 64 MN-major, X 64 rows; B 32 rows (the weights'
-// gradient 64); one row where ids name the rows.
+// gradient 64), or one where b_rows has ids.
 constexpr uint32_t kExpertsBoxA = 128, kExpertsBoxMn = 64, kExpertsBoxB = 32;
+// Whether lists of M positions are short on average: the product then has
+// tiles for few columns, and gathers rows itself.
+bool experts_few(int64_t M, int64_t E);
 cudaError_t launch_experts(ExpertsKind kind, bool e8, int type, const CUtensorMap &a,
                            const CUtensorMap &b, ExpertsParams p, int sms, size_t smem_optin,
                            cudaStream_t stream);
@@ -174,6 +180,12 @@ cudaError_t experts_status_read_and_clear(int *code);
 // row[p] = the row that map names for positions of a list, -1 for the others.
 cudaError_t launch_listed_rows(const int32_t *offsets, int32_t E, int32_t M, RowMap map,
                                int32_t *row, cudaStream_t stream);
+// to[p] = the row (pitch bytes, a multiple of 16) that map names for positions
+// of a list, zeros for the others and where also names none; *holes (may be
+// NULL) is set to 1 if a position of a list gets zeros.
+cudaError_t launch_gather_rows(const int32_t *offsets, int32_t E, int32_t M, RowMap map,
+                               RowMap also, const void *from, int64_t pitch, void *to,
+                               int32_t *holes, int sms, cudaStream_t stream);
 
 cudaError_t launch_rmsnorm(const void *X, int dtype, int64_t N, int64_t D, const void *residual,
                            const void *weight, int weight_dtype, float eps, void *total, void *out,
