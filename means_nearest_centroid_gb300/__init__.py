@@ -890,9 +890,9 @@ def kmassign_experts_grad(dout, X, W, offsets=None, rows=None, slots: int = 1, p
     arguments are the forward call's.  ``dX`` has X's type, ``dW`` is fp32 (the
     default ``dtype``) or X's type; one that is not needed is None.
     """
-    code = _need_product_types(X, W, None, None)
-    if code == 3:
+    if isinstance(X, torch.Tensor) and X.dtype == _E4M3:
         raise TypeError("X must be bfloat16 or float16, got torch.float8_e4m3fn")
+    code = _need_product_types(X, W, None, None)
     slots = int(slots)
     R, D, E, F, M = _need_lists(X, W, offsets, rows, slots, places)
     _need_cuda(dout, "dout", X.dtype)

@@ -61,8 +61,10 @@ constexpr uint32_t kPartA = kRowsA * 128;          // A's k-block in a CTA
 constexpr uint32_t kAtomBytes = 64 * 128;          // MN-major: 64 elements by 64 rows
 constexpr int kScaleStages = 8;
 constexpr uint32_t kGroupBarrier = 1;              // named barriers of the consumers' groups
-// 16-bit k-blocks between two additions to registers: 2,048 elements.
-constexpr int kSegment = 32;
+// 16-bit k-blocks between two additions to registers: 2,048 elements, or 512
+// positions of a weights' gradient, whose lists may be long and whose result is
+// fp32.
+constexpr int kSegment = 32, kSegmentRows = 8;
 
 // Barriers: full and empty of each stage, of the accumulators, of the scales;
 // one for each loader's k-blocks with missing rows; the issuers' last MMAs'.
@@ -319,7 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
     constexpr bool kAMn = KIND != kForward;         // A is MN-major
     constexpr bool kBMn = KIND == kWeightsGrad;
     constexpr bool kFixes = KIND == kWeightsGrad;   // loaders zero missing rows
-    constexpr int kSeg = E8 ? 1 : kSegment;
+    constexpr int kSeg = E8 ? 1 : KIND == kWeightsGrad ? kSegmentRows : kSegment;
     constexpr int kElems = E8 ? 128 : 64;           // elements of a k-block
     constexpr bool kGathers = KIND == kForward && NT == 64;
     constexpr uint32_t kStageBytes = stage_bytes(NT);
@@ -726,7 +728,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
                         mbar_arrive(bar(kScE + s));
                 }
             }
-            if (!ok)
+            // A group stores together or, after a wait of any of its warps ran out,
+            // leaves together: no warp waits at its barrier for one that has left.
+            if (!(ok = named_bar_and(kGroupBarrier + group, 128, ok)))
                 break;
             const int32_t m = w.m0 + static_cast<int>(rank) * kRowsA;
             if (p.out_type == kBf16)

@@ -368,13 +368,14 @@ int kmassign_rmsnorm_grad(const void *dout, int32_t dtype, int64_t N, int64_t D,
         !aligned(weight, static_cast<uintptr_t>(kma::dtype_bytes(weight_dtype))) ||
         !aligned(rstd, 4) || !aligned(dweight, 4))
         return KMASSIGN_ERR_ALIGN;
+    if (N == 0 && dweight == nullptr)
+        return KMASSIGN_OK;
     const void *ptrs[7] = {dout, total, weight, rstd, dtotal, dX, dweight};
     int rc = check_device_ptrs(ptrs, 7);
     if (rc != KMASSIGN_OK)
         return rc;
     if (N == 0)
-        return dweight == nullptr ? KMASSIGN_OK
-                                  : done(cudaMemsetAsync(dweight, 0, static_cast<size_t>(D) * 4, st));
+        return done(cudaMemsetAsync(dweight, 0, static_cast<size_t>(D) * 4, st));
     cudaMemPool_t pool;
     int sms;
     if ((rc = kma::library_device(&pool, &sms)) != KMASSIGN_OK)

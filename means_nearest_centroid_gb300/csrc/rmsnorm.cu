@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const NormArgs a, int warp
             for (int d = kLanes / 2; d > 0; d /= 2)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             const float scale = fmaxf(top, kLeast) / kTop;
-            const float inverse = 1.0f / scale;
+            const float inverse = __fdividef(1.0f, scale);   // scale is a normal number
             const int first = column<VE>(j, warps, warp, lane);
             if (lane % kLanes == 0 && first < a.D)
                 a.scales[row * blocks + first / 128] = scale;
@@ -250,13 +250,15 @@ __global__ void __launch_bounds__(512) rmsnorm_grad_kernel(const NormGradArgs a,
     for (int64_t row = group; row < a.N; row += groups, slot ^= 1) {
         const int64_t at = row * a.D;
         const float rstd = __ldg(a.rstd + row);
-        Raw<T, VE> rd[NV], rt[NV];
+        Raw<T, VE> rd[NV], rt[NV], rs[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = column<VE>(j, warps, warp, lane);
             if (col < a.D) {
                 rd[j] = load_raw<T, VE>(static_cast<const T *>(a.dout) + at + col);
                 rt[j] = load_raw<T, VE>(static_cast<const T *>(a.total) + at + col);
+                if (a.dtotal != nullptr)
+                    rs[j] = load_raw<T, VE>(static_cast<const T *>(a.dtotal) + at + col);
             }
         }
         float dot = 0.0f;
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(512) rmsnorm_grad_kernel(const NormGradArgs a,
                     o[i] = (d[i] * w[i] - t[i] * rstd * c) * rstd;
                 if (a.dtotal != nullptr) {
                     float r[VE];
-                    widen<T, VE>(load_raw<T, VE>(static_cast<const T *>(a.dtotal) + at + col), r);
+                    widen<T, VE>(rs[j], r);
 #pragma unroll
                     for (int i = 0; i < VE; ++i)
                         o[i] += r[i];
@@ -336,18 +338,25 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 int warps_for(int64_t D, int elems) { return static_cast<int>((D + 32 * elems - 1) / (32 * elems)); }
 
-// Vectors a thread: the row in one warp where rows are many, up to `most`
-// vectors; spread over up to 16 warps where they are few.
+// Vectors a thread: a row in one warp, or in several where it takes more than
+// `elems` elements a lane, in up to 16; spread over up to 16 warps where rows
+// are few.  (More than 32 elements cost the norm its occupancy: 65,536 x 2,048
+// bf16 to 8 bits 64 a lane 190 us, 32 140.  The gradient holds three rows and a
+// sum: 32 elements in 16 bits, 8 in fp32, 16,384 x 4,096 of which 141 us, with
+// 32 183.)
 template <int VE>
-int vectors_for(int64_t N, int64_t D, int least, int most, int sms)
+int vectors_for(int64_t N, int64_t D, int elems, int sms)
 {
-    const int64_t few = 4 * static_cast<int64_t>(sms);
-    int nv = least;
-    while (nv < most && warps_for(D, VE * nv) > (N <= few ? 16 : 1))
+    const bool few = N <= 4 * static_cast<int64_t>(sms);
+    int nv = VE == 1 ? 4 : 1;
+    while (VE * nv < 64) {
+        const int warps = warps_for(D, VE * nv);
+        if (warps == 1 || (warps <= 16 && (few || VE * nv >= elems)))
+            break;
         nv *= VE == 1 ? 4 : 2;
+    }
     return nv;
 }
-
 template <typename T, bool CODES, int VE, int NV>
 cudaError_t run_norm(const NormArgs &a, cudaStream_t s)
 {
@@ -368,7 +377,7 @@ cudaError_t norm_shape(const NormArgs &a, int sms, cudaStream_t s)
     const bool wide = a.D % VE == 0 && aligned16(a.x) && aligned16(a.residual) &&
                       aligned16(a.weight) && aligned16(a.total) && aligned16(a.out);
     if (!wide) {
-        switch (vectors_for<1>(a.N, a.D, 4, 64, sms)) {
+        switch (vectors_for<1>(a.N, a.D, 4, sms)) {
         case 4:
             return run_norm<T, CODES, 1, 4>(a, s);
         case 16:
@@ -377,7 +386,7 @@ cudaError_t norm_shape(const NormArgs &a, int sms, cudaStream_t s)
             return run_norm<T, CODES, 1, 64>(a, s);
         }
     }
-    switch (vectors_for<VE>(a.N, a.D, 1, 64 / VE, sms)) {
+    switch (vectors_for<VE>(a.N, a.D, 32, sms)) {
     case 1:
         return run_norm<T, CODES, VE, 1>(a, s);
     case 2:
@@ -397,17 +406,23 @@ cudaError_t norm_type(const NormArgs &a, bool codes, int sms, cudaStream_t s)
     return codes ? norm_shape<T, true>(a, sms, s) : norm_shape<T, false>(a, sms, s);
 }
 
-// Row groups of the gradient: eight warps' worth of blocks an SM, fewer where
-// rows are few.
-int grad_groups(int64_t N, int sms)
+
+// Row groups of the gradient: as many as are resident at once by their
+// registers, fewer where rows are few.  (65,536 x 2,048 bf16: 16 warps an SM 182
+// us, 12 208, 24, which do not all fit, 215.)
+int grad_groups(int64_t N, int warps, int elems, int sms)
 {
-    return static_cast<int>(std::min<int64_t>(N, 8 * static_cast<int64_t>(sms)));
+    const int resident = elems <= 4 ? 40 : elems <= 8 ? 32 : 16;
+    return static_cast<int>(
+        std::min<int64_t>(N, sms * static_cast<int64_t>(std::max(1, resident / warps))));
 }
 
 template <typename T, int VE, int NV>
-cudaError_t run_grad(const NormGradArgs &a, int groups, cudaStream_t s)
+cudaError_t run_grad(const NormGradArgs &a, int sms, int *groups_out, cudaStream_t s)
 {
     const int warps = warps_for(a.D, VE * NV);
+    const int groups = grad_groups(a.N, warps, VE * NV, sms);
+    *groups_out = groups;
     if (warps == 1)
         rmsnorm_grad_kernel<T, VE, NV><<<(groups + 3) / 4, 128, 0, s>>>(a, 1, groups);
     else
@@ -416,35 +431,32 @@ cudaError_t run_grad(const NormGradArgs &a, int groups, cudaStream_t s)
 }
 
 template <typename T>
-cudaError_t grad_type(const NormGradArgs &a, int groups, int sms, cudaStream_t s)
+cudaError_t grad_type(const NormGradArgs &a, int sms, int *groups, cudaStream_t s)
 {
     constexpr int VE = 16 / sizeof(T);
     const bool wide = a.D % VE == 0 && aligned16(a.dout) && aligned16(a.total) &&
                       aligned16(a.weight) && aligned16(a.dtotal) && aligned16(a.dx);
     if (!wide) {
-        switch (vectors_for<1>(a.N, a.D, 4, 64, sms)) {
+        switch (vectors_for<1>(a.N, a.D, 4, sms)) {
         case 4:
-            return run_grad<T, 1, 4>(a, groups, s);
+            return run_grad<T, 1, 4>(a, sms, groups, s);
         case 16:
-            return run_grad<T, 1, 16>(a, groups, s);
+            return run_grad<T, 1, 16>(a, sms, groups, s);
         default:
-            return run_grad<T, 1, 64>(a, groups, s);
+            return run_grad<T, 1, 64>(a, sms, groups, s);
         }
     }
-    int nv = vectors_for<VE>(a.N, a.D, 1, 32 / VE, sms);
-    if (warps_for(a.D, VE * nv) > 16)
-        nv = 64 / VE;
-    switch (nv) {
+    switch (vectors_for<VE>(a.N, a.D, VE == 4 ? 8 : 32, sms)) {
     case 1:
-        return run_grad<T, VE, 1>(a, groups, s);
+        return run_grad<T, VE, 1>(a, sms, groups, s);
     case 2:
-        return run_grad<T, VE, 2>(a, groups, s);
+        return run_grad<T, VE, 2>(a, sms, groups, s);
     case 4:
-        return run_grad<T, VE, 4>(a, groups, s);
+        return run_grad<T, VE, 4>(a, sms, groups, s);
     case 8:
-        return run_grad<T, VE, 8>(a, groups, s);
+        return run_grad<T, VE, 8>(a, sms, groups, s);
     default:
-        return run_grad<T, VE, 64 / VE>(a, groups, s);
+        return run_grad<T, VE, 64 / VE>(a, sms, groups, s);
     }
 }
 
@@ -466,7 +478,7 @@ cudaError_t launch_rmsnorm(const void *X, int dtype, int64_t N, int64_t D, const
 
 size_t rmsnorm_grad_parts_bytes(int64_t N, int64_t D, int sms)
 {
-    return static_cast<size_t>(grad_groups(N, sms)) * D * sizeof(float);
+    return static_cast<size_t>(grad_groups(N, 1, 1, sms)) * D * sizeof(float);
 }
 
 cudaError_t launch_rmsnorm_grad(const void *dout, int dtype, int64_t N, int64_t D,
@@ -474,12 +486,12 @@ cudaError_t launch_rmsnorm_grad(const void *dout, int dtype, int64_t N, int64_t 
                                 const float *rstd, const void *dtotal, void *dX, float *dweight,
                                 float *parts, int sms, cudaStream_t stream)
 {
-    const int groups = grad_groups(N, sms);
+    int groups = 0;
     const NormGradArgs a{dout, total, weight, dtotal, weight_dtype == kFp32,
                          rstd, N,     static_cast<int32_t>(D), dX, dweight != nullptr ? parts : nullptr};
-    cudaError_t e = dtype == kFp32   ? grad_type<float>(a, groups, sms, stream)
-                    : dtype == kBf16 ? grad_type<__nv_bfloat16>(a, groups, sms, stream)
-                                     : grad_type<__half>(a, groups, sms, stream);
+    cudaError_t e = dtype == kFp32   ? grad_type<float>(a, sms, &groups, stream)
+                    : dtype == kBf16 ? grad_type<__nv_bfloat16>(a, sms, &groups, stream)
+                                     : grad_type<__half>(a, sms, &groups, stream);
     if (e == cudaSuccess && dweight != nullptr) {
         join_parts_kernel<<<static_cast<unsigned>((D + 31) / 32), 1024, 0, stream>>>(
             parts, groups, static_cast<int>(D), dweight);
