@@ -28,10 +28,10 @@
 // the way; the scale warp forms those products for the tile's columns.
 //
 // Contraction over positions (weights' gradient): a k-block may end behind the
-// list's last position, or name rows that do not exist.  Those rows must be
-// zero in both operands (0 * NaN is NaN).  The loading warp then waits for that
-// k-block's rows on a barrier of its own, zeroes them in shared memory and
-// arrives at the pair's barrier itself.
+// list's last position, or hold positions that lack a row.  Those rows must be
+// zero in both operands (0 * NaN is NaN).  The copies of such a k-block complete
+// on barriers of this CTA; a warp waits for them, zeroes the rows in shared
+// memory and passes the k-block on to the pair.
 //
 // Schedule: persistent clusters, tiles dealt out in turn; the tiles of expert e
 // follow from the lists' lengths (a prefix sum that each CTA forms at its
@@ -59,20 +59,21 @@ static_assert(4 * consumer_regs(16) + other_regs(16) <= 5 * 96, "the launch's re
 constexpr int kRowsA = 128;                        // rows of A a CTA holds
 constexpr uint32_t kPartA = kRowsA * 128;          // A's k-block in a CTA
 constexpr uint32_t kAtomBytes = 64 * 128;          // MN-major: 64 elements by 64 rows
-constexpr int kScaleStages = 8;
+// Scales: a ring of groups of four k-blocks (one hand-over for four segments).
+constexpr int kScaleStages = 2, kScaleGroup = 4;
+__host__ __device__ constexpr uint32_t scale_bytes(int NT) { return kScaleGroup * NT * 4u; }
 constexpr uint32_t kGroupBarrier = 1;              // named barriers of the consumers' groups
 // 16-bit k-blocks between two additions to registers: 2,048 elements, or 512
-// positions of a weights' gradient, whose lists may be long and whose result is
-// fp32.
+// positions of a weights' gradient in fp32.
 constexpr int kSegment = 32, kSegmentRows = 8;
 
 // Barriers: full and empty of each stage, of the accumulators, of the scales;
-// one for each loader's k-blocks with missing rows; the issuers' last MMAs'.
+// those of each operand's stages while rows are missing; the issuers' last MMAs'.
 constexpr int kMaxRing = 10;
 constexpr int kFull = 0, kEmpty = kFull + kMaxRing;
 constexpr int kAccF = kEmpty + kMaxRing, kAccE = kAccF + 2;
 constexpr int kScF = kAccE + 2, kScE = kScF + kScaleStages;
-constexpr int kFix = kScE + kScaleStages, kLast = kFix + 2;
+constexpr int kFixA = kScE + kScaleStages, kFixB = kFixA + kMaxRing, kLast = kFixB + kMaxRing;
 constexpr int kBars = kLast + 2;
 
 struct Tile {
@@ -96,7 +97,7 @@ __host__ __device__ inline Layout layout_of(int NT, int stages, int E, bool scal
     l.staging = stages * stage_bytes(NT);         // shared by the groups of consumers
     l.dst = l.staging + 16384u;           // [group][tile parity][columns]
     l.scale = l.dst + 2u * NT * 4u;
-    l.lists = l.scale + (scaled ? kScaleStages * NT * 4u : 0u);
+    l.lists = l.scale + (scaled ? kScaleStages * scale_bytes(NT) : 0u);
     l.bars = (l.lists + 3u * static_cast<uint32_t>(E + 1) * 4u + 15u) / 16u * 16u;
     l.end = l.bars + kBars * 8u + 16u;
     return l;
@@ -144,10 +145,12 @@ struct Schedule {
         w.e = lo;
         w.lo = begin[lo];
         w.hi = end[lo];
-        // an expert's positions in even parts of at most NT, each a multiple of 32
-        const int parts = before[lo + 1] - before[lo];
-        w.n = ((w.hi - w.lo + parts - 1) / parts + 31) / 32 * 32;
-        w.n0 = w.lo + (q - before[lo]) * w.n;
+        // an expert's positions, in units of 32, in parts as even as can be
+        const int parts = before[lo + 1] - before[lo], part = q - before[lo];
+        const int units = (w.hi - w.lo + 31) / 32;
+        const int each = units / parts, more = units - each * parts;
+        w.n = 32 * (each + (part < more));
+        w.n0 = w.lo + 32 * (part * each + min(part, more));
         w.kblocks = p.kblocks;
         return w;
     }
@@ -321,7 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
     constexpr bool kAMn = KIND != kForward;         // A is MN-major
     constexpr bool kBMn = KIND == kWeightsGrad;
     constexpr bool kFixes = KIND == kWeightsGrad;   // loaders zero missing rows
-    constexpr int kSeg = E8 ? 1 : KIND == kWeightsGrad ? kSegmentRows : kSegment;
+    const int kSeg = E8 ? 1 : p.segment;            // k-blocks between additions
     constexpr int kElems = E8 ? 128 : 64;           // elements of a k-block
     constexpr bool kGathers = KIND == kForward && NT == 64;
     constexpr uint32_t kStageBytes = stage_bytes(NT);
@@ -341,7 +344,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
     const Layout lay = layout_of(NT, p.stages, p.E, E8);
     uint8_t *const sbase = smem_raw + (base - raw);
     int32_t *const lists = reinterpret_cast<int32_t *>(sbase + lay.lists);
-    float *const scales = reinterpret_cast<float *>(sbase + lay.scale);
     volatile uint32_t *tmem_slot =
         reinterpret_cast<volatile uint32_t *>(sbase + lay.bars + kBars * 8);
     volatile uint32_t *abort_flag = tmem_slot + 1;
@@ -358,14 +360,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxRing; ++s) {
-            // the leader's loaders; both CTAs' where a loader may zero rows
+            // the leader's loaders; both CTAs' where rows may be missing
             mbar_init(bar(kFull + s), kFixes ? 4 : kTwo ? 1 : 2);
             mbar_init(bar(kEmpty + s), 1);
+            mbar_init(bar(kFixA + s), 1);
+            mbar_init(bar(kFixB + s), 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(bar(kAccF + a), 1);
             mbar_init(bar(kAccE + a), 2 * CW);
-            mbar_init(bar(kFix + a), 1);
             mbar_init(bar(kLast + a), 1);
         }
         for (int s = 0; s < kScaleStages; ++s) {
@@ -402,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(CW)));
     if ((warp == kWarpA && !kTwo) || warp == kWarpB) {
         const bool is_a = warp == kWarpA;
-        uint32_t stage = 0, phase = 0, fixes = 0;
+        uint32_t stage = 0, phase = 0;
         bool ok = true;
         auto next_stage = [&]() {
             if (++stage == stages) {
@@ -426,38 +429,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
                         break;
                     const uint32_t dst = is_a ? part_a(stage) : part_b(stage);
                     const uint32_t full = lead_bar(kFull + stage);
-                    const uint32_t own_fix = bar(kFix + (is_a ? 0 : 1));
+                    const uint32_t own = bar((is_a ? kFixA : kFixB) + stage);
                     if (lane == 0) {
-                        if (fix)
-                            mbar_arrive_expect_tx(own_fix, bytes);
+                        if (fix)   // the fixing warp goes on from here
+                            mbar_arrive_expect_tx(own, bytes);
                         else if (leader)
                             mbar_arrive_expect_tx(bar(kFull + stage), 2 * bytes);
                         else
                             mbar_arrive_cluster(full);
-                        const uint32_t done = fix ? map_to_rank(own_fix, rank) : full;
+                        const uint32_t done = fix ? map_to_rank(own, rank) : full;
                         for (int a = 0; a < atoms; ++a)
                             tma_load_2d_pair(dst + a * kAtomBytes, tmap, done, x + 64 * a, at);
                     }
                     __syncwarp();
-                    if (fix) {
-                        ok = wait_warp(own_fix, fixes & 1u, abort_flag, p.timeout_ns);
-                        ++fixes;
-                        if (!ok)
-                            break;
-                        // lane l: whether positions l and 32 + l are missing
-                        const uint32_t gone[2] = {
-                            __ballot_sync(0xffffffffu, missing(p, at + lane, w.hi)),
-                            __ballot_sync(0xffffffffu, missing(p, at + 32 + lane, w.hi))};
-                        // whole rows: the swizzle moves 16-byte pieces within a row
-                        for (int i = lane; i < 64 * 8; i += 32)
-                            if (gone[i >> 8] >> (i >> 3 & 31) & 1u)
-                                for (int a = 0; a < atoms; ++a)
-                                    st_shared_v4_u32(dst + a * kAtomBytes + 16 * i, 0, 0, 0, 0);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive_release_cluster(full);
-                    }
                 }
             }
         } else if (is_a) {
@@ -584,6 +568,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
             }
         }
     } else if (warp == kWarpScale) {
+        if constexpr (kFixes) {
+            // K-blocks with missing rows: once both operands have landed here the
+            // rows are zeroed and the pair's barrier gets both loaders' arrivals.
+            // (The loaders themselves go on: waiting for such a block, the last of
+            // most tiles, they fell behind by 1.5 us a tile.)
+            const bool holes = p.holes != nullptr && *p.holes != 0;
+            uint32_t stage = 0, used = 0;   // bit s: parity of stage s's next such block
+            bool ok = true;
+            for (int t = first; ok && t < plan.total; t += step) {
+                const Tile w = plan.tile(t);
+                const int atoms_b = w.n / 128;
+                for (int kb = 0; kb < w.kblocks; ++kb) {
+                    const int at = w.lo + kb * 64;
+                    if (at + 64 > w.hi || holes) {
+                        if (!(ok = wait_warp(bar(kFixA + stage), used >> stage & 1u, abort_flag,
+                                             p.timeout_ns) &&
+                                   wait_warp(bar(kFixB + stage), used >> stage & 1u, abort_flag,
+                                             p.timeout_ns)))
+                            break;
+                        used ^= 1u << stage;
+                        // lane l: whether positions l and 32 + l are missing
+                        const uint32_t gone[2] = {
+                            __ballot_sync(0xffffffffu, missing(p, at + lane, w.hi)),
+                            __ballot_sync(0xffffffffu, missing(p, at + 32 + lane, w.hi))};
+                        // whole rows: the swizzle moves 16-byte pieces within a row
+                        for (int i = lane; i < 64 * 8; i += 32)
+                            if (gone[i >> 8] >> (i >> 3 & 31) & 1u) {
+                                for (int a = 0; a < 2; ++a)
+                                    st_shared_v4_u32(part_a(stage) + a * kAtomBytes + 16 * i, 0, 0,
+                                                     0, 0);
+                                for (int a = 0; a < atoms_b; ++a)
+                                    st_shared_v4_u32(part_b(stage) + a * kAtomBytes + 16 * i, 0, 0,
+                                                     0, 0);
+                            }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane < 2)
+                            mbar_arrive_release_cluster(lead_bar(kFull + stage));
+                    }
+                    if (++stage == stages)
+                        stage = 0;
+                }
+            }
+        }
         if constexpr (E8) {
             // For each k-block the products of the columns' scales and the
             // scale of this CTA's 128 rows of weights.
@@ -598,43 +626,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
                 int32_t row[kPer];
 #pragma unroll
                 for (int i = 0; i < kPer; ++i)
-                    row[i] = max(row_of(p.from, w.n0 + 32 * i + lane, w.hi), 0);
-                // Two k-blocks are loaded ahead: a load takes about as long as
-                // the tensor cores need for both.
-                float v[3][kPer], one[3];
-                auto load = [&](int kb, float (&to)[kPer], float &ws_kb) {
-                    if (kb < w.kblocks) {
-                        ws_kb = __ldg(ws + kb);
+                    row[i] = NT == 256 ? min(w.n0 + 32 * i + lane, p.M - 1)
+                                       : max(row_of(p.from, w.n0 + 32 * i + lane, w.hi), 0);
+                for (int k0 = 0; k0 < w.kblocks; k0 += kScaleGroup, ++n) {
+                    const uint32_t s = n % kScaleStages;
+                    float *const to = reinterpret_cast<float *>(sbase + lay.scale +
+                                                                s * scale_bytes(NT));
+                    float v[kScaleGroup][kPer], one[kScaleGroup];
+#pragma unroll
+                    for (int j = 0; j < kScaleGroup; ++j) {
+                        const int kb = min(k0 + j, w.kblocks - 1);
+                        one[j] = __ldg(ws + kb);
 #pragma unroll
                         for (int i = 0; i < kPer; ++i)
-                            if (32 * i < w.n)
-                                to[i] = __ldg(p.xscale +
-                                              static_cast<int64_t>(row[i]) * w.kblocks + kb);
+                            v[j][i] = __ldg(
+                                p.xscale +
+                                (NT == 256 ? static_cast<int64_t>(kb) * p.M + row[i]
+                                           : static_cast<int64_t>(row[i]) * w.kblocks + kb));
                     }
-                };
-                load(0, v[0], one[0]);
-                load(1, v[1], one[1]);
-                // unrolled: a value that is moved is waited for
-                for (int k0 = 0; ok && k0 < w.kblocks; k0 += 3) {
+                    if (!(ok = wait_warp(bar(kScE + s), ((n / kScaleStages) & 1u) ^ 1u, abort_flag,
+                                         p.timeout_ns)))
+                        break;
 #pragma unroll
-                    for (int j = 0; j < 3; ++j) {
-                        const int kb = k0 + j;
-                        if (kb >= w.kblocks)
-                            break;
-                        const uint32_t s = n % kScaleStages;
-                        load(kb + 2, v[(j + 2) % 3], one[(j + 2) % 3]);
-                        if (!(ok = wait_warp(bar(kScE + s), ((n / kScaleStages) & 1u) ^ 1u,
-                                             abort_flag, p.timeout_ns)))
-                            break;
+                    for (int j = 0; j < kScaleGroup; ++j)
 #pragma unroll
                         for (int i = 0; i < kPer; ++i)
-                            if (32 * i < w.n)
-                                scales[s * NT + 32 * i + lane] = v[j][i] * one[j];
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(bar(kScF + s));
-                        ++n;
-                    }
+                            to[j * NT + 32 * i + lane] = v[j][i] * one[j];
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar(kScF + s));
                 }
             }
         }
@@ -685,12 +705,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
 #pragma unroll
             for (int i = 0; i < kGroupCols; ++i)
                 sum.v[i / 8][i / 4 % 2][i % 4] = 0.0f;
-            for (int k0 = 0; k0 < w.kblocks; k0 += kSeg, ++acc, ++n) {
+            for (int k0 = 0; k0 < w.kblocks; k0 += kSeg, ++acc) {
                 const uint32_t as = acc & 1u;
                 const uint32_t s = n % kScaleStages;
-                if (E8 && !(ok = wait_warp(bar(kScF + s), (n / kScaleStages) & 1u, abort_flag,
-                                           p.timeout_ns)))
+                if (E8 && k0 % kScaleGroup == 0 &&
+                    !(ok = wait_warp(bar(kScF + s), (n / kScaleStages) & 1u, abort_flag,
+                                     p.timeout_ns)))
                     break;
+                const float *const scales =
+                    reinterpret_cast<const float *>(sbase + lay.scale + s * scale_bytes(NT)) +
+                    k0 % kScaleGroup * NT;
+                const bool last = k0 % kScaleGroup == kScaleGroup - 1 || k0 == w.kblocks - 1;
                 if (!(ok = wait_warp(bar(kAccF + as), (acc >> 1) & 1u, abort_flag, p.timeout_ns)))
                     break;
                 tc_fence_after();
@@ -702,7 +727,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 f[j] = *reinterpret_cast<const float2 *>(
-                                    scales + s * NT + c0 + c + 8 * j + 2 * (lane & 3));
+                                    scales + c0 + c + 8 * j + 2 * (lane & 3));
                         }
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -724,9 +749,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive_cluster(lead_bar(kAccE + as));
-                    if (E8)
+                    if (E8 && last)
                         mbar_arrive(bar(kScE + s));
                 }
+                n += last;
             }
             // A group stores together or, after a wait of any of its warps ran out,
             // leaves together: no warp waits at its barrier for one that has left.
@@ -762,8 +788,11 @@ __global__ void __launch_bounds__(256)
 
 // Rows in the lists' order: to[p] = the row that map names for position p,
 // zeros where there is none in map or in also (*holes is then set, if given).
-// A power of two of lanes a row, up to eight 16-byte pieces in flight a lane.
-__global__ void __launch_bounds__(256, 4)
+// A power of two of lanes a row, up to four 16-byte pieces in flight a lane.
+// Bound by L2, which every byte crosses twice (131,072 rows of 4,096 bytes of a
+// matrix of 16,384: 120 us, 8.9 TB/s; bulk copies through shared memory 147);
+// streaming stores leave the matrix in L2 (with plain ones 129).
+__global__ void __launch_bounds__(256)
     gather_rows_kernel(const int32_t *offsets, int32_t E, int32_t M, RowMap map, RowMap also,
                        const uint4 *from, int32_t units, int32_t lanes, uint4 *to, int32_t *holes)
 {
@@ -771,8 +800,8 @@ __global__ void __launch_bounds__(256, 4)
     const int32_t hi = offsets == nullptr ? M : min(max(__ldg(offsets + E), 0), M);
     const int32_t mine = threadIdx.x & (lanes - 1);
     const int32_t rows = 256 / lanes;
-    for (int64_t at = blockIdx.x * static_cast<int64_t>(rows) + threadIdx.x / lanes; at < M;
-         at += gridDim.x * static_cast<int64_t>(rows)) {
+    const int64_t at = blockIdx.x * static_cast<int64_t>(rows) + threadIdx.x / lanes;
+    if (at < M) {
         const int32_t p = static_cast<int32_t>(at);
         int32_t row = -1;
         if (p >= lo && p < hi) {
@@ -786,18 +815,43 @@ __global__ void __launch_bounds__(256, 4)
         uint4 *const dst = to + at * units;
         int32_t u = mine;
         if (row >= 0) {
-            for (; u + 7 * lanes < units; u += 8 * lanes) {
-                uint4 v[8];
+            for (; u + 3 * lanes < units; u += 4 * lanes) {
+                uint4 v[4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
+                for (int k = 0; k < 4; ++k)
                     v[k] = __ldg(src + u + k * lanes);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    dst[u + k * lanes] = v[k];
+                for (int k = 0; k < 4; ++k)
+                    __stcs(dst + u + k * lanes, v[k]);
             }
         }
         for (; u < units; u += lanes)
             dst[u] = row >= 0 ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+    }
+}
+
+// to[b][p] = the scale of k-block b of the row that map names for position p (0:
+// none): scales of neighbouring columns of a tile then stand together.
+__global__ void __launch_bounds__(256)
+    gather_scales_kernel(int32_t M, RowMap map, const float *from, int32_t kblocks, float *to)
+{
+    __shared__ float tile[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t p0 = 32 * static_cast<int64_t>(blockIdx.x);
+    for (int b0 = 0; b0 < kblocks; b0 += 32) {
+#pragma unroll
+        for (int i = warp; i < 32; i += 8) {
+            const int32_t row = p0 + i < M ? row_of(map, static_cast<int32_t>(p0 + i), M) : -1;
+            tile[i][lane] = row >= 0 && b0 + lane < kblocks
+                                ? __ldg(from + static_cast<int64_t>(row) * kblocks + b0 + lane)
+                                : 0.0f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = warp; i < 32; i += 8)
+            if (b0 + i < kblocks && p0 + lane < M)
+                to[static_cast<int64_t>(b0 + i) * M + p0 + lane] = tile[lane][i];
+        __syncthreads();
     }
 }
 
@@ -860,6 +914,7 @@ cudaError_t launch_experts(ExpertsKind kind, bool e8, int type, const CUtensorMa
 {
     p.idesc = idesc_base(e8 ? 0u : type == kBf16 ? 1u : 0u, kind != kForward, kind == kWeightsGrad,
                          2 * kRowsA);
+    p.segment = kind == kWeightsGrad && p.out_type == kFp32 ? kSegmentRows : kSegment;
     const bool few = experts_few(p.M, p.E);
     switch (kind) {
     case kForward:
@@ -884,17 +939,24 @@ cudaError_t launch_listed_rows(const int32_t *offsets, int32_t E, int32_t M, Row
     return cudaGetLastError();
 }
 
+cudaError_t launch_gather_scales(int32_t M, RowMap map, const float *from, int32_t kblocks, float *to,
+                                 cudaStream_t stream)
+{
+    gather_scales_kernel<<<static_cast<unsigned>((static_cast<int64_t>(M) + 31) / 32), 256, 0,
+                           stream>>>(M, map, from, kblocks, to);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_gather_rows(const int32_t *offsets, int32_t E, int32_t M, RowMap map,
                                RowMap also, const void *from, int64_t pitch, void *to,
-                               int32_t *holes, int sms, cudaStream_t stream)
+                               int32_t *holes, cudaStream_t stream)
 {
     const int32_t units = static_cast<int32_t>(pitch / 16);
     int32_t lanes = 32;
     while (lanes > 1 && lanes / 2 >= units)
         lanes /= 2;
     const int64_t blocks = (static_cast<int64_t>(M) * lanes + 255) / 256;
-    gather_rows_kernel<<<static_cast<unsigned>(std::min<int64_t>(blocks, 16 * sms)), 256, 0,
-                         stream>>>(offsets, E, M, map, also, static_cast<const uint4 *>(from),
+    gather_rows_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(offsets, E, M, map, also, static_cast<const uint4 *>(from),
                                    units, lanes, static_cast<uint4 *>(to), holes);
     return cudaGetLastError();
 }

@@ -156,20 +156,23 @@ int kmassign_experts(const void *X, int32_t dtype, int64_t R, int64_t D, const v
     // its own, and are then loaded in whole boxes.
     const int64_t pitch = D * (e8 ? 1 : 2);
     const bool few = kma::experts_few(M, E);
-    Scratch sorted(rows != nullptr && !few ? static_cast<size_t>(M * pitch) : 0, dev.pool, st);
-    if (!sorted.ok())
+    const int32_t kblocks = static_cast<int32_t>((pitch + 127) / 128);
+    const size_t codes = rows != nullptr && !few ? static_cast<size_t>(M * pitch) : 0;
+    Scratch scratch(codes + (e8 && !few ? static_cast<size_t>(M) * kblocks * 4 : 0), dev.pool, st);
+    if (!scratch.ok())
         return KMASSIGN_ERR_CUDA;
+    uint8_t *const sorted = codes > 0 ? scratch.get() : nullptr;
     const RowMap from = map_of(rows, slots, R);
     const bool gathers = rows != nullptr && few;
     CUtensorMap a, b;
     if (!weights_map(&a, dtype, W, E, F, D, kma::kExpertsBoxA) ||
-        (sorted.get() != nullptr
-             ? !rows_map(&b, dtype, sorted.get(), M, D, kma::kExpertsBoxB)
+        (sorted != nullptr
+             ? !rows_map(&b, dtype, sorted, M, D, kma::kExpertsBoxB)
              : !rows_map(&b, dtype, X, R, D, gathers ? 1 : kma::kExpertsBoxB)))
         return KMASSIGN_ERR_CUDA;
     ExpertsParams p = params_of(s, offsets);
     p.mdim = static_cast<int32_t>(F);
-    p.kblocks = static_cast<int32_t>((pitch + 127) / 128);
+    p.kblocks = kblocks;
     p.fblocks = static_cast<int32_t>((F + 127) / 128);
     p.b_rows = gathers ? from : map_of(nullptr, 1, M);
     p.from = from;
@@ -180,13 +183,18 @@ int kmassign_experts(const void *X, int32_t dtype, int64_t R, int64_t D, const v
     p.xscale = xscale;
     p.wscale = wscale;
     cudaError_t e = cudaSuccess;
-    if (sorted.get() != nullptr)
-        e = kma::launch_gather_rows(offsets, p.E, p.M, from, map_of(nullptr, 1, M), X, pitch,
-                                    sorted.get(), nullptr, dev.sms, st);
+    if (sorted != nullptr)
+        e = kma::launch_gather_rows(offsets, p.E, p.M, from, map_of(nullptr, 1, M), X, pitch, sorted,
+                                    nullptr, st);
+    if (e == cudaSuccess && e8 && !few) {
+        float *const by_block = reinterpret_cast<float *>(scratch.get() + codes);
+        e = kma::launch_gather_scales(p.M, from, xscale, kblocks, by_block, st);
+        p.xscale = by_block;
+    }
     if (e == cudaSuccess)
         e = kma::launch_experts(kma::kForward, e8, dtype, a, b, p, dev.sms, dev.smem, st);
     rc = done(e);
-    return sorted.release() ? rc : KMASSIGN_ERR_CUDA;
+    return scratch.release() ? rc : KMASSIGN_ERR_CUDA;
 }
 
 int kmassign_experts_grad(const void *dout, int32_t dtype, int64_t out_rows, int64_t F,
@@ -256,7 +264,7 @@ int kmassign_experts_grad(const void *dout, int32_t dtype, int64_t out_rows, int
     }
     if (e == cudaSuccess && places != nullptr)
         e = kma::launch_gather_rows(offsets, static_cast<int32_t>(E), static_cast<int32_t>(M),
-                                    placed, from, dout, 2 * F, dy_sorted, holes, dev.sms, st);
+                                    placed, from, dout, 2 * F, dy_sorted, holes, st);
     ExpertsParams p = params_of(s, offsets);
     p.mdim = static_cast<int32_t>(D);
     p.b_rows = p.places = map_of(nullptr, 1, M);
@@ -266,7 +274,7 @@ int kmassign_experts_grad(const void *dout, int32_t dtype, int64_t out_rows, int
     if (e == cudaSuccess && dW != nullptr) {
         if (e == cudaSuccess && rows != nullptr)
             e = kma::launch_gather_rows(offsets, p.E, p.M, from, placed, X, 2 * D, by_position,
-                                        holes, dev.sms, st);
+                                        holes, st);
         if (!rows_map(&a, dtype, rows != nullptr ? by_position : X, rows != nullptr ? M : R, D,
                       kma::kExpertsBoxMn) ||
             !rows_map(&b, dtype, dy, dy_rows, F, kma::kExpertsBoxMn))

@@ -157,9 +157,12 @@ struct ExpertsParams {
     bool zero_rest;           // rows of no list are written 0
     void *out;
     int32_t out_type;
-    const float *xscale, *wscale;   // 8 bits: [rows, kblocks], [E, fblocks, kblocks]
+    // 8 bits: [rows, kblocks] of few positions, else [kblocks, M] by launch_gather_scales
+    const float *xscale;
+    const float *wscale;      // [E, fblocks, kblocks]
     int32_t fblocks;
-    int32_t stages;           // set by launch_experts, like idesc
+    // set by launch_experts: depth of the ring, k-blocks between additions to registers, MMA shape
+    int32_t stages, segment;
     uint32_t idesc;
     uint64_t timeout_ns;
 };
@@ -185,7 +188,11 @@ cudaError_t launch_listed_rows(const int32_t *offsets, int32_t E, int32_t M, Row
 // NULL) is set to 1 if a position of a list gets zeros.
 cudaError_t launch_gather_rows(const int32_t *offsets, int32_t E, int32_t M, RowMap map,
                                RowMap also, const void *from, int64_t pitch, void *to,
-                               int32_t *holes, int sms, cudaStream_t stream);
+                               int32_t *holes, cudaStream_t stream);
+
+// to[b][p] = from[the row that map names for position p][b], 0 where it names none.
+cudaError_t launch_gather_scales(int32_t M, RowMap map, const float *from, int32_t kblocks, float *to,
+                                 cudaStream_t stream);
 
 cudaError_t launch_rmsnorm(const void *X, int dtype, int64_t N, int64_t D, const void *residual,
                            const void *weight, int weight_dtype, float eps, void *total, void *out,

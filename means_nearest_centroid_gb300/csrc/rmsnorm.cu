@@ -198,7 +198,11 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const NormArgs a, int warp
             for (int d = kLanes / 2; d > 0; d /= 2)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             const float scale = fmaxf(top, kLeast) / kTop;
-            const float inverse = __fdividef(1.0f, scale);   // scale is a normal number
+            // y / scale, rounded to nearest: the product with the reciprocal, corrected
+            // by its residual (Markstein 1990).  A row's values are often exactly
+            // between two codes, and the product alone falls on either side.
+            const float inverse = __frcp_rn(scale);
+            const float back = scale < INFINITY ? scale : 0.0f;
             const int first = column<VE>(j, warps, warp, lane);
             if (lane % kLanes == 0 && first < a.D)
                 a.scales[row * blocks + first / 128] = scale;
@@ -208,8 +212,10 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const NormArgs a, int warp
                 if (col < a.D) {
                     float q[VE];
 #pragma unroll
-                    for (int i = 0; i < VE; ++i)
-                        q[i] = t[j + k][i] * inverse;
+                    for (int i = 0; i < VE; ++i) {
+                        const float y = t[j + k][i], product = y * inverse;
+                        q[i] = fmaf(fmaf(-product, back, y), inverse, product);
+                    }
                     store_codes<VE>(static_cast<uint8_t *>(a.out) + at + col, q);
                 }
             }
