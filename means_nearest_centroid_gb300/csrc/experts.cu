@@ -316,6 +316,22 @@ __device__ __forceinline__ void store_columns(const Frags<COLS> &sum, int cols, 
     }
 }
 
+// Zeros in the rows of no list, before the first and behind the last: one of
+// `of` warps' share.
+__device__ __forceinline__ void zero_rows(const ExpertsParams &p, const int32_t *lists, int64_t warp,
+                                          int64_t of, int lane)
+{
+    const int32_t lo = lists[0], hi = lists[p.E + 1 + p.E - 1];
+    const int32_t rest = p.M - (hi - lo);
+    const int64_t units = static_cast<int64_t>(p.mdim) * dtype_bytes(p.out_type) / 16;
+    for (int64_t r = warp; r < rest; r += of) {
+        const int64_t row = r < lo ? r : r - lo + hi;
+        uint4 *out = static_cast<uint4 *>(p.out) + row * units;
+        for (int64_t i = lane; i < units; i += 32)
+            out[i] = make_uint4(0, 0, 0, 0);
+    }
+}
+
 template <ExpertsKind KIND, bool E8, int NT, int CW>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
     experts_kernel(const __grid_constant__ CUtensorMap amap,
@@ -666,19 +682,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
         const int q = warp & 3, group = warp >> 2;
         const int c0 = group * kGroupCols;
         const uint32_t tmem_warp = tmem_base + (static_cast<uint32_t>(q) << 21) + c0;
-        if (p.zero_rest) {
-            // Rows of no list: before the first and behind the last.
-            const int32_t lo = p.E > 0 ? lists[0] : 0, hi = lists[p.E + 1 + p.E - 1];
-            const int32_t rest = p.M - (hi - lo);
-            const int64_t units = static_cast<int64_t>(p.mdim) * dtype_bytes(p.out_type) / 16;
-            for (int64_t r = blockIdx.x * CW + warp; r < rest;
-                 r += gridDim.x * CW) {
-                const int64_t row = r < lo ? r : r - lo + hi;
-                uint4 *out = static_cast<uint4 *>(p.out) + row * units;
-                for (int64_t i = lane; i < units; i += 32)
-                    out[i] = make_uint4(0, 0, 0, 0);
-            }
-        }
+        if (p.zero_rest)
+            zero_rows(p, lists, blockIdx.x * CW + warp, gridDim.x * CW, lane);
         const int thread = threadIdx.x & 127;
         uint8_t *const staging = sbase + lay.staging + group * kStagingBytes;
         int32_t *const dsts = reinterpret_cast<int32_t *>(sbase + lay.dst) + group * 2 * kGroupCols;
@@ -774,6 +779,317 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
     if (warp == kWarpMma) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, kTmemColumns);
+    }
+}
+
+// ---- 8 bits, many positions -------------------------------------------------
+//
+// Here a tile's rows are positions (256 of a list) and its columns elements of
+// the output (256).  A thread of the consumers then holds one position's row, so
+// that a segment's scale is one number a thread, which it loads itself: the sums
+// cost one FMA an element and nothing else.  (With positions as columns each
+// element needs its column's scale out of shared memory; 32,768 x 4,096 x 4,096 in
+// 8 lists took XX us there.)  Lists are rounded up to 256 for it, so only products
+// of many positions an expert come here.
+
+constexpr int kLoad8 = 8, kIssue8 = 9;   // warps behind the 8 of consumers; two issue
+
+struct Tile8 {
+    int32_t e, m0, n0, n, hi;
+};
+
+struct Layout8 {
+    uint32_t staging, lists, bars, end;
+};
+
+__host__ __device__ inline Layout8 layout8_of(int stages, int E)
+{
+    Layout8 l;
+    l.staging = stages * stage_bytes(256);   // 2 KiB a warp of consumers
+    l.lists = l.staging + 16384u;
+    l.bars = (l.lists + 3u * static_cast<uint32_t>(E + 1) * 4u + 15u) / 16u * 16u;
+    l.end = l.bars + kBars * 8u + 16u;
+    return l;
+}
+
+// A warp's rows (lane l: row l's next 64 bytes, as four pieces) to shared
+// memory and from there to the output, four lanes to a row.
+__device__ __forceinline__ void store_rows(uint8_t *stage, const uint4 (&v)[4], uint8_t *out,
+                                           int64_t pitch, int32_t dst, int32_t bytes, int lane)
+{
+    __syncwarp();
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+        *reinterpret_cast<uint4 *>(stage + lane * 64 + 16 * (p ^ (lane >> 1 & 3))) = v[p];
+    __syncwarp();
+    const int piece = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 8 * i + (lane >> 2);
+        const int32_t d = __shfl_sync(0xffffffffu, dst, row);
+        if (d >= 0 && 16 * piece < bytes)
+            *reinterpret_cast<uint4 *>(out + d * pitch + 16 * piece) =
+                *reinterpret_cast<const uint4 *>(stage + row * 64 + 16 * (piece ^ (row >> 1 & 3)));
+    }
+}
+
+template <typename O>
+__device__ __forceinline__ void store_sums(const float (&sum)[128], uint8_t *stage, void *out,
+                                           int32_t mdim, int32_t f, int32_t dst, bool zero, int lane)
+{
+    constexpr int kCols = 64 / sizeof(O);
+    const int64_t pitch = static_cast<int64_t>(mdim) * sizeof(O);
+#pragma unroll
+    for (int c = 0; c < 128; c += kCols) {
+        uint4 v[4];
+        if constexpr (sizeof(O) == 2) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                v[p] = make_uint4(pack_two<O>(sum[c + 8 * p], sum[c + 8 * p + 1]),
+                                  pack_two<O>(sum[c + 8 * p + 2], sum[c + 8 * p + 3]),
+                                  pack_two<O>(sum[c + 8 * p + 4], sum[c + 8 * p + 5]),
+                                  pack_two<O>(sum[c + 8 * p + 6], sum[c + 8 * p + 7]));
+        } else {
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                v[p] = make_uint4(__float_as_uint(sum[c + 4 * p]), __float_as_uint(sum[c + 4 * p + 1]),
+                                  __float_as_uint(sum[c + 4 * p + 2]),
+                                  __float_as_uint(sum[c + 4 * p + 3]));
+        }
+        if (zero) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                v[p] = make_uint4(0, 0, 0, 0);
+        }
+        const int32_t left = mdim - (f + c);
+        if (left <= 0)   // the same for the whole warp
+            break;
+        store_rows(stage, v, static_cast<uint8_t *>(out) + (f + c) * sizeof(O), pitch, dst,
+                   min(64, left * static_cast<int>(sizeof(O))), lane);
+    }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
+    experts8_kernel(const __grid_constant__ CUtensorMap amap,
+                    const __grid_constant__ CUtensorMap bmap, const ExpertsParams p)
+{
+    constexpr uint32_t kStageBytes = stage_bytes(256);
+    constexpr uint16_t kBoth = 0x3;
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const Layout8 lay = layout8_of(p.stages, p.E);
+    uint8_t *const sbase = smem_raw + (base - raw);
+    int32_t *const lists = reinterpret_cast<int32_t *>(sbase + lay.lists);
+    volatile uint32_t *tmem_slot =
+        reinterpret_cast<volatile uint32_t *>(sbase + lay.bars + kBars * 8);
+    volatile uint32_t *abort_flag = tmem_slot + 1;
+    auto bar = [&](int i) -> uint32_t { return base + lay.bars + 8u * static_cast<uint32_t>(i); };
+    auto lead_bar = [&](int i) -> uint32_t { return map_to_rank(bar(i), 0); };
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kMaxRing; ++s) {
+            mbar_init(bar(kFull + s), 1);
+            mbar_init(bar(kEmpty + s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(bar(kAccF + a), 1);
+            mbar_init(bar(kAccE + a), 2 * 8);
+            mbar_init(bar(kLast + a), 1);
+        }
+        *abort_flag = 0u;
+        fence_mbar_init();
+    }
+    if (warp == kLoad8) {
+        tmem_alloc_pair(smem_addr(const_cast<uint32_t *>(tmem_slot)), 512);
+        tmem_relinquish_pair();
+    } else if (warp == 1) {
+        form_lists<256>(p, lists, lane);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // both CTAs' barriers exist before any cross-CTA signal
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int32_t *const begin = lists, *const end = lists + (p.E + 1),
+                        *const before = lists + 2 * (p.E + 1);
+    const int nblocks = (p.mdim + 255) / 256;
+    const int total = before[p.E] * nblocks;
+    const int first = static_cast<int>(blockIdx.x >> 1);
+    const int step = static_cast<int>(gridDim.x >> 1);
+    const uint32_t stages = static_cast<uint32_t>(p.stages);
+    auto tile = [&](int t) -> Tile8 {
+        const int q = t / nblocks;
+        int lo = 0, hi = p.E;   // before[lo] <= q < before[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (before[mid] <= q)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        Tile8 w;
+        w.e = lo;
+        w.m0 = begin[lo] + (q - before[lo]) * 256;
+        w.hi = end[lo];
+        w.n0 = (t - q * nblocks) * 256;
+        w.n = min(256, (p.mdim - w.n0 + 31) / 32 * 32);
+        return w;
+    };
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(8)));
+        uint32_t stage = 0, phase = 0;
+        bool ok = true;
+        auto next_stage = [&]() {
+            if (++stage == stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        };
+        if (warp == kLoad8) {
+            if (lane == 0) {
+                tma_prefetch_desc(&amap);
+                tma_prefetch_desc(&bmap);
+                for (int t = first; ok && t < total; t += step) {
+                    const Tile8 w = tile(t);
+                    const int m = w.m0 + static_cast<int>(rank) * kRowsA;
+                    const int n = w.n0 + static_cast<int>(rank) * (w.n / 2);
+                    for (int kb = 0; kb < p.kblocks; ++kb, next_stage()) {
+                        if (!(ok = wait1(bar(kEmpty + stage), phase ^ 1u, abort_flag, p.timeout_ns)))
+                            break;
+                        if (leader)
+                            mbar_arrive_expect_tx(bar(kFull + stage), 2 * kStageBytes);
+                        const uint32_t full = lead_bar(kFull + stage);
+                        const uint32_t to = base + stage * kStageBytes;
+                        tma_load_2d_pair(to, &amap, full, kb * 128, m);
+                        tma_load_3d_pair(to + kPartA, &bmap, full, kb * 128, n, w.e);
+                    }
+                }
+                if (!ok) {   // see experts_kernel
+                    const uint64_t t0 = globaltimer_ns();
+                    while (globaltimer_ns() - t0 < 1000000ull) {
+                    }
+                }
+            }
+            __syncwarp();
+        } else if (leader && (warp == kIssue8 || warp == kIssue8 + 1)) {
+            // One warp for each accumulator: a segment has a hand-over at both ends.
+            const uint32_t me = static_cast<uint32_t>(warp - kIssue8);
+            uint32_t acc = 0;
+            bool issued = false;
+            for (int t = first; ok && t < total; t += step) {
+                const Tile8 w = tile(t);
+                const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
+                for (int kb = 0; kb < p.kblocks; ++kb, ++acc, next_stage()) {
+                    if ((acc & 1u) != me)
+                        continue;
+                    if (!(ok = wait_warp(bar(kAccE + me), ((acc >> 1) & 1u) ^ 1u, abort_flag,
+                                         p.timeout_ns) &&
+                               wait_warp(bar(kFull + stage), phase, abort_flag, p.timeout_ns)))
+                        break;
+                    tc_fence_after();
+                    const uint64_t a = sw128_kmajor_desc(base + stage * kStageBytes);
+                    const uint64_t b = sw128_kmajor_desc(base + stage * kStageBytes + kPartA);
+                    if (elect_one()) {
+#pragma unroll
+                        for (uint32_t k = 0; k < 4; ++k)
+                            mma_f8_pair(tmem_base + me * 256, a + 2u * k, b + 2u * k, idesc, k != 0);
+                        mma_commit_pair(bar(kEmpty + stage), kBoth);
+                        mma_commit_pair(bar(kAccF + me), kBoth);
+                    }
+                    __syncwarp();
+                    issued = true;
+                }
+            }
+            if (issued) {
+                if (elect_one())
+                    mma_commit_pair(bar(kLast + me), 0x1);
+                __syncwarp();
+                wait_warp(bar(kLast + me), 0u, abort_flag, kDrainLimitNs, false);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(consumer_regs(8)));
+        const int q = warp & 3, group = warp >> 2;
+        const uint32_t tmem_warp =
+            tmem_base + (static_cast<uint32_t>(q) << 21) + static_cast<uint32_t>(group) * 128u;
+        uint8_t *const staging = sbase + lay.staging + warp * 2048;
+        if (p.zero_rest)
+            zero_rows(p, lists, blockIdx.x * 8 + warp, gridDim.x * 8, lane);
+        uint32_t acc = 0;
+        bool ok = true;
+        for (int t = first; ok && t < total; t += step) {
+            const Tile8 w = tile(t);
+            const int at = w.m0 + static_cast<int>(rank) * kRowsA + 32 * q + lane;
+            const int32_t row = row_of(p.from, at, w.hi);
+            const int32_t dst = row_of(p.places, at, w.hi);
+            const int f0 = w.n0 + 128 * group;
+            const int cols = min(128, w.n - 128 * group);   // may be none
+            const float *const xs = p.xscale + static_cast<int64_t>(max(row, 0)) * p.kblocks;
+            const float *const ws =
+                p.wscale +
+                (static_cast<int64_t>(w.e) * p.fblocks + min(f0 >> 7, p.fblocks - 1)) * p.kblocks;
+            float sum[128];
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+                sum[i] = 0.0f;
+            float x_next = __ldg(xs), w_next = __ldg(ws);
+            for (int kb = 0; kb < p.kblocks; ++kb, ++acc) {
+                const float scale = x_next * w_next;
+                if (kb + 1 < p.kblocks) {
+                    x_next = __ldg(xs + kb + 1);
+                    w_next = __ldg(ws + kb + 1);
+                }
+                const uint32_t as = acc & 1u;
+                if (!(ok = wait_warp(bar(kAccF + as), (acc >> 1) & 1u, abort_flag, p.timeout_ns)))
+                    break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    if (c < cols) {
+                        float v[32];
+                        tmem_ld_32x32b_x32(tmem_warp + as * 256 + c, v);
+                        tmem_wait_ld();
+                        if (c + 32 >= cols) {   // the last: the accumulator may be written again
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive_cluster(lead_bar(kAccE + as));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            sum[c + i] = fmaf(v[i], scale, sum[c + i]);
+                    }
+                }
+                if (cols <= 0 && lane == 0)
+                    mbar_arrive_cluster(lead_bar(kAccE + as));
+            }
+            if (!ok)
+                break;
+            if (cols <= 0)
+                continue;
+            if (p.out_type == kBf16)
+                store_sums<__nv_bfloat16>(sum, staging, p.out, p.mdim, f0, dst, row < 0, lane);
+            else if (p.out_type == kFp16)
+                store_sums<__half>(sum, staging, p.out, p.mdim, f0, dst, row < 0, lane);
+            else
+                store_sums<float>(sum, staging, p.out, p.mdim, f0, dst, row < 0, lane);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // no CTA leaves while its pair can still touch its memory
+    if (warp == kLoad8) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 512);
     }
 }
 
@@ -894,6 +1210,7 @@ cudaError_t experts_prepare(size_t smem_optin)
                              (const void *)experts_kernel<kForward, false, 256, kWide>,
                              (const void *)experts_kernel<kForward, true, 64, 8>,
                              (const void *)experts_kernel<kForward, true, 256, kWideE8>,
+                             (const void *)experts8_kernel,
                              (const void *)experts_kernel<kRowsGrad, false, 64, 8>,
                              (const void *)experts_kernel<kRowsGrad, false, 256, kWide>,
                              (const void *)experts_kernel<kWeightsGrad, false, 256, kWide>};
@@ -907,6 +1224,25 @@ cudaError_t experts_prepare(size_t smem_optin)
 }
 
 bool experts_few(int64_t M, int64_t E) { return M <= 32 * E; }
+
+bool experts8_many(int64_t M, int64_t E) { return M >= 256 * E; }
+
+cudaError_t launch_experts8(const CUtensorMap &a, const CUtensorMap &b, ExpertsParams p, int sms,
+                            size_t smem_optin, cudaStream_t stream)
+{
+    p.stages = 0;
+    for (int s = kMaxRing; s >= 2 && p.stages == 0; --s)
+        if (1024u + layout8_of(s, p.E).end <= smem_optin)
+            p.stages = s;
+    if (p.stages == 0)
+        return cudaErrorInvalidConfiguration;
+    p.idesc = idesc_base(0u, false, false, 2 * kRowsA);
+    const int64_t tiles =
+        (std::min<int64_t>(p.E, p.M) + p.M / 256) * ((p.mdim + 255) / 256);
+    const int grid = 2 * static_cast<int>(std::min<int64_t>(tiles, sms / 2));
+    experts8_kernel<<<grid, 384, 1024u + layout8_of(p.stages, p.E).end, stream>>>(a, b, p);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_experts(ExpertsKind kind, bool e8, int type, const CUtensorMap &a,
                            const CUtensorMap &b, ExpertsParams p, int sms, size_t smem_optin,

@@ -179,6 +179,11 @@ bool experts_few(int64_t M, int64_t E);
 cudaError_t launch_experts(ExpertsKind kind, bool e8, int type, const CUtensorMap &a,
                            const CUtensorMap &b, ExpertsParams p, int sms, size_t smem_optin,
                            cudaStream_t stream);
+// 8 bits with many positions an expert: rows of X in boxes of 128 (a), of W in
+// boxes of 128 (b), xscale by row.
+bool experts8_many(int64_t M, int64_t E);
+cudaError_t launch_experts8(const CUtensorMap &a, const CUtensorMap &b, ExpertsParams p, int sms,
+                            size_t smem_optin, cudaStream_t stream);
 cudaError_t experts_status_read_and_clear(int *code);
 // row[p] = the row that map names for positions of a list, -1 for the others.
 cudaError_t launch_listed_rows(const int32_t *offsets, int32_t E, int32_t M, RowMap map,
