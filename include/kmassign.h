@@ -532,8 +532,8 @@ int kmassign_clip(const void *const *grads, void *const *out, const int64_t *siz
  * sum is multiplied by the fp32 product of its two scales) and rounded once.  A
  * row's bits depend on neither the other rows nor the lists.
  * M = 0 or out_rows = 0 writes nothing.  Errors: KMASSIGN_ERR_SHAPE also for E,
- * slots, or M above R (without rows) or out_rows (without places), or R = 0 with
- * places; F or D KMASSIGN_ERR_UNSUPPORTED_D; types KMASSIGN_ERR_ARG.
+ * slots, M >= 2^30, M above R (without rows) or out_rows (without places), or R = 0
+ * with places; F or D KMASSIGN_ERR_UNSUPPORTED_D; types KMASSIGN_ERR_ARG.
  */
 int kmassign_experts(const void *X, int32_t dtype, int64_t R, int64_t D, const void *W, int64_t E,
                      int64_t F, const float *xscale, const float *wscale, const int32_t *offsets,

@@ -826,6 +826,8 @@ def _need_lists(X, W, offsets, rows, slots, places):
         M = rows.numel()
     elif slots != 1:
         raise ValueError("slots needs rows")
+    if not 1 <= slots < 2 ** 31:
+        raise ValueError(f"slots must be positive, got {slots}")
     if places is not None:
         _need_cuda(places, "places", torch.int32)
         if rows is not None and places.numel() != M:
@@ -856,8 +858,8 @@ def kmassign_experts(X, W, offsets=None, rows=None, slots: int = 1, places=None,
     if code == 3:
         _need_shape(xscale, "xscale", (R, _blocks(D)))
         _need_shape(wscale, "wscale", (*W.shape[:-2], _blocks(F), _blocks(D)))
-    if X.requires_grad or W.requires_grad:
-        _need_detached("kmassign_experts", "X or W")
+    if any(t is not None and t.requires_grad for t in (X, W, xscale, wscale)):
+        _need_detached("kmassign_experts", "X, W or a scale")
     given = out is not None
     if not given:
         out = _new((M, F), dtype or (torch.bfloat16 if code == 3 else X.dtype), X.device, stream,
@@ -901,22 +903,19 @@ def kmassign_experts_grad(dout, X, W, offsets=None, rows=None, slots: int = 1, p
         raise ValueError(f"dout must have shape {(M, F)}, got {tuple(dout.shape)}")
     if not (need_x or need_w):
         raise ValueError("neither gradient is needed")
+    if (dX is not None and not need_x) or (dW is not None and not need_w):
+        raise ValueError("a gradient is given but not needed")
     if dout.requires_grad or X.requires_grad or W.requires_grad:
         _need_detached("kmassign_experts_grad", "dout, X or W")
     given = dX, dW
-    if not need_x:
-        if dX is not None:
-            raise ValueError("dX is given but not needed")
-    elif dX is None:
-        dX = _new((R, D), X.dtype, X.device, stream)
-    else:
+    if dX is not None:
         _need_cuda(dX, "dX", X.dtype)
         _need_shape(dX, "dX", (R, D))
-    if not need_w:
-        if dW is not None:
-            raise ValueError("dW is given but not needed")
-    elif dW is None:
-        dW = _new(W.shape, dtype or torch.float32, X.device, stream)
+    elif need_x:
+        dX = _new((R, D), X.dtype, X.device, stream)
+    if dW is None:
+        if need_w:
+            dW = _new(W.shape, dtype or torch.float32, X.device, stream)
     else:
         if dtype is not None and dW.dtype != dtype:
             raise TypeError(f"dW must be {dtype}, got {dW.dtype}")

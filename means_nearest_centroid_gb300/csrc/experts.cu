@@ -37,6 +37,7 @@
 // follow from the lists' lengths (a prefix sum that each CTA forms at its
 // start), so that no host code has to know them.
 #include "experts_ptx.cuh"
+#include "launch.cuh"
 #include "learn.h"
 #include "pipeline.cuh"
 #include "vec.cuh"
@@ -82,8 +83,8 @@ struct Tile {
     int32_t kblocks;
 };
 
-// Shared memory behind the ring: the consumers' staging and row numbers, scales, then the lists' starts, ends and the
-// tiles before each expert, then barriers.
+// Shared memory behind the ring: the consumers' staging and row numbers, scales,
+// then the lists' starts, ends and the tiles before each expert, then barriers.
 struct Layout {
     uint32_t ring, staging, dst, scale, lists, bars, end;
 };
@@ -394,6 +395,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
         *abort_flag = 0u;
         fence_mbar_init();
     }
+    wait_for_previous();
+    let_next_start();   // all blocks of this launch are resident: the next one may set itself up
     if (warp == kWarpMma) {
         tmem_alloc_pair(smem_addr(const_cast<uint32_t *>(tmem_slot)), kTmemColumns);
         tmem_relinquish_pair();
@@ -503,7 +506,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
                     if (!(ok = wait_warp(bar(kEmpty + stage), phase ^ 1u, abort_flag, p.timeout_ns)))
                         break;
                     if (leader && lane == 0)
-                        mbar_arrive_expect_tx(bar(kFull + stage), 2 * (bytes + (kTwo ? kPartA : 0)));
+                        mbar_arrive_expect_tx(bar(kFull + stage),
+                                              2 * (bytes + (kTwo ? kPartA : 0)));
                     const uint32_t full = lead_bar(kFull + stage);
                     if (kTwo && lane == 31)
                         tma_load_3d_pair(part_a(stage), &amap, full, kb * kElems,
@@ -765,11 +769,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
                 break;
             const int32_t m = w.m0 + static_cast<int>(rank) * kRowsA;
             if (p.out_type == kBf16)
-                store_columns<__nv_bfloat16, kGroupCols, kStagingBytes>(sum, cols, staging, dst, p.out, m, p.mdim, group, thread);
+                store_columns<__nv_bfloat16, kGroupCols, kStagingBytes>(sum, cols, staging, dst, p.out, m,
+                                              p.mdim, group, thread);
             else if (p.out_type == kFp16)
-                store_columns<__half, kGroupCols, kStagingBytes>(sum, cols, staging, dst, p.out, m, p.mdim, group, thread);
+                store_columns<__half, kGroupCols, kStagingBytes>(sum, cols, staging, dst, p.out, m,
+                                              p.mdim, group, thread);
             else
-                store_columns<float, kGroupCols, kStagingBytes>(sum, cols, staging, dst, p.out, m, p.mdim, group, thread);
+                store_columns<float, kGroupCols, kStagingBytes>(sum, cols, staging, dst, p.out, m,
+                                              p.mdim, group, thread);
         }
     }
 
@@ -906,6 +913,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         *abort_flag = 0u;
         fence_mbar_init();
     }
+    wait_for_previous();
+    let_next_start();   // all blocks of this launch are resident: the next one may set itself up
     if (warp == kLoad8) {
         tmem_alloc_pair(smem_addr(const_cast<uint32_t *>(tmem_slot)), 512);
         tmem_relinquish_pair();
@@ -1096,6 +1105,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
 __global__ void __launch_bounds__(256)
     listed_rows_kernel(const int32_t *offsets, int32_t E, int32_t M, RowMap map, int32_t *row)
 {
+    wait_for_previous();
     const int32_t lo = offsets == nullptr ? 0 : min(max(__ldg(offsets), 0), M);
     const int32_t hi = offsets == nullptr ? M : min(max(__ldg(offsets + E), 0), M);
     for (int64_t at = blockIdx.x * 256 + threadIdx.x; at < M; at += gridDim.x * 256)
@@ -1112,6 +1122,8 @@ __global__ void __launch_bounds__(256)
     gather_rows_kernel(const int32_t *offsets, int32_t E, int32_t M, RowMap map, RowMap also,
                        const uint4 *from, int32_t units, int32_t lanes, uint4 *to, int32_t *holes)
 {
+    wait_for_previous();
+    let_next_start();
     const int32_t lo = offsets == nullptr ? 0 : min(max(__ldg(offsets), 0), M);
     const int32_t hi = offsets == nullptr ? M : min(max(__ldg(offsets + E), 0), M);
     const int32_t mine = threadIdx.x & (lanes - 1);
@@ -1152,6 +1164,8 @@ __global__ void __launch_bounds__(256)
     gather_scales_kernel(int32_t M, RowMap map, const float *from, int32_t kblocks, float *to)
 {
     __shared__ float tile[32][33];
+    wait_for_previous();
+    let_next_start();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t p0 = 32 * static_cast<int64_t>(blockIdx.x);
     for (int b0 = 0; b0 < kblocks; b0 += 32) {
@@ -1198,8 +1212,7 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, ExpertsParams p, 
                               : mblocks * (std::min<int64_t>(p.E, p.M) + p.M / NT);
     const int grid =
         2 * static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tiles, sms / 2)));
-    experts_kernel<KIND, E8, NT, CW><<<grid, threads_of(CW), smem, stream>>>(a, b, p);
-    return cudaGetLastError();
+    return launch_after(experts_kernel<KIND, E8, NT, CW>, grid, threads_of(CW), smem, stream, a, b, p);
 }
 
 }  // namespace
@@ -1240,8 +1253,8 @@ cudaError_t launch_experts8(const CUtensorMap &a, const CUtensorMap &b, ExpertsP
     const int64_t tiles =
         (std::min<int64_t>(p.E, p.M) + p.M / 256) * ((p.mdim + 255) / 256);
     const int grid = 2 * static_cast<int>(std::min<int64_t>(tiles, sms / 2));
-    experts8_kernel<<<grid, 384, 1024u + layout8_of(p.stages, p.E).end, stream>>>(a, b, p);
-    return cudaGetLastError();
+    return launch_after(experts8_kernel, grid, 384, 1024u + layout8_of(p.stages, p.E).end, stream, a,
+                        b, p);
 }
 
 cudaError_t launch_experts(ExpertsKind kind, bool e8, int type, const CUtensorMap &a,
@@ -1270,17 +1283,17 @@ cudaError_t launch_experts(ExpertsKind kind, bool e8, int type, const CUtensorMa
 cudaError_t launch_listed_rows(const int32_t *offsets, int32_t E, int32_t M, RowMap map,
                                int32_t *row, cudaStream_t stream)
 {
-    const int blocks = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(M) + 255) / 256, 4096));
-    listed_rows_kernel<<<blocks, 256, 0, stream>>>(offsets, E, M, map, row);
-    return cudaGetLastError();
+    const int blocks =
+        static_cast<int>(std::min<int64_t>((static_cast<int64_t>(M) + 255) / 256, 4096));
+    return launch_after(listed_rows_kernel, blocks, 256, 0, stream, offsets, E, M, map, row);
 }
 
 cudaError_t launch_gather_scales(int32_t M, RowMap map, const float *from, int32_t kblocks, float *to,
                                  cudaStream_t stream)
 {
-    gather_scales_kernel<<<static_cast<unsigned>((static_cast<int64_t>(M) + 31) / 32), 256, 0,
-                           stream>>>(M, map, from, kblocks, to);
-    return cudaGetLastError();
+    return launch_after(gather_scales_kernel,
+                        static_cast<unsigned>((static_cast<int64_t>(M) + 31) / 32), 256, 0, stream, M,
+                        map, from, kblocks, to);
 }
 
 cudaError_t launch_gather_rows(const int32_t *offsets, int32_t E, int32_t M, RowMap map,
@@ -1292,9 +1305,9 @@ cudaError_t launch_gather_rows(const int32_t *offsets, int32_t E, int32_t M, Row
     while (lanes > 1 && lanes / 2 >= units)
         lanes /= 2;
     const int64_t blocks = (static_cast<int64_t>(M) * lanes + 255) / 256;
-    gather_rows_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(offsets, E, M, map, also, static_cast<const uint4 *>(from),
-                                   units, lanes, static_cast<uint4 *>(to), holes);
-    return cudaGetLastError();
+    return launch_after(gather_rows_kernel, static_cast<unsigned>(blocks), 256, 0, stream, offsets, E,
+                        M, map, also, static_cast<const uint4 *>(from), units, lanes,
+                        static_cast<uint4 *>(to), holes);
 }
 
 cudaError_t experts_status_read_and_clear(int *code)

@@ -69,7 +69,7 @@ struct Shape {
 int check_shape(const Shape &s, int32_t type, const int32_t *offsets, const int32_t *rows,
                 const int32_t *places)
 {
-    if (s.R < 0 || s.R >= kLimit || s.M < 0 || s.M >= kLimit - 65536 || s.out_rows < 0 ||
+    if (s.R < 0 || s.R >= kLimit || s.M < 0 || s.M >= kLimit / 2 || s.out_rows < 0 ||
         s.out_rows >= kLimit || s.E < 1 || s.E > KMASSIGN_EXPERTS_MAX || s.slots < 1 ||
         (rows == nullptr && (s.M > s.R || s.slots != 1)) ||
         (places == nullptr && s.M > s.out_rows) || (offsets == nullptr && s.E != 1))

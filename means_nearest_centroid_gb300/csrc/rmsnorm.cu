@@ -10,6 +10,7 @@
 // it is longer or where rows are few, so it is read once for its statistics and
 // its output alike.  Sums are fp32.  A warp's piece of a row is a whole number
 // of 128-column blocks, so the scales need shuffles only.
+#include "launch.cuh"
 #include "learn.h"
 #include "vec.cuh"
 
@@ -116,6 +117,8 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(const NormArgs a, int warp
     const int64_t row =
         warps == 1 ? blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5)
                    : blockIdx.x;
+    wait_for_previous();
+    let_next_start();
     if (row >= a.N)
         return;   // whole warps; with several warps a row, never
     const int64_t at = row * a.D;
@@ -243,6 +246,8 @@ __global__ void __launch_bounds__(512) rmsnorm_grad_kernel(const NormGradArgs a,
     const int lane = threadIdx.x & 31;
     const int warp = warps == 1 ? 0 : threadIdx.x >> 5;
     const int group = warps == 1 ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    wait_for_previous();
+    let_next_start();
     if (group >= groups)
         return;   // whole warps
     float dw[NV][VE];
@@ -327,6 +332,7 @@ __global__ void __launch_bounds__(1024)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
     float v = 0.0f;
+    wait_for_previous();
     if (col < D) {
 #pragma unroll 8
         for (int g = warp; g < groups; g += 32)
@@ -367,13 +373,9 @@ template <typename T, bool CODES, int VE, int NV>
 cudaError_t run_norm(const NormArgs &a, cudaStream_t s)
 {
     const int warps = warps_for(a.D, VE * NV);
-    if (warps == 1)
-        rmsnorm_kernel<T, CODES, VE, NV>
-            <<<static_cast<unsigned>((a.N + 3) / 4), 128, 0, s>>>(a, 1);
-    else
-        rmsnorm_kernel<T, CODES, VE, NV>
-            <<<static_cast<unsigned>(a.N), 32 * warps, 0, s>>>(a, warps);
-    return cudaGetLastError();
+    return launch_after(rmsnorm_kernel<T, CODES, VE, NV>,
+                        static_cast<unsigned>(warps == 1 ? (a.N + 3) / 4 : a.N),
+                        warps == 1 ? 128 : 32 * warps, 0, s, a, warps);
 }
 
 template <typename T, bool CODES>
@@ -429,11 +431,8 @@ cudaError_t run_grad(const NormGradArgs &a, int sms, int *groups_out, cudaStream
     const int warps = warps_for(a.D, VE * NV);
     const int groups = grad_groups(a.N, warps, VE * NV, sms);
     *groups_out = groups;
-    if (warps == 1)
-        rmsnorm_grad_kernel<T, VE, NV><<<(groups + 3) / 4, 128, 0, s>>>(a, 1, groups);
-    else
-        rmsnorm_grad_kernel<T, VE, NV><<<groups, 32 * warps, 0, s>>>(a, warps, groups);
-    return cudaGetLastError();
+    return launch_after(rmsnorm_grad_kernel<T, VE, NV>, warps == 1 ? (groups + 3) / 4 : groups,
+                        warps == 1 ? 128 : 32 * warps, 0, s, a, warps, groups);
 }
 
 template <typename T>
@@ -498,11 +497,9 @@ cudaError_t launch_rmsnorm_grad(const void *dout, int dtype, int64_t N, int64_t 
     cudaError_t e = dtype == kFp32   ? grad_type<float>(a, sms, &groups, stream)
                     : dtype == kBf16 ? grad_type<__nv_bfloat16>(a, sms, &groups, stream)
                                      : grad_type<__half>(a, sms, &groups, stream);
-    if (e == cudaSuccess && dweight != nullptr) {
-        join_parts_kernel<<<static_cast<unsigned>((D + 31) / 32), 1024, 0, stream>>>(
-            parts, groups, static_cast<int>(D), dweight);
-        e = cudaGetLastError();
-    }
+    if (e == cudaSuccess && dweight != nullptr)
+        e = launch_after(join_parts_kernel, static_cast<unsigned>((D + 31) / 32), 1024, 0, stream,
+                         parts, groups, static_cast<int>(D), dweight);
     return e;
 }
 

@@ -658,7 +658,9 @@ def test_python_refusals(dev):
         (lambda: km.kmassign_experts(X, W, off[:2]), ValueError, "offsets"),
         (lambda: km.kmassign_experts(X, W, off, rows=rows.long()), TypeError, "rows"),
         (lambda: km.kmassign_experts(X, W, off, slots=2), ValueError, "slots"),
-        (lambda: km.kmassign_experts(X, W, off, rows=rows, slots=0), km.KmassignError, "SHAPE"),
+        (lambda: km.kmassign_experts(X, W, off, rows=rows, slots=0), ValueError, "slots"),
+        (lambda: km.kmassign_experts(X, W, off, rows=rows, slots=2**32 + 1), ValueError, "slots"),
+        (lambda: km.kmassign_experts(q, v, off, xscale=s.clone().requires_grad_(), wscale=t), RuntimeError, "requires grad"),
         (lambda: km.kmassign_experts(X, W, off, rows=rows, places=rows[:5]), ValueError, "places"),
         (lambda: km.kmassign_experts(X, W, off, out=d[:5]), ValueError, "out"),
         (lambda: km.kmassign_experts(X, W, off, out=d.half()), TypeError, "out"),

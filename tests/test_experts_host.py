@@ -34,7 +34,7 @@ def experts(lib, X=A, dtype=BF16, R=40, D=64, W=B, E=4, F=64, xs=NULL, ws=NULL, 
     (dict(dtype=0), "ARG"), (dict(dtype=4), "ARG"), (dict(dtype=-1), "ARG"), (dict(out_dtype=3), "ARG"),
     (dict(out_dtype=FP16), "ARG"), (dict(dtype=E4M3, out_dtype=E4M3, xs=E_, ws=E_), "ARG"),
     (dict(xs=E_), "ARG"), (dict(ws=E_), "ARG"),
-    (dict(R=-1), "SHAPE"), (dict(R=2**31), "SHAPE"), (dict(M=-1), "SHAPE"), (dict(M=2**31), "SHAPE"),
+    (dict(R=-1), "SHAPE"), (dict(R=2**31), "SHAPE"), (dict(M=-1), "SHAPE"), (dict(M=2**31), "SHAPE"), (dict(M=2**30, R=2**31 - 1, out_rows=2**31 - 1), "SHAPE"),
     (dict(E=0), "SHAPE"), (dict(E=1025), "SHAPE"), (dict(slots=0), "SHAPE"), (dict(slots=2), "SHAPE"),
     (dict(M=41), "SHAPE"), (dict(M=41, rows=E_), "SHAPE"), (dict(M=41, places=E_), "SHAPE"),
     (dict(out_rows=39), "SHAPE"), (dict(offsets=NULL), "SHAPE"), (dict(out_rows=2**31), "SHAPE"),
