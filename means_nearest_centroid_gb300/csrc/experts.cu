@@ -11,14 +11,20 @@
 // columns are the positions (the weights' gradient: F).  So a ragged list costs
 // what its positions need, rounded up to 32, instead of a whole tile of 128 or
 // 256; and in a step of few points the weights, which are then all that
-// counts, are the operand whose 128 rows a CTA streams.
+// counts, are the operand whose 128 rows a CTA streams.  (8 bits with many
+// positions are the other way round: experts8_kernel below.)
 //   operand A (128 rows of 128 bytes a CTA and stage): W[e] K-major (forward)
 //     or MN-major (rows' gradient); X MN-major (weights' gradient)
 //   operand B (n / 2 rows a CTA): the positions' rows, K-major; for the
 //     weights' gradient dY MN-major
 // A k-block is 128 bytes: 64 16-bit or 128 8-bit elements of the contraction,
-// four MMAs.  Rows named by a list are fetched by the copy engine itself
-// (gather4), four to an instruction, a lane each.
+// four MMAs.
+//
+// Rows named by ids.  Few positions: the copy engine fetches them (gather4, four
+// rows an instruction, a lane each).  That takes it 75 clocks an instruction,
+// which many positions cannot wait for (131,072 positions of 2,048: the product
+// 1,100 us); nor for copies by threads (cp.async: 18 bytes a clock and SM, 460
+// us).  There a pass of its own gathers the rows first (116 us of 463).
 //
 // Sums: the tensor cores accumulate in fp32 in tensor memory; every kSegment
 // k-blocks the consumer warps add what stands there to fp32 registers (rounded
@@ -26,6 +32,12 @@
 // accumulator, which does not round to nearest.  With 8-bit operands a segment
 // is one k-block of 128, and is multiplied by the product of its two scales on
 // the way; the scale warp forms those products for the tile's columns.
+//
+// Measured on GB300: 131,072 positions in 64 lists, 2,048 x 1,024 bf16: forward
+// 314 us (1,750 TFLOP/s; torch.bmm over equal lists 287-298), rows' gradient 327,
+// weights' 326 (fp32: 358).  32,768 in 8 lists, 4,096 x 4,096: 555 (1,980;
+// torch.bmm 525-537).  256 lists of 128 of 2,048 x 1,024: 201, bound by HBM (1.27
+// GB).  Sixteen points to 8 of 256 experts: 74 us for 428 MB, bound by HBM.
 //
 // Contraction over positions (weights' gradient): a k-block may end behind the
 // list's last position, or hold positions that lack a row.  Those rows must be
@@ -48,15 +60,13 @@ namespace kma {
 
 namespace {
 
-// A block: CW (8 or 16) warps of consumers, then one each for A, B, the MMAs
-// and the scales.  Registers a thread: the launch's (65,536 over the threads),
-// of which the last warpgroup gives up some for the consumers, who hold up to
-// 128 (8 warps) or 64 (16) sums.
-constexpr int threads_of(int CW) { return 32 * (CW + 4); }
-__host__ __device__ constexpr int consumer_regs(int CW) { return CW == 8 ? 208 : 104; }
-__host__ __device__ constexpr int other_regs(int CW) { return CW == 8 ? 80 : 64; }
-static_assert(2 * consumer_regs(8) + other_regs(8) <= 3 * 168, "the launch's registers");
-static_assert(4 * consumer_regs(16) + other_regs(16) <= 5 * 96, "the launch's registers");
+constexpr int kConsumers = 8;   // warps; then one each for A, B, the MMAs and the scales or fixes
+constexpr int kWarpA = 8, kWarpB = 9, kWarpMma = 10, kWarpScale = 11, kWarpFix = 11;
+constexpr int kThreads = 32 * 12;
+// Registers a thread: the two warpgroups of consumers hold up to 128 sums each,
+// the third gives up some of the launch's for them.
+constexpr int kConsumerRegs = 208, kOtherRegs = 80;
+static_assert(2 * kConsumerRegs + kOtherRegs <= 3 * 168, "the launch's registers");
 constexpr int kRowsA = 128;                        // rows of A a CTA holds
 constexpr uint32_t kPartA = kRowsA * 128;          // A's k-block in a CTA
 constexpr uint32_t kAtomBytes = 64 * 128;          // MN-major: 64 elements by 64 rows
@@ -64,6 +74,7 @@ constexpr uint32_t kAtomBytes = 64 * 128;          // MN-major: 64 elements by 6
 constexpr int kScaleStages = 2, kScaleGroup = 4;
 __host__ __device__ constexpr uint32_t scale_bytes(int NT) { return kScaleGroup * NT * 4u; }
 constexpr uint32_t kGroupBarrier = 1;              // named barriers of the consumers' groups
+constexpr uint32_t kStagingBytes = 8192;           // of a group, for its way to the output
 // 16-bit k-blocks between two additions to registers: 2,048 elements, or 512
 // positions of a weights' gradient in fp32.
 constexpr int kSegment = 32, kSegmentRows = 8;
@@ -95,8 +106,8 @@ __host__ __device__ inline Layout layout_of(int NT, int stages, int E, bool scal
 {
     Layout l;
     l.ring = 0;
-    l.staging = stages * stage_bytes(NT);         // shared by the groups of consumers
-    l.dst = l.staging + 16384u;           // [group][tile parity][columns]
+    l.staging = stages * stage_bytes(NT);
+    l.dst = l.staging + 2u * kStagingBytes;       // [group][tile parity][columns]
     l.scale = l.dst + 2u * NT * 4u;
     l.lists = l.scale + (scaled ? kScaleStages * scale_bytes(NT) : 0u);
     l.bars = (l.lists + 3u * static_cast<uint32_t>(E + 1) * 4u + 15u) / 16u * 16u;
@@ -204,6 +215,8 @@ __device__ __forceinline__ int32_t row_of(const RowMap &m, int32_t at, int32_t h
     return row < m.rows ? row : -1;
 }
 
+__device__ __forceinline__ void zero16(uint32_t addr) { st_shared_v4_u32(addr, 0, 0, 0, 0); }
+
 // Weights' gradient: whether a position adds nothing.
 __device__ __forceinline__ bool missing(const ExpertsParams &p, int32_t at, int32_t hi)
 {
@@ -235,8 +248,8 @@ struct Frags {
 __device__ __forceinline__ void store_matrices(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
                                                uint32_t d)
 {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
-                 "r"(a), "r"(b), "r"(c), "r"(d)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                 ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                  : "memory");
 }
 
@@ -253,23 +266,19 @@ __device__ __forceinline__ uint32_t pack_two(float a, float b)
 // rows of the output by way of shared memory, some columns at a time: a column's
 // 128 elements stand together there, their 16-byte pieces at piece ^ (column %
 // 8) so that no two lanes meet in a bank, and are stored as one run of 256 bytes
-// (fp32: 512).  BYTES of staging hold one buffer, or two that take turns where
-// both hold 8 columns.
+// (fp32: 512).  Two buffers of 4 KiB take turns.
 // `dst`: the output rows of the group's columns; -1: none, -2 - row: a row of
 // zeros.
-template <typename O, int COLS, int BYTES>
+template <typename O, int COLS>
 __device__ __forceinline__ void store_columns(const Frags<COLS> &sum, int cols, uint8_t *stage,
                                               const int32_t *dst, void *out, int32_t m,
                                               int32_t mdim, int group, int thread)
 {
     constexpr int kColBytes = 128 * sizeof(O);
-    constexpr int kBuffers = BYTES >= 2 * 8 * kColBytes ? 2 : 1;
-    constexpr int kCols = BYTES / kBuffers / kColBytes < COLS ? BYTES / kBuffers / kColBytes : COLS;
+    constexpr int kCols = kStagingBytes / 2 / kColBytes;
     constexpr int kLanes = kColBytes / 16;           // threads to a column
     constexpr int kPerThread = 16 / sizeof(O);
     static_assert(kCols % 8 == 0 && COLS % kCols == 0, "whole matrices");
-    // columns come in multiples of 32: the next tile starts with the other buffer
-    static_assert(kBuffers == 1 || 32 % (2 * kCols) == 0, "an even number of turns");
     const int piece = thread % kLanes;
     const int lane = thread & 31, q = thread >> 5;
     const bool inside = m + piece * kPerThread < mdim;
@@ -277,9 +286,7 @@ __device__ __forceinline__ void store_columns(const Frags<COLS> &sum, int cols, 
 #pragma unroll
     for (int c = 0; c < COLS; c += kCols) {
         if (c < cols) {
-            uint8_t *const buf = stage + (c / kCols % kBuffers) * (BYTES / kBuffers);
-            if (kBuffers == 1)
-                named_bar_sync(kGroupBarrier + group, 128);
+            uint8_t *const buf = stage + (c / kCols & 1) * (kStagingBytes / 2);
 #pragma unroll
             for (int j = 0; j < kCols / 8; ++j) {
                 const float(&v)[2][4] = sum.v[c / 8 + j];
@@ -319,8 +326,8 @@ __device__ __forceinline__ void store_columns(const Frags<COLS> &sum, int cols, 
 
 // Zeros in the rows of no list, before the first and behind the last: one of
 // `of` warps' share.
-__device__ __forceinline__ void zero_rows(const ExpertsParams &p, const int32_t *lists, int64_t warp,
-                                          int64_t of, int lane)
+__device__ __forceinline__ void zero_rows(const ExpertsParams &p, const int32_t *lists,
+                                          int64_t warp, int64_t of, int lane)
 {
     const int32_t lo = lists[0], hi = lists[p.E + 1 + p.E - 1];
     const int32_t rest = p.M - (hi - lo);
@@ -333,25 +340,19 @@ __device__ __forceinline__ void zero_rows(const ExpertsParams &p, const int32_t 
     }
 }
 
-template <ExpertsKind KIND, bool E8, int NT, int CW>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
+template <ExpertsKind KIND, bool E8, int NT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     experts_kernel(const __grid_constant__ CUtensorMap amap,
                    const __grid_constant__ CUtensorMap bmap, const ExpertsParams p)
 {
     constexpr bool kAMn = KIND != kForward;         // A is MN-major
     constexpr bool kBMn = KIND == kWeightsGrad;
-    constexpr bool kFixes = KIND == kWeightsGrad;   // loaders zero missing rows
+    constexpr bool kFixes = KIND == kWeightsGrad;   // missing rows are zeroed
     const int kSeg = E8 ? 1 : p.segment;            // k-blocks between additions
     constexpr int kElems = E8 ? 128 : 64;           // elements of a k-block
     constexpr bool kGathers = KIND == kForward && NT == 64;
     constexpr uint32_t kStageBytes = stage_bytes(NT);
-    constexpr int kWarpA = CW, kWarpB = CW + 1, kWarpMma = CW + 2, kWarpScale = CW + 3;
-    // 8 bits: every k-block is a segment with an accumulator to hand over, which
-    // takes the issuing warp about as long again as its MMAs take.  So two warps
-    // issue, one for each accumulator, and one loader brings both operands.
-    constexpr bool kTwo = E8 && NT == 256;
-    constexpr int kGroupCols = NT / (CW / 4);       // columns of a group of consumers
-    constexpr uint32_t kStagingBytes = 16384 / (CW / 4);   // of a group
+    constexpr int kGroupCols = NT / 2;              // columns of a group of consumers
     constexpr uint32_t kTmemColumns = 2 * NT;       // two accumulators
     constexpr uint16_t kBoth = 0x3;
 
@@ -366,6 +367,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
     volatile uint32_t *abort_flag = tmem_slot + 1;
     auto bar = [&](int i) -> uint32_t { return base + lay.bars + 8u * static_cast<uint32_t>(i); };
     auto lead_bar = [&](int i) -> uint32_t { return map_to_rank(bar(i), 0); };
+    // Bounded waits on barrier i, of a warp and of one thread.
+    auto wait = [&](int i, uint32_t parity) {
+        return wait_warp(bar(i), parity, abort_flag, p.timeout_ns);
+    };
+    auto wait_one = [&](int i, uint32_t parity) {
+        return wait1(bar(i), parity, abort_flag, p.timeout_ns);
+    };
     auto part_a = [&](uint32_t stage) { return base + stage * kStageBytes; };
     auto part_b = [&](uint32_t stage) { return base + stage * kStageBytes + kPartA; };
 
@@ -378,19 +386,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxRing; ++s) {
             // the leader's loaders; both CTAs' where rows may be missing
-            mbar_init(bar(kFull + s), kFixes ? 4 : kTwo ? 1 : 2);
+            mbar_init(bar(kFull + s), kFixes ? 4 : 2);
             mbar_init(bar(kEmpty + s), 1);
             mbar_init(bar(kFixA + s), 1);
             mbar_init(bar(kFixB + s), 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(bar(kAccF + a), 1);
-            mbar_init(bar(kAccE + a), 2 * CW);
-            mbar_init(bar(kLast + a), 1);
+            mbar_init(bar(kAccE + a), 2 * kConsumers);
         }
+        mbar_init(bar(kLast), 1);
         for (int s = 0; s < kScaleStages; ++s) {
             mbar_init(bar(kScF + s), 1);
-            mbar_init(bar(kScE + s), CW);
+            mbar_init(bar(kScE + s), kConsumers);
         }
         *abort_flag = 0u;
         fence_mbar_init();
@@ -420,274 +428,258 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
         }
     };
 
-    if (warp >= CW) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(CW)));
-    if ((warp == kWarpA && !kTwo) || warp == kWarpB) {
-        const bool is_a = warp == kWarpA;
-        uint32_t stage = 0, phase = 0;
-        bool ok = true;
-        auto next_stage = [&]() {
-            if (++stage == stages) {
-                stage = 0;
-                phase ^= 1u;
-            }
-        };
-        if constexpr (kFixes) {
-            // Rows of positions, 64 to a k-block, as atoms of 64 columns.
-            const void *tmap = is_a ? &amap : &bmap;
-            const bool holes = p.holes != nullptr && *p.holes != 0;
-            for (int t = first; ok && t < plan.total; t += step) {
-                const Tile w = plan.tile(t);
-                const int atoms = is_a ? 2 : w.n / 128;
-                const int x = (is_a ? w.m0 : w.n0) + static_cast<int>(rank) * 64 * atoms;
-                const uint32_t bytes = atoms * kAtomBytes;
-                for (int kb = 0; ok && kb < w.kblocks; ++kb, next_stage()) {
-                    const int at = w.lo + kb * 64;
-                    const bool fix = at + 64 > w.hi || holes;
-                    if (!(ok = wait_warp(bar(kEmpty + stage), phase ^ 1u, abort_flag, p.timeout_ns)))
-                        break;
-                    const uint32_t dst = is_a ? part_a(stage) : part_b(stage);
-                    const uint32_t full = lead_bar(kFull + stage);
-                    const uint32_t own = bar((is_a ? kFixA : kFixB) + stage);
-                    if (lane == 0) {
-                        if (fix)   // the fixing warp goes on from here
-                            mbar_arrive_expect_tx(own, bytes);
-                        else if (leader)
-                            mbar_arrive_expect_tx(bar(kFull + stage), 2 * bytes);
-                        else
-                            mbar_arrive_cluster(full);
-                        const uint32_t done = fix ? map_to_rank(own, rank) : full;
-                        for (int a = 0; a < atoms; ++a)
-                            tma_load_2d_pair(dst + a * kAtomBytes, tmap, done, x + 64 * a, at);
-                    }
-                    __syncwarp();
-                }
-            }
-        } else if (is_a) {
-            // The weights of the tile's 128 rows of this CTA.
-            if (lane == 0) {
-                tma_prefetch_desc(&amap);
-                for (int t = first; ok && t < plan.total; t += step) {
-                    const Tile w = plan.tile(t);
-                    const int m = w.m0 + static_cast<int>(rank) * kRowsA;
-                    for (int kb = 0; kb < w.kblocks; ++kb, next_stage()) {
-                        if (!(ok = wait1(bar(kEmpty + stage), phase ^ 1u, abort_flag, p.timeout_ns)))
-                            break;
-                        if (leader)
-                            mbar_arrive_expect_tx(bar(kFull + stage), 2 * kPartA);
-                        const uint32_t full = lead_bar(kFull + stage);
-                        if (kAMn) {
-                            tma_load_3d_pair(part_a(stage), &amap, full, m, kb * 64, w.e);
-                            tma_load_3d_pair(part_a(stage) + kAtomBytes, &amap, full, m + 64,
-                                             kb * 64, w.e);
-                        } else {
-                            tma_load_3d_pair(part_a(stage), &amap, full, kb * kElems, m, w.e);
-                        }
-                    }
-                }
-            }
-        } else {
-            // The positions' rows: this CTA's half of the tile's columns.
-            if (lane == 0)
-                tma_prefetch_desc(&bmap);
-            for (int t = first; ok && t < plan.total; t += step) {
-                const Tile w = plan.tile(t);
-                const int half = w.n / 2;
-                const int at = w.n0 + static_cast<int>(rank) * half;
-                const int boxes = (half + 31) / 32;
-                const uint32_t bytes = gathers ? half * 128 : boxes * 4096;
-                int32_t row[4];
-                if (kGathers) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)   // none: any row, the column is zero or not stored
-                        row[i] = gathers ? max(row_of(p.b_rows, at + 4 * lane + i, w.hi), 0) : 0;
-                }
-                for (int kb = 0; kb < w.kblocks; ++kb, next_stage()) {
-                    if (!(ok = wait_warp(bar(kEmpty + stage), phase ^ 1u, abort_flag, p.timeout_ns)))
-                        break;
-                    if (leader && lane == 0)
-                        mbar_arrive_expect_tx(bar(kFull + stage),
-                                              2 * (bytes + (kTwo ? kPartA : 0)));
-                    const uint32_t full = lead_bar(kFull + stage);
-                    if (kTwo && lane == 31)
-                        tma_load_3d_pair(part_a(stage), &amap, full, kb * kElems,
-                                         w.m0 + static_cast<int>(rank) * kRowsA, w.e);
-                    if (gathers) {
-                        if (4 * lane < half)
-                            tma_gather4_pair(part_b(stage) + 512 * lane, &bmap, full, kb * kElems,
-                                             row);
-                    } else if (lane < boxes) {
-                        tma_load_2d_pair(part_b(stage) + 4096 * lane, &bmap, full, kb * kElems,
-                                         at + 32 * lane);
-                    }
-                }
-            }
-        }
-        if (!ok && lane == 0)
-            let_copies_land();
-        __syncwarp();
-    } else if (warp == kWarpMma || (warp == kWarpA && kTwo)) {
-        if (leader) {
-            const uint32_t me = kTwo && warp == kWarpA;
-            uint32_t stage = 0, phase = 0, acc = 0;
-            bool ok = true, issued = false;
+    if (warp >= kConsumers) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kWarpA || warp == kWarpB) {
+            const bool is_a = warp == kWarpA;
+            uint32_t stage = 0, phase = 0;
+            bool ok = true;
             auto next_stage = [&]() {
                 if (++stage == stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
             };
-            for (int t = first; ok && t < plan.total; t += step) {
-                const Tile w = plan.tile(t);
-                const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
-                for (int k0 = 0; ok && k0 < w.kblocks; k0 += kSeg, ++acc) {
-                    const uint32_t as = acc & 1u;
-                    if (kTwo && as != me) {
-                        next_stage();
-                        continue;
-                    }
-                    if (!(ok = wait_warp(bar(kAccE + as), ((acc >> 1) & 1u) ^ 1u, abort_flag,
-                                         p.timeout_ns)))
-                        break;
-                    tc_fence_after();
-                    const uint32_t d = tmem_base + as * NT;
-                    const int k1 = min(k0 + kSeg, w.kblocks);
-                    for (int kb = k0; kb < k1; ++kb, next_stage()) {
-                        if (!(ok = wait_operands(bar(kFull + stage), phase, kFixes, abort_flag,
-                                                 p.timeout_ns)))
+            if constexpr (kFixes) {
+                // Rows of positions, 64 to a k-block, as atoms of 64 columns.
+                const void *tmap = is_a ? &amap : &bmap;
+                const bool holes = p.holes != nullptr && *p.holes != 0;
+                for (int t = first; ok && t < plan.total; t += step) {
+                    const Tile w = plan.tile(t);
+                    const int atoms = is_a ? 2 : w.n / 128;
+                    const int x = (is_a ? w.m0 : w.n0) + static_cast<int>(rank) * 64 * atoms;
+                    const uint32_t bytes = atoms * kAtomBytes;
+                    for (int kb = 0; ok && kb < w.kblocks; ++kb, next_stage()) {
+                        const int at = w.lo + kb * 64;
+                        const bool fix = at + 64 > w.hi || holes;
+                        if (!(ok = wait(kEmpty + stage, phase ^ 1u)))
                             break;
-                        const uint64_t a = kAMn ? sw128_mnmajor_desc(part_a(stage), kAtomBytes)
-                                                : sw128_kmajor_desc(part_a(stage));
-                        const uint64_t b = kBMn ? sw128_mnmajor_desc(part_b(stage), kAtomBytes)
-                                                : sw128_kmajor_desc(part_b(stage));
-                        // 32 bytes of K, or 16 rows of it, an MMA
-                        constexpr uint32_t kStepA = kAMn ? 128u : 2u, kStepB = kBMn ? 128u : 2u;
-                        if (elect_one()) {
-#pragma unroll
-                            for (uint32_t k = 0; k < 4; ++k) {
-                                const uint32_t add = kb != k0 || k != 0;
-                                if (E8)
-                                    mma_f8_pair(d, a + kStepA * k, b + kStepB * k, idesc, add);
-                                else
-                                    mma_bf16_pair(d, a + kStepA * k, b + kStepB * k, idesc, add);
-                            }
-                            mma_commit_pair(bar(kEmpty + stage), kBoth);
-                            if (kb == k1 - 1)
-                                mma_commit_pair(bar(kAccF + as), kBoth);
+                        const uint32_t dst = is_a ? part_a(stage) : part_b(stage);
+                        const uint32_t full = lead_bar(kFull + stage);
+                        const uint32_t own = bar((is_a ? kFixA : kFixB) + stage);
+                        if (lane == 0) {
+                            if (fix)   // the fixing warp goes on from here
+                                mbar_arrive_expect_tx(own, bytes);
+                            else if (leader)
+                                mbar_arrive_expect_tx(bar(kFull + stage), 2 * bytes);
+                            else
+                                mbar_arrive_cluster(full);
+                            const uint32_t done = fix ? map_to_rank(own, rank) : full;
+                            for (int a = 0; a < atoms; ++a)
+                                tma_load_2d_pair(dst + a * kAtomBytes, tmap, done, x + 64 * a, at);
                         }
                         __syncwarp();
-                        issued = true;
                     }
                 }
-            }
-            if (issued) {
-                if (elect_one())
-                    mma_commit_pair(bar(kLast + me), 0x1);
-                __syncwarp();
-                wait_warp(bar(kLast + me), 0u, abort_flag, kDrainLimitNs, false);
-            }
-        }
-    } else if (warp == kWarpScale) {
-        if constexpr (kFixes) {
-            // K-blocks with missing rows: once both operands have landed here the
-            // rows are zeroed and the pair's barrier gets both loaders' arrivals.
-            // (The loaders themselves go on: waiting for such a block, the last of
-            // most tiles, they fell behind by 1.5 us a tile.)
-            const bool holes = p.holes != nullptr && *p.holes != 0;
-            uint32_t stage = 0, used = 0;   // bit s: parity of stage s's next such block
-            bool ok = true;
-            for (int t = first; ok && t < plan.total; t += step) {
-                const Tile w = plan.tile(t);
-                const int atoms_b = w.n / 128;
-                for (int kb = 0; kb < w.kblocks; ++kb) {
-                    const int at = w.lo + kb * 64;
-                    if (at + 64 > w.hi || holes) {
-                        if (!(ok = wait_warp(bar(kFixA + stage), used >> stage & 1u, abort_flag,
-                                             p.timeout_ns) &&
-                                   wait_warp(bar(kFixB + stage), used >> stage & 1u, abort_flag,
-                                             p.timeout_ns)))
-                            break;
-                        used ^= 1u << stage;
-                        // lane l: whether positions l and 32 + l are missing
-                        const uint32_t gone[2] = {
-                            __ballot_sync(0xffffffffu, missing(p, at + lane, w.hi)),
-                            __ballot_sync(0xffffffffu, missing(p, at + 32 + lane, w.hi))};
-                        // whole rows: the swizzle moves 16-byte pieces within a row
-                        for (int i = lane; i < 64 * 8; i += 32)
-                            if (gone[i >> 8] >> (i >> 3 & 31) & 1u) {
-                                for (int a = 0; a < 2; ++a)
-                                    st_shared_v4_u32(part_a(stage) + a * kAtomBytes + 16 * i, 0, 0,
-                                                     0, 0);
-                                for (int a = 0; a < atoms_b; ++a)
-                                    st_shared_v4_u32(part_b(stage) + a * kAtomBytes + 16 * i, 0, 0,
-                                                     0, 0);
+            } else if (is_a) {
+                // The weights of the tile's 128 rows of this CTA.
+                if (lane == 0) {
+                    tma_prefetch_desc(&amap);
+                    for (int t = first; ok && t < plan.total; t += step) {
+                        const Tile w = plan.tile(t);
+                        const int m = w.m0 + static_cast<int>(rank) * kRowsA;
+                        for (int kb = 0; kb < w.kblocks; ++kb, next_stage()) {
+                            if (!(ok = wait_one(kEmpty + stage, phase ^ 1u)))
+                                break;
+                            if (leader)
+                                mbar_arrive_expect_tx(bar(kFull + stage), 2 * kPartA);
+                            const uint32_t full = lead_bar(kFull + stage);
+                            if (kAMn) {
+                                tma_load_3d_pair(part_a(stage), &amap, full, m, kb * 64, w.e);
+                                tma_load_3d_pair(part_a(stage) + kAtomBytes, &amap, full, m + 64,
+                                                 kb * 64, w.e);
+                            } else {
+                                tma_load_3d_pair(part_a(stage), &amap, full, kb * kElems, m, w.e);
                             }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane < 2)
-                            mbar_arrive_release_cluster(lead_bar(kFull + stage));
+                        }
                     }
-                    if (++stage == stages)
+                }
+            } else {
+                // The positions' rows: this CTA's half of the tile's columns.
+                if (lane == 0)
+                    tma_prefetch_desc(&bmap);
+                for (int t = first; ok && t < plan.total; t += step) {
+                    const Tile w = plan.tile(t);
+                    const int half = w.n / 2;
+                    const int at = w.n0 + static_cast<int>(rank) * half;
+                    const int boxes = (half + 31) / 32;
+                    const uint32_t bytes = gathers ? half * 128 : boxes * 4096;
+                    int32_t row[4];
+                    if (kGathers) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)   // none: any row, the column is not used
+                            row[i] = !gathers ? 0
+                                              : max(row_of(p.b_rows, at + 4 * lane + i, w.hi), 0);
+                    }
+                    for (int kb = 0; kb < w.kblocks; ++kb, next_stage()) {
+                        if (!(ok = wait(kEmpty + stage, phase ^ 1u)))
+                            break;
+                        if (leader && lane == 0)
+                            mbar_arrive_expect_tx(bar(kFull + stage), 2 * bytes);
+                        const uint32_t full = lead_bar(kFull + stage);
+                        if (gathers) {
+                            if (4 * lane < half)
+                                tma_gather4_pair(part_b(stage) + 512 * lane, &bmap, full,
+                                                 kb * kElems, row);
+                        } else if (lane < boxes) {
+                            tma_load_2d_pair(part_b(stage) + 4096 * lane, &bmap, full, kb * kElems,
+                                             at + 32 * lane);
+                        }
+                    }
+                }
+            }
+            if (!ok && lane == 0)
+                let_copies_land();
+            __syncwarp();
+        } else if (warp == kWarpMma) {
+            if (leader) {
+                uint32_t stage = 0, phase = 0, acc = 0;
+                bool ok = true, issued = false;
+                auto next_stage = [&]() {
+                    if (++stage == stages) {
                         stage = 0;
-                }
-            }
-        }
-        if constexpr (E8) {
-            // For each k-block the products of the columns' scales and the
-            // scale of this CTA's 128 rows of weights.
-            uint32_t n = 0;
-            bool ok = true;
-            for (int t = first; ok && t < plan.total; t += step) {
-                const Tile w = plan.tile(t);
-                const int fb = min((w.m0 >> 7) + static_cast<int>(rank), p.fblocks - 1);
-                const float *ws =
-                    p.wscale + (static_cast<int64_t>(w.e) * p.fblocks + fb) * w.kblocks;
-                constexpr int kPer = NT / 32;   // columns a lane
-                int32_t row[kPer];
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    row[i] = NT == 256 ? min(w.n0 + 32 * i + lane, p.M - 1)
-                                       : max(row_of(p.from, w.n0 + 32 * i + lane, w.hi), 0);
-                for (int k0 = 0; k0 < w.kblocks; k0 += kScaleGroup, ++n) {
-                    const uint32_t s = n % kScaleStages;
-                    float *const to = reinterpret_cast<float *>(sbase + lay.scale +
-                                                                s * scale_bytes(NT));
-                    float v[kScaleGroup][kPer], one[kScaleGroup];
-#pragma unroll
-                    for (int j = 0; j < kScaleGroup; ++j) {
-                        const int kb = min(k0 + j, w.kblocks - 1);
-                        one[j] = __ldg(ws + kb);
-#pragma unroll
-                        for (int i = 0; i < kPer; ++i)
-                            v[j][i] = __ldg(
-                                p.xscale +
-                                (NT == 256 ? static_cast<int64_t>(kb) * p.M + row[i]
-                                           : static_cast<int64_t>(row[i]) * w.kblocks + kb));
+                        phase ^= 1u;
                     }
-                    if (!(ok = wait_warp(bar(kScE + s), ((n / kScaleStages) & 1u) ^ 1u, abort_flag,
-                                         p.timeout_ns)))
-                        break;
+                };
+                for (int t = first; ok && t < plan.total; t += step) {
+                    const Tile w = plan.tile(t);
+                    const uint32_t idesc = p.idesc | static_cast<uint32_t>(w.n >> 3) << 17;
+                    for (int k0 = 0; ok && k0 < w.kblocks; k0 += kSeg, ++acc) {
+                        const uint32_t as = acc & 1u;
+                        if (!(ok = wait(kAccE + as, ((acc >> 1) & 1u) ^ 1u)))
+                            break;
+                        tc_fence_after();
+                        const uint32_t d = tmem_base + as * NT;
+                        const int k1 = min(k0 + kSeg, w.kblocks);
+                        for (int kb = k0; kb < k1; ++kb, next_stage()) {
+                            if (!(ok = wait_operands(bar(kFull + stage), phase, kFixes, abort_flag,
+                                                     p.timeout_ns)))
+                                break;
+                            const uint64_t a = kAMn ? sw128_mnmajor_desc(part_a(stage), kAtomBytes)
+                                                    : sw128_kmajor_desc(part_a(stage));
+                            const uint64_t b = kBMn ? sw128_mnmajor_desc(part_b(stage), kAtomBytes)
+                                                    : sw128_kmajor_desc(part_b(stage));
+                            // 32 bytes of K, or 16 rows of it, an MMA
+                            constexpr uint32_t kStepA = kAMn ? 128u : 2u, kStepB = kBMn ? 128u : 2u;
+                            if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < kScaleGroup; ++j)
-#pragma unroll
-                        for (int i = 0; i < kPer; ++i)
-                            to[j * NT + 32 * i + lane] = v[j][i] * one[j];
+                                for (uint32_t k = 0; k < 4; ++k) {
+                                    const uint32_t add = kb != k0 || k != 0;
+                                    if (E8)
+                                        mma_f8_pair(d, a + kStepA * k, b + kStepB * k, idesc, add);
+                                    else
+                                        mma_bf16_pair(d, a + kStepA * k, b + kStepB * k, idesc,
+                                                      add);
+                                }
+                                mma_commit_pair(bar(kEmpty + stage), kBoth);
+                                if (kb == k1 - 1)
+                                    mma_commit_pair(bar(kAccF + as), kBoth);
+                            }
+                            __syncwarp();
+                            issued = true;
+                        }
+                    }
+                }
+                if (issued) {
+                    if (elect_one())
+                        mma_commit_pair(bar(kLast), 0x1);
                     __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(bar(kScF + s));
+                    wait_warp(bar(kLast), 0u, abort_flag, kDrainLimitNs, false);
+                }
+            }
+        } else {   // kWarpScale, kWarpFix
+            if constexpr (kFixes) {
+                // K-blocks with missing rows: once both operands have landed here the
+                // rows are zeroed and the pair's barrier gets both loaders' arrivals.
+                // (The loaders themselves go on: waiting for such a block, the last of
+                // most tiles, they fell behind by 1.5 us a tile.)
+                const bool holes = p.holes != nullptr && *p.holes != 0;
+                uint32_t stage = 0, used = 0;   // bit s: parity of stage s's next such block
+                bool ok = true;
+                for (int t = first; ok && t < plan.total; t += step) {
+                    const Tile w = plan.tile(t);
+                    const int atoms_b = w.n / 128;
+                    for (int kb = 0; kb < w.kblocks; ++kb) {
+                        const int at = w.lo + kb * 64;
+                        if (at + 64 > w.hi || holes) {
+                            if (!(ok = wait(kFixA + stage, used >> stage & 1u) &&
+                                       wait(kFixB + stage, used >> stage & 1u)))
+                                break;
+                            used ^= 1u << stage;
+                            // lane l: whether positions l and 32 + l are missing
+                            const uint32_t gone[2] = {
+                                __ballot_sync(0xffffffffu, missing(p, at + lane, w.hi)),
+                                __ballot_sync(0xffffffffu, missing(p, at + 32 + lane, w.hi))};
+                            // whole rows: the swizzle moves 16-byte pieces within a row
+                            for (int i = lane; i < 64 * 8; i += 32)
+                                if (gone[i >> 8] >> (i >> 3 & 31) & 1u) {
+                                    for (int a = 0; a < 2; ++a)
+                                        zero16(part_a(stage) + a * kAtomBytes + 16 * i);
+                                    for (int a = 0; a < atoms_b; ++a)
+                                        zero16(part_b(stage) + a * kAtomBytes + 16 * i);
+                                }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane < 2)
+                                mbar_arrive_release_cluster(lead_bar(kFull + stage));
+                        }
+                        if (++stage == stages)
+                            stage = 0;
+                    }
+                }
+            }
+            if constexpr (E8) {
+                // For each k-block the products of the columns' scales and the
+                // scale of this CTA's 128 rows of weights.
+                uint32_t n = 0;
+                bool ok = true;
+                for (int t = first; ok && t < plan.total; t += step) {
+                    const Tile w = plan.tile(t);
+                    const int fb = min((w.m0 >> 7) + static_cast<int>(rank), p.fblocks - 1);
+                    const float *ws =
+                        p.wscale + (static_cast<int64_t>(w.e) * p.fblocks + fb) * w.kblocks;
+                    constexpr int kPer = NT / 32;   // columns a lane
+                    int32_t row[kPer];
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i)
+                        row[i] = max(row_of(p.from, w.n0 + 32 * i + lane, w.hi), 0);
+                    for (int k0 = 0; k0 < w.kblocks; k0 += kScaleGroup, ++n) {
+                        const uint32_t s = n % kScaleStages;
+                        float *const to = reinterpret_cast<float *>(sbase + lay.scale +
+                                                                    s * scale_bytes(NT));
+                        float v[kScaleGroup][kPer], one[kScaleGroup];
+#pragma unroll
+                        for (int j = 0; j < kScaleGroup; ++j) {
+                            const int kb = min(k0 + j, w.kblocks - 1);
+                            one[j] = __ldg(ws + kb);
+#pragma unroll
+                            for (int i = 0; i < kPer; ++i)
+                                v[j][i] =
+                                    __ldg(p.xscale + static_cast<int64_t>(row[i]) * w.kblocks + kb);
+                        }
+                        if (!(ok = wait(kScE + s, ((n / kScaleStages) & 1u) ^ 1u)))
+                            break;
+#pragma unroll
+                        for (int j = 0; j < kScaleGroup; ++j)
+#pragma unroll
+                            for (int i = 0; i < kPer; ++i)
+                                to[j * NT + 32 * i + lane] = v[j][i] * one[j];
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(bar(kScF + s));
+                    }
                 }
             }
         }
-    }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(consumer_regs(CW)));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
         // Consumers: warp q of four holds 32 of the CTA's 128 rows, the two
         // groups of four the lower and the upper half of the columns.
         const int q = warp & 3, group = warp >> 2;
         const int c0 = group * kGroupCols;
         const uint32_t tmem_warp = tmem_base + (static_cast<uint32_t>(q) << 21) + c0;
         if (p.zero_rest)
-            zero_rows(p, lists, blockIdx.x * CW + warp, gridDim.x * CW, lane);
+            zero_rows(p, lists, blockIdx.x * kConsumers + warp, gridDim.x * kConsumers, lane);
         const int thread = threadIdx.x & 127;
         uint8_t *const staging = sbase + lay.staging + group * kStagingBytes;
         int32_t *const dsts = reinterpret_cast<int32_t *>(sbase + lay.dst) + group * 2 * kGroupCols;
@@ -718,14 +710,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
                 const uint32_t as = acc & 1u;
                 const uint32_t s = n % kScaleStages;
                 if (E8 && k0 % kScaleGroup == 0 &&
-                    !(ok = wait_warp(bar(kScF + s), (n / kScaleStages) & 1u, abort_flag,
-                                     p.timeout_ns)))
+                    !(ok = wait(kScF + s, (n / kScaleStages) & 1u)))
                     break;
                 const float *const scales =
                     reinterpret_cast<const float *>(sbase + lay.scale + s * scale_bytes(NT)) +
                     k0 % kScaleGroup * NT;
                 const bool last = k0 % kScaleGroup == kScaleGroup - 1 || k0 == w.kblocks - 1;
-                if (!(ok = wait_warp(bar(kAccF + as), (acc >> 1) & 1u, abort_flag, p.timeout_ns)))
+                if (!(ok = wait(kAccF + as, (acc >> 1) & 1u)))
                     break;
                 tc_fence_after();
 #pragma unroll
@@ -769,14 +760,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
                 break;
             const int32_t m = w.m0 + static_cast<int>(rank) * kRowsA;
             if (p.out_type == kBf16)
-                store_columns<__nv_bfloat16, kGroupCols, kStagingBytes>(sum, cols, staging, dst, p.out, m,
-                                              p.mdim, group, thread);
+                store_columns<__nv_bfloat16, kGroupCols>(sum, cols, staging, dst, p.out, m, p.mdim,
+                                                         group, thread);
             else if (p.out_type == kFp16)
-                store_columns<__half, kGroupCols, kStagingBytes>(sum, cols, staging, dst, p.out, m,
-                                              p.mdim, group, thread);
+                store_columns<__half, kGroupCols>(sum, cols, staging, dst, p.out, m, p.mdim,
+                                                  group, thread);
             else
-                store_columns<float, kGroupCols, kStagingBytes>(sum, cols, staging, dst, p.out, m,
-                                              p.mdim, group, thread);
+                store_columns<float, kGroupCols>(sum, cols, staging, dst, p.out, m, p.mdim,
+                                                 group, thread);
         }
     }
 
@@ -795,9 +786,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(CW), 1)
 // the output (256).  A thread of the consumers then holds one position's row, so
 // that a segment's scale is one number a thread, which it loads itself: the sums
 // cost one FMA an element and nothing else.  (With positions as columns each
-// element needs its column's scale out of shared memory; 32,768 x 4,096 x 4,096 in
-// 8 lists took XX us there.)  Lists are rounded up to 256 for it, so only products
-// of many positions an expert come here.
+// element needs its column's scale out of shared memory, and the rest of a
+// segment's hand-over does not hide that: 32,768 positions in 8 lists, 4,096 x
+// 4,096, took 700 us, here 518, 2,120 TFLOP/s.)  What bounds it is the hand-over
+// of two accumulators for each 128 of the contraction: 1,140 clocks a k-block
+// whose MMAs take 512.  More and smaller accumulators (four of 128 columns, 1,050
+// us), half-tiles with barriers of their own and longer waits between polls were
+// no faster.  Lists are rounded up to 256, so only products of many positions an
+// expert come here.
 
 constexpr int kLoad8 = 8, kIssue8 = 9;   // warps behind the 8 of consumers; two issue
 
@@ -808,12 +804,13 @@ struct Tile8 {
 struct Layout8 {
     uint32_t staging, lists, bars, end;
 };
+constexpr uint32_t kWarpStaging = 2048;   // 64 bytes of a warp's 32 rows
 
 __host__ __device__ inline Layout8 layout8_of(int stages, int E)
 {
     Layout8 l;
-    l.staging = stages * stage_bytes(256);   // 2 KiB a warp of consumers
-    l.lists = l.staging + 16384u;
+    l.staging = stages * stage_bytes(256);
+    l.lists = l.staging + kConsumers * kWarpStaging;
     l.bars = (l.lists + 3u * static_cast<uint32_t>(E + 1) * 4u + 15u) / 16u * 16u;
     l.end = l.bars + kBars * 8u + 16u;
     return l;
@@ -842,7 +839,8 @@ __device__ __forceinline__ void store_rows(uint8_t *stage, const uint4 (&v)[4], 
 
 template <typename O>
 __device__ __forceinline__ void store_sums(const float (&sum)[128], uint8_t *stage, void *out,
-                                           int32_t mdim, int32_t f, int32_t dst, bool zero, int lane)
+                                           int32_t mdim, int32_t f, int32_t dst, bool zero,
+                                           int lane)
 {
     constexpr int kCols = 64 / sizeof(O);
     const int64_t pitch = static_cast<int64_t>(mdim) * sizeof(O);
@@ -859,9 +857,9 @@ __device__ __forceinline__ void store_sums(const float (&sum)[128], uint8_t *sta
         } else {
 #pragma unroll
             for (int p = 0; p < 4; ++p)
-                v[p] = make_uint4(__float_as_uint(sum[c + 4 * p]), __float_as_uint(sum[c + 4 * p + 1]),
-                                  __float_as_uint(sum[c + 4 * p + 2]),
-                                  __float_as_uint(sum[c + 4 * p + 3]));
+                v[p] = make_uint4(
+                    __float_as_uint(sum[c + 4 * p]), __float_as_uint(sum[c + 4 * p + 1]),
+                    __float_as_uint(sum[c + 4 * p + 2]), __float_as_uint(sum[c + 4 * p + 3]));
         }
         if (zero) {
 #pragma unroll
@@ -876,7 +874,7 @@ __device__ __forceinline__ void store_sums(const float (&sum)[128], uint8_t *sta
     }
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     experts8_kernel(const __grid_constant__ CUtensorMap amap,
                     const __grid_constant__ CUtensorMap bmap, const ExpertsParams p)
 {
@@ -894,6 +892,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     volatile uint32_t *abort_flag = tmem_slot + 1;
     auto bar = [&](int i) -> uint32_t { return base + lay.bars + 8u * static_cast<uint32_t>(i); };
     auto lead_bar = [&](int i) -> uint32_t { return map_to_rank(bar(i), 0); };
+    // Bounded waits on barrier i, of a warp and of one thread.
+    auto wait = [&](int i, uint32_t parity) {
+        return wait_warp(bar(i), parity, abort_flag, p.timeout_ns);
+    };
+    auto wait_one = [&](int i, uint32_t parity) {
+        return wait1(bar(i), parity, abort_flag, p.timeout_ns);
+    };
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -907,7 +912,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(bar(kAccF + a), 1);
-            mbar_init(bar(kAccE + a), 2 * 8);
+            mbar_init(bar(kAccE + a), 2 * kConsumers);
             mbar_init(bar(kLast + a), 1);
         }
         *abort_flag = 0u;
@@ -953,7 +958,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     };
 
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(8)));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         uint32_t stage = 0, phase = 0;
         bool ok = true;
         auto next_stage = [&]() {
@@ -971,7 +976,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
                     const int m = w.m0 + static_cast<int>(rank) * kRowsA;
                     const int n = w.n0 + static_cast<int>(rank) * (w.n / 2);
                     for (int kb = 0; kb < p.kblocks; ++kb, next_stage()) {
-                        if (!(ok = wait1(bar(kEmpty + stage), phase ^ 1u, abort_flag, p.timeout_ns)))
+                        if (!(ok = wait_one(kEmpty + stage, phase ^ 1u)))
                             break;
                         if (leader)
                             mbar_arrive_expect_tx(bar(kFull + stage), 2 * kStageBytes);
@@ -999,9 +1004,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
                 for (int kb = 0; kb < p.kblocks; ++kb, ++acc, next_stage()) {
                     if ((acc & 1u) != me)
                         continue;
-                    if (!(ok = wait_warp(bar(kAccE + me), ((acc >> 1) & 1u) ^ 1u, abort_flag,
-                                         p.timeout_ns) &&
-                               wait_warp(bar(kFull + stage), phase, abort_flag, p.timeout_ns)))
+                    if (!(ok = wait(kAccE + me, ((acc >> 1) & 1u) ^ 1u) &&
+                               wait(kFull + stage, phase)))
                         break;
                     tc_fence_after();
                     const uint64_t a = sw128_kmajor_desc(base + stage * kStageBytes);
@@ -1009,7 +1013,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
                     if (elect_one()) {
 #pragma unroll
                         for (uint32_t k = 0; k < 4; ++k)
-                            mma_f8_pair(tmem_base + me * 256, a + 2u * k, b + 2u * k, idesc, k != 0);
+                            mma_f8_pair(tmem_base + me * 256, a + 2u * k, b + 2u * k, idesc,
+                                        k != 0);
                         mma_commit_pair(bar(kEmpty + stage), kBoth);
                         mma_commit_pair(bar(kAccF + me), kBoth);
                     }
@@ -1025,13 +1030,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(consumer_regs(8)));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
         const int q = warp & 3, group = warp >> 2;
         const uint32_t tmem_warp =
             tmem_base + (static_cast<uint32_t>(q) << 21) + static_cast<uint32_t>(group) * 128u;
-        uint8_t *const staging = sbase + lay.staging + warp * 2048;
+        uint8_t *const staging = sbase + lay.staging + warp * kWarpStaging;
         if (p.zero_rest)
-            zero_rows(p, lists, blockIdx.x * 8 + warp, gridDim.x * 8, lane);
+            zero_rows(p, lists, blockIdx.x * kConsumers + warp, gridDim.x * kConsumers, lane);
         uint32_t acc = 0;
         bool ok = true;
         for (int t = first; ok && t < total; t += step) {
@@ -1057,7 +1062,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
                     w_next = __ldg(ws + kb + 1);
                 }
                 const uint32_t as = acc & 1u;
-                if (!(ok = wait_warp(bar(kAccF + as), (acc >> 1) & 1u, abort_flag, p.timeout_ns)))
+                if (!(ok = wait(kAccF + as, (acc >> 1) & 1u)))
                     break;
                 tc_fence_after();
 #pragma unroll
@@ -1158,33 +1163,6 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// to[b][p] = the scale of k-block b of the row that map names for position p (0:
-// none): scales of neighbouring columns of a tile then stand together.
-__global__ void __launch_bounds__(256)
-    gather_scales_kernel(int32_t M, RowMap map, const float *from, int32_t kblocks, float *to)
-{
-    __shared__ float tile[32][33];
-    wait_for_previous();
-    let_next_start();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t p0 = 32 * static_cast<int64_t>(blockIdx.x);
-    for (int b0 = 0; b0 < kblocks; b0 += 32) {
-#pragma unroll
-        for (int i = warp; i < 32; i += 8) {
-            const int32_t row = p0 + i < M ? row_of(map, static_cast<int32_t>(p0 + i), M) : -1;
-            tile[i][lane] = row >= 0 && b0 + lane < kblocks
-                                ? __ldg(from + static_cast<int64_t>(row) * kblocks + b0 + lane)
-                                : 0.0f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = warp; i < 32; i += 8)
-            if (b0 + i < kblocks && p0 + lane < M)
-                to[static_cast<int64_t>(b0 + i) * M + p0 + lane] = tile[lane][i];
-        __syncthreads();
-    }
-}
-
 // Ring depth that fits beside the lists and scales.
 int stages_for(int NT, int E, bool scaled, size_t smem)
 {
@@ -1194,10 +1172,7 @@ int stages_for(int NT, int E, bool scaled, size_t smem)
     return 0;
 }
 
-// Consumer warps of the wide tiles.
-constexpr int kWide = 8, kWideE8 = 16;
-
-template <ExpertsKind KIND, bool E8, int NT, int CW>
+template <ExpertsKind KIND, bool E8, int NT>
 cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, ExpertsParams p, int sms,
                    size_t smem_optin, cudaStream_t stream)
 {
@@ -1212,35 +1187,10 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, ExpertsParams p, 
                               : mblocks * (std::min<int64_t>(p.E, p.M) + p.M / NT);
     const int grid =
         2 * static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tiles, sms / 2)));
-    return launch_after(experts_kernel<KIND, E8, NT, CW>, grid, threads_of(CW), smem, stream, a, b, p);
+    return launch_after(experts_kernel<KIND, E8, NT>, grid, kThreads, smem, stream, a, b, p);
 }
 
-}  // namespace
-
-cudaError_t experts_prepare(size_t smem_optin)
-{
-    const void *kernels[] = {(const void *)experts_kernel<kForward, false, 64, 8>,
-                             (const void *)experts_kernel<kForward, false, 256, kWide>,
-                             (const void *)experts_kernel<kForward, true, 64, 8>,
-                             (const void *)experts_kernel<kForward, true, 256, kWideE8>,
-                             (const void *)experts8_kernel,
-                             (const void *)experts_kernel<kRowsGrad, false, 64, 8>,
-                             (const void *)experts_kernel<kRowsGrad, false, 256, kWide>,
-                             (const void *)experts_kernel<kWeightsGrad, false, 256, kWide>};
-    for (const void *k : kernels) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem_optin));
-        if (e != cudaSuccess)
-            return e;
-    }
-    return cudaSuccess;
-}
-
-bool experts_few(int64_t M, int64_t E) { return M <= 32 * E; }
-
-bool experts8_many(int64_t M, int64_t E) { return M >= 256 * E; }
-
-cudaError_t launch_experts8(const CUtensorMap &a, const CUtensorMap &b, ExpertsParams p, int sms,
+cudaError_t launch8(const CUtensorMap &a, const CUtensorMap &b, ExpertsParams p, int sms,
                             size_t smem_optin, cudaStream_t stream)
 {
     p.stages = 0;
@@ -1253,9 +1203,35 @@ cudaError_t launch_experts8(const CUtensorMap &a, const CUtensorMap &b, ExpertsP
     const int64_t tiles =
         (std::min<int64_t>(p.E, p.M) + p.M / 256) * ((p.mdim + 255) / 256);
     const int grid = 2 * static_cast<int>(std::min<int64_t>(tiles, sms / 2));
-    return launch_after(experts8_kernel, grid, 384, 1024u + layout8_of(p.stages, p.E).end, stream, a,
-                        b, p);
+    return launch_after(experts8_kernel, grid, kThreads, 1024u + layout8_of(p.stages, p.E).end,
+                        stream, a, b, p);
 }
+
+}  // namespace
+
+cudaError_t experts_prepare(size_t smem_optin)
+{
+    const void *kernels[] = {(const void *)experts_kernel<kForward, false, 64>,
+                             (const void *)experts_kernel<kForward, false, 256>,
+                             (const void *)experts_kernel<kForward, true, 64>,
+                             (const void *)experts8_kernel,
+                             (const void *)experts_kernel<kRowsGrad, false, 64>,
+                             (const void *)experts_kernel<kRowsGrad, false, 256>,
+                             (const void *)experts_kernel<kWeightsGrad, false, 256>};
+    for (const void *k : kernels) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(smem_optin));
+        if (e != cudaSuccess)
+            return e;
+    }
+    return cudaSuccess;
+}
+
+// Rows by ids, 64 lists of 32 / 64 positions of 2,048 in 16 bits, 1,024 columns:
+// narrow tiles 50 / 63 us, wide ones behind a pass that gathers the rows 55 / 60.
+// In 8 bits, 64 / 96 positions: narrow 40 / 58, positions as rows 52 / 54 (256
+// lists: 131 / 212 and 171 / 180).
+bool experts_few(int64_t M, int64_t E, bool e8) { return M <= (e8 ? 64 : 32) * E; }
 
 cudaError_t launch_experts(ExpertsKind kind, bool e8, int type, const CUtensorMap &a,
                            const CUtensorMap &b, ExpertsParams p, int sms, size_t smem_optin,
@@ -1264,19 +1240,19 @@ cudaError_t launch_experts(ExpertsKind kind, bool e8, int type, const CUtensorMa
     p.idesc = idesc_base(e8 ? 0u : type == kBf16 ? 1u : 0u, kind != kForward, kind == kWeightsGrad,
                          2 * kRowsA);
     p.segment = kind == kWeightsGrad && p.out_type == kFp32 ? kSegmentRows : kSegment;
-    const bool few = experts_few(p.M, p.E);
+    const bool few = experts_few(p.M, p.E, e8);
     switch (kind) {
     case kForward:
         if (e8)
-            return few ? launch<kForward, true, 64, 8>(a, b, p, sms, smem_optin, stream)
-                       : launch<kForward, true, 256, kWideE8>(a, b, p, sms, smem_optin, stream);
-        return few ? launch<kForward, false, 64, 8>(a, b, p, sms, smem_optin, stream)
-                   : launch<kForward, false, 256, kWide>(a, b, p, sms, smem_optin, stream);
+            return few ? launch<kForward, true, 64>(a, b, p, sms, smem_optin, stream)
+                       : launch8(b, a, p, sms, smem_optin, stream);
+        return few ? launch<kForward, false, 64>(a, b, p, sms, smem_optin, stream)
+                   : launch<kForward, false, 256>(a, b, p, sms, smem_optin, stream);
     case kRowsGrad:
-        return few ? launch<kRowsGrad, false, 64, 8>(a, b, p, sms, smem_optin, stream)
-                   : launch<kRowsGrad, false, 256, kWide>(a, b, p, sms, smem_optin, stream);
+        return few ? launch<kRowsGrad, false, 64>(a, b, p, sms, smem_optin, stream)
+                   : launch<kRowsGrad, false, 256>(a, b, p, sms, smem_optin, stream);
     default:
-        return launch<kWeightsGrad, false, 256, kWide>(a, b, p, sms, smem_optin, stream);
+        return launch<kWeightsGrad, false, 256>(a, b, p, sms, smem_optin, stream);
     }
 }
 
@@ -1288,14 +1264,6 @@ cudaError_t launch_listed_rows(const int32_t *offsets, int32_t E, int32_t M, Row
     return launch_after(listed_rows_kernel, blocks, 256, 0, stream, offsets, E, M, map, row);
 }
 
-cudaError_t launch_gather_scales(int32_t M, RowMap map, const float *from, int32_t kblocks, float *to,
-                                 cudaStream_t stream)
-{
-    return launch_after(gather_scales_kernel,
-                        static_cast<unsigned>((static_cast<int64_t>(M) + 31) / 32), 256, 0, stream, M,
-                        map, from, kblocks, to);
-}
-
 cudaError_t launch_gather_rows(const int32_t *offsets, int32_t E, int32_t M, RowMap map,
                                RowMap also, const void *from, int64_t pitch, void *to,
                                int32_t *holes, cudaStream_t stream)
@@ -1305,8 +1273,8 @@ cudaError_t launch_gather_rows(const int32_t *offsets, int32_t E, int32_t M, Row
     while (lanes > 1 && lanes / 2 >= units)
         lanes /= 2;
     const int64_t blocks = (static_cast<int64_t>(M) * lanes + 255) / 256;
-    return launch_after(gather_rows_kernel, static_cast<unsigned>(blocks), 256, 0, stream, offsets, E,
-                        M, map, also, static_cast<const uint4 *>(from), units, lanes,
+    return launch_after(gather_rows_kernel, static_cast<unsigned>(blocks), 256, 0, stream, offsets,
+                        E, M, map, also, static_cast<const uint4 *>(from), units, lanes,
                         static_cast<uint4 *>(to), holes);
 }
 

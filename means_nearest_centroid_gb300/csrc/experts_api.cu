@@ -155,23 +155,19 @@ int kmassign_experts(const void *X, int32_t dtype, int64_t R, int64_t D, const v
     // Many positions: their rows first come into the lists' order, by a pass of
     // its own, and are then loaded in whole boxes.
     const int64_t pitch = D * (e8 ? 1 : 2);
-    const bool few = kma::experts_few(M, E);
-    const bool many8 = e8 && kma::experts8_many(M, E);
+    const bool few = kma::experts_few(M, E, e8);
+    // 8 bits and many: positions are the tile's rows
+    const uint32_t box = e8 && !few ? kma::kExpertsBoxA : kma::kExpertsBoxB;
     const int32_t kblocks = static_cast<int32_t>((pitch + 127) / 128);
-    const size_t codes = rows != nullptr && !few ? static_cast<size_t>(M * pitch) : 0;
-    const bool by_blocks = e8 && !few && !many8;   // scales in another order
-    Scratch scratch(codes + (by_blocks ? static_cast<size_t>(M) * kblocks * 4 : 0), dev.pool, st);
-    if (!scratch.ok())
+    Scratch sorted(rows != nullptr && !few ? static_cast<size_t>(M * pitch) : 0, dev.pool, st);
+    if (!sorted.ok())
         return KMASSIGN_ERR_CUDA;
-    uint8_t *const sorted = codes > 0 ? scratch.get() : nullptr;
     const RowMap from = map_of(rows, slots, R);
     const bool gathers = rows != nullptr && few;
     CUtensorMap a, b;
     if (!weights_map(&a, dtype, W, E, F, D, kma::kExpertsBoxA) ||
-        (sorted != nullptr
-             ? !rows_map(&b, dtype, sorted, M, D, many8 ? kma::kExpertsBoxA : kma::kExpertsBoxB)
-             : !rows_map(&b, dtype, X, R, D,
-                         gathers ? 1 : many8 ? kma::kExpertsBoxA : kma::kExpertsBoxB)))
+        (sorted.get() != nullptr ? !rows_map(&b, dtype, sorted.get(), M, D, box)
+                                 : !rows_map(&b, dtype, X, R, D, gathers ? 1 : box)))
         return KMASSIGN_ERR_CUDA;
     ExpertsParams p = params_of(s, offsets);
     p.mdim = static_cast<int32_t>(F);
@@ -186,19 +182,13 @@ int kmassign_experts(const void *X, int32_t dtype, int64_t R, int64_t D, const v
     p.xscale = xscale;
     p.wscale = wscale;
     cudaError_t e = cudaSuccess;
-    if (sorted != nullptr)
-        e = kma::launch_gather_rows(offsets, p.E, p.M, from, map_of(nullptr, 1, M), X, pitch, sorted,
-                                    nullptr, st);
-    if (e == cudaSuccess && by_blocks) {
-        float *const by_block = reinterpret_cast<float *>(scratch.get() + codes);
-        e = kma::launch_gather_scales(p.M, from, xscale, kblocks, by_block, st);
-        p.xscale = by_block;
-    }
+    if (sorted.get() != nullptr)
+        e = kma::launch_gather_rows(offsets, p.E, p.M, from, map_of(nullptr, 1, M), X, pitch,
+                                    sorted.get(), nullptr, st);
     if (e == cudaSuccess)
-        e = many8 ? kma::launch_experts8(b, a, p, dev.sms, dev.smem, st)
-                  : kma::launch_experts(kma::kForward, e8, dtype, a, b, p, dev.sms, dev.smem, st);
+        e = kma::launch_experts(kma::kForward, e8, dtype, a, b, p, dev.sms, dev.smem, st);
     rc = done(e);
-    return scratch.release() ? rc : KMASSIGN_ERR_CUDA;
+    return sorted.release() ? rc : KMASSIGN_ERR_CUDA;
 }
 
 int kmassign_experts_grad(const void *dout, int32_t dtype, int64_t out_rows, int64_t F,

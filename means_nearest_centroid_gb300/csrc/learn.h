@@ -157,9 +157,7 @@ struct ExpertsParams {
     bool zero_rest;           // rows of no list are written 0
     void *out;
     int32_t out_type;
-    // 8 bits: [rows, kblocks] of few positions, else [kblocks, M] by launch_gather_scales
-    const float *xscale;
-    const float *wscale;      // [E, fblocks, kblocks]
+    const float *xscale, *wscale;   // 8 bits: [rows, kblocks], [E, fblocks, kblocks]
     int32_t fblocks;
     // set by launch_experts: depth of the ring, k-blocks between additions to registers, MMA shape
     int32_t stages, segment;
@@ -175,15 +173,10 @@ cudaError_t experts_prepare(size_t smem_optin);
 constexpr uint32_t kExpertsBoxA = 128, kExpertsBoxMn = 64, kExpertsBoxB = 32;
 // Whether lists of M positions are short on average: the product then has
 // tiles for few columns, and gathers rows itself.
-bool experts_few(int64_t M, int64_t E);
+bool experts_few(int64_t M, int64_t E, bool e8);
 cudaError_t launch_experts(ExpertsKind kind, bool e8, int type, const CUtensorMap &a,
                            const CUtensorMap &b, ExpertsParams p, int sms, size_t smem_optin,
                            cudaStream_t stream);
-// 8 bits with many positions an expert: rows of X in boxes of 128 (a), of W in
-// boxes of 128 (b), xscale by row.
-bool experts8_many(int64_t M, int64_t E);
-cudaError_t launch_experts8(const CUtensorMap &a, const CUtensorMap &b, ExpertsParams p, int sms,
-                            size_t smem_optin, cudaStream_t stream);
 cudaError_t experts_status_read_and_clear(int *code);
 // row[p] = the row that map names for positions of a list, -1 for the others.
 cudaError_t launch_listed_rows(const int32_t *offsets, int32_t E, int32_t M, RowMap map,
@@ -194,10 +187,6 @@ cudaError_t launch_listed_rows(const int32_t *offsets, int32_t E, int32_t M, Row
 cudaError_t launch_gather_rows(const int32_t *offsets, int32_t E, int32_t M, RowMap map,
                                RowMap also, const void *from, int64_t pitch, void *to,
                                int32_t *holes, cudaStream_t stream);
-
-// to[b][p] = from[the row that map names for position p][b], 0 where it names none.
-cudaError_t launch_gather_scales(int32_t M, RowMap map, const float *from, int32_t kblocks, float *to,
-                                 cudaStream_t stream);
 
 cudaError_t launch_rmsnorm(const void *X, int dtype, int64_t N, int64_t D, const void *residual,
                            const void *weight, int weight_dtype, float eps, void *total, void *out,
