@@ -1232,11 +1232,14 @@ const char *kmassign_strerror(int code)
         return "a required pointer is NULL";
     case KMASSIGN_ERR_ALIGN:
         return "X and C (and cnorm) must be 16-byte aligned; idx and minscore 4-byte aligned; "
-               "the buffers of learned assignments to their elements";
+               "the buffers of learned assignments to their elements, the matrices of experts' "
+               "products to 16 bytes";
     case KMASSIGN_ERR_SHAPE:
-        return "shape out of range: need 0 <= N < 2^31 and 1 <= K < 2^31 (routing: 1 <= E <= 1024)";
+        return "shape out of range: need 0 <= N < 2^31 and 1 <= K < 2^31 (routing and experts' "
+               "products: 1 <= E <= 1024; positions of a product: one row each, M < 2^30)";
     case KMASSIGN_ERR_UNSUPPORTED_D:
-        return "unsupported D: need a multiple of 16 in [16, 256] (lookup: 1 to 65536)";
+        return "unsupported D: need a multiple of 16 in [16, 256] (lookup: 1 to 65536; experts' "
+               "products: D and F multiples of 8, D of 16 in 8 bits, to 65536; norm: 1 to 32768)";
     case KMASSIGN_ERR_CUDA:
         return "a CUDA runtime or driver call failed";
     case KMASSIGN_ERR_TIMEOUT:

@@ -223,6 +223,16 @@ __device__ __forceinline__ bool missing(const ExpertsParams &p, int32_t at, int3
     return row_of(p.from, at, hi) < 0 || row_of(p.placed, at, hi) < 0;
 }
 
+// Copies in flight may complete on the other CTA's barriers, out of this one's
+// sight: after a wait has run out they get time to land (they take
+// microseconds) before either CTA leaves.
+__device__ __forceinline__ void let_copies_land()
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {
+    }
+}
+
 // Waits for a stage's operands (a whole warp).  Where threads of either CTA may
 // have written them, the wait acquires at the cluster's scope.
 __device__ __forceinline__ bool wait_operands(uint32_t bar, uint32_t parity, bool threads_write,
@@ -420,13 +430,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int first = static_cast<int>(blockIdx.x >> 1);
     const int step = static_cast<int>(gridDim.x >> 1);
     const uint32_t stages = static_cast<uint32_t>(p.stages);
-    // Copies in flight complete on the leader's barriers, out of a CTA's sight:
-    // after a wait has run out they get time to land (they take microseconds).
-    auto let_copies_land = [&]() {
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 1000000ull) {
-        }
-    };
 
     if (warp >= kConsumers) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -528,8 +531,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (!ok && lane == 0)
-                let_copies_land();
             __syncwarp();
         } else if (warp == kWarpMma) {
             if (leader) {
@@ -771,6 +772,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
 
+    if (threadIdx.x == 0 && *abort_flag)
+        let_copies_land();
     tc_fence_before();
     __syncthreads();
     cluster_sync();   // no CTA leaves while its pair can still touch its memory
@@ -788,11 +791,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // cost one FMA an element and nothing else.  (With positions as columns each
 // element needs its column's scale out of shared memory, and the rest of a
 // segment's hand-over does not hide that: 32,768 positions in 8 lists, 4,096 x
-// 4,096, took 700 us, here 518, 2,120 TFLOP/s.)  What bounds it is the hand-over
-// of two accumulators for each 128 of the contraction: 1,140 clocks a k-block
-// whose MMAs take 512.  More and smaller accumulators (four of 128 columns, 1,050
-// us), half-tiles with barriers of their own and longer waits between polls were
-// no faster.  Lists are rounded up to 256, so only products of many positions an
+// 4,096, took 700 us, here 518, 2,120 TFLOP/s.)  What bounds it: a k-block takes
+// 1,140 clocks, of which its MMAs are 512; the rest is the loads of the
+// accumulator, which the MMAs do not overlap (a tile of 128 columns takes 730: 320
+// clocks for a segment's hand-over and 3.2 a column, where the MMAs take 2).  As
+// long: two CTAs with MMAs and hand-overs of their own and the weights multicast
+// (537 us), scales loaded four k-blocks at a time (558), 64 columns in flight a
+// warp (605).  Slower: 128 columns and four accumulators (667).  Lists are rounded
+// up to 256, so only products of many positions an
 // expert come here.
 
 constexpr int kLoad8 = 8, kIssue8 = 9;   // warps behind the 8 of consumers; two issue
@@ -986,11 +992,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tma_load_3d_pair(to + kPartA, &bmap, full, kb * 128, n, w.e);
                     }
                 }
-                if (!ok) {   // see experts_kernel
-                    const uint64_t t0 = globaltimer_ns();
-                    while (globaltimer_ns() - t0 < 1000000ull) {
-                    }
-                }
             }
             __syncwarp();
         } else if (leader && (warp == kIssue8 || warp == kIssue8 + 1)) {
@@ -1098,6 +1099,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
 
+    if (threadIdx.x == 0 && *abort_flag)
+        let_copies_land();
     tc_fence_before();
     __syncthreads();
     cluster_sync();   // no CTA leaves while its pair can still touch its memory

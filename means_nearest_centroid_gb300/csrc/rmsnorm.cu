@@ -5,7 +5,11 @@
 //   8 bits: for each block of 128 columns scale = max |y| / 448, codes e4m3(y / scale)
 //   g = w dy,  dx = rstd (g - t rstd mean(g t rstd)) + dt,  dw = sum over rows of dy t rstd
 //
-// Both are bound by memory: every element crosses HBM once in each direction.
+// Both are bound by memory: every element crosses HBM once in each direction
+// (65,536 x 2,048 bf16: residual added, to 8 bits 137 us, 6.9 TB/s; gradients with
+// the residual's 187 us, 5.7 TB/s, of which the partial rows of the weight's take 8).
+// Rows at odd addresses are read element by element (30,011 x 777 fp32 gradients 69
+// us, 4.1 TB/s).
 // A row lives in the registers of one warp, or of the warps of one block where
 // it is longer or where rows are few, so it is read once for its statistics and
 // its output alike.  Sums are fp32.  A warp's piece of a row is a whole number
