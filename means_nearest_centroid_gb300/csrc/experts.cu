@@ -73,8 +73,7 @@ constexpr uint32_t kAtomBytes = 64 * 128;          // MN-major: 64 elements by 6
 // Scales: a ring of groups of four k-blocks (one hand-over for four segments).
 constexpr int kScaleStages = 2, kScaleGroup = 4;
 __host__ __device__ constexpr uint32_t scale_bytes(int NT) { return kScaleGroup * NT * 4u; }
-constexpr uint32_t kGroupBarrier = 1;              // named barriers of the consumers' groups
-constexpr uint32_t kStagingBytes = 8192;           // of a group, for its way to the output
+constexpr uint32_t kWarpStaging = 2048;            // of a warp of consumers, for its way out
 // 16-bit k-blocks between two additions to registers: 2,048 elements, or 512
 // positions of a weights' gradient in fp32.
 constexpr int kSegment = 32, kSegmentRows = 8;
@@ -94,10 +93,10 @@ struct Tile {
     int32_t kblocks;
 };
 
-// Shared memory behind the ring: the consumers' staging and row numbers, scales,
-// then the lists' starts, ends and the tiles before each expert, then barriers.
+// Shared memory behind the ring: the consumers' staging, scales, then the lists'
+// starts, ends and the tiles before each expert, then barriers.
 struct Layout {
-    uint32_t ring, staging, dst, scale, lists, bars, end;
+    uint32_t ring, staging, scale, lists, bars, end;
 };
 
 __host__ __device__ constexpr uint32_t stage_bytes(int NT) { return kPartA + NT / 2 * 128; }
@@ -107,8 +106,7 @@ __host__ __device__ inline Layout layout_of(int NT, int stages, int E, bool scal
     Layout l;
     l.ring = 0;
     l.staging = stages * stage_bytes(NT);
-    l.dst = l.staging + 2u * kStagingBytes;       // [group][tile parity][columns]
-    l.scale = l.dst + 2u * NT * 4u;
+    l.scale = l.staging + kConsumers * kWarpStaging;
     l.lists = l.scale + (scaled ? kScaleStages * scale_bytes(NT) : 0u);
     l.bars = (l.lists + 3u * static_cast<uint32_t>(E + 1) * 4u + 15u) / 16u * 16u;
     l.end = l.bars + kBars * 8u + 16u;
@@ -272,64 +270,58 @@ __device__ __forceinline__ uint32_t pack_two(float a, float b)
     return r;
 }
 
-// A group's threads (four warps, 128 rows of the tile) turn their columns into
-// rows of the output by way of shared memory, some columns at a time: a column's
-// 128 elements stand together there, their 16-byte pieces at piece ^ (column %
-// 8) so that no two lanes meet in a bank, and are stored as one run of 256 bytes
-// (fp32: 512).  Two buffers of 4 KiB take turns.
-// `dst`: the output rows of the group's columns; -1: none, -2 - row: a row of
-// zeros.
-template <typename O, int COLS>
-__device__ __forceinline__ void store_columns(const Frags<COLS> &sum, int cols, uint8_t *stage,
-                                              const int32_t *dst, void *out, int32_t m,
-                                              int32_t mdim, int group, int thread)
+// 32 columns of a warp's fragments become rows of the output by way of the warp's
+// own shared memory: 64 bytes of 32 rows (fp32: 128 bytes of 16, twice), whose
+// 16-byte pieces are moved about so that no two lanes meet in a bank, and which
+// go out a row to four lanes (fp32: eight).  No warp waits for another: with four
+// warps meeting over runs of 256 bytes the weights' gradient of 256 lists of 128,
+// whose stores take longer than its product, took 285 us (here 259; fp32 440, 384).
+// dst: lane c has column c's row of the output; -1: none, -2 - row: a row of zeros.
+template <typename O>
+__device__ __forceinline__ void store_columns(const float (*v)[2][4], uint8_t *stage, int32_t dst,
+                                              void *out, int32_t f, int32_t mdim, int lane)
 {
-    constexpr int kColBytes = 128 * sizeof(O);
-    constexpr int kCols = kStagingBytes / 2 / kColBytes;
-    constexpr int kLanes = kColBytes / 16;           // threads to a column
-    constexpr int kPerThread = 16 / sizeof(O);
-    static_assert(kCols % 8 == 0 && COLS % kCols == 0, "whole matrices");
-    const int piece = thread % kLanes;
-    const int lane = thread & 31, q = thread >> 5;
-    const bool inside = m + piece * kPerThread < mdim;
-    O *const to = static_cast<O *>(out) + m + piece * kPerThread;
+    constexpr int kCols = sizeof(O) == 2 ? 32 : 16;   // at a time
+    constexpr int kPieces = 2 * sizeof(O);            // of 16 bytes in a row's 32 elements
+    const int piece = lane % kPieces;
+    const bool inside = f + piece * (16 / static_cast<int>(sizeof(O))) < mdim;
+    uint8_t *const to =
+        static_cast<uint8_t *>(out) + f * static_cast<int64_t>(sizeof(O)) + 16 * piece;
+    const int64_t pitch = static_cast<int64_t>(mdim) * sizeof(O);
+    auto at = [&](int col, int p) {
+        return stage + col * (32 * sizeof(O)) +
+               16 * (p ^ (sizeof(O) == 2 ? col >> 1 & 3 : col & 7));
+    };
 #pragma unroll
-    for (int c = 0; c < COLS; c += kCols) {
-        if (c < cols) {
-            uint8_t *const buf = stage + (c / kCols & 1) * (kStagingBytes / 2);
+    for (int c = 0; c < 32; c += kCols) {
+        __syncwarp();
 #pragma unroll
-            for (int j = 0; j < kCols / 8; ++j) {
-                const float(&v)[2][4] = sum.v[c / 8 + j];
-                if constexpr (sizeof(O) == 2) {
-                    const int col = 8 * j + (lane & 7);
-                    const int at = (4 * q + (lane >> 3)) ^ (lane & 7);
-                    store_matrices(smem_addr(buf) + col * kColBytes + 16 * at,
-                                   pack_two<O>(v[0][0], v[0][1]), pack_two<O>(v[0][2], v[0][3]),
-                                   pack_two<O>(v[1][0], v[1][1]), pack_two<O>(v[1][2], v[1][3]));
-                } else {
+        for (int j = 0; j < kCols / 8; ++j) {
+            const float(&w)[2][4] = v[c / 8 + j];
+            if constexpr (sizeof(O) == 2) {
+                store_matrices(smem_addr(at(8 * j + (lane & 7), lane >> 3)),
+                               pack_two<O>(w[0][0], w[0][1]), pack_two<O>(w[0][2], w[0][3]),
+                               pack_two<O>(w[1][0], w[1][1]), pack_two<O>(w[1][2], w[1][3]));
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int col = 8 * j + 2 * (lane & 3) + (i & 1);
-                        const int f = 32 * q + 16 * (i >> 2) + 8 * (i >> 1 & 1) + (lane >> 2);
-                        *reinterpret_cast<float *>(buf + col * kColBytes +
-                                                   16 * ((f >> 2) ^ (col & 7)) + 4 * (f & 3)) =
-                            v[i >> 2][i & 3];
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const int row = 16 * (i >> 2) + 8 * (i >> 1 & 1) + (lane >> 2);
+                    *reinterpret_cast<float *>(at(8 * j + 2 * (lane & 3) + (i & 1), row >> 2) +
+                                               4 * (row & 3)) = w[i >> 2][i & 3];
                 }
             }
-            named_bar_sync(kGroupBarrier + group, 128);
+        }
+        __syncwarp();
 #pragma unroll
-            for (int i = 0; i < kCols; i += 128 / kLanes) {
-                const int col = i + thread / kLanes;
-                const int32_t d = dst[c + col];
-                uint4 v = *reinterpret_cast<const uint4 *>(buf + col * kColBytes +
-                                                           16 * (piece ^ (col & 7)));
-                if (d < -1)
-                    v = make_uint4(0, 0, 0, 0);
-                const int32_t row = d < -1 ? -2 - d : d;
-                if (row >= 0 && inside)
-                    *reinterpret_cast<uint4 *>(to + static_cast<int64_t>(row) * mdim) = v;
-            }
+        for (int i = 0; i < kCols; i += 32 / kPieces) {
+            const int col = i + lane / kPieces;
+            const int32_t d = __shfl_sync(0xffffffffu, dst, c + col);
+            uint4 w = *reinterpret_cast<const uint4 *>(at(col, piece));
+            if (d < -1)
+                w = make_uint4(0, 0, 0, 0);
+            const int32_t row = d < -1 ? -2 - d : d;
+            if (row >= 0 && inside)
+                *reinterpret_cast<uint4 *>(to + row * pitch) = w;
         }
     }
 }
@@ -681,28 +673,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t tmem_warp = tmem_base + (static_cast<uint32_t>(q) << 21) + c0;
         if (p.zero_rest)
             zero_rows(p, lists, blockIdx.x * kConsumers + warp, gridDim.x * kConsumers, lane);
-        const int thread = threadIdx.x & 127;
-        uint8_t *const staging = sbase + lay.staging + group * kStagingBytes;
-        int32_t *const dsts = reinterpret_cast<int32_t *>(sbase + lay.dst) + group * 2 * kGroupCols;
-        uint32_t acc = 0, n = 0, used = 0;
+        uint8_t *const staging = sbase + lay.staging + warp * kWarpStaging;
+        uint32_t acc = 0, n = 0;
         bool ok = true;
         for (int t = first; ok && t < plan.total; t += step) {
             const Tile w = plan.tile(t);
             const int cols = min(max(w.n - c0, 0), kGroupCols);
-            int32_t *const dst = dsts + kGroupCols * (used & 1u);
-            if (cols > 0 && thread < kGroupCols) {
-                const int32_t at = w.n0 + c0 + thread;   // this thread's column
-                int32_t d;
+            int32_t dst[kGroupCols / 32];   // of columns 32 i + lane
+#pragma unroll
+            for (int i = 0; i < kGroupCols / 32; ++i) {
+                const int32_t at = w.n0 + c0 + 32 * i + lane;
                 if (KIND == kWeightsGrad) {
-                    d = at < p.ndim ? w.e * p.ndim + at : -1;
+                    dst[i] = at < p.ndim ? w.e * p.ndim + at : -1;
                 } else {
-                    d = row_of(p.places, at, w.hi);
-                    if (d >= 0 && row_of(p.from, at, w.hi) < 0)
-                        d = -2 - d;
+                    dst[i] = row_of(p.places, at, w.hi);
+                    if (dst[i] >= 0 && row_of(p.from, at, w.hi) < 0)
+                        dst[i] = -2 - dst[i];
                 }
-                dst[thread] = d;
             }
-            used += cols > 0;
             Frags<kGroupCols> sum;
 #pragma unroll
             for (int i = 0; i < kGroupCols; ++i)
@@ -755,20 +743,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 n += last;
             }
-            // A group stores together or, after a wait of any of its warps ran out,
-            // leaves together: no warp waits at its barrier for one that has left.
-            if (!(ok = named_bar_and(kGroupBarrier + group, 128, ok)))
+            if (!ok)
                 break;
-            const int32_t m = w.m0 + static_cast<int>(rank) * kRowsA;
-            if (p.out_type == kBf16)
-                store_columns<__nv_bfloat16, kGroupCols>(sum, cols, staging, dst, p.out, m, p.mdim,
-                                                         group, thread);
-            else if (p.out_type == kFp16)
-                store_columns<__half, kGroupCols>(sum, cols, staging, dst, p.out, m, p.mdim,
-                                                  group, thread);
-            else
-                store_columns<float, kGroupCols>(sum, cols, staging, dst, p.out, m, p.mdim,
-                                                 group, thread);
+            const int32_t f = w.m0 + static_cast<int>(rank) * kRowsA + 32 * q;
+#pragma unroll
+            for (int i = 0; i < kGroupCols / 32; ++i) {
+                if (32 * i < cols) {
+                    const float(*const v)[2][4] = sum.v + 4 * i;
+                    if (p.out_type == kBf16)
+                        store_columns<__nv_bfloat16>(v, staging, dst[i], p.out, f, p.mdim, lane);
+                    else if (p.out_type == kFp16)
+                        store_columns<__half>(v, staging, dst[i], p.out, f, p.mdim, lane);
+                    else
+                        store_columns<float>(v, staging, dst[i], p.out, f, p.mdim, lane);
+                }
+            }
         }
     }
 
@@ -810,7 +799,6 @@ struct Tile8 {
 struct Layout8 {
     uint32_t staging, lists, bars, end;
 };
-constexpr uint32_t kWarpStaging = 2048;   // 64 bytes of a warp's 32 rows
 
 __host__ __device__ inline Layout8 layout8_of(int stages, int E)
 {

@@ -60,20 +60,6 @@ __device__ __forceinline__ void mbar_acquire_cluster(uint32_t bar, uint32_t pari
                  : "memory");
 }
 
-// Whether p is true in all of the `count` threads that meet at a named barrier.
-__device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t count, bool p)
-{
-    uint32_t all;
-    asm volatile("{\n\t.reg .pred q, r;\n\t"
-                 "setp.ne.u32 q, %3, 0;\n\t"
-                 "barrier.cta.red.and.pred r, %1, %2, q;\n\t"
-                 "selp.u32 %0, 1, 0, r;\n\t}"
-                 : "=r"(all)
-                 : "r"(id), "r"(count), "r"(static_cast<uint32_t>(p))
-                 : "memory");
-    return all != 0;
-}
-
 // MN-major operand tile, 128-byte swizzle: atoms of 64 16-bit elements along M
 // or N by 64 rows of K (128 bytes a row, 8-row groups 1024 bytes apart, the
 // stride byte offset); the next 64 elements lie `lbo` bytes on (the leading

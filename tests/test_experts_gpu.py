@@ -559,6 +559,69 @@ def test_nothing_in_nothing_out(dev):
     assert dX.shape == (0, 8) and (dw == 0).all()
 
 
+def test_elements_past_32_bits(dev):
+    """Outputs of more than 2^31 elements, checked at both ends."""
+    g = gen_of(dev, 13)
+    M, D, F = 1_100_000, 16, 2048
+    X, W = ints(g, (M, D), 2, BF16), ints(g, (2, F, D), 2, BF16)
+    ends = torch.tensor([0, 1, M // 2, M - 2, M - 1], device=dev)
+    out = km.kmassign_experts(X, W, offsets_of([5, M - 5], dev))
+    ref = torch.stack([X[i].double() @ W[int(i >= 5)].double().t() for i in ends.tolist()])
+    assert torch.equal(out[ends], ref.to(BF16))
+    dX, _ = km.kmassign_experts_grad(out, X, W, offsets_of([5, M - 5], dev), need_w=False)
+    ref = torch.stack([out[i].double() @ W[int(i >= 5)].double() for i in ends.tolist()])
+    assert torch.equal(dX[ends], ref.to(BF16))
+    del out, dX
+    E, F, D = 1024, 2048, 1032
+    X, dout = ints(g, (2 * E, D), 2, BF16), ints(g, (2 * E, F), 2, BF16)
+    _, dW = km.kmassign_experts_grad(dout, X, torch.empty(E, F, D, device=dev, dtype=BF16),
+                                     offsets_of([2] * E, dev), need_x=False, dtype=BF16)
+    for e in (0, 511, 1023):
+        ref = dout[2 * e:2 * e + 2].double().t() @ X[2 * e:2 * e + 2].double()
+        assert torch.equal(dW[e], ref.to(BF16))
+    del dW
+    N, D = 70_000, 32768
+    x = torch.empty(N, D, device=dev, dtype=BF16).normal_(generator=g)
+    out, _, _, rstd = km.kmassign_rmsnorm(x)
+    dX, _ = km.kmassign_rmsnorm_grad(x, x, None, rstd)
+    for i in (0, N - 1):
+        srstd, y = ref_norm(x[i:i + 1], None, 1e-6)
+        rel = (sums_of(D) / 2 + 8) * U
+        assert ((out[i].double() - y[0]).abs() <= (rel + 2 * U + OUT[BF16]) * y[0].abs() * 1.001).all()
+        n = x[i].double() * rstd[i].double()
+        want = rstd[i].double() * (x[i].double() - n * (x[i].double() * n).mean())
+        size = x[i].double().abs() + n.abs() * (x[i].double() * n).abs().mean()
+        err = rstd[i].double() * (sums_of(D) + 16) * U * size
+        assert ((dX[i].double() - want).abs() <= err + OUT[BF16] * (want.abs() + err) * 1.001).all()
+
+
+@pytest.mark.parametrize("M", [20_000, 70_000])
+def test_the_largest_number_of_lists(dev, M):
+    """1,024 of them, with narrow and wide tiles, forward and back, in 16 and 8 bits."""
+    g = gen_of(dev, M)
+    E, D, F = 1024, 16, 24
+    lengths = spread(M, E, g)
+    off = offsets_of(lengths, dev)
+    expert = torch.arange(E, device=dev).repeat_interleave(torch.tensor(lengths, device=dev))
+    X, W, dout = ints(g, (M, D), 3, BF16), ints(g, (E, F, D), 3, BF16), ints(g, (M, F), 2, BF16)
+    w = W.double()[expert]
+    ref = torch.einsum("md,mfd->mf", X.double(), w)
+    assert torch.equal(km.kmassign_experts(X, W, off), ref.to(BF16))
+    rows = torch.randperm(M, generator=g, device=dev).int()
+    out = km.kmassign_experts(X, W, off, rows=rows, places=rows)
+    want = torch.empty_like(ref)
+    want[rows.long()] = torch.einsum("md,mfd->mf", X.double()[rows.long()], w)
+    assert torch.equal(out, want.to(BF16))
+    dX, dW = km.kmassign_experts_grad(dout, X, W, off)
+    assert torch.equal(dX, torch.einsum("mf,mfd->md", dout.double(), w).to(BF16))
+    each = torch.einsum("mf,md->mfd", dout.double(), X.double())
+    assert torch.equal(dW, torch.zeros(E, F, D, dtype=torch.float64, device=dev).index_add_(0, expert, each).float())
+    q, v, xs, ws = whole_8_bits(g, M, D, E, F)
+    x, w = values(q, v, xs, ws)
+    ref = torch.einsum("md,mfd->mf", x, w[expert])
+    assert torch.equal(km.kmassign_experts(q, v, off, xscale=xs, wscale=ws, dtype=FP32), ref.float())
+
+
 # ---- how calls are made -----------------------------------------------------------------
 
 def test_captured_calls_replay(dev):
