@@ -7,9 +7,11 @@
 //
 // Both are bound by memory: every element crosses HBM once in each direction
 // (65,536 x 2,048 bf16: residual added, to 8 bits 137 us, 6.9 TB/s; gradients with
-// the residual's 187 us, 5.7 TB/s, of which the partial rows of the weight's take 8).
-// Rows at odd addresses are read element by element (30,011 x 777 fp32 gradients 69
-// us, 4.1 TB/s).
+// the residual's 165 us, 6.5 TB/s, of which the partial rows of the weight's take 8).
+// The gradient is near the issue rate: with single products and elements widened
+// one by one it took 188 us at 1,030 instructions a warp and row of 32 a lane.
+// Rows at odd addresses are read element by element (30,011 x 777 fp32 gradients 60
+// us, 4.7 TB/s; by aligned vectors, ends apart and the weight moved, 110).
 // A row lives in the registers of one warp, or of the warps of one block where
 // it is longer or where rows are few, so it is read once for its statistics and
 // its output alike.  Sums are fp32.  A warp's piece of a row is a whole number
@@ -240,6 +242,36 @@ struct NormGradArgs {
     float *parts;   // [groups, D], or NULL
 };
 
+// A row's elements in pairs (alone where a vector is one element): two products an
+// instruction.
+template <int VE>
+using Pair = std::remove_reference_t<decltype(Sums<VE>().p[0])>;
+template <int VE>
+constexpr int kPairs = VE == 1 ? 1 : VE / 2;
+
+__device__ __forceinline__ float both(float v, float) { return v; }
+__device__ __forceinline__ uint64_t both(float v, uint64_t) { return pair(v, v); }
+__device__ __forceinline__ float times(float a, float b) { return a * b; }
+__device__ __forceinline__ uint64_t times(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float fma_of(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ uint64_t fma_of(uint64_t a, uint64_t b, uint64_t c)
+{
+    fma_pair(c, a, b);
+    return c;
+}
+__device__ __forceinline__ float sum_of(float v) { return v; }
+__device__ __forceinline__ float sum_of(uint64_t v)
+{
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    return a + b;
+}
+
 template <typename T, int VE, int NV>
 struct GradRow {
     Raw<T, VE> d[NV], t[NV], s[NV];
@@ -250,7 +282,8 @@ struct GradRow {
 // share of the weight's gradient in registers; one partial row a group.  Where a
 // lane holds 16 bytes of a row, the next row is on its way while this one's sum is
 // joined, and the weight stays in registers (30,011 x 777 fp32 73 to 60 us, bf16 110
-// to 55; with 32 bytes 60,000 x 1,024 fp32 118 to 133, so not there).
+// to 55; with 32 bytes 60,000 x 1,024 fp32 118 to 133, and through shared memory
+// 65,536 x 2,048 bf16 165 to 177, so not there).
 template <typename T, int VE, int NV>
 __global__ void __launch_bounds__(512, VE * NV <= 8 ? 2 : 1)
     rmsnorm_grad_kernel(const NormGradArgs a, int warps, int groups)
@@ -263,21 +296,35 @@ __global__ void __launch_bounds__(512, VE * NV <= 8 ? 2 : 1)
     let_next_start();
     if (group >= groups)
         return;   // whole warps
-    float dw[NV][VE];
+    Sums<VE> dw[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < VE; ++i)
-            dw[j][i] = 0.0f;
+        dw[j].zero();
     const float mean = 1.0f / static_cast<float>(a.D);
     constexpr bool kAhead = VE * NV * sizeof(T) <= 16;
-    float kept[kAhead ? NV : 1][VE];   // the weight
+    Sums<VE> kept[kAhead ? NV : 1] = {};   // the weight
+    const auto load_w = [&](int j, Sums<VE> &w) {
+        float f[VE];
+        load_weight<T, VE>(a.weight, a.weight_fp32, column<VE>(j, warps, warp, lane), f);
+        w.set(f);
+    };
+    const auto weight_at = [&](int j, Sums<VE> &w) {
+        if constexpr (kAhead)
+            w = kept[j];
+        else
+            load_w(j, w);
+    };
+    const auto load = [](const Raw<T, VE> &r, Sums<VE> &to) {
+        float f[VE];
+        widen<T, VE>(r, f);
+        to.set(f);
+    };
     if constexpr (kAhead) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = column<VE>(j, warps, warp, lane);
             if (col < a.D)
-                load_weight<T, VE>(a.weight, a.weight_fp32, col, kept[j]);
+                load_w(j, kept[j]);
         }
     }
     const auto load_row = [&](GradRow<T, VE, NV> &r, int64_t row) {
@@ -308,48 +355,45 @@ __global__ void __launch_bounds__(512, VE * NV <= 8 ? 2 : 1)
             load_row(now, row);
         }
         const float rstd = now.rstd;
-        float dot = 0.0f;
+        const Pair<VE> rr = both(rstd, Pair<VE>{});
+        Pair<VE> dots = {};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = column<VE>(j, warps, warp, lane);
             if (col < a.D) {
-                float d[VE], t[VE], w[VE];
-                widen<T, VE>(now.d[j], d);
-                widen<T, VE>(now.t[j], t);
-                if constexpr (kAhead)
-                    memcpy(w, kept[j], sizeof(w));
-                else
-                    load_weight<T, VE>(a.weight, a.weight_fp32, col, w);
+                Sums<VE> d, t, w;
+                load(now.d[j], d);
+                load(now.t[j], t);
+                weight_at(j, w);
 #pragma unroll
-                for (int i = 0; i < VE; ++i) {
-                    const float n = t[i] * rstd;
-                    dw[j][i] = fmaf(d[i], n, dw[j][i]);
-                    dot = fmaf(d[i] * w[i], n, dot);
+                for (int i = 0; i < kPairs<VE>; ++i) {
+                    const Pair<VE> n = times(t.p[i], rr);
+                    dw[j].p[i] = fma_of(d.p[i], n, dw[j].p[i]);
+                    dots = fma_of(times(d.p[i], w.p[i]), n, dots);
                 }
             }
         }
-        const float c = block_sum(dot, buf, warps, slot) * mean;
+        const float c = block_sum(sum_of(dots), buf, warps, slot) * mean;
+        const Pair<VE> minus_c = both(-c, Pair<VE>{});
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = column<VE>(j, warps, warp, lane);
             if (col < a.D) {
-                float d[VE], t[VE], w[VE], o[VE];
-                widen<T, VE>(now.d[j], d);
-                widen<T, VE>(now.t[j], t);
-                if constexpr (kAhead)
-                    memcpy(w, kept[j], sizeof(w));
+                Sums<VE> d, t, w, r;
+                load(now.d[j], d);
+                load(now.t[j], t);
+                weight_at(j, w);
+                if (a.dtotal != nullptr)
+                    load(now.s[j], r);
                 else
-                    load_weight<T, VE>(a.weight, a.weight_fp32, col, w);
+                    r.zero();
 #pragma unroll
-                for (int i = 0; i < VE; ++i)
-                    o[i] = (d[i] * w[i] - t[i] * rstd * c) * rstd;
-                if (a.dtotal != nullptr) {
-                    float r[VE];
-                    widen<T, VE>(now.s[j], r);
-#pragma unroll
-                    for (int i = 0; i < VE; ++i)
-                        o[i] += r[i];
+                for (int i = 0; i < kPairs<VE>; ++i) {
+                    const Pair<VE> g = times(d.p[i], w.p[i]), n = times(t.p[i], rr);
+                    r.p[i] = fma_of(fma_of(n, minus_c, g), rr, r.p[i]);
                 }
+                float o[VE];
+                r.get(o);
                 store_raw<T, VE>(static_cast<T *>(a.dx) + at + col, narrow<T, VE>(o));
             }
         }
@@ -358,9 +402,12 @@ __global__ void __launch_bounds__(512, VE * NV <= 8 ? 2 : 1)
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = column<VE>(j, warps, warp, lane);
-            if (col < a.D)
+            if (col < a.D) {
+                float f[VE];
+                dw[j].get(f);
                 for (int i = 0; i < VE; ++i)
-                    a.parts[static_cast<int64_t>(group) * a.D + col + i] = dw[j][i];
+                    a.parts[static_cast<int64_t>(group) * a.D + col + i] = f[i];
+            }
         }
     }
 }
@@ -459,7 +506,7 @@ cudaError_t norm_type(const NormArgs &a, bool codes, int sms, cudaStream_t s)
 
 // Row groups of the gradient: as many as are resident at once by their
 // registers (64 up to 8 elements a lane), fewer where rows are few.  (65,536 x
-// 2,048 bf16: 16 warps an SM 182 us, 12 208, 24, which do not all fit, 215.)
+// 2,048 bf16: 16 warps an SM 182 us, 12 208, 24, which do not all fit, 215; now 165.)
 int grad_groups(int64_t N, int warps, int elems, int sms)
 {
     const int resident = elems <= 8 ? 32 : 16;

@@ -8,6 +8,7 @@
 
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 namespace kma {
 
@@ -63,25 +64,60 @@ __device__ __forceinline__ Raw<T, VE> load_raw(const T *p)
     return *reinterpret_cast<const Raw<T, VE> *>(p);
 }
 
+// Two 16-bit elements of a word at a time, as they lie: one instruction an
+// element up, one for both down.
 template <typename T, int VE>
 __device__ __forceinline__ void widen(const Raw<T, VE> &r, float (&f)[VE])
 {
-    T e[VE];
-    memcpy(e, &r, sizeof(r));
+    if constexpr (sizeof(T) == 2 && VE % 2 == 0) {
+        uint32_t u[VE / 2];
+        memcpy(u, &r, sizeof(r));
 #pragma unroll
-    for (int i = 0; i < VE; ++i)
-        f[i] = Elem<T>::up(e[i]);
+        for (int i = 0; i < VE / 2; ++i) {
+            if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+                f[2 * i] = __uint_as_float(u[i] << 16);
+                f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            } else {
+                __half2 h;
+                memcpy(&h, &u[i], sizeof(h));
+                const float2 v = __half22float2(h);
+                f[2 * i] = v.x;
+                f[2 * i + 1] = v.y;
+            }
+        }
+    } else {
+        T e[VE];
+        memcpy(e, &r, sizeof(r));
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+            f[i] = Elem<T>::up(e[i]);
+    }
 }
 
 template <typename T, int VE>
 __device__ __forceinline__ Raw<T, VE> narrow(const float (&f)[VE])
 {
-    T e[VE];
-#pragma unroll
-    for (int i = 0; i < VE; ++i)
-        e[i] = Elem<T>::down(f[i]);
     Raw<T, VE> r;
-    memcpy(&r, e, sizeof(r));
+    if constexpr (sizeof(T) == 2 && VE % 2 == 0) {
+        uint32_t u[VE / 2];
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i) {
+            if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                memcpy(&u[i], &h, sizeof(h));
+            } else {
+                const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+                memcpy(&u[i], &h, sizeof(h));
+            }
+        }
+        memcpy(&r, u, sizeof(r));
+    } else {
+        T e[VE];
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+            e[i] = Elem<T>::down(f[i]);
+        memcpy(&r, e, sizeof(r));
+    }
     return r;
 }
 
