@@ -34,8 +34,8 @@
 // the way; the scale warp forms those products for the tile's columns.
 //
 // Measured on GB300: 131,072 positions in 64 lists, 2,048 x 1,024 bf16: forward
-// 314 us (1,750 TFLOP/s; torch.bmm over equal lists 287-298), rows' gradient 327,
-// weights' 326 (fp32: 358).  32,768 in 8 lists, 4,096 x 4,096: 555 (1,980;
+// 314 us (1,750 TFLOP/s; torch.bmm over equal lists 287-298), rows' gradient 324,
+// weights' 316 (fp32: 350).  32,768 in 8 lists, 4,096 x 4,096: 555 (1,980;
 // torch.bmm 525-537).  256 lists of 128 of 2,048 x 1,024: 201, bound by HBM (1.27
 // GB).  Sixteen points to 8 of 256 experts: 74 us for 428 MB, bound by HBM.
 //
