@@ -514,9 +514,11 @@ int kmassign_clip(const void *const *grads, void *const *out, const int64_t *siz
  *             one for each row and 128 columns
  *   wscale    E4M3 only, fp32 [E, ceil(F / 128), ceil(D / 128)]: one for each
  *             128 x 128 block of W[e]
- *   offsets   int32 [E + 1], not descending, in [0, M] (kmassign_lists'); values
- *             outside are clamped, lists that overlap give rows of either.  NULL
- *             with E = 1: one list of all M positions (a plain product)
+ *   offsets   int32 [E + 1], not descending, in [0, M] (kmassign_lists').  Values
+ *             outside are clamped and a list starts no earlier than the one before
+ *             it ends: with others the results mean nothing, but nothing out of
+ *             range is touched.  NULL with E = 1: one list of all M positions (a
+ *             plain product)
  *   rows      int32 [M] or NULL (slots = 1, M <= R): position p takes row p.  With
  *             kmassign_lists' order over ids [N, k] and slots = k the points'
  *             own rows are taken.  An id that names no row gives a row of zeros

@@ -167,19 +167,37 @@ struct Schedule {
 };
 
 // Starts, ends and tiles before each expert, by one warp.  What the offsets
-// hold is clamped to [0, M], an end to its start: no position is out of range,
-// whatever they are.
+// hold is clamped to [0, M], and no list starts before the one in front of it
+// ends: whatever they are, no position is out of range and the lists have at most
+// M positions together, so that the tiles' numbers fit 31 bits.
 template <int NT>
 __device__ void form_lists(const ExpertsParams &p, int32_t *lists, int lane)
 {
     int32_t *begin = lists, *end = lists + (p.E + 1), *before = lists + 2 * (p.E + 1);
-    int done = 0;
+    const auto offset = [&](int e) { return min(max(__ldg(p.offsets + e), 0), p.M); };
+    int done = 0, reached = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
         const int e = e0 + lane;
         int lo = 0, hi = 0;
         if (e < p.E) {
-            lo = p.offsets == nullptr ? 0 : min(max(__ldg(p.offsets + e), 0), p.M);
-            hi = p.offsets == nullptr ? p.M : min(max(__ldg(p.offsets + e + 1), lo), p.M);
+            lo = p.offsets == nullptr ? 0 : offset(e);
+            hi = p.offsets == nullptr ? p.M : offset(e + 1);
+        }
+        if (__any_sync(0xffffffffu, e < p.E && (hi < lo || lo < reached))) {
+            const int start = max(reached, __shfl_sync(0xffffffffu, lo, 0));
+            hi = max(hi, start);
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int other = __shfl_up_sync(0xffffffffu, hi, d);
+                if (lane >= d)
+                    hi = max(hi, other);
+            }
+            lo = __shfl_up_sync(0xffffffffu, hi, 1);
+            if (lane == 0)
+                lo = start;
+        }
+        reached = __shfl_sync(0xffffffffu, hi, 31);   // of the last group: not used
+        if (e < p.E) {
             begin[e] = lo;
             end[e] = hi;
         }

@@ -211,6 +211,21 @@ def test_offsets_that_are_none_stay_in_bounds(dev, bad):
     assert dX.isfinite().all() and dW.isfinite().all()
 
 
+@pytest.mark.parametrize("M,E", [(10, 40), (3000, 40), (3000, 7)])
+def test_lists_that_overlap_stay_in_bounds(dev, M, E):
+    """Every other list would be all positions: the first has them, and nothing else is touched."""
+    D, F = 16, 264
+    X = torch.ones(M, D, device=dev, dtype=BF16)
+    W = torch.arange(1, E + 1, device=dev).view(E, 1, 1).expand(E, F, D).to(BF16).contiguous()
+    offsets = torch.tensor([0, M] * (E // 2 + 1), device=dev)[:E + 1].int()
+    guard = torch.full((M + 200, F), 7.0, device=dev, dtype=BF16)
+    km.kmassign_experts(X, W, offsets, out=guard[100:100 + M])
+    assert (guard[:100] == 7).all() and (guard[100 + M:] == 7).all() and (guard[100:100 + M] == D).all()
+    dW = km.kmassign_experts_grad(torch.ones(M, F, device=dev, dtype=BF16), X, W, offsets, need_x=False)[1]
+    assert (dW[0] == M).all() and not dW[1:].any()
+    assert km.kmassign_check() == 0
+
+
 def test_a_plain_product(dev):
     g = gen_of(dev, 3)
     for M, D, F in ((1, 8, 8), (37, 264, 392), (1000, 72, 200)):
