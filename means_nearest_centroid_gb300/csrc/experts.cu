@@ -60,8 +60,8 @@ namespace kma {
 
 namespace {
 
-constexpr int kConsumers = 8;   // warps; then one each for A, B, the MMAs and the scales or fixes
-constexpr int kWarpA = 8, kWarpB = 9, kWarpMma = 10, kWarpScale = 11, kWarpFix = 11;
+constexpr int kConsumers = 8;   // warps; then one each for A, B, the MMAs,
+constexpr int kWarpA = 8, kWarpB = 9, kWarpMma = 10;   // and the last, scales or fixes
 constexpr int kThreads = 32 * 12;
 // Registers a thread: the two warpgroups of consumers hold up to 128 sums each,
 // the third gives up some of the launch's for them.
@@ -96,7 +96,7 @@ struct Tile {
 // Shared memory behind the ring: the consumers' staging, scales, then the lists'
 // starts, ends and the tiles before each expert, then barriers.
 struct Layout {
-    uint32_t ring, staging, scale, lists, bars, end;
+    uint32_t staging, scale, lists, bars, end;
 };
 
 __host__ __device__ constexpr uint32_t stage_bytes(int NT) { return kPartA + NT / 2 * 128; }
@@ -104,7 +104,6 @@ __host__ __device__ constexpr uint32_t stage_bytes(int NT) { return kPartA + NT 
 __host__ __device__ inline Layout layout_of(int NT, int stages, int E, bool scaled)
 {
     Layout l;
-    l.ring = 0;
     l.staging = stages * stage_bytes(NT);
     l.scale = l.staging + kConsumers * kWarpStaging;
     l.lists = l.scale + (scaled ? kScaleStages * scale_bytes(NT) : 0u);
@@ -598,7 +597,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     wait_warp(bar(kLast), 0u, abort_flag, kDrainLimitNs, false);
                 }
             }
-        } else {   // kWarpScale, kWarpFix
+        } else {
             if constexpr (kFixes) {
                 // K-blocks with missing rows: once both operands have landed here the
                 // rows are zeroed and the pair's barrier gets both loaders' arrivals.
@@ -805,8 +804,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // long: two CTAs with MMAs and hand-overs of their own and the weights multicast
 // (537 us), scales loaded four k-blocks at a time (558), 64 columns in flight a
 // warp (605).  Slower: 128 columns and four accumulators (667).  Lists are rounded
-// up to 256, so only products of many positions an
-// expert come here.
+// up to 256, so only products of many positions an expert come here.
 
 constexpr int kLoad8 = 8, kIssue8 = 9;   // warps behind the 8 of consumers; two issue
 
@@ -1200,7 +1198,7 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, ExpertsParams p, 
 }
 
 cudaError_t launch8(const CUtensorMap &a, const CUtensorMap &b, ExpertsParams p, int sms,
-                            size_t smem_optin, cudaStream_t stream)
+                    size_t smem_optin, cudaStream_t stream)
 {
     p.stages = 0;
     for (int s = kMaxRing; s >= 2 && p.stages == 0; --s)

@@ -437,7 +437,10 @@ __global__ void __launch_bounds__(1024)
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-int warps_for(int64_t D, int elems) { return static_cast<int>((D + 32 * elems - 1) / (32 * elems)); }
+int warps_for(int64_t D, int elems)
+{
+    return static_cast<int>((D + 32 * elems - 1) / (32 * elems));
+}
 
 // Vectors a thread: a row in one warp, or in several where it takes more than
 // `elems` elements a lane, in up to 16; spread over up to 16 warps where rows
@@ -458,6 +461,7 @@ int vectors_for(int64_t N, int64_t D, int elems, int sms)
     }
     return nv;
 }
+
 template <typename T, bool CODES, int VE, int NV>
 cudaError_t run_norm(const NormArgs &a, cudaStream_t s)
 {
@@ -502,7 +506,6 @@ cudaError_t norm_type(const NormArgs &a, bool codes, int sms, cudaStream_t s)
 {
     return codes ? norm_shape<T, true>(a, sms, s) : norm_shape<T, false>(a, sms, s);
 }
-
 
 // Row groups of the gradient: as many as are resident at once by their
 // registers (64 up to 8 elements a lane), fewer where rows are few.  (65,536 x
@@ -582,7 +585,8 @@ cudaError_t launch_rmsnorm_grad(const void *dout, int dtype, int64_t N, int64_t 
 {
     int groups = 0;
     const NormGradArgs a{dout, total, weight, dtotal, weight_dtype == kFp32,
-                         rstd, N,     static_cast<int32_t>(D), dX, dweight != nullptr ? parts : nullptr};
+                         rstd, N,     static_cast<int32_t>(D), dX,
+                         dweight != nullptr ? parts : nullptr};
     cudaError_t e = dtype == kFp32   ? grad_type<float>(a, sms, &groups, stream)
                     : dtype == kBf16 ? grad_type<__nv_bfloat16>(a, sms, &groups, stream)
                                      : grad_type<__half>(a, sms, &groups, stream);
