@@ -535,6 +535,24 @@ def test_norm_gradients(dev, N, D, dtype):
     assert again is dt and torch.equal(again, dX)
 
 
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16], ids=str)
+@pytest.mark.parametrize("N,D", [(12000, 40), (12000, 33), (3000, 500), (4000, 129), (11000, 256)])
+def test_norm_gradients_of_many_rows(dev, N, D, dtype):
+    """More rows than are in flight, so that each group takes several in turn; in place as well."""
+    test_norm_gradients(dev, N, D, dtype)
+    g = gen_of(dev, 6)
+    x, dout, w = (torch.randn(*shape, generator=g, device=dev).to(dtype) for shape in ((N, D), (N, D), (D,)))
+    rstd = torch.rand(N, generator=g, device=dev)
+    dX, dw = km.kmassign_rmsnorm_grad(dout, x, w, rstd)
+    rows = torch.randperm(N, generator=g, device=dev)[:100]
+    few, _ = km.kmassign_rmsnorm_grad(dout[rows], x[rows], w, rstd[rows])
+    there, again = km.kmassign_rmsnorm_grad(dout, x, w, rstd, dX=dout)
+    assert there is dout and torch.equal(there, dX) and torch.equal(again, dw)
+    # Other rows beside it leave a row's sum as it was, but for the number of warps it takes: 2 (sums_of(D) + 8)
+    # roundings of |n| mean |g n| < 10, and half a step of the result on both sides.
+    assert torch.allclose(few.double(), dX[rows].double(), rtol=2 * OUT[dtype] + 1e-5, atol=1e-4)
+
+
 def test_norm_gradients_are_differences(dev):
     g = gen_of(dev, 5)
     N, D, h = 4, 24, 1e-5
