@@ -858,7 +858,8 @@ def kmassign_experts(X, W, offsets=None, rows=None, slots: int = 1, places=None,
     if code == 3:
         _need_shape(xscale, "xscale", (R, _blocks(D)))
         _need_shape(wscale, "wscale", (*W.shape[:-2], _blocks(F), _blocks(D)))
-    if any(t is not None and t.requires_grad for t in (X, W, xscale, wscale)):
+    if X.requires_grad or W.requires_grad or (
+            code == 3 and (xscale.requires_grad or wscale.requires_grad)):
         _need_detached("kmassign_experts", "X, W or a scale")
     given = out is not None
     if not given:
@@ -869,9 +870,11 @@ def kmassign_experts(X, W, offsets=None, rows=None, slots: int = 1, places=None,
     out_code = _need_float(out, "out")
     if code != 3 and out_code not in (0, code):
         raise TypeError(f"out must be {X.dtype} or float32, got {out.dtype}")
-    out_rows, out_cols = _need_matrix(out, "out")
-    if out_cols != F or (places is None and out_rows != M):
-        raise ValueError(f"out must have shape {(M, F)}, got {tuple(out.shape)}")
+    out_rows = M
+    if given:
+        out_rows, out_cols = _need_matrix(out, "out")
+        if out_cols != F or (places is None and out_rows != M):
+            raise ValueError(f"out must have shape {(M, F)}, got {tuple(out.shape)}")
     rc = library().kmassign_experts(
         X.data_ptr(), code, R, D, W.data_ptr(), E, F, _ptr(xscale), _ptr(wscale), _ptr(offsets), M,
         _ptr(rows), slots, _ptr(places), out.data_ptr(), out_code, out_rows,
@@ -1026,7 +1029,9 @@ def kmassign_rmsnorm_grad(dout, total, weight, rstd, dtotal=None, dX=None, dweig
     if dtotal is not None:
         _need_cuda(dtotal, "dtotal", total.dtype)
         _need_shape(dtotal, "dtotal", (N, D))
-    if any(t is not None and t.requires_grad for t in (dout, total, weight, rstd, dtotal)):
+    if dout.requires_grad or total.requires_grad or rstd.requires_grad or (
+            weight is not None and weight.requires_grad) or (
+            dtotal is not None and dtotal.requires_grad):
         _need_detached("kmassign_rmsnorm_grad", "an input")
     given = [t for t in (dX, dweight) if t is not None]
     if dX is None:
