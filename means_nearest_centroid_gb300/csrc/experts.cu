@@ -1139,9 +1139,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 __global__ void __launch_bounds__(256)
-    listed_rows_kernel(const int32_t *offsets, int32_t E, int32_t M, RowMap map, int32_t *row)
+    listed_rows_kernel(const int32_t *offsets, int32_t E, int32_t M, RowMap map, int32_t *row,
+                       int32_t *zero)
 {
     wait_for_previous();
+    if (zero != nullptr && blockIdx.x == 0 && threadIdx.x == 0)
+        *zero = 0;
     const int32_t lo = offsets == nullptr ? 0 : min(max(__ldg(offsets), 0), M);
     const int32_t hi = offsets == nullptr ? M : min(max(__ldg(offsets + E), 0), M);
     for (int64_t at = blockIdx.x * 256 + threadIdx.x; at < M; at += gridDim.x * 256)
@@ -1288,11 +1291,11 @@ cudaError_t launch_experts(ExpertsKind kind, bool e8, int type, const CUtensorMa
 }
 
 cudaError_t launch_listed_rows(const int32_t *offsets, int32_t E, int32_t M, RowMap map,
-                               int32_t *row, cudaStream_t stream)
+                               int32_t *row, int32_t *zero, cudaStream_t stream)
 {
     const int blocks =
         static_cast<int>(std::min<int64_t>((static_cast<int64_t>(M) + 255) / 256, 4096));
-    return launch_after(listed_rows_kernel, blocks, 256, 0, stream, offsets, E, M, map, row);
+    return launch_after(listed_rows_kernel, blocks, 256, 0, stream, offsets, E, M, map, row, zero);
 }
 
 cudaError_t launch_gather_rows(const int32_t *offsets, int32_t E, int32_t M, RowMap map,

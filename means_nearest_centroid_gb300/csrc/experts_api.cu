@@ -253,7 +253,11 @@ int kmassign_experts_grad(const void *dout, int32_t dtype, int64_t out_rows, int
     if (gathers) {
         holes = reinterpret_cast<int32_t *>(q);
         q += 16;
-        if (dW != nullptr)
+        // a position whose place is missing has a gradient of zeros: it may be summed
+        if (sum)
+            e = kma::launch_listed_rows(offsets, static_cast<int32_t>(E), static_cast<int32_t>(M),
+                                        from, reinterpret_cast<int32_t *>(q), holes, st);
+        else if (dW != nullptr)
             e = cudaMemsetAsync(holes, 0, 4, st);
     }
     if (e == cudaSuccess && places != nullptr)
@@ -300,11 +304,8 @@ int kmassign_experts_grad(const void *dout, int32_t dtype, int64_t out_rows, int
         int32_t *sorted = reinterpret_cast<int32_t *>(q + 2 * ids);
         int32_t *total = reinterpret_cast<int32_t *>(q + 3 * ids);
         uint8_t *const space = q + 3 * ids + 16;
-        // a position whose place is missing has a gradient of zeros: it may be summed
-        e = kma::launch_listed_rows(offsets, p.E, p.M, from, row, st);
-        if (e == cudaSuccess)
-            e = kma::launch_lists(row, M, R, order, sorted, nullptr, total, space, dX,
-                                  static_cast<size_t>(R) * D * 2, dev.sms, st);
+        e = kma::launch_lists(row, M, R, order, sorted, nullptr, total, space, dX,
+                              static_cast<size_t>(R) * D * 2, dev.sms, st);
         if (e == cudaSuccess)
             e = kma::launch_lookup_grad(by_position, dtype, row, nullptr, nullptr, M, 1, R, D, 1.0f,
                                         -1, false, order, sorted, total,

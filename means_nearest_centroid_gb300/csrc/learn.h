@@ -178,9 +178,10 @@ cudaError_t launch_experts(ExpertsKind kind, bool e8, int type, const CUtensorMa
                            const CUtensorMap &b, ExpertsParams p, int sms, size_t smem_optin,
                            cudaStream_t stream);
 cudaError_t experts_status_read_and_clear(int *code);
-// row[p] = the row that map names for positions of a list, -1 for the others.
+// row[p] = the row that map names for positions of a list, -1 for the others;
+// *zero = 0 (may be NULL).
 cudaError_t launch_listed_rows(const int32_t *offsets, int32_t E, int32_t M, RowMap map,
-                               int32_t *row, cudaStream_t stream);
+                               int32_t *row, int32_t *zero, cudaStream_t stream);
 // to[p] = the row (pitch bytes, a multiple of 16) that map names for positions
 // of a list, zeros for the others and where also names none; *holes (may be
 // NULL) is set to 1 if a position of a list gets zeros.
