@@ -519,9 +519,10 @@ int kmassign_clip(const void *const *grads, void *const *out, const int64_t *siz
  *             it ends: with others the results mean nothing, but nothing out of
  *             range is touched.  NULL with E = 1: one list of all M positions (a
  *             plain product)
- *   rows      int32 [M] or NULL (slots = 1, M <= R): position p takes row p.  With
- *             kmassign_lists' order over ids [N, k] and slots = k the points'
- *             own rows are taken.  An id that names no row gives a row of zeros
+ *   rows      int32 [M] or NULL (slots = 1 unless M = 0, M <= R): position p takes
+ *             row p.  With kmassign_lists' order over ids [N, k] and slots = k the
+ *             points' own rows are taken.  An id that names no row gives a row of
+ *             zeros
  *   places    int32 [M] or NULL (M <= out_rows): position p goes to row p.  Ids
  *             outside [0, out_rows) are not written, and rows that no position
  *             names stay as they were; an id named twice holds either product

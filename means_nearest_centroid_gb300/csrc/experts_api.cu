@@ -71,7 +71,7 @@ int check_shape(const Shape &s, int32_t type, const int32_t *offsets, const int3
 {
     if (s.R < 0 || s.R >= kLimit || s.M < 0 || s.M >= kLimit / 2 || s.out_rows < 0 ||
         s.out_rows >= kLimit || s.E < 1 || s.E > KMASSIGN_EXPERTS_MAX || s.slots < 1 ||
-        (rows == nullptr && (s.M > s.R || s.slots != 1)) ||
+        (rows == nullptr && (s.M > s.R || (s.M > 0 && s.slots != 1))) ||
         (places == nullptr && s.M > s.out_rows) || (offsets == nullptr && s.E != 1))
         return KMASSIGN_ERR_SHAPE;
     const int64_t step = type == KMASSIGN_E4M3 ? 16 : 8;

@@ -116,6 +116,15 @@ def test_norms_of_nothing_do_nothing(lib):
     assert norm_grad(lib, N=0, dout=NULL, total=NULL, rstd=NULL, dX=NULL) == 0
 
 
+def test_a_batch_without_points_may_have_slots(lib):
+    """An empty tensor's pointer is NULL: no positions, whatever the slots of a point."""
+    for e8 in (dict(), dict(dtype=E4M3, xs=E_, ws=E_)):
+        assert experts(lib, M=0, slots=8, **e8) == 0
+        assert experts(lib, M=0, R=0, X=NULL, slots=8, out=NULL, out_rows=0, **e8) == 0
+        assert experts(lib, M=0, slots=0, **e8) == S["KMASSIGN_ERR_SHAPE"]
+    assert grad(lib, M=0, slots=8, dX=NULL, dW=NULL) == S["KMASSIGN_ERR_NULL"]   # the next check
+
+
 @pytest.mark.parametrize("call", [
     lambda x: km.kmassign_experts(x, x), lambda x: km.kmassign_experts_grad(x, x, x),
     lambda x: km.kmassign_rmsnorm(x), lambda x: km.kmassign_rmsnorm_grad(x, x, None, x[:, 0]),
