@@ -549,9 +549,8 @@ int kmassign_experts(const void *X, int32_t dtype, int64_t R, int64_t D, const v
  *     dW[e] = sum over p of list e of dY_p . X[rows[p] / slots]^T
  *   dout   dtype [out_rows, F]
  *   dX     dtype [R, D] or NULL, every row written (0 where no position names
- *          it).  With rows each position's product is rounded to dtype before
- *          the sum over positions (fp32, in the lists' order), as the forward
- *          product of a row is
+ *          it).  With rows the positions' products are added in fp32, in the
+ *          lists' order, and rounded once
  *   dW     dw_dtype [E, F, D] or NULL (not both), KMASSIGN_FP32 or dtype; zeros
  *          for an expert without positions
  * A position whose row or place does not exist adds nothing.  Everything else,

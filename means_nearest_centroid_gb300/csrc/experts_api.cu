@@ -4,6 +4,7 @@
 #include "kmassign.h"
 #include "learn.h"
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
@@ -49,14 +50,15 @@ bool rows_map(CUtensorMap *m, int32_t type, const void *p, int64_t rows, int64_t
     return kma::encode_tiled(m, map_type(type), p, 2, dims, strides, boxes);
 }
 
-// W as [E][F][D].
+// W as [E][F][D], or the first `cols` of its rows' D elements.
 bool weights_map(CUtensorMap *m, int32_t type, const void *p, int64_t E, int64_t F, int64_t D,
-                 uint32_t box)
+                 int64_t cols, uint32_t box)
 {
     const uint64_t es = type == KMASSIGN_E4M3 ? 1 : 2;
-    const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(F),
+    const uint64_t dims[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(F),
                               static_cast<uint64_t>(E)};
-    const uint64_t strides[2] = {dims[0] * es, dims[0] * dims[1] * es};
+    const uint64_t strides[2] = {static_cast<uint64_t>(D) * es,
+                                 static_cast<uint64_t>(D) * dims[1] * es};
     const uint32_t boxes[3] = {static_cast<uint32_t>(128 / es), box, 1};
     return kma::encode_tiled(m, map_type(type), p, 3, dims, strides, boxes);
 }
@@ -104,6 +106,18 @@ ExpertsParams params_of(const Shape &s, const int32_t *offsets)
     p.M = static_cast<int32_t>(s.M);
     p.timeout_ns = kma::wait_timeout_ns();
     return p;
+}
+
+// How many columns of the rows' gradients are formed in fp32 at a time where they are
+// summed by row: all where they take half of the GiB that the pool keeps, else half, which
+// take the room of X's 16-bit rows.  (15,009 positions of 1,000: both gradients 133 us, in
+// halves 154; 131,072 of 2,048, 1 GiB: 1,137 back to back but 1,286 alone, for the pool
+// then maps memory in every call, in halves 1,164 and 1,210; of 7,168: 3,200 and 5,100,
+// 3,070 and 3,745.)
+int64_t sum_columns(int64_t M, int64_t D)
+{
+    constexpr int64_t kRoom = int64_t(1) << 29;
+    return M * D * 4 <= kRoom ? D : std::min(D, (D + 511) / 512 * 256);
 }
 
 RowMap map_of(const int32_t *ids, int32_t slots, int64_t rows)
@@ -165,7 +179,7 @@ int kmassign_experts(const void *X, int32_t dtype, int64_t R, int64_t D, const v
     const RowMap from = map_of(rows, slots, R);
     const bool gathers = rows != nullptr && few;
     CUtensorMap a, b;
-    if (!weights_map(&a, dtype, W, E, F, D, kma::kExpertsBoxA) ||
+    if (!weights_map(&a, dtype, W, E, F, D, D, kma::kExpertsBoxA) ||
         (sorted.get() != nullptr ? !rows_map(&b, dtype, sorted.get(), M, D, box)
                                  : !rows_map(&b, dtype, X, R, D, gathers ? 1 : box)))
         return KMASSIGN_ERR_CUDA;
@@ -228,15 +242,19 @@ int kmassign_experts_grad(const void *dout, int32_t dtype, int64_t out_rows, int
     }
     // Rows that ids name come into the lists' order first.  Without row ids
     // position p's gradient is row p's; with them the rows' gradients are formed
-    // position by position, in the rows' type, and summed by row like those of a
-    // lookup (sorted, no atomics).
+    // position by position, in fp32, and summed by row like those of a lookup
+    // (sorted, no atomics), so many columns at a time.
     const RowMap from = map_of(rows, slots, R), placed = map_of(places, 1, out_rows);
     const bool sum = dX != nullptr && rows != nullptr;
+    const int64_t cols = sum_columns(M, D), rest = D - (D - 1) / cols * cols;
     const size_t ids = sum ? up16(static_cast<size_t>(M) * 4) : 0;
     const size_t sort = sum ? up16(kma::lists_scratch_bytes(M, R, dev.sms)) : 0;
-    const size_t parts = sum ? up16(kma::lookup_grad_parts_bytes(M, D, dev.sms)) : 0;
+    const size_t parts = sum ? up16(std::max(kma::lookup_grad_parts_bytes(M, cols, dev.sms),
+                                             kma::lookup_grad_parts_bytes(M, rest, dev.sms)))
+                             : 0;
     // X's rows, and later the rows' gradients
-    const size_t each = rows != nullptr ? static_cast<size_t>(M) * D * 2 : 0;
+    const size_t each = std::max(rows != nullptr && dW != nullptr ? static_cast<size_t>(M) * D * 2 : 0,
+                                 sum ? static_cast<size_t>(M) * cols * 4 : 0);
     const size_t dys = places != nullptr ? static_cast<size_t>(M) * F * 2 : 0;
     const bool gathers = rows != nullptr || places != nullptr;
     Scratch scratch(each + dys + (gathers ? 16 : 0) + 3 * ids + (sum ? 16 : 0) + sort + parts,
@@ -284,34 +302,36 @@ int kmassign_experts_grad(const void *dout, int32_t dtype, int64_t out_rows, int
         if (e == cudaSuccess)
             e = kma::launch_experts(kma::kWeightsGrad, false, dtype, a, b, p, dev.sms, dev.smem, st);
     }
-    if (e == cudaSuccess && dX != nullptr) {
-        if (!weights_map(&a, dtype, W, E, F, D, kma::kExpertsBoxMn) ||
-            !rows_map(&b, dtype, dy, dy_rows, F, kma::kExpertsBoxB))
-            return KMASSIGN_ERR_CUDA;
-        p.kblocks = static_cast<int32_t>((F + 63) / 64);
-        p.from = placed;
-        p.zero_rest = rows == nullptr;
-        p.out = rows == nullptr ? dX : by_position;
-        p.out_type = dtype;
-        e = kma::launch_experts(kma::kRowsGrad, false, dtype, a, b, p, dev.sms, dev.smem, st);
-        if (e == cudaSuccess && rows == nullptr && R > M)
-            e = cudaMemsetAsync(static_cast<uint8_t *>(dX) + static_cast<size_t>(M) * D * 2, 0,
-                                static_cast<size_t>(R - M) * D * 2, st);
-    }
-    if (e == cudaSuccess && sum) {
-        int32_t *row = reinterpret_cast<int32_t *>(q);
-        int32_t *order = reinterpret_cast<int32_t *>(q + ids);
-        int32_t *sorted = reinterpret_cast<int32_t *>(q + 2 * ids);
-        int32_t *total = reinterpret_cast<int32_t *>(q + 3 * ids);
-        uint8_t *const space = q + 3 * ids + 16;
+    int32_t *const row = reinterpret_cast<int32_t *>(q);
+    int32_t *const order = reinterpret_cast<int32_t *>(q + ids);
+    int32_t *const sorted = reinterpret_cast<int32_t *>(q + 2 * ids);
+    int32_t *const total = reinterpret_cast<int32_t *>(q + 3 * ids);
+    uint8_t *const space = q + 3 * ids + 16;
+    if (e == cudaSuccess && sum)
         e = kma::launch_lists(row, M, R, order, sorted, nullptr, total, space, dX,
                               static_cast<size_t>(R) * D * 2, dev.sms, st);
-        if (e == cudaSuccess)
-            e = kma::launch_lookup_grad(by_position, dtype, row, nullptr, nullptr, M, 1, R, D, 1.0f,
-                                        -1, false, order, sorted, total,
-                                        reinterpret_cast<float *>(space + sort), dX, dtype, nullptr,
-                                        dev.sms, st);
+    const int64_t width = sum ? cols : D;
+    for (int64_t d = 0; e == cudaSuccess && dX != nullptr && d < D; d += width) {
+        const int64_t n = std::min(width, D - d);
+        if (!weights_map(&a, dtype, static_cast<const uint8_t *>(W) + 2 * d, E, F, D, n,
+                         kma::kExpertsBoxMn) ||
+            !rows_map(&b, dtype, dy, dy_rows, F, kma::kExpertsBoxB))
+            return KMASSIGN_ERR_CUDA;
+        p.mdim = static_cast<int32_t>(n);
+        p.kblocks = static_cast<int32_t>((F + 63) / 64);
+        p.from = placed;
+        p.zero_rest = !sum;
+        p.out = sum ? by_position : dX;
+        p.out_type = sum ? KMASSIGN_FP32 : dtype;
+        e = kma::launch_experts(kma::kRowsGrad, false, dtype, a, b, p, dev.sms, dev.smem, st);
+        if (e == cudaSuccess && sum)
+            e = kma::launch_sum_rows(reinterpret_cast<const float *>(by_position), M, n, order,
+                                     sorted, total, reinterpret_cast<float *>(space + sort),
+                                     static_cast<uint8_t *>(dX) + 2 * d, dtype, D, dev.sms, st);
     }
+    if (e == cudaSuccess && dX != nullptr && rows == nullptr && R > M)
+        e = cudaMemsetAsync(static_cast<uint8_t *>(dX) + static_cast<size_t>(M) * D * 2, 0,
+                            static_cast<size_t>(R - M) * D * 2, st);
     rc = done(e);
     return scratch.release() ? rc : KMASSIGN_ERR_CUDA;
 }

@@ -121,6 +121,12 @@ cudaError_t launch_lookup_grad(const void *dout, int dtype, const int32_t *idx,
                                const int32_t *order, const int32_t *rows, const int32_t *total,
                                float *parts, void *dtable, int grad_dtype, float *dweights,
                                int sms, cudaStream_t stream);
+// out[r] = the sum of from's rows (fp32 [M, D]) that are sorted to r, rounded once
+// to dtype (16 bits); out's rows are pitch elements apart.  D and pitch are multiples
+// of 4, from and out 16-byte aligned; order, rows, total, parts as above.
+cudaError_t launch_sum_rows(const float *from, int64_t M, int64_t D, const int32_t *order,
+                            const int32_t *rows, const int32_t *total, float *parts, void *out,
+                            int dtype, int64_t pitch, int sms, cudaStream_t stream);
 // Whether launch_lookup_grad can form dweights (else NULL there, and
 // launch_dweights).
 bool dweights_with_dtable(int64_t D);

@@ -413,6 +413,7 @@ struct GradArgs {
     int32_t chunk;             // sorted places per chunk, a multiple of 8
     int32_t slices;            // column slices of a row
     int32_t k, K, D;
+    int32_t pitch;             // elements from a row of dtable to the next
     int32_t skip;              // a row that takes no gradient, or -1
     float scale;
     bool accumulate;
@@ -421,7 +422,7 @@ struct GradArgs {
 template <typename G, int VE>
 __device__ __forceinline__ void put(const GradArgs &a, int32_t r, int col, const float (&acc)[VE])
 {
-    G *p = static_cast<G *>(a.dtable) + static_cast<int64_t>(r) * a.D + col;
+    G *p = static_cast<G *>(a.dtable) + static_cast<int64_t>(r) * a.pitch + col;
     float f[VE];
 #pragma unroll
     for (int v = 0; v < VE; ++v)
@@ -728,28 +729,50 @@ int64_t chunk_places(int64_t M, int64_t D, int sms)
     return std::min<int64_t>(512, std::max<int64_t>(16, (want + 7) / 8 * 8));
 }
 
+template <typename T, typename G, int VE, bool DW = false>
+cudaError_t segments_launch(const GradArgs &a, cudaStream_t stream)
+{
+    return by_group(a.D, [&](auto LG) {
+        constexpr int kGroup = decltype(LG)::value, kUnits = kThreads / kGroup;
+        const int64_t want = (a.chunks * a.slices + kUnits - 1) / kUnits;
+        if (want > 0x7fffffff)
+            return cudaErrorInvalidValue;
+        const unsigned blocks = static_cast<unsigned>(want);
+        cudaError_t e =
+            launch_after(segment_kernel<T, G, VE, kGroup, DW>, blocks, kThreads, 0, stream, a);
+        if (e == cudaSuccess && a.chunks > 1)
+            e = launch_after(join_kernel<G, VE, kGroup>, blocks, kThreads, 0, stream, a);
+        return e;
+    });
+}
+
 template <typename T, typename G>
 cudaError_t grad_launch(const GradArgs &a, int ve, cudaStream_t stream)
 {
     return by_elems<T>(ve, [&](auto VE) {
-        return by_group(a.D, [&](auto LG) {
-            constexpr int kUnits = kThreads / decltype(LG)::value;
-            const int64_t want = (a.chunks * a.slices + kUnits - 1) / kUnits;
-            if (want > 0x7fffffff)
-                return cudaErrorInvalidValue;
-            const unsigned blocks = static_cast<unsigned>(want);
-            cudaError_t e =
-                a.dweights != nullptr
-                    ? launch_after(segment_kernel<T, G, decltype(VE)::value, decltype(LG)::value, true>,
-                                   blocks, kThreads, 0, stream, a)
-                    : launch_after(segment_kernel<T, G, decltype(VE)::value, decltype(LG)::value, false>,
-                                   blocks, kThreads, 0, stream, a);
-            if (e == cudaSuccess && a.chunks > 1)
-                e = launch_after(join_kernel<G, decltype(VE)::value, decltype(LG)::value>,
-                                 blocks, kThreads, 0, stream, a);
-            return e;
-        });
+        constexpr int kElems = decltype(VE)::value;
+        return a.dweights != nullptr ? segments_launch<T, G, kElems, true>(a, stream)
+                                     : segments_launch<T, G, kElems>(a, stream);
     });
+}
+
+// What does not depend on the entry point: rows of D elements, as far apart.
+GradArgs grad_args(const void *dout, int64_t M, int64_t D, const int32_t *order,
+                   const int32_t *rows, const int32_t *total, float *parts, void *dtable, int sms)
+{
+    GradArgs a{};
+    a.dout = dout;
+    a.order = order;
+    a.rows = rows;
+    a.total = total;
+    a.dtable = dtable;
+    a.parts = parts;
+    a.M = M;
+    a.slices = static_cast<int32_t>(column_slices(D));
+    a.chunk = static_cast<int32_t>(chunk_places(M, D, sms));
+    a.chunks = (M + a.chunk - 1) / a.chunk;
+    a.D = a.pitch = static_cast<int32_t>(D);
+    return a;
 }
 
 }  // namespace
@@ -877,24 +900,13 @@ cudaError_t launch_lookup_grad(const void *dout, int dtype, const int32_t *idx,
         {{dout, dtype_bytes(dtype)},
          {dweights != nullptr ? table : nullptr, dtype_bytes(dtype)},
          {dtable, dtype_bytes(grad_dtype)}});
-    GradArgs a{};
-    a.dout = dout;
+    GradArgs a = grad_args(dout, M, D, order, rows, total, parts, dtable, sms);
     a.weights = weights;
     a.idx = idx;
     a.table = table;
     a.dweights = dweights;
-    a.order = order;
-    a.rows = rows;
-    a.total = total;
-    a.dtable = dtable;
-    a.parts = parts;
-    a.M = M;
-    a.slices = static_cast<int32_t>(column_slices(D));
-    a.chunk = static_cast<int32_t>(chunk_places(M, D, sms));
-    a.chunks = (M + a.chunk - 1) / a.chunk;
     a.k = k;
     a.K = static_cast<int32_t>(K);
-    a.D = static_cast<int32_t>(D);
     a.skip = skip;
     a.scale = scale;
     a.accumulate = accumulate;
@@ -904,6 +916,19 @@ cudaError_t launch_lookup_grad(const void *dout, int dtype, const int32_t *idx,
             return grad_launch<T, float>(a, ve, stream);
         return grad_launch<T, T>(a, ve, stream);
     });
+}
+
+cudaError_t launch_sum_rows(const float *from, int64_t M, int64_t D, const int32_t *order,
+                            const int32_t *rows, const int32_t *total, float *parts, void *out,
+                            int dtype, int64_t pitch, int sms, cudaStream_t stream)
+{
+    GradArgs a = grad_args(from, M, D, order, rows, total, parts, out, sms);
+    a.k = 1;
+    a.pitch = static_cast<int32_t>(pitch);
+    a.skip = -1;
+    a.scale = 1.0f;
+    return dtype == kBf16 ? segments_launch<float, __nv_bfloat16, 4>(a, stream)
+                          : segments_launch<float, __half, 4>(a, stream);
 }
 
 }  // namespace kma

@@ -7,7 +7,7 @@ import torch
 
 import means_nearest_centroid_gb300 as km
 from test_experts_gpu import (  # noqa: F401
-    BF16, E4M3, FP32, dev, no_kernel_gave_up)
+    BF16, E4M3, FP16, FP32, OUT, U, dev, gen_of, ints, no_kernel_gave_up)
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +36,68 @@ def test_a_batch_without_points(dev, k):  # noqa: F811
     assert (given == 7).all()
     dX, dW = km.kmassign_experts_grad(dout, some, W, off, rows=order, slots=k)
     assert dX.shape == some.shape and not dX.any() and not dW.any()
+
+
+# ---- rows' gradients by ids --------------------------------------------------------
+
+def exact_rows_gradient(dout, W, off, rows, slots, R):
+    """In 64 bits, nothing rounded; and the sum of magnitudes."""
+    dX = torch.zeros(R, W.shape[2], dtype=torch.float64, device=W.device)
+    size = dX.clone()
+    for e in range(W.shape[0]):
+        p = torch.arange(int(off[e]), int(off[e + 1]), device=W.device)
+        r, d, w = rows.view(-1)[p].long() // slots, dout[p].double(), W[e].double()
+        dX.index_add_(0, r, d @ w)
+        size.index_add_(0, r, d.abs() @ w.abs())
+    return dX, size
+
+
+@pytest.mark.parametrize("E,N,k,D,F", [(4, 30, 2, 40, 64), (8, 700, 4, 520, 136), (64, 500, 8, 264, 72),
+                                       (2, 9, 2, 2048, 1000), (6, 3000, 3, 72, 2056)])
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=str)
+def test_a_point_s_gradient_is_rounded_once(dev, E, N, k, D, F, dtype):  # noqa: F811
+    """The products of a point's positions cancel for the most part: what is left of them is as near as
+    fp32 sums of F and k terms and one rounding allow."""
+    g = gen_of(dev, N + D)
+    order, off = km.kmassign_lists(torch.randint(0, E, (N, k), generator=g, device=dev).int(), E)
+    W = torch.randn(E, F, D, generator=g, device=dev).to(dtype)
+    dout = torch.randn(N * k, F, generator=g, device=dev).to(dtype)
+    X = torch.zeros(N, D, device=dev, dtype=dtype)
+    ref, size = exact_rows_gradient(dout, W, off, order, k, N)
+    for need_w in (False, True):
+        dX, _ = km.kmassign_experts_grad(dout, X, W, off, rows=order, slots=k, need_w=need_w)
+        assert ((dX.double() - ref).abs() <= OUT[dtype] * ref.abs() * 1.01 + (2 * F + k) * U * size + 2.0 ** -25).all()
+    # an error that is even over half a step either way has a root mean square of 1 / sqrt(3) of that at most
+    # (one rounding gives 0.42, one more of each product 0.60)
+    assert (dX.double() - ref).norm() <= 0.578 * OUT[dtype] * ref.norm()
+
+
+@pytest.mark.parametrize("N", [5, 600])
+def test_products_past_fp16_that_cancel(dev, N):  # noqa: F811
+    """Each position's product is beyond fp16's largest number, a point's sum is not."""
+    E, D, F = 2, 48, 128
+    g = gen_of(dev, N)
+    idx = torch.tensor([[0, 1]], device=dev).int().repeat(N, 1)
+    order, off = km.kmassign_lists(idx, E)
+    W = torch.empty(E, F, D, device=dev, dtype=FP16)
+    W[0], W[1] = 8, -8
+    W[1, 0] += ints(g, (D,), 5, FP16)
+    dout = torch.full((2 * N, F), 128.0, device=dev, dtype=FP16)
+    dX, dW = km.kmassign_experts_grad(dout, torch.ones(N, D, device=dev, dtype=FP16), W, off, rows=order, slots=2)
+    ref, size = exact_rows_gradient(dout, W, off, order, 2, N)
+    assert size.min() > 2 * 65504 and ref.abs().max() <= 640
+    assert torch.equal(dX, ref.to(FP16)) and (dW == 128 * N).all()
+
+
+@pytest.mark.parametrize("D", [1000, 776])
+def test_rows_gradients_of_many_positions(dev, D):  # noqa: F811
+    """Whole numbers, more columns and positions than are held at once."""
+    g = gen_of(dev, D)
+    E, N, k, F = 5, 40_000, 4, 16
+    order, off = km.kmassign_lists(torch.randint(-1, E, (N, k), generator=g, device=dev).int(), E)
+    W, dout = ints(g, (E, F, D), 4, BF16), ints(g, (N * k, F), 4, BF16)
+    ref, _ = exact_rows_gradient(dout, W, off, order, k, N)
+    X = torch.zeros(N, D, device=dev, dtype=BF16)
+    for need_w in (False, True):
+        dX, _ = km.kmassign_experts_grad(dout, X, W, off, rows=order, slots=k, need_w=need_w)
+        assert torch.equal(dX, ref.to(BF16))
