@@ -403,13 +403,8 @@ int kmassign_rmsnorm_grad(const void *dout, int32_t dtype, int64_t N, int64_t D,
     int sms;
     if ((rc = kma::library_device(&pool, &sms)) != KMASSIGN_OK)
         return rc;
-    Scratch scratch(dweight == nullptr ? 0 : kma::rmsnorm_grad_parts_bytes(N, D, sms), pool, st);
-    if (!scratch.ok())
-        return KMASSIGN_ERR_CUDA;
-    rc = done(kma::launch_rmsnorm_grad(dout, dtype, N, D, total, weight, weight_dtype, rstd, dtotal,
-                                       dX, dweight, reinterpret_cast<float *>(scratch.get()), sms,
-                                       st));
-    return scratch.release() ? rc : KMASSIGN_ERR_CUDA;
+    return done(kma::launch_rmsnorm_grad(dout, dtype, N, D, total, weight, weight_dtype, rstd,
+                                         dtotal, dX, dweight, pool, sms, st));
 }
 
 }  // extern "C"

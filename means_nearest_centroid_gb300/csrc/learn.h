@@ -199,10 +199,10 @@ cudaError_t launch_rmsnorm(const void *X, int dtype, int64_t N, int64_t D, const
                            const void *weight, int weight_dtype, float eps, void *total, void *out,
                            int out_dtype, float *scales, float *rstd, int sms,
                            cudaStream_t stream);
-size_t rmsnorm_grad_parts_bytes(int64_t N, int64_t D, int sms);
+// The weight's partial sums are an allocation of its own from the pool, if dweight is given.
 cudaError_t launch_rmsnorm_grad(const void *dout, int dtype, int64_t N, int64_t D,
                                 const void *total, const void *weight, int weight_dtype,
                                 const float *rstd, const void *dtotal, void *dX, float *dweight,
-                                float *parts, int sms, cudaStream_t stream);
+                                cudaMemPool_t pool, int sms, cudaStream_t stream);
 
 }  // namespace kma

@@ -517,43 +517,60 @@ int grad_groups(int64_t N, int warps, int elems, int sms)
         std::min<int64_t>(N, sms * static_cast<int64_t>(std::max(1, resident / warps))));
 }
 
-template <typename T, int VE, int NV>
-cudaError_t run_grad(const NormGradArgs &a, int sms, int *groups_out, cudaStream_t s)
+// The gradient's shape: vectors of ve elements, nv of them a thread, warps of a row,
+// groups of rows (and partial rows of the weight's gradient).
+struct GradShape {
+    int ve, nv, warps, groups;
+};
+
+GradShape grad_shape(const NormGradArgs &a, int dtype, int sms)
 {
-    const int warps = warps_for(a.D, VE * NV);
-    const int groups = grad_groups(a.N, warps, VE * NV, sms);
-    *groups_out = groups;
-    return launch_after(rmsnorm_grad_kernel<T, VE, NV>, warps == 1 ? (groups + 3) / 4 : groups,
-                        warps == 1 ? 128 : 32 * warps, 0, s, a, warps, groups);
+    const int most = 16 / dtype_bytes(dtype);
+    const bool wide = a.D % most == 0 && aligned16(a.dout) && aligned16(a.total) &&
+                      aligned16(a.weight) && aligned16(a.dtotal) && aligned16(a.dx);
+    GradShape g;
+    g.ve = wide ? most : 1;
+    g.nv = !wide       ? vectors_for<1>(a.N, a.D, 4, sms)
+           : most == 4 ? vectors_for<4>(a.N, a.D, 8, sms)
+                       : vectors_for<8>(a.N, a.D, 32, sms);
+    g.warps = warps_for(a.D, g.ve * g.nv);
+    g.groups = grad_groups(a.N, g.warps, g.ve * g.nv, sms);
+    return g;
+}
+
+template <typename T, int VE, int NV>
+cudaError_t run_grad(const NormGradArgs &a, const GradShape &g, cudaStream_t s)
+{
+    return launch_after(rmsnorm_grad_kernel<T, VE, NV>,
+                        g.warps == 1 ? (g.groups + 3) / 4 : g.groups,
+                        g.warps == 1 ? 128 : 32 * g.warps, 0, s, a, g.warps, g.groups);
 }
 
 template <typename T>
-cudaError_t grad_type(const NormGradArgs &a, int sms, int *groups, cudaStream_t s)
+cudaError_t grad_type(const NormGradArgs &a, const GradShape &g, cudaStream_t s)
 {
     constexpr int VE = 16 / sizeof(T);
-    const bool wide = a.D % VE == 0 && aligned16(a.dout) && aligned16(a.total) &&
-                      aligned16(a.weight) && aligned16(a.dtotal) && aligned16(a.dx);
-    if (!wide) {
-        switch (vectors_for<1>(a.N, a.D, 4, sms)) {
+    if (g.ve == 1) {
+        switch (g.nv) {
         case 4:
-            return run_grad<T, 1, 4>(a, sms, groups, s);
+            return run_grad<T, 1, 4>(a, g, s);
         case 16:
-            return run_grad<T, 1, 16>(a, sms, groups, s);
+            return run_grad<T, 1, 16>(a, g, s);
         default:
-            return run_grad<T, 1, 64>(a, sms, groups, s);
+            return run_grad<T, 1, 64>(a, g, s);
         }
     }
-    switch (vectors_for<VE>(a.N, a.D, VE == 4 ? 8 : 32, sms)) {
+    switch (g.nv) {
     case 1:
-        return run_grad<T, VE, 1>(a, sms, groups, s);
+        return run_grad<T, VE, 1>(a, g, s);
     case 2:
-        return run_grad<T, VE, 2>(a, sms, groups, s);
+        return run_grad<T, VE, 2>(a, g, s);
     case 4:
-        return run_grad<T, VE, 4>(a, sms, groups, s);
+        return run_grad<T, VE, 4>(a, g, s);
     case 8:
-        return run_grad<T, VE, 8>(a, sms, groups, s);
+        return run_grad<T, VE, 8>(a, g, s);
     default:
-        return run_grad<T, VE, 64 / VE>(a, sms, groups, s);
+        return run_grad<T, VE, 64 / VE>(a, g, s);
     }
 }
 
@@ -573,27 +590,26 @@ cudaError_t launch_rmsnorm(const void *X, int dtype, int64_t N, int64_t D, const
     return norm_type<__half>(a, codes, sms, stream);
 }
 
-size_t rmsnorm_grad_parts_bytes(int64_t N, int64_t D, int sms)
-{
-    return static_cast<size_t>(grad_groups(N, 1, 1, sms)) * D * sizeof(float);
-}
-
 cudaError_t launch_rmsnorm_grad(const void *dout, int dtype, int64_t N, int64_t D,
                                 const void *total, const void *weight, int weight_dtype,
                                 const float *rstd, const void *dtotal, void *dX, float *dweight,
-                                float *parts, int sms, cudaStream_t stream)
+                                cudaMemPool_t pool, int sms, cudaStream_t stream)
 {
-    int groups = 0;
-    const NormGradArgs a{dout, total, weight, dtotal, weight_dtype == kFp32,
-                         rstd, N,     static_cast<int32_t>(D), dX,
-                         dweight != nullptr ? parts : nullptr};
-    cudaError_t e = dtype == kFp32   ? grad_type<float>(a, sms, &groups, stream)
-                    : dtype == kBf16 ? grad_type<__nv_bfloat16>(a, sms, &groups, stream)
-                                     : grad_type<__half>(a, sms, &groups, stream);
+    NormGradArgs a{dout, total, weight, dtotal, weight_dtype == kFp32,
+                   rstd, N,     static_cast<int32_t>(D), dX, nullptr};
+    const GradShape g = grad_shape(a, dtype, sms);
+    Scratch parts(dweight == nullptr ? 0 : static_cast<size_t>(g.groups) * D * sizeof(float), pool,
+                  stream);
+    if (!parts.ok())
+        return cudaErrorMemoryAllocation;
+    a.parts = reinterpret_cast<float *>(parts.get());
+    cudaError_t e = dtype == kFp32   ? grad_type<float>(a, g, stream)
+                    : dtype == kBf16 ? grad_type<__nv_bfloat16>(a, g, stream)
+                                     : grad_type<__half>(a, g, stream);
     if (e == cudaSuccess && dweight != nullptr)
         e = launch_after(join_parts_kernel, static_cast<unsigned>((D + 31) / 32), 1024, 0, stream,
-                         parts, groups, static_cast<int>(D), dweight);
-    return e;
+                         a.parts, g.groups, static_cast<int>(D), dweight);
+    return parts.release() ? e : cudaErrorUnknown;
 }
 
 }  // namespace kma

@@ -2,12 +2,16 @@
 
 Tolerances and helpers are those of test_experts_gpu; whole numbers are compared bit for bit."""
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
 import means_nearest_centroid_gb300 as km
 from test_experts_gpu import (  # noqa: F401
-    BF16, E4M3, FP16, FP32, OUT, U, dev, gen_of, ints, no_kernel_gave_up)
+    BF16, E4M3, FP16, FP32, OUT, ROOT, U, dev, gen_of, ints, no_kernel_gave_up)
 
 pytestmark = pytest.mark.gpu
 
@@ -101,3 +105,34 @@ def test_rows_gradients_of_many_positions(dev, D):  # noqa: F811
     for need_w in (False, True):
         dX, _ = km.kmassign_experts_grad(dout, X, W, off, rows=order, slots=k, need_w=need_w)
         assert torch.equal(dX, ref.to(BF16))
+
+
+# ---- the norm's gradients -------------------------------------------------------------
+
+ROOM = """
+import sys
+import torch
+import means_nearest_centroid_gb300 as km
+for N, D, dtype in ((6000, 32768, torch.bfloat16), (6000, 16384, torch.float32), (6000, 7168, torch.bfloat16)):
+    x = torch.ones(N, D, device="cuda", dtype=dtype)
+    dx, w, dw = torch.empty_like(x), torch.ones(D, device="cuda"), torch.empty(D, device="cuda")
+    rstd = torch.ones(N, device="cuda")
+    small = torch.ones(8, 8, device="cuda", dtype=dtype)
+    km.kmassign_rmsnorm_grad(x, x, None, rstd, dX=dx)
+    km.kmassign_rmsnorm_grad(small, small, w[:8], rstd[:8])
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    km.kmassign_rmsnorm_grad(x, x, w, rstd, dX=dx, dweight=dw)
+    torch.cuda.synchronize()
+    print(free - torch.cuda.mem_get_info()[0])
+"""
+
+
+def test_the_weight_s_partial_sums_take_little_room(dev):  # noqa: F811
+    """A row of partial sums for each group of rows in flight: of these long rows up to four groups an SM,
+    150 rows to 610 of 28 to 128 KB, 20 MB at most."""
+    out = subprocess.run([sys.executable, "-c", ROOM], cwd=ROOT, env=dict(os.environ, PYTHONPATH=ROOT), capture_output=True,
+                         text=True, timeout=300)
+    assert out.returncode == 0, out.stderr[-2000:]
+    used = [int(line) for line in out.stdout.split()]
+    assert len(used) == 3 and max(used) <= 72 << 20, used
