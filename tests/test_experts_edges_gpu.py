@@ -11,7 +11,7 @@ import torch
 
 import means_nearest_centroid_gb300 as km
 from test_experts_gpu import (  # noqa: F401
-    BF16, E4M3, FP16, FP32, OUT, ROOT, U, dev, gen_of, ints, no_kernel_gave_up)
+    BF16, E4M3, FP16, FP32, OUT, ROOT, U, dev, gen_of, ints, no_kernel_gave_up, offsets_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -109,6 +109,20 @@ def test_rows_gradients_of_many_positions(dev, D):  # noqa: F811
 
 # ---- the norm's gradients -------------------------------------------------------------
 
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16], ids=str)
+@pytest.mark.parametrize("N,D", [(1, 40), (12000, 40), (12000, 33), (3000, 500), (4000, 129), (11000, 256), (5000, 2048),
+                                 (700, 8200), (2000, 777)])
+def test_weights_gradient_of_whole_numbers_comes_out_exactly(dev, N, D, dtype):  # noqa: F811
+    """rstd are powers of two and the sums fit 24 bits, so that a row that is left out or counted twice shows."""
+    g = gen_of(dev, N + D)
+    x, dout = ints(g, (N, D), 3, dtype), ints(g, (N, D), 3, dtype)
+    rstd = 2.0 ** ints(g, (N,), 1, FP32)
+    w = torch.ones(D, device=dev)
+    ref = (dout.double() * x.double() * rstd.double()[:, None]).sum(0)
+    _, dw = km.kmassign_rmsnorm_grad(dout, x, w, rstd)
+    assert torch.equal(dw.double(), ref)
+
+
 ROOM = """
 import sys
 import torch
@@ -136,3 +150,39 @@ def test_the_weight_s_partial_sums_take_little_room(dev):  # noqa: F811
     assert out.returncode == 0, out.stderr[-2000:]
     used = [int(line) for line in out.stdout.split()]
     assert len(used) == 3 and max(used) <= 72 << 20, used
+
+
+# ---- 8 bits -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("N,D", [(300, 128), (4001, 1000), (64, 16384), (2000, 777), (3, 20000)])
+@pytest.mark.parametrize("bits", [3, 8, 24])
+def test_codes_are_the_quotients_rounded_to_nearest(dev, N, D, bits):  # noqa: F811
+    """Values of few bits, whose quotients are often between two codes; blocks of every size."""
+    g = gen_of(dev, N + D + bits)
+    x = torch.randn(N, D, generator=g, device=dev) if bits == 24 else ints(g, (N, D), 2 ** bits, FP32)
+    for w in (torch.ones(D, device=dev), 2.0 ** torch.randint(-110, 100, (D,), generator=g, device=dev).float(),
+              2.0 ** -100 * torch.rand(D, generator=g, device=dev), torch.randn(D, generator=g, device=dev)):
+        y, _, _, rstd = km.kmassign_rmsnorm(x, w)
+        codes, scales, _, same = km.kmassign_rmsnorm(x, w, dtype=E4M3)
+        nb = -(-D // 128)
+        tops = torch.nn.functional.pad(y, (0, nb * 128 - D)).view(N, nb, 128).abs().amax(-1).clamp(min=2.0 ** -100)
+        assert torch.equal(rstd, same) and torch.equal(scales, tops / torch.full_like(tops, 448))
+        want = (y / scales.repeat_interleave(128, 1)[:, :D]).to(E4M3)
+        assert torch.equal(codes.float(), want.float())
+
+
+@pytest.mark.parametrize("D", [144, 1040, 2048])
+def test_in_8_bits_a_row_s_bits_depend_on_nothing_else(dev, D):  # noqa: F811
+    """Alone, among few and among many: other kernels, the same sums."""
+    g = gen_of(dev, D)
+    F, nb = 136, -(-D // 128)
+    X = torch.randn(600, D, generator=g, device=dev).to(E4M3)
+    W = torch.randn(3, F, D, generator=g, device=dev).to(E4M3)
+    xs, ws = torch.rand(600, nb, generator=g, device=dev), torch.rand(3, 2, nb, generator=g, device=dev)
+    kw = dict(wscale=ws, dtype=FP32)
+    many = km.kmassign_experts(X, W, offsets_of([0, 600, 0], dev), xscale=xs, **kw)
+    few = km.kmassign_experts(X[:50], W, offsets_of([0, 50, 0], dev), xscale=xs[:50], **kw)
+    one = km.kmassign_experts(X[49:50], W[1], xscale=xs[49:50], wscale=ws[1], dtype=FP32)
+    rows = torch.arange(600, device=dev).flip(0).int()
+    back = km.kmassign_experts(X, W, offsets_of([0, 600, 0], dev), rows=rows, xscale=xs, **kw)
+    assert torch.equal(many[:50], few) and torch.equal(many[49:50], one) and torch.equal(back.flip(0), many)
