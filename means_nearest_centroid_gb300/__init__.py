@@ -416,7 +416,8 @@ def kmassign_lloyd(X, C, iters: int, idx=None, stream=None):
 # ---- learned assignments: routing, lookup, inverted lists, clipping ----------
 #
 # These calls are not recorded by autograd.  In grad mode they refuse inputs that
-# require grad (but for the bias, which the weights do not depend on).
+# require grad (but for the bias, which the weights do not depend on), and in any
+# mode inputs with a forward-mode tangent.
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _SCORES = {"softmax": 0, "sigmoid": 1}
@@ -445,6 +446,20 @@ def _need_detached(where, name):
             "under torch.no_grad() or in a torch.autograd.Function (gradients: "
             "kmassign_route_grad, kmassign_lookup_grad, kmassign_experts_grad, "
             "kmassign_rmsnorm_grad)")
+
+
+_forward_ad = torch.autograd.forward_ad
+
+
+def _need_no_tangent(where, *tensors):
+    """Raises for an input with a forward-mode tangent (also under no_grad, where torch keeps them)."""
+    if getattr(_forward_ad, "_current_level", 0) < 0:   # the common case: no forward mode
+        return
+    for t in tensors:
+        if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+            raise RuntimeError(
+                f"{where}: an input carries a forward-mode tangent, and the result would carry "
+                "none; call it with the primal or in a torch.autograd.Function with a jvp")
 
 
 # Tells autograd that a call wrote to these tensors of the caller, as torch's in-place operations
@@ -506,6 +521,7 @@ def kmassign_route(logits, k: int, score: str = "softmax", bias=None, groups: in
     N, E = _need_matrix(logits, "logits")
     if logits.requires_grad:
         _need_detached("kmassign_route", "logits")
+    _need_no_tangent("kmassign_route", logits)
     k, groups = int(k), int(groups)
     if bias is not None:
         _need_cuda(bias, "bias", torch.float32)
@@ -550,6 +566,7 @@ def kmassign_route_grad(logits, idx, dweights, score: str = "softmax", renorm: b
     _need_shape(dweights, "dweights", (N, k))
     if logits.requires_grad or dweights.requires_grad:
         _need_detached("kmassign_route_grad", "logits or dweights")
+    _need_no_tangent("kmassign_route_grad", logits, dweights)
     given = dlogits is not None
     if not given:
         dlogits = _new((N, E), logits.dtype, logits.device, stream)
@@ -611,6 +628,7 @@ def kmassign_lookup(table, idx, weights=None, scale: float = 1.0, out=None, stre
         _need_shape(weights, "weights", idx.shape)
     if table.requires_grad or (weights is not None and weights.requires_grad):
         _need_detached("kmassign_lookup", "table or weights")
+    _need_no_tangent("kmassign_lookup", table, weights)
     given = out is not None
     if not given:
         out = _new((N, D), table.dtype, table.device, stream)
@@ -662,6 +680,7 @@ def kmassign_lookup_grad(dout, idx, K: int, weights=None, table=None, scale: flo
     if dout.requires_grad or (weights is not None and
                               (weights.requires_grad or table.requires_grad)):
         _need_detached("kmassign_lookup_grad", "dout, weights or table")
+    _need_no_tangent("kmassign_lookup_grad", dout, weights, None if weights is None else table)
     if dtable is None:
         if accumulate:
             raise ValueError("accumulate needs a given dtable")
@@ -707,6 +726,8 @@ def _tensor_arrays(tensors, where, name):
         plain = False
     if not plain:
         codes = _need_floats(tensors, where, name)
+    if getattr(_forward_ad, "_current_level", 0) >= 0:
+        _need_no_tangent(where, *tensors)
     return (array.array("Q", list(map(_pointer, tensors))),
             array.array("q", list(map(_size, tensors))), array.array("i", codes))
 
@@ -861,6 +882,7 @@ def kmassign_experts(X, W, offsets=None, rows=None, slots: int = 1, places=None,
     if X.requires_grad or W.requires_grad or (
             code == 3 and (xscale.requires_grad or wscale.requires_grad)):
         _need_detached("kmassign_experts", "X, W or a scale")
+    _need_no_tangent("kmassign_experts", X, W, xscale, wscale)
     given = out is not None
     if not given:
         out = _new((M, F), dtype or (torch.bfloat16 if code == 3 else X.dtype), X.device, stream,
@@ -910,6 +932,7 @@ def kmassign_experts_grad(dout, X, W, offsets=None, rows=None, slots: int = 1, p
         raise ValueError("a gradient is given but not needed")
     if dout.requires_grad or X.requires_grad or W.requires_grad:
         _need_detached("kmassign_experts_grad", "dout, X or W")
+    _need_no_tangent("kmassign_experts_grad", dout, X, W)
     given = dX, dW
     if dX is not None:
         _need_cuda(dX, "dX", X.dtype)
@@ -970,6 +993,7 @@ def kmassign_rmsnorm(X, weight=None, residual=None, eps: float = 1e-6, dtype=Non
     if X.requires_grad or (weight is not None and weight.requires_grad) or (
             residual is not None and residual.requires_grad):
         _need_detached("kmassign_rmsnorm", "X, weight or residual")
+    _need_no_tangent("kmassign_rmsnorm", X, weight, residual)
     given = [t for t in (out, scales, total, rstd) if t is not None]
     if dtype is None:
         dtype = X.dtype if out is None else out.dtype
@@ -1033,6 +1057,7 @@ def kmassign_rmsnorm_grad(dout, total, weight, rstd, dtotal=None, dX=None, dweig
             weight is not None and weight.requires_grad) or (
             dtotal is not None and dtotal.requires_grad):
         _need_detached("kmassign_rmsnorm_grad", "an input")
+    _need_no_tangent("kmassign_rmsnorm_grad", dout, total, weight, rstd, dtotal)
     given = [t for t in (dX, dweight) if t is not None]
     if dX is None:
         dX = _new((N, D), total.dtype, total.device, stream)

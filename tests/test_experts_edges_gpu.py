@@ -186,3 +186,35 @@ def test_in_8_bits_a_row_s_bits_depend_on_nothing_else(dev, D):  # noqa: F811
     rows = torch.arange(600, device=dev).flip(0).int()
     back = km.kmassign_experts(X, W, offsets_of([0, 600, 0], dev), rows=rows, xscale=xs, **kw)
     assert torch.equal(many[:50], few) and torch.equal(many[49:50], one) and torch.equal(back.flip(0), many)
+
+
+# ---- how calls are made -----------------------------------------------------------------
+
+def test_calls_refuse_forward_mode_tangents(dev):  # noqa: F811
+    """Any input that a result depends on, also under no_grad; a primal beside a dual level is taken."""
+    X, W = torch.ones(6, 16, device=dev, dtype=BF16), torch.ones(2, 8, 16, device=dev, dtype=BF16)
+    q, v, s, t = X.to(E4M3), W.to(E4M3), torch.ones(6, 1, device=dev), torch.ones(2, 1, 1, device=dev)
+    off, d = torch.tensor([0, 3, 6], device=dev).int(), torch.ones(6, 8, device=dev, dtype=BF16)
+    idx, w, rstd = torch.zeros(6, 1, device=dev).int(), torch.ones(6, 1, device=dev), torch.ones(6, device=dev)
+    calls = [
+        (lambda a, b: km.kmassign_experts(a, b, off), X, W),
+        (lambda a, b: km.kmassign_experts(q, v, off, xscale=a, wscale=b), s, t),
+        (lambda a, b, c: km.kmassign_experts_grad(a, b, c, off), d, X, W),
+        (lambda a, b, c: km.kmassign_rmsnorm(a, b, residual=c), X, W[0, 0], X),
+        (lambda a, b, c, e, f: km.kmassign_rmsnorm_grad(a, b, c, e, dtotal=f), X, X, W[0, 0], rstd, X),
+        (lambda a: km.kmassign_route(a, 2), X),
+        (lambda a, b: km.kmassign_route_grad(a, idx, b), X, w),
+        (lambda a, b: km.kmassign_lookup(a, idx, weights=b), X, w),
+        (lambda a, b, c: km.kmassign_lookup_grad(a, idx, 6, weights=b, table=c), X, w, X),
+        (lambda a: km.kmassign_grad_norm([rstd, a]), X),
+        (lambda a: km.kmassign_clip([rstd.clone(), a], 1.0), X.clone()),
+    ]
+    forward = torch.autograd.forward_ad
+    with forward.dual_level():
+        for call, *args in calls:
+            call(*args)
+            for i, x in enumerate(args):
+                dual = args[:i] + [forward.make_dual(x, torch.ones_like(x))] + args[i + 1:]
+                for mode in (torch.no_grad, torch.enable_grad):
+                    with mode(), pytest.raises(RuntimeError, match="tangent"):
+                        call(*dual)

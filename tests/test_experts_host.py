@@ -135,3 +135,28 @@ def test_host_tensors_are_refused(call):
             call(x)
     with pytest.raises(TypeError):
         call([[1.0]])
+
+
+def test_forward_mode_tangents_are_refused():
+    """Also under no_grad, which keeps them; not where a Function's own jvp takes over."""
+    forward = torch.autograd.forward_ad
+    x = torch.ones(3)
+    km._need_no_tangent("here", x, None)
+    with forward.dual_level():
+        dual = forward.make_dual(x, x)
+        km._need_no_tangent("here", x, None, forward.unpack_dual(dual).primal)
+        for mode in (torch.no_grad, torch.enable_grad):
+            with mode(), pytest.raises(RuntimeError, match="here.*tangent"):
+                km._need_no_tangent("here", x, None, dual)
+
+        class Own(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x):
+                km._need_no_tangent("here", x)
+                return 2 * x
+
+            @staticmethod
+            def jvp(ctx, t):
+                return 2 * t
+        assert torch.equal(forward.unpack_dual(Own.apply(dual)).tangent, 2 * x)
+    km._need_no_tangent("here", dual)
