@@ -186,7 +186,7 @@ __device__ void form_lists(const ExpertsParams &p, int32_t *lists, int lane)
             const int e = first + i;
             at[i] = e > p.E               ? p.M
                     : p.offsets == nullptr ? (e == 0 ? 0 : p.M)
-                                           : min(max(__ldg(p.offsets + e), 0), p.M);
+                                           : min(max(p.offsets[e], 0), p.M);
         }
 #pragma unroll
         for (int i = 0; i < kEach; ++i)
@@ -244,7 +244,7 @@ __device__ __forceinline__ int32_t row_of(const RowMap &m, int32_t at, int32_t h
         return -1;
     if (m.ids == nullptr)
         return at;
-    const int32_t id = __ldg(m.ids + at);
+    const int32_t id = m.ids[at];
     if (id < 0)
         return -1;
     const int32_t row = m.slots == 1 ? id : id / m.slots;
@@ -683,11 +683,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < kScaleGroup; ++j) {
                             const int kb = min(k0 + j, w.kblocks - 1);
-                            one[j] = __ldg(ws + kb);
+                            one[j] = ws[kb];
 #pragma unroll
                             for (int i = 0; i < kPer; ++i)
                                 v[j][i] =
-                                    __ldg(p.xscale + static_cast<int64_t>(row[i]) * w.kblocks + kb);
+                                    p.xscale[static_cast<int64_t>(row[i]) * w.kblocks + kb];
                         }
                         if (!(ok = wait(kScE + s, ((n / kScaleStages) & 1u) ^ 1u)))
                             break;
@@ -1083,12 +1083,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 128; ++i)
                 sum[i] = 0.0f;
-            float x_next = __ldg(xs), w_next = __ldg(ws);
+            float x_next = *xs, w_next = *ws;
             for (int kb = 0; kb < p.kblocks; ++kb, ++acc) {
                 const float scale = x_next * w_next;
                 if (kb + 1 < p.kblocks) {
-                    x_next = __ldg(xs + kb + 1);
-                    w_next = __ldg(ws + kb + 1);
+                    x_next = xs[kb + 1];
+                    w_next = ws[kb + 1];
                 }
                 const uint32_t as = acc & 1u;
                 if (!(ok = wait(kAccF + as, (acc >> 1) & 1u)))
@@ -1145,8 +1145,8 @@ __global__ void __launch_bounds__(256)
     wait_for_previous();
     if (zero != nullptr && blockIdx.x == 0 && threadIdx.x == 0)
         *zero = 0;
-    const int32_t lo = offsets == nullptr ? 0 : min(max(__ldg(offsets), 0), M);
-    const int32_t hi = offsets == nullptr ? M : min(max(__ldg(offsets + E), 0), M);
+    const int32_t lo = offsets == nullptr ? 0 : min(max(offsets[0], 0), M);
+    const int32_t hi = offsets == nullptr ? M : min(max(offsets[E], 0), M);
     for (int64_t at = blockIdx.x * 256 + threadIdx.x; at < M; at += gridDim.x * 256)
         row[at] = at < lo ? -1 : row_of(map, static_cast<int32_t>(at), hi);
 }
@@ -1163,8 +1163,8 @@ __global__ void __launch_bounds__(256)
 {
     wait_for_previous();
     let_next_start();
-    const int32_t lo = offsets == nullptr ? 0 : min(max(__ldg(offsets), 0), M);
-    const int32_t hi = offsets == nullptr ? M : min(max(__ldg(offsets + E), 0), M);
+    const int32_t lo = offsets == nullptr ? 0 : min(max(offsets[0], 0), M);
+    const int32_t hi = offsets == nullptr ? M : min(max(offsets[E], 0), M);
     const int32_t mine = threadIdx.x & (lanes - 1);
     const int32_t rows = 256 / lanes;
     const int64_t at = blockIdx.x * static_cast<int64_t>(rows) + threadIdx.x / lanes;
@@ -1186,14 +1186,14 @@ __global__ void __launch_bounds__(256)
                 uint4 v[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    v[k] = __ldg(src + u + k * lanes);
+                    v[k] = src[u + k * lanes];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     __stcs(dst + u + k * lanes, v[k]);
             }
         }
         for (; u < units; u += lanes)
-            dst[u] = row >= 0 ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+            dst[u] = row >= 0 ? src[u] : make_uint4(0, 0, 0, 0);
     }
 }
 

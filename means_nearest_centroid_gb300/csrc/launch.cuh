@@ -2,6 +2,10 @@
 // start its set-up while the kernel before it in the stream still runs, and
 // calls wait_for_previous() before it touches anything that kernel wrote (or
 // reads).  A kernel that lets its successor do so calls let_next_start().
+//
+// A kernel so launched may be running while its inputs are still written.  It
+// reads them with plain loads: __ldg (and const __restrict__) would promise that
+// they do not change while it runs, which lets the compiler move the loads.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThreads) lists_scatter_kernel(const SortArgs 
 // memory.  The first digit's pass drops ids outside [0, K).
 template <int THREADS, int ITEMS>
 __global__ void __launch_bounds__(THREADS)
-    lists_one_block_kernel(const int32_t *__restrict__ idx, int32_t M, int32_t K, int32_t bits,
+    lists_one_block_kernel(const int32_t *idx, int32_t M, int32_t K, int32_t bits,
                            int32_t *__restrict__ order, int32_t *__restrict__ rows,
                            int32_t *__restrict__ offsets, int32_t *__restrict__ total, Fill fill)
 {
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(THREADS)
             pos[u] = i;
             if (u < items && i < n) {
                 if (shift == 0) {
-                    const int32_t r = __ldg(idx + i);
+                    const int32_t r = idx[i];
                     row[u] = r >= 0 && r < K ? r : -1;
                 } else {
                     row[u] = s_row[i];
@@ -520,7 +520,7 @@ __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kCluste
                 if (pass > 0) {
                     item[u] = pairs[i];
                 } else {
-                    const int32_t r = __ldg(a.idx + block * kShare + i);
+                    const int32_t r = a.idx[block * kShare + i];
                     if (r >= 0 && r < a.K)
                         item[u].x = r;
                 }

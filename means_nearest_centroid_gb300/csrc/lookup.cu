@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, VE == 1 ? 2 : 3) segment_kernel(cons
         const int64_t threads = static_cast<int64_t>(gridDim.x) * kThreads;
         for (int64_t f = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; f < a.M;
              f += threads)
-            if (static_cast<uint32_t>(__ldg(a.idx + f)) >= static_cast<uint32_t>(a.K))
+            if (static_cast<uint32_t>(a.idx[f]) >= static_cast<uint32_t>(a.K))
                 a.dweights[f] = 0.0f;
     }
     const int lane = threadIdx.x & (LG - 1);
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, VE == 1 ? 2 : 3) segment_kernel(cons
             f = a.order[s];
             row = a.rows[s];
             point = a.k == 1 ? f : f / a.k;
-            w = a.weights != nullptr ? __ldg(a.weights + f) : 1.0f;
+            w = a.weights != nullptr ? a.weights[f] : 1.0f;
         }
         const int n = min(LG, a.chunk - s0);
         for (int u0 = 0; u0 < n; u0 += U) {

@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(512, VE * NV <= 8 ? 2 : 1)
     }
     const auto load_row = [&](GradRow<T, VE, NV> &r, int64_t row) {
         const int64_t at = row * a.D;
-        r.rstd = __ldg(a.rstd + row);
+        r.rstd = a.rstd[row];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int col = column<VE>(j, warps, warp, lane);

@@ -2,6 +2,8 @@
 comes back before anything touches CUDA."""
 
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -160,3 +162,21 @@ def test_forward_mode_tangents_are_refused():
                 return 2 * t
         assert torch.equal(forward.unpack_dual(Own.apply(dual)).tangent, 2 * x)
     km._need_no_tangent("here", dual)
+
+
+def test_kernels_that_start_early_use_plain_loads():
+    """A kernel that may start before the one in front of it ends runs while its inputs are written: loads that
+    promise constant memory for as long as it runs (__ldg, const __restrict__) are not for it."""
+    csrc = os.path.join(os.path.dirname(km.__file__), "csrc")
+    early = 0
+    for name in sorted(os.listdir(csrc)):
+        with open(os.path.join(csrc, name)) as f:
+            helpers, *kernels = f.read().split("__global__")
+        starts = ["wait_for_previous()" in k for k in kernels]
+        early += sum(starts)
+        if kernels and all(starts):
+            assert "__ldg" not in helpers, name
+        for kernel, is_early in zip(kernels, starts):
+            if is_early:
+                assert not re.search(r"__ldg|ld\.global\.nc|const \w+ \*__restrict__", kernel), (name, kernel[:120])
+    assert early >= 16
