@@ -259,13 +259,16 @@ __device__ __forceinline__ bool missing(const ExpertsParams &p, int32_t at, int3
     return row_of(p.from, at, hi) < 0 || row_of(p.placed, at, hi) < 0;
 }
 
-// Copies in flight may complete on the other CTA's barriers, out of this one's
-// sight: after a wait has run out they get time to land (they take
-// microseconds) before either CTA leaves.
-__device__ __forceinline__ void let_copies_land()
+// After a wait has run out: no warp of the CTA issues copies any more (one thread calls
+// this behind the block's barrier), but some may be in flight, and they complete on the
+// leader's barriers, whose phases need both CTAs' copies of a stage and may never end.
+// They get as long as the bound that ran out, from 1 ms to the teardown's limit, before
+// either CTA leaves.  (All CTAs' rings are 48 MB at most, 8 us at HBM's rate.)
+__device__ __forceinline__ void let_copies_land(uint64_t bound_ns)
 {
+    const uint64_t limit = min(max(bound_ns, uint64_t(1000000)), kDrainLimitNs);
     const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < 1000000ull) {
+    while (globaltimer_ns() - t0 < limit) {
     }
 }
 
@@ -800,10 +803,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
 
-    if (threadIdx.x == 0 && *abort_flag)
-        let_copies_land();
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag)
+        let_copies_land(p.timeout_ns);
     cluster_sync();   // no CTA leaves while its pair can still touch its memory
     if (warp == kWarpMma) {
         tc_fence_after();
@@ -1127,10 +1130,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
 
-    if (threadIdx.x == 0 && *abort_flag)
-        let_copies_land();
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag)
+        let_copies_land(p.timeout_ns);
     cluster_sync();   // no CTA leaves while its pair can still touch its memory
     if (warp == kLoad8) {
         tc_fence_after();

@@ -218,3 +218,28 @@ def test_calls_refuse_forward_mode_tangents(dev):  # noqa: F811
                 for mode in (torch.no_grad, torch.enable_grad):
                     with mode(), pytest.raises(RuntimeError, match="tangent"):
                         call(*dual)
+
+
+def test_weights_gradient_with_a_short_wait_bound(dev):  # noqa: F811
+    """A wait of its that runs out is reported, whole and cut k-blocks alike, and the next call is right. (Segments
+    of 32 k-blocks: see the test of the other products.)"""
+    g = gen_of(dev, 7)
+    E, per, D, F = 8, 8200, 2048, 1024
+    M = E * per
+    X, W, d = ints(g, (M, D), 1, BF16), torch.zeros(E, F, D, device=dev, dtype=BF16), ints(g, (M, F), 1, BF16)
+    off = offsets_of([per] * E, dev)
+    rows = torch.arange(M, device=dev).int()
+    rows[::97] = -1
+    for kw in (dict(), dict(rows=rows)):
+        def call():
+            return km.kmassign_experts_grad(d, X, W, off, need_x=False, dtype=BF16, **kw)[1]
+        want = call()
+        try:
+            km.kmassign_set_wait_timeout(100)
+            call()
+            rc = km.kmassign_check()
+        finally:
+            km.kmassign_set_wait_timeout(0)
+        assert rc == km.STATUS["KMASSIGN_ERR_TIMEOUT"], km.kmassign_strerror(rc)
+        assert km.kmassign_check() == 0
+        assert torch.equal(call(), want) and km.kmassign_check() == 0
