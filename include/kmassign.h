@@ -525,7 +525,8 @@ int kmassign_clip(const void *const *grads, void *const *out, const int64_t *siz
  *             zeros
  *   places    int32 [M] or NULL (M <= out_rows): position p goes to row p.  Ids
  *             outside [0, out_rows) are not written, and rows that no position
- *             names stay as they were; an id named twice holds either product
+ *             names stay as they were; in a row named twice each element is that of
+ *             either product
  *   out       out_dtype [out_rows, F]: X's type or KMASSIGN_FP32; any of the three
  *             types in 8 bits.  Without places the rows of positions of no list
  *             (before offsets[0], from offsets[E] to M) are zeros; rows past M
@@ -572,8 +573,9 @@ int kmassign_experts_grad(const void *dout, int32_t dtype, int64_t out_rows, int
  *                residual themselves)
  *   out          y as dtype (may be X, or total), or as KMASSIGN_E4M3 codes with
  *   scales       fp32 [N, ceil(D / 128)], written: the largest |y| of each 128
- *                columns (at least 2^-100) / 448; code = e4m3(y / scale), to
- *                nearest.  This is kmassign_experts' xscale
+ *                columns (NaN passed over, at least 2^-100) / 448; code = e4m3(y /
+ *                scale), to nearest, of the fp32 y.  This is kmassign_experts'
+ *                xscale
  *   rstd         fp32 [N], written, or NULL
  * Sums are fp32 (t^2 has to stay in fp32's range).  N = 0 launches nothing.
  * Errors: D KMASSIGN_ERR_UNSUPPORTED_D; types, or eps negative or not finite

@@ -823,9 +823,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // element needs its column's scale out of shared memory, and the rest of a
 // segment's hand-over does not hide that: 32,768 positions in 8 lists, 4,096 x
 // 4,096, took 700 us, here 518, 2,120 TFLOP/s.)  What bounds it: a k-block takes
-// 1,140 clocks, of which its MMAs are 512; the rest is the loads of the
-// accumulator, which the MMAs do not overlap (a tile of 128 columns takes 730: 320
-// clocks for a segment's hand-over and 3.2 a column, where the MMAs take 2).  As
+// 1,140 clocks, of which its MMAs are 512; the rest is taken for the loads of the
+// accumulator, which the MMAs would not overlap (a tile of 128 columns takes 730, which
+// gives 320 clocks for a segment's hand-over and 3.2 a column, where the MMAs take 2).  As
 // long: two CTAs with MMAs and hand-overs of their own and the weights multicast
 // (537 us), scales loaded four k-blocks at a time (558), 64 columns in flight a
 // warp (605).  Slower: 128 columns and four accumulators (667).  Lists are rounded
@@ -1157,9 +1157,9 @@ __global__ void __launch_bounds__(256)
 // Rows in the lists' order: to[p] = the row that map names for position p,
 // zeros where there is none in map or in also (*holes is then set, if given).
 // A power of two of lanes a row, up to four 16-byte pieces in flight a lane.
-// Bound by L2, which every byte crosses twice (131,072 rows of 4,096 bytes of a
-// matrix of 16,384: 120 us, 8.9 TB/s; bulk copies through shared memory 147);
-// streaming stores leave the matrix in L2 (with plain ones 129).
+// Bound by HBM, for the most part by what it writes (131,072 rows of 4,096 bytes of a
+// matrix of 16,384: 118 us for 604 MB, DRAM 79% busy, L2 46%; bulk copies through shared
+// memory 147); streaming stores leave the matrix in L2 (with plain ones 129).
 __global__ void __launch_bounds__(256)
     gather_rows_kernel(const int32_t *offsets, int32_t E, int32_t M, RowMap map, RowMap also,
                        const uint4 *from, int32_t units, int32_t lanes, uint4 *to, int32_t *holes)
@@ -1267,7 +1267,9 @@ cudaError_t experts_prepare(size_t smem_optin)
 // Rows by ids, 64 lists of 32 / 64 positions of 2,048 in 16 bits, 1,024 columns:
 // narrow tiles 50 / 63 us, wide ones behind a pass that gathers the rows 55 / 60.
 // In 8 bits, 64 / 96 positions: narrow 40 / 58, positions as rows 52 / 54 (256
-// lists: 131 / 212 and 171 / 180).
+// lists: 131 / 212 and 171 / 180).  The rule knows the mean length only: 8,192 positions
+// of 256 lists take 186 us by narrow and 187 by wide tiles where all lists have some, but
+// 135 and 72 on 64 of them, 105 and 35 on one (8 bits 115 and 166, 86 and 62, 66 and 34).
 bool experts_few(int64_t M, int64_t E, bool e8) { return M <= (e8 ? 64 : 32) * E; }
 
 cudaError_t launch_experts(ExpertsKind kind, bool e8, int type, const CUtensorMap &a,

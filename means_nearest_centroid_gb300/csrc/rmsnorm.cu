@@ -5,11 +5,12 @@
 //   8 bits: for each block of 128 columns scale = max |y| / 448, codes e4m3(y / scale)
 //   g = w dy,  dx = rstd (g - t rstd mean(g t rstd)) + dt,  dw = sum over rows of dy t rstd
 //
-// Both are bound by memory: every element crosses HBM once in each direction
-// (65,536 x 2,048 bf16: residual added, to 8 bits 137 us, 6.9 TB/s; gradients with
-// the residual's 165 us, 6.5 TB/s, of which the partial rows of the weight's take 8).
-// The gradient is near the issue rate: with single products and elements widened
-// one by one it took 188 us at 1,030 instructions a warp and row of 32 a lane.
+// Every element crosses HBM once in each direction.  The norm is bound by that (65,536
+// x 2,048 bf16, residual added, to 8 bits: 137 us, 6.9 TB/s, DRAM 84% busy).  The
+// gradient with the residual's takes 178 us there (6.0 TB/s; 165 in calls on the same
+// tensors), of which the partial rows of the weight's are 8; neither DRAM (62% busy) nor
+// the issue slots (54%) are full with the 16 warps an SM that its 128 registers allow.
+// With single products and elements widened one by one the 165 us were 178.
 // Rows at odd addresses are read element by element (30,011 x 777 fp32 gradients 60
 // us, 4.7 TB/s; by aligned vectors, ends apart and the weight moved, 110).
 // A row lives in the registers of one warp, or of the warps of one block where
