@@ -107,6 +107,20 @@ def test_rows_gradients_of_many_positions(dev, D):  # noqa: F811
         assert torch.equal(dX, ref.to(BF16))
 
 
+@pytest.mark.parametrize("M,D", [(1, 8), (77, 8), (3000, 24), (160_000, 1000)])
+def test_rows_gradients_of_rows_named_by_many(dev, M, D):  # noqa: F811
+    """Three of a hundred rows take every position: sums that span the chunks of both halves of the columns."""
+    g = gen_of(dev, M + D)
+    E, F, R = 3, 16, 100
+    rows = torch.tensor([0, 57, 99], device=dev).int()[torch.randint(0, 3, (M,), generator=g, device=dev)]
+    off = offsets_of([M // 3, 0, M - M // 3], dev)
+    W, dout = ints(g, (E, F, D), 2, BF16), ints(g, (M, F), 2, BF16)
+    ref, size = exact_rows_gradient(dout, W, off, rows, 1, R)
+    assert size.max() < 2 ** 24
+    dX, _ = km.kmassign_experts_grad(dout, torch.zeros(R, D, device=dev, dtype=BF16), W, off, rows=rows, need_w=False)
+    assert torch.equal(dX, ref.to(BF16))
+
+
 # ---- the norm's gradients -------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", [FP32, BF16, FP16], ids=str)
